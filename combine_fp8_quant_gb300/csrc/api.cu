@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/moeperm.h"
+#include "api_util.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -139,19 +140,6 @@ using namespace moeperm;
 
 namespace {
 
-constexpr int kMaxK = 32;
-constexpr int kMaxL = 1024;
-constexpr int64_t kMaxAssignments = int64_t(1) << 20;
-constexpr int kMaxHidden = 32768;   // one pass of 2 chunks x 1024 threads per row
-constexpr size_t kWsHeader = 256;  // reserved header before the chunk table
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int num_sms_cached() {
-  int n = 0;
-  return device_attr_cached(cudaDevAttrMultiProcessorCount, &n) == cudaSuccess ? n : 0;
-}
-
 bool fmt_ok(int fmt, int g) {
   if (g == 128) return fmt == MOE_SCALE_UE8M0_U8 || fmt == MOE_SCALE_UE8M0_PACKED ||
                        fmt == MOE_SCALE_F32_POW2 || fmt == MOE_SCALE_F32;
@@ -164,8 +152,6 @@ bool ld_ok(int fmt, int64_t ld, int64_t rows_per_block, int G) {
   if (fmt == MOE_SCALE_UE8M0_PACKED) return ld >= rows_per_block && ld % 4 == 0 && ld > 0;
   return ld >= G;
 }
-
-moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
 struct DispatchCommon {
   const void* x; int64_t ldx; int32_t T; const int32_t* d_num_tokens; int32_t H;
@@ -342,10 +328,10 @@ moe_status_t moe_combine(const void* y, int64_t ldy, int64_t R, const int32_t* s
   const int sms = num_sms_cached();
   if (sms <= 0) return MOE_ERR_CUDA;
   CombineArgs ca{};
-  ca.y = static_cast<const uint16_t*>(y); ca.ldy = ldy; ca.R = R; ca.src2dst = src2dst; ca.w = w;
+  ca.y = y; ca.ldy = ldy; ca.R = R; ca.src2dst = src2dst; ca.w = w;
   ca.T = T; ca.d_num_tokens = d_num_tokens; ca.K = K; ca.H = H;
-  ca.out = static_cast<uint16_t*>(out); ca.status = d_status;
-  return cuda_status(launch_combine(ca, sms, reinterpret_cast<cudaStream_t>(stream)));
+  ca.out = out; ca.status = d_status;
+  return cuda_status(launch_combine(ca, kBF16, sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 static moe_status_t repack_common(int to_slab, const void* src, void* dst, int32_t elem_bytes,
@@ -449,6 +435,7 @@ moe_status_t moe_status_sync(const int32_t* d_status, moe_stream_t stream) {
   if (cudaMemcpyAsync(&v, d_status, sizeof(v), cudaMemcpyDeviceToHost, s) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (cudaStreamSynchronize(s) != cudaSuccess) return MOE_ERR_CUDA;
+  if (v & MOE_STATUS_TIMEOUT) return MOE_ERR_TIMEOUT;
   if (v & MOE_STATUS_BAD_LAYOUT) return MOE_ERR_BAD_LAYOUT;
   if (v & MOE_STATUS_LIVE_OVERFLOW) return MOE_ERR_LIVE_OVERFLOW;
   if (v & MOE_STATUS_OVERFLOW) return MOE_ERR_OVERFLOW;
@@ -463,6 +450,7 @@ const char* moe_status_string(moe_status_t s) {
     case MOE_ERR_LIVE_OVERFLOW: return "live-row count larger than the buffer";
     case MOE_ERR_BAD_LAYOUT: return "prefix sums or row indices inconsistent with the buffers";
     case MOE_ERR_CUDA: return "CUDA runtime error";
+    case MOE_ERR_TIMEOUT: return "a wait inside a kernel ran out; its outputs are incomplete";
   }
   return "unknown status";
 }

@@ -1,0 +1,182 @@
+// api_block.cu -- the C ABI of the calls around the dispatch (include/moeperm.h):
+// plain permute, combine for every type, their gradients, and the norms around
+// a block. Host-side argument validation and launches only.
+#include "../../include/moeperm.h"
+#include "api_util.h"
+#include "kernels.h"
+
+using namespace moeperm;
+
+namespace {
+
+cudaStream_t cu(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
+
+// Which parts a norm call has: a block output or a pre norm, and a post norm or
+// a gate only with a block output (whose pointer may be NULL without rows).
+bool norm_parts_ok(int32_t T, const void* y, const float* w_post, const float* gate, int mode,
+                   const float* w_pre) {
+  if (mode != MOE_GATE_NONE && mode != MOE_GATE_CHANNEL && mode != MOE_GATE_TOKEN) return false;
+  if (T <= 0) return true;
+  if (!y && (!w_pre || w_post || mode != MOE_GATE_NONE)) return false;
+  return mode == MOE_GATE_NONE || (gate && aligned16(gate));
+}
+
+// Rows of a norm: at most 2048 16-byte vectors.
+bool norm_shape_ok(int32_t T, int32_t H, int es) {
+  return es != 0 && T >= 0 && H > 0 && (int64_t)H * es % 16 == 0 && (int64_t)H * es <= 2048 * 16;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_permute(const void* x, int64_t ldx, moe_elem_t type, int32_t T,
+                         const int32_t* d_num_tokens, int32_t H, const int32_t* topk_ids,
+                         const float* topk_weights, int32_t K, int32_t E, int32_t L, int32_t block_e,
+                         void* xs, int32_t* m_indices, int64_t bound, int32_t* src2dst, int32_t* counts,
+                         int32_t* starts, int32_t* psum, int32_t* total, float* row_weights,
+                         void* workspace, size_t workspace_bytes, int32_t* d_status, moe_stream_t stream) {
+  const int es = elem_bytes(type);
+  if (es == 0 || T < 0 || H <= 0 || H > kMaxHidden || (int64_t)H * es % 16) return MOE_ERR_INVALID_ARG;
+  if (K < 1 || K > kMaxK || L < 1 || L > kMaxL || E < L || block_e < 1) return MOE_ERR_INVALID_ARG;
+  const int64_t A = (int64_t)T * K;
+  if (A > kMaxAssignments) return MOE_ERR_INVALID_ARG;
+  const RouteGeom geom = route_geometry(A, L, route_table_pref(H, L));
+  if (geom.S == 0) return MOE_ERR_INVALID_ARG;
+  if (bound < moe_compact_bound(A, L, block_e) || bound >= (int64_t(1) << 31)) return MOE_ERR_INVALID_ARG;
+  if (T > 0 && (!rows_ok(x, ldx, H, es) || !topk_ids || !src2dst)) return MOE_ERR_INVALID_ARG;
+  if (bound > 0 && (!m_indices || !xs || !aligned16(xs))) return MOE_ERR_INVALID_ARG;
+  if (!counts || !starts || !psum || !total || (row_weights && !topk_weights)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < moe_workspace_bytes(T, K, L))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+
+  PermuteArgs a{};
+  ScatterArgs& s = a.s;
+  s.x = static_cast<const uint16_t*>(x); s.T = T; s.d_num_tokens = d_num_tokens; s.H = H;
+  s.ids = topk_ids; s.w = topk_weights; s.K = K; s.L = L; s.E = E; s.mode = kModeCompact;
+  s.block_e = block_e; s.xq = static_cast<uint8_t*>(xs); s.src2dst = src2dst;
+  s.row_weights = row_weights; s.m_indices = m_indices; s.bound = bound; s.counts = counts;
+  s.starts = starts; s.psum = psum; s.total = total; s.status = d_status;
+  a.ldx_bytes = ldx * es;
+  a.row_bytes = H * es;
+  constexpr int kPiece = 16384;  // largest piece of a row moved at once
+  a.units = (a.row_bytes + kPiece - 1) / kPiece;
+  a.unit_bytes = ((a.row_bytes + a.units - 1) / a.units + 15) / 16 * 16;
+  if (A > kSmallSlots) {
+    s.chunk = geom.chunk;
+    s.nchunks = (int32_t)geom.nchunks;
+    s.table = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + kWsHeader);
+    RoutePlanArgs rp{};
+    rp.ids = topk_ids; rp.d_num_tokens = d_num_tokens; rp.T = T; rp.K = K; rp.L = L;
+    rp.chunk = s.chunk; rp.nchunks = s.nchunks; rp.lrank = src2dst;
+    rp.table = const_cast<int32_t*>(s.table); rp.status = d_status;
+    if (launch_route_plan(rp, geom, cu(stream)) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return cuda_status(launch_permute(a, sms, /*after_route_plan=*/A > kSmallSlots, cu(stream)));
+}
+
+moe_status_t moe_combine_ex(const void* y, int64_t ldy, moe_elem_t type, int64_t R,
+                            const int32_t* src2dst, const float* w, int32_t T,
+                            const int32_t* d_num_tokens, int32_t K, int32_t H, void* out,
+                            int32_t* d_status, moe_stream_t stream) {
+  const int es = elem_bytes(type);
+  if (es == 0 || T < 0 || K < 1 || K > kMaxK || H <= 0 || (int64_t)H * es % 16 || R < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!src2dst || !out || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if (R > 0 && !rows_ok(y, ldy, H, es)) return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  CombineArgs a{};
+  a.y = y; a.ldy = ldy; a.R = R; a.src2dst = src2dst; a.w = w; a.T = T;
+  a.d_num_tokens = d_num_tokens; a.K = K; a.H = H; a.out = out; a.status = d_status;
+  return cuda_status(launch_combine(a, (int)type, sms, cu(stream)));
+}
+
+moe_status_t moe_combine_grad(const void* dout, int64_t ldd, const void* y, int64_t ldy, moe_elem_t type,
+                              int64_t R, const int32_t* src2dst, const float* w, int32_t T,
+                              const int32_t* d_num_tokens, int32_t K, int32_t H, void* dy, int64_t lddy,
+                              float* dw, int32_t* d_status, moe_stream_t stream) {
+  const int es = elem_bytes(type);
+  if (es == 0 || T < 0 || K < 1 || K > kMaxK || H <= 0 || (int64_t)H * es % 16 || R < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (!dy && !dw) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!src2dst || !rows_ok(dout, ldd, H, es)) return MOE_ERR_INVALID_ARG;
+  if (R > 0 && dw && !rows_ok(y, ldy, H, es)) return MOE_ERR_INVALID_ARG;
+  if (R > 0 && dy && !rows_ok(dy, lddy, H, es)) return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  CombineGradArgs a{};
+  a.dout = dout; a.ldd = ldd; a.y = y; a.ldy = ldy; a.R = R; a.src2dst = src2dst; a.w = w; a.T = T;
+  a.d_num_tokens = d_num_tokens; a.K = K; a.H = H; a.dy = dy; a.lddy = lddy; a.dw = dw; a.status = d_status;
+  return cuda_status(launch_combine_grad(a, (int)type, sms, cu(stream)));
+}
+
+moe_status_t moe_block_norm(const void* x, int64_t ldx, const void* y, int64_t ldy, moe_elem_t type,
+                            int32_t T, int32_t H, const float* w_post, const float* gate,
+                            moe_gate_t gate_mode, float scale, const float* w_pre, float eps, void* x_out,
+                            void* h, float* rstd_post, float* rstd_pre, moe_stream_t stream) {
+  const int es = elem_bytes(type);
+  if (!norm_shape_ok(T, H, es) || !norm_parts_ok(T, y, w_post, gate, gate_mode, w_pre))
+    return MOE_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || !aligned16(w_post) || !aligned16(w_pre)) return MOE_ERR_INVALID_ARG;
+  if (T == 0) return MOE_OK;
+  if (!rows_ok(x, ldx, H, es) || (y && (!rows_ok(y, ldy, H, es) || !x_out || !aligned16(x_out))) ||
+      (w_pre && (!h || !aligned16(h))))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  NormArgs a{};
+  a.x = x; a.ldx = ldx; a.y = y; a.ldy = ldy; a.T = T; a.H = H; a.w_post = w_post; a.gate = gate;
+  a.gate_mode = gate_mode; a.scale = scale; a.w_pre = w_pre; a.eps = eps; a.x_out = x_out; a.h = h;
+  a.rstd_post = rstd_post; a.rstd_pre = rstd_pre;
+  return cuda_status(launch_block_norm(a, (int)type, sms, cu(stream)));
+}
+
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H) {
+  if (T < 0 || H < 1) return 0;
+  const int64_t parts = T < 1 ? 1 : T < kNormParts ? T : kNormParts;
+  return (size_t)3 * parts * H * sizeof(float);
+}
+
+moe_status_t moe_block_norm_grad(const void* dx_out, int64_t ld_dxo, const void* dh, int64_t ld_dh,
+                                 const void* x_out, int64_t ldx, const void* y, int64_t ldy,
+                                 moe_elem_t type, int32_t T, int32_t H, const float* w_post,
+                                 const float* gate, moe_gate_t gate_mode, float scale, const float* w_pre,
+                                 const float* rstd_post, const float* rstd_pre, void* dx, void* dy,
+                                 float* dw_post, float* dgate, float* dw_pre, void* workspace,
+                                 size_t workspace_bytes, moe_stream_t stream) {
+  const int es = elem_bytes(type);
+  if (!norm_shape_ok(T, H, es) || !norm_parts_ok(T, y, w_post, gate, gate_mode, w_pre))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w_post) || !aligned16(w_pre)) return MOE_ERR_INVALID_ARG;
+  if ((w_post && !dw_post) || (w_pre && !dw_pre)) return MOE_ERR_INVALID_ARG;
+  if (gate_mode == MOE_GATE_CHANNEL && !dgate) return MOE_ERR_INVALID_ARG;
+  if ((w_post || w_pre || gate_mode == MOE_GATE_CHANNEL) &&
+      (!workspace || !aligned16(workspace) || workspace_bytes < moe_block_norm_workspace_bytes(T, H)))
+    return MOE_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (dx_out && !rows_ok(dx_out, ld_dxo, H, es)) return MOE_ERR_INVALID_ARG;
+    if (w_pre && (!rows_ok(dh, ld_dh, H, es) || !rows_ok(x_out, ldx, H, es) || !rstd_pre))
+      return MOE_ERR_INVALID_ARG;
+    if (y && (!rows_ok(y, ldy, H, es) || !dy || !aligned16(dy))) return MOE_ERR_INVALID_ARG;
+    if (w_post && !rstd_post) return MOE_ERR_INVALID_ARG;
+    if (gate_mode == MOE_GATE_TOKEN && !dgate) return MOE_ERR_INVALID_ARG;
+    if (!dx || !aligned16(dx)) return MOE_ERR_INVALID_ARG;
+  }
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  NormArgs a{};
+  a.x = x_out; a.ldx = ldx; a.y = y; a.ldy = ldy; a.T = T; a.H = H; a.w_post = w_post; a.gate = gate;
+  a.gate_mode = gate_mode; a.scale = scale; a.w_pre = w_pre;
+  a.rstd_post = const_cast<float*>(rstd_post); a.rstd_pre = const_cast<float*>(rstd_pre);
+  a.dxo = dx_out; a.ld_dxo = ld_dxo; a.dh = dh; a.ld_dh = ld_dh; a.dx = dx; a.dy = dy;
+  a.dw_post = dw_post; a.dgate = dgate; a.dw_pre = dw_pre; a.ws = static_cast<float*>(workspace);
+  a.parts = T < 1 ? 1 : T < kNormParts ? T : kNormParts;
+  return cuda_status(launch_block_norm_grad(a, (int)type, sms, cu(stream)));
+}
+
+}  // extern "C"

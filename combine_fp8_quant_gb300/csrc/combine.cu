@@ -17,6 +17,7 @@
 // 4 + 2: 96% of the copy bandwidth instead of 93%). y is read once per kept
 // slot and out written once: the kernel is bound by HBM reads.
 #include "common.cuh"
+#include "elem.cuh"
 #include "kernels.h"
 
 namespace moeperm {
@@ -51,12 +52,15 @@ __device__ __forceinline__ Slot load_slot(const CombineArgs& p, int t, int n_liv
   return s;
 }
 
-template <int kBatch>  // source rows in flight per lane
+template <int TYPE, int kBatch>  // element type; source rows in flight per lane
 __global__ void __launch_bounds__(kThreads, kMinBlocks) combine_kernel(CombineArgs p) {
   const int lane = threadIdx.x & 31;
   const int gwarp = (int)((blockIdx.x * kThreads + threadIdx.x) >> 5);
   const int nwarps = (int)((gridDim.x * kThreads) >> 5);
-  const int nch = p.H / 8;                  // 8-element chunks per row
+  constexpr int N = Vec<TYPE>::kN;          // elements per 16-byte chunk
+  const uint8_t* y = static_cast<const uint8_t*>(p.y);
+  const int64_t ldy = p.ldy * Vec<TYPE>::kBytes;
+  const int nch = p.H / N;                  // chunks per row
   const int spt = (nch + 31) / 32;          // slices per token
   const int n_live = live_count(p.d_num_tokens, p.T, p.status, blockIdx.x == 0 && threadIdx.x == 0);
   // unit (t, s) advances by nwarps units per step: (dt, ds) with a carry, no division in the loop
@@ -71,9 +75,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) combine_kernel(CombineAr
     }
     const Slot nxt = load_slot(p, tn, n_live, lane);
     const int c = s * 32 + lane;
-    float acc[8];
+    float acc[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    for (int j = 0; j < N; ++j) acc[j] = 0.0f;
     for (int k0 = 0; k0 < p.K; k0 += kBatch) {
       uint4 v[kBatch];
       unsigned kept = 0;  // bit j: slot k0 + j contributes
@@ -82,31 +86,22 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) combine_kernel(CombineAr
         int row = __shfl_sync(0xffffffffu, cur.row, (k0 + j) & 31);
         if (k0 + j >= p.K) row = -1;
         kept |= (row >= 0 ? 1u : 0u) << j;
-        v[j] = (row >= 0 && c < nch) ? ld_nc_v4(p.y + (int64_t)row * p.ldy + c * 8)
+        v[j] = (row >= 0 && c < nch) ? ld_nc_v4(y + (int64_t)row * ldy + c * 16)
                                      : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         const float wk = __shfl_sync(0xffffffffu, cur.w, (k0 + j) & 31);
         if ((kept >> j) & 1u) {
-          acc[0] = __fmaf_rn(wk, bf16_lo(v[j].x), acc[0]);
-          acc[1] = __fmaf_rn(wk, bf16_hi(v[j].x), acc[1]);
-          acc[2] = __fmaf_rn(wk, bf16_lo(v[j].y), acc[2]);
-          acc[3] = __fmaf_rn(wk, bf16_hi(v[j].y), acc[3]);
-          acc[4] = __fmaf_rn(wk, bf16_lo(v[j].z), acc[4]);
-          acc[5] = __fmaf_rn(wk, bf16_hi(v[j].z), acc[5]);
-          acc[6] = __fmaf_rn(wk, bf16_lo(v[j].w), acc[6]);
-          acc[7] = __fmaf_rn(wk, bf16_hi(v[j].w), acc[7]);
+          float f[N];
+          Vec<TYPE>::unpack(v[j], f);
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[i] = __fmaf_rn(wk, f[i], acc[i]);
         }
       }
     }
     if (c < nch) {
-      uint4 o;
-      o.x = pack_bf16x2(acc[0], acc[1]);
-      o.y = pack_bf16x2(acc[2], acc[3]);
-      o.z = pack_bf16x2(acc[4], acc[5]);
-      o.w = pack_bf16x2(acc[6], acc[7]);
-      st_v4(p.out + (int64_t)t * p.H + c * 8, o);
+      st_v4(static_cast<uint8_t*>(p.out) + ((int64_t)t * nch + c) * 16, Vec<TYPE>::pack(acc));
     }
     cur = nxt;
     t = tn;
@@ -114,35 +109,42 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) combine_kernel(CombineAr
   }
 }
 
-template <int kBatch>
+template <int TYPE, int kBatch>
 cudaError_t launch_batch(const CombineArgs& a, int num_sms, cudaStream_t s) {
   int per_sm = 0;
-  cudaError_t err = occupancy(combine_kernel<kBatch>, kThreads, 0, &per_sm);
+  cudaError_t err = occupancy(combine_kernel<TYPE, kBatch>, kThreads, 0, &per_sm);
   if (err != cudaSuccess) return err;
   if (per_sm < 1) per_sm = 1;
-  const int64_t spt = (a.H / 8 + 31) / 32;
+  const int64_t spt = (a.H / Vec<TYPE>::kN + 31) / 32;
   const int64_t units = (int64_t)a.T * spt;
   int64_t grid = (int64_t)num_sms * per_sm;
   const int64_t need = (units + (kThreads / 32) - 1) / (kThreads / 32);
   if (grid > need) grid = need;
   if (grid < 1) grid = 1;
-  combine_kernel<kBatch><<<(unsigned)grid, kThreads, 0, s>>>(a);
+  combine_kernel<TYPE, kBatch><<<(unsigned)grid, kThreads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-}  // namespace
-
-cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t s) {
+template <int TYPE>
+cudaError_t launch_type(const CombineArgs& a, int num_sms, cudaStream_t s) {
   // the fewest batches of at most kMaxBatch rows, of equal size
   static_assert(kMaxBatch == 4, "one case per batch size below");
   const int nb = (a.K + kMaxBatch - 1) / kMaxBatch;
   const int batch = (a.K + nb - 1) / nb;
   switch (batch) {
-    case 1: return launch_batch<1>(a, num_sms, s);
-    case 2: return launch_batch<2>(a, num_sms, s);
-    case 3: return launch_batch<3>(a, num_sms, s);
-    default: return launch_batch<4>(a, num_sms, s);
+    case 1: return launch_batch<TYPE, 1>(a, num_sms, s);
+    case 2: return launch_batch<TYPE, 2>(a, num_sms, s);
+    case 3: return launch_batch<TYPE, 3>(a, num_sms, s);
+    default: return launch_batch<TYPE, 4>(a, num_sms, s);
   }
+}
+
+}  // namespace
+
+cudaError_t launch_combine(const CombineArgs& a, int type, int num_sms, cudaStream_t s) {
+  if (type == kF16) return launch_type<kF16>(a, num_sms, s);
+  if (type == kF32) return launch_type<kF32>(a, num_sms, s);
+  return launch_type<kBF16>(a, num_sms, s);
 }
 
 }  // namespace moeperm

@@ -19,6 +19,7 @@ namespace moeperm {
 constexpr int kStOverflow = 0x1;
 constexpr int kStLiveOverflow = 0x2;
 constexpr int kStBadLayout = 0x4;
+constexpr int kStTimeout = 0x8;  // a bounded wait inside a kernel ran out
 
 // Scale layouts (same values as moe_scale_fmt_t).
 constexpr int kFmtU8 = 0;
@@ -67,6 +68,20 @@ __device__ __forceinline__ uint32_t amax16_bf16(const uint4& a, const uint4& b) 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// fp16 pair -> floats (exact), and back (round to nearest even, overflow to infinity).
+__device__ __forceinline__ float2 f16x2_to_float2(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(w));
+  return f;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -204,6 +219,59 @@ __device__ __forceinline__ void bulk_wait_read() {
 __device__ __forceinline__ void bulk_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
+// Bulk (TMA) copy of `bytes` from global to shared memory, completing on an
+// mbarrier's transaction count (addresses 16-byte aligned, bytes a multiple of 16).
+__device__ __forceinline__ void bulk_load_g2s(uint32_t sdst, const void* gsrc, uint32_t bytes,
+                                              uint32_t mbar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               ::"r"(sdst), "l"(gsrc), "r"(bytes), "r"(mbar)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_store_s2g(void* gdst, uint32_t ssrc, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+               ::"l"(gdst), "r"(ssrc), "r"(bytes)
+               : "memory");
+}
+
+// mbarriers (shared-memory addresses). Every wait is bounded: it gives up
+// after kWaitCycles of the SM clock (about two seconds, where the longest
+// legitimate wait is far below a millisecond) and the caller flags
+// kStTimeout instead of hanging the GPU.
+constexpr long long kWaitCycles = 4000000000ll;
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void mbar_init(uint32_t mbar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(mbar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_init_fence() {
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_expect_tx(uint32_t mbar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(mbar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(mbar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t mbar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\t"
+               "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+               "selp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok)
+               : "r"(mbar), "r"(parity)
+               : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity) {
+  if (mbar_try_wait(mbar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(mbar, parity))
+    if (clock64() - t0 > kWaitCycles) return false;
+  return true;
+}
+
 // Asynchronous 16-byte copy global -> shared (both addresses 16-byte
 // aligned), completed by cp_async_wait_all() in the issuing thread.
 __device__ __forceinline__ void cp_async16(void* sdst, const void* gsrc) {

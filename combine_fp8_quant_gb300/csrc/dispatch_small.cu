@@ -23,36 +23,30 @@
 //   5. quantise its tokens (a 16-element chunk pair per thread per pass,
 //      xor-shuffle group max, exponent from the float's bits, hardware e4m3
 //      converts) and store each 16-byte vector to every destination row.
-#include <climits>
-
 #include "common.cuh"
 #include "kernels.h"
+#include "layout.cuh"
 #include "scales.cuh"
 
 namespace moeperm {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = kSmallWarps;
 constexpr int kThreads = kWarps * 32;
 constexpr int kCPT = 2;
-
 
 template <int GSZ, int FMT, int S>
 __global__ void __launch_bounds__(kThreads) dispatch_small_kernel(ScatterArgs p) {
   extern __shared__ int32_t sm[];
   __shared__ int32_t s_wsum[33];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int L = p.L, K = p.K, H = p.H;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int K = p.K, H = p.H;
   const int nch = H / 16, G = H / GSZ, G4 = (G + 3) / 4;
-  int32_t* hw = sm;                   // [kWarps][L] per-warp counters -> warp bases
-  int32_t* st = hw + kWarps * L;      // [L] expert row base (compact start, masked 0)
-  int32_t* ps = st + L;               // [L] count, then compact psum
-  int32_t* rows_all = ps + L;         // [T*K] row of every slot
-  int32_t* exps_all = rows_all + (int64_t)p.T * K;  // [T*K] expert of every slot
+  const int32_t* rows_all = small_rows(p, sm);              // [T*K] row of every slot
+  const int32_t* exps_all = rows_all + (int64_t)p.T * K;    // [T*K] expert of every slot
 
   const int n_live = live_count(p.d_num_tokens, p.T, p.status, blockIdx.x == 0 && tid == 0);
-  const int64_t A = (int64_t)p.T * K, A_live = (int64_t)n_live * K;
 
   // 1. first token's loads
   const int t0 = blockIdx.x;
@@ -69,115 +63,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_small_kernel(ScatterArgs p)
     }
   }
 
-  // 2. stable ranks of all slots
-  for (int i = tid; i < kWarps * L; i += kThreads) hw[i] = 0;
-  const int base = warp * 32 * S;
-  int32_t r[S];
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int64_t a = base + i * 32 + lane;
-    const int e = (a < A_live) ? __ldg(p.ids + a) : -1;
-    r[i] = (e >= 0 && e < L) ? e : -1;
-  }
-  __syncthreads();
-  int32_t* myhw = hw + warp * L;
-  const unsigned lt_mask = (1u << lane) - 1u;
-  const int nbits = (L > 1) ? 32 - __clz(L - 1) : 0;
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int e = r[i];
-    unsigned m = __ballot_sync(0xffffffffu, e >= 0);
-    for (int b = 0; b < nbits; ++b) {
-      const unsigned bit = (unsigned)(e >> b) & 1u;
-      const unsigned bal = __ballot_sync(0xffffffffu, bit);
-      m &= bit ? bal : ~bal;
-    }
-    const unsigned peers = (e >= 0) ? m : 0u;
-    const int lower = __popc(peers & lt_mask);
-    int rank = 0;
-    if (e >= 0) rank = myhw[e] + lower;
-    __syncwarp();
-    if (e >= 0 && lower == 0) myhw[e] += __popc(peers);
-    __syncwarp();
-    r[i] = (e >= 0) ? ((rank << 11) | (e + 1)) : 0;
-  }
-  __syncthreads();
-
-  // 3. warp bases and counts per expert; segment starts
-  for (int e = tid; e < L; e += kThreads) {
-    int run = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const int c = hw[w * L + e];
-      hw[w * L + e] = run;
-      run += c;
-    }
-    ps[e] = run;
-  }
-  __syncthreads();
-  if (p.mode == kModeCompact) {
-    const int total = aligned_starts(ps, st, L, p.block_e, INT_MAX, s_wsum);
-    for (int e = tid; e < L; e += kThreads) ps[e] += st[e];  // count -> psum
-    if (blockIdx.x == 0 && tid == 0) *p.total = total;
-    __syncthreads();
-    if (blockIdx.x == 0)
-      for (int e = tid; e < L; e += kThreads) {
-        p.counts[e] = ps[e] - st[e];
-        p.starts[e] = st[e];
-        p.psum[e] = ps[e];
-      }
-    if (p.m_indices != nullptr)
-      for (int64_t rr = (int64_t)blockIdx.x * kThreads + tid; rr < p.bound;
-           rr += (int64_t)gridDim.x * kThreads) {
-        int lo2 = 0, hi2 = L - 1;  // largest e with start[e] <= rr (start[0] = 0)
-        while (lo2 < hi2) {
-          const int mid = (lo2 + hi2 + 1) >> 1;
-          if (st[mid] <= rr) lo2 = mid; else hi2 = mid - 1;
-        }
-        p.m_indices[rr] = (rr < ps[lo2]) ? lo2 : -1;
-      }
-  } else {
-    // masked: slab rows need no start, so st takes the expanded-layout starts
-    // of the slab's real rows when psum is asked for (PR #29525 _build_layout)
-    bool overflow = false;
-    for (int e = tid; e < L; e += kThreads) {
-      if (blockIdx.x == 0) p.masked_m[e] = min(ps[e], p.cap);
-      if (ps[e] > p.cap) overflow = true;
-    }
-    if (overflow && blockIdx.x == 0) set_status(p.status, kStOverflow);
-    if (p.psum != nullptr && blockIdx.x == 0) {  // uniform over the CTA
-      aligned_starts(ps, st, L, p.block_e, p.cap, s_wsum);
-      for (int e = tid; e < L; e += kThreads) p.psum[e] = st[e] + min(ps[e], p.cap);
-    }
-    __syncthreads();
-  }
-
-  // 4. rows of all slots (each lane resolves its own slots)
-#pragma unroll
-  for (int i = 0; i < S; ++i) {
-    const int64_t a = base + i * 32 + lane;
-    if (a >= A) continue;
-    const int pk = r[i];
-    int row = -1;
-    if (pk) {
-      const int e = (pk & 0x7FF) - 1;
-      const int j = hw[warp * L + e] + (pk >> 11);  // rank among all slots of e
-      if (p.mode == kModeCompact) row = st[e] + j;
-      else if (j < p.cap) row = e * p.cap + j;
-    }
-    rows_all[a] = row;
-    exps_all[a] = pk ? (pk & 0x7FF) - 1 : -1;
-  }
-  __syncthreads();
-
-  // src2dst and row weights of this CTA's tokens (each slot written once)
-  for (int t = blockIdx.x; t < p.T; t += gridDim.x)
-    for (int k = tid; k < K; k += kThreads) {
-      const int64_t a = (int64_t)t * K + k;
-      const int row = rows_all[a];
-      p.src2dst[a] = row;
-      if (row >= 0 && p.row_weights != nullptr) p.row_weights[row] = __ldg(p.w + a);
-    }
+  // 2-4. every slot's row (small_layout), the layout outputs and this CTA's
+  // src2dst and row weights
+  small_layout<S>(p, sm, s_wsum, n_live);
 
   // 5. quantise + scatter this CTA's tokens
   for (int t = t0; t < n_live; t += gridDim.x) {
@@ -234,7 +122,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_small_kernel(ScatterArgs p)
 
 template <int GSZ, int FMT, int S>
 cudaError_t launch_s(const ScatterArgs& a, int num_sms, cudaStream_t s) {
-  const size_t smem = ((size_t)kWarps * a.L + 2 * (size_t)a.L + 2 * (size_t)a.T * a.K) * sizeof(int32_t);
+  const size_t smem = small_layout_bytes(a);
   cudaError_t err = opt_in_smem(dispatch_small_kernel<GSZ, FMT, S>, smem);
   if (err != cudaSuccess) return err;
   int per_sm = 0;

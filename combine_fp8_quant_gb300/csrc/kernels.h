@@ -104,10 +104,23 @@ cudaError_t launch_dispatch_small(const ScatterArgs& a, int g, int fmt, int num_
                                   cudaStream_t s);
 
 // ---------------------------------------------------------------------------
-// Combine
+// Plain permute: the rows themselves, unquantised, into the compact layout.
 // ---------------------------------------------------------------------------
+struct PermuteArgs {
+  ScatterArgs s;               // routing and layout (mode compact); s.x, s.xq: raw row bytes
+  int64_t ldx_bytes;
+  int32_t row_bytes;
+  int32_t unit_bytes, units;   // a row moves in `units` pieces of unit_bytes (the last shorter)
+  int32_t stages;              // pieces in flight per CTA (set at launch)
+};
+cudaError_t launch_permute(const PermuteArgs& a, int num_sms, bool after_route_plan, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Combine (element types: same values as moe_elem_t)
+// ---------------------------------------------------------------------------
+constexpr int kBF16 = 0, kF16 = 1, kF32 = 2, kE4M3 = 3;
 struct CombineArgs {
-  const uint16_t* y;
+  const void* y;
   int64_t ldy;
   int64_t R;
   const int32_t* src2dst;
@@ -115,10 +128,67 @@ struct CombineArgs {
   int32_t T;
   const int32_t* d_num_tokens;
   int32_t K, H;
-  uint16_t* out;
+  void* out;
   int32_t* status;
 };
-cudaError_t launch_combine(const CombineArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_combine(const CombineArgs& a, int type, int num_sms, cudaStream_t s);
+
+// Gradients of the combine with respect to the rows and the weights.
+struct CombineGradArgs {
+  const void* dout;
+  int64_t ldd;
+  const void* y;               // needed for dw only
+  int64_t ldy;
+  int64_t R;
+  const int32_t* src2dst;
+  const float* w;
+  int32_t T;
+  const int32_t* d_num_tokens;
+  int32_t K, H;
+  void* dy;                    // optional
+  int64_t lddy;
+  float* dw;                   // optional
+  int32_t* status;
+};
+cudaError_t launch_combine_grad(const CombineGradArgs& a, int type, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Norms around a block
+// ---------------------------------------------------------------------------
+constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2;
+struct NormArgs {
+  const void* x;               // forward: the residual stream; backward: the stream after the sum
+  int64_t ldx;
+  const void* y;               // the block's output (optional)
+  int64_t ldy;
+  int32_t T, H;
+  const float* w_post;         // optional
+  const float* gate;           // [H] or [T] by gate_mode
+  int32_t gate_mode;
+  float scale;
+  const float* w_pre;          // optional
+  float eps;
+  void* x_out;                 // with y
+  void* h;                     // with w_pre
+  float* rstd_post;            // forward: optional outputs; backward: inputs
+  float* rstd_pre;
+  // backward only
+  const void* dxo;             // optional
+  int64_t ld_dxo;
+  const void* dh;              // with w_pre
+  int64_t ld_dh;
+  void* dx;
+  void* dy;                    // with y
+  float* dw_post;
+  float* dgate;
+  float* dw_pre;
+  float* ws;                   // [3][parts][H] partial sums
+  int32_t parts;
+};
+// Rows of partial sums the backward pass may use (the grid's upper limit).
+constexpr int kNormParts = 304;
+cudaError_t launch_block_norm(const NormArgs& a, int type, int num_sms, cudaStream_t s);
+cudaError_t launch_block_norm_grad(const NormArgs& a, int type, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Expanded <-> slab repack

@@ -60,6 +60,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "layout.cuh"
 #include "scales.cuh"
 
 namespace moeperm {
@@ -172,72 +173,6 @@ __device__ __forceinline__ void load_row(uint4 (&v)[CPT][2], const uint16_t* xro
   }
 }
 
-// Layout prologue of a dispatch CTA (see the file comment). Leaves in shared
-// memory: the exclusive per-expert prefix over chunks (tbl), the expert row
-// base (st: compact start, masked 0) and, for compact, psum (ps).
-__device__ void layout_prologue(const ScatterArgs& p, int32_t* tbl, int32_t* st, int32_t* ps,
-                                int32_t* s_wsum) {
-  const int tid = threadIdx.x, bd = blockDim.x;
-  const int L = p.L, NC = p.nchunks;
-  // the whole table in flight at once: 16-byte asynchronous copies (the
-  // table starts 16-byte aligned in the workspace), the odd tail by loads
-  const int n = NC * L, n4 = n / 4;
-  for (int i = tid; i < n4; i += bd) cp_async16(tbl + 4 * i, p.table + 4 * i);
-  for (int i = 4 * n4 + tid; i < n; i += bd) tbl[i] = __ldcg(p.table + i);
-  cp_async_wait_all();
-  __syncthreads();
-  for (int e = tid; e < L; e += bd) {
-    int run = 0, c = 0;
-    for (; c + 8 <= NC; c += 8) {  // 8 loads in flight, then 8 stores
-      int h[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = tbl[(c + j) * L + e];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        tbl[(c + j) * L + e] = run;
-        run += h[j];
-      }
-    }
-    for (; c < NC; ++c) {
-      const int h = tbl[c * L + e];
-      tbl[c * L + e] = run;
-      run += h;
-    }
-    ps[e] = run;  // count, for now
-  }
-  __syncthreads();
-  if (p.mode == kModeCompact) {
-    // segment starts: exclusive scan of align(count) over experts
-    const int total = aligned_starts(ps, st, L, p.block_e, INT_MAX, s_wsum);
-    for (int e = tid; e < L; e += bd) ps[e] += st[e];  // count -> psum
-    if (blockIdx.x == 0 && tid == 0) *p.total = total;
-    __syncthreads();
-    if (blockIdx.x == 0) {
-      for (int e = tid; e < L; e += bd) {
-        p.counts[e] = ps[e] - st[e];
-        p.starts[e] = st[e];
-        p.psum[e] = ps[e];
-      }
-    }
-  } else {
-    // masked: masked_m = min(count, cap) and the overflow flag; st is free
-    // here (slab rows need no start) and takes the expanded-layout starts of
-    // the slab's real rows when psum is asked for (PR #29525 _build_layout)
-    bool overflow = false;
-    for (int e = tid; e < L; e += bd) {
-      const int cnt = ps[e];
-      if (blockIdx.x == 0) p.masked_m[e] = min(cnt, p.cap);
-      if (cnt > p.cap) overflow = true;
-    }
-    if (overflow && blockIdx.x == 0) set_status(p.status, kStOverflow);
-    if (p.psum != nullptr && blockIdx.x == 0) {  // uniform over the CTA
-      aligned_starts(ps, st, L, p.block_e, p.cap, s_wsum);
-      for (int e = tid; e < L; e += bd) p.psum[e] = st[e] + min(ps[e], p.cap);
-    }
-    __syncthreads();
-  }
-}
-
 // Quantises one thread's 16-element chunk (a, b) of a row: the group maximum
 // over the GSZ/16 lanes of the group (xor shuffles over sign-cleared bf16
 // bits), the group's exponent e (or plain fp32 scale sval) and the 16 e4m3
@@ -262,30 +197,6 @@ __device__ __forceinline__ uint4 quant_chunk(const uint4& a, const uint4& b, int
     q1 = quant8(b, inv);
   }
   return make_uint4(q0.x, q0.y, q1.x, q1.y);
-}
-
-// Row of slot a (expert e, chunk-local rank lr) from the prologue's tables;
-// -1 if dropped. A rank that does not fit the layout (only possible if the
-// workspace was altered between the launches) flags BAD_LAYOUT and drops the
-// slot, so no write ever leaves the buffers.
-__device__ __forceinline__ int slot_row(const ScatterArgs& p, const int32_t* tbl, const int32_t* st,
-                                        int64_t a, int e, int lr) {
-  if (e < 0 || e >= p.L) return -1;
-  const int base = tbl[(int)(a / p.chunk) * p.L + e];
-  if (p.mode == kModeCompact) {
-    const int row = st[e] + base + lr;
-    if (lr < 0 || row < 0 || (int64_t)row >= p.bound) {
-      set_status(p.status, kStBadLayout);
-      return -1;
-    }
-    return row;
-  }
-  const int j = base + lr;
-  if (lr < 0 || j < 0) {
-    set_status(p.status, kStBadLayout);
-    return -1;
-  }
-  return j < p.cap ? e * p.cap + j : -1;
 }
 
 template <int GSZ, int FMT, int CPT>

@@ -24,9 +24,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoeperm.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_OVERFLOW = 0, 1, 2
-MOE_ERR_LIVE_OVERFLOW, MOE_ERR_BAD_LAYOUT, MOE_ERR_CUDA = 3, 4, 5
-STATUS_OVERFLOW, STATUS_LIVE_OVERFLOW, STATUS_BAD_LAYOUT = 1, 2, 4
+MOE_ERR_LIVE_OVERFLOW, MOE_ERR_BAD_LAYOUT, MOE_ERR_CUDA, MOE_ERR_TIMEOUT = 3, 4, 5, 6
+STATUS_OVERFLOW, STATUS_LIVE_OVERFLOW, STATUS_BAD_LAYOUT, STATUS_TIMEOUT = 1, 2, 4, 8
 FMT = {"u8": 0, "packed": 1, "f32pow2": 2, "f32": 3, "mx": 4}
+
+ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+GATE = {"none": 0, "channel": 1, "token": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -57,7 +60,7 @@ def load(path: str | None = None):
 
 
 def _declare(L):
-    vp, i32, i64, sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
+    vp, i32, i64, sz, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
     sig = {
         "moe_compact_bound": (i64, [i64, i32, i32]),
         "moe_should_use_masked": (i32, [i32, i32]),
@@ -78,6 +81,16 @@ def _declare(L):
                                        i64, vp, i64, vp, vp, vp]),
         "fp8_requant_per_tensor": (i32, [vp, i64, vp, i32, i32, vp, vp, vp]),
         "fp8_requant_per_tensor_ex": (i32, [vp, i64, vp, i32, i32, i32, i32, vp, vp, vp, sz, vp]),
+        "moe_permute": (i32, [vp, i64, i32, i32, vp, i32, vp, vp, i32, i32, i32, i32, vp, vp, i64,
+                              vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "moe_combine_ex": (i32, [vp, i64, i32, i64, vp, vp, i32, vp, i32, i32, vp, vp, vp]),
+        "moe_combine_grad": (i32, [vp, i64, vp, i64, i32, i64, vp, vp, i32, vp, i32, i32, vp, i64,
+                                   vp, vp, vp]),
+        "moe_block_norm": (i32, [vp, i64, vp, i64, i32, i32, i32, vp, vp, i32, f32, vp, f32, vp, vp,
+                                 vp, vp, vp]),
+        "moe_block_norm_workspace_bytes": (sz, [i32, i32]),
+        "moe_block_norm_grad": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32,
+                                      f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "moe_status_sync": (i32, [vp, vp]),
         "moe_status_string": (C.c_char_p, [i32]),
         "moe_version": (C.c_char_p, []),
@@ -225,6 +238,52 @@ def fp8_requant_per_tensor_ex(q, ldq, s_tok, s_fmt, T, H, mode, q_out, d_scale_o
         _ptr(d_scale_out), _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
+def moe_permute(x, ldx, dtype, T, d_num_tokens, H, topk_ids, topk_weights, K, E, L, block_e, xs,
+                m_indices, bound, src2dst, counts, starts, psum, total, row_weights, workspace,
+                workspace_bytes, d_status, stream=None) -> int:
+    return int(lib().moe_permute(
+        _ptr(x), ldx, ELEM[dtype], T, _ptr(d_num_tokens), H, _ptr(topk_ids), _ptr(topk_weights), K,
+        E, L, block_e, _ptr(xs), _ptr(m_indices), bound, _ptr(src2dst), _ptr(counts), _ptr(starts),
+        _ptr(psum), _ptr(total), _ptr(row_weights), _ptr(workspace), workspace_bytes,
+        _ptr(d_status), _stream(stream)))
+
+
+def moe_combine_ex(y, ldy, dtype, R, src2dst, w, T, d_num_tokens, K, H, out, d_status,
+                   stream=None) -> int:
+    return int(lib().moe_combine_ex(_ptr(y), ldy, ELEM[dtype], R, _ptr(src2dst), _ptr(w), T,
+                                    _ptr(d_num_tokens), K, H, _ptr(out), _ptr(d_status),
+                                    _stream(stream)))
+
+
+def moe_combine_grad(dout, ldd, y, ldy, dtype, R, src2dst, w, T, d_num_tokens, K, H, dy, lddy, dw,
+                     d_status, stream=None) -> int:
+    return int(lib().moe_combine_grad(_ptr(dout), ldd, _ptr(y), ldy, ELEM[dtype], R,
+                                      _ptr(src2dst), _ptr(w), T, _ptr(d_num_tokens), K, H,
+                                      _ptr(dy), lddy, _ptr(dw), _ptr(d_status), _stream(stream)))
+
+
+def moe_block_norm(x, ldx, y, ldy, dtype, T, H, w_post, gate, gate_mode, scale, w_pre, eps, x_out,
+                   h, rstd_post, rstd_pre, stream=None) -> int:
+    return int(lib().moe_block_norm(_ptr(x), ldx, _ptr(y), ldy, ELEM[dtype], T, H, _ptr(w_post),
+                                    _ptr(gate), GATE[gate_mode], scale, _ptr(w_pre), eps,
+                                    _ptr(x_out), _ptr(h), _ptr(rstd_post), _ptr(rstd_pre),
+                                    _stream(stream)))
+
+
+def moe_block_norm_workspace_bytes(T: int, H: int) -> int:
+    return int(lib().moe_block_norm_workspace_bytes(T, H))
+
+
+def moe_block_norm_grad(dx_out, ld_dxo, dh, ld_dh, x_out, ldx, y, ldy, dtype, T, H, w_post, gate,
+                        gate_mode, scale, w_pre, rstd_post, rstd_pre, dx, dy, dw_post, dgate,
+                        dw_pre, workspace, workspace_bytes, stream=None) -> int:
+    return int(lib().moe_block_norm_grad(
+        _ptr(dx_out), ld_dxo, _ptr(dh), ld_dh, _ptr(x_out), ldx, _ptr(y), ldy, ELEM[dtype], T, H,
+        _ptr(w_post), _ptr(gate), GATE[gate_mode], scale, _ptr(w_pre), _ptr(rstd_post),
+        _ptr(rstd_pre), _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
 def moe_status_sync(d_status, stream=None) -> int:
     return int(lib().moe_status_sync(_ptr(d_status), _stream(stream)))
 
@@ -343,16 +402,206 @@ def quant_group(x, group_size=128, scale_fmt="packed", num_live=None, status=Non
     return dict(xq=xq, scales=sc, ld_s=ld, status=st)
 
 
+def _like(t, shape, dtype, dev, name):
+    """The caller's output tensor, checked, or a new one. Outputs are dense."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"moeperm: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """Row stride of a 2-D tensor whose rows are dense; checks shape and dtype when given."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"moeperm: {name} must be 2-D with dense rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"moeperm: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"moeperm: {name} must be {dtype}, not {t.dtype}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vec(t, n, name, dtype=torch.float32):
+    """A dense vector argument of n elements (or None)."""
+    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"moeperm: {name} must be a contiguous {dtype} tensor of {n} elements")
+    return t
+
+
+def _elem(t, allowed, name):
+    if t.dtype not in allowed:
+        raise ValueError(f"moeperm: {name} must be one of {[str(d) for d in allowed]}, not {t.dtype}")
+    return t.dtype
+
+
+FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+
+
 def combine(y, src2dst, weights=None, num_tokens=None, status=None, out=None):
-    """out[t] = bf16(sum_k w[t,k] * y[src2dst[t,k]]) (fp32 accumulation)."""
+    """out[t] = sum_k w[t,k] * y[src2dst[t,k]] in fp32, rounded once to y's type
+    (bfloat16, float16 or float32)."""
     T, K = src2dst.shape
     R, H = y.shape
     dev = y.device
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+    dtype = y.dtype if y.dtype in FLOATS else torch.bfloat16
+    out = torch.empty((T, H), dtype=dtype, device=dev) if out is None else out
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
-    _check(moe_combine(y, y.stride(0), R, src2dst, weights, T, num_tokens, K, H, out, st),
-           "moe_combine")
+    if dtype == torch.bfloat16:
+        _check(moe_combine(y, y.stride(0), R, src2dst, weights, T, num_tokens, K, H, out, st),
+               "moe_combine")
+    else:
+        _check(moe_combine_ex(y, y.stride(0), dtype, R, src2dst, weights, T, num_tokens, K, H, out,
+                              st), "moe_combine_ex")
     return out
+
+
+def permute(x, topk_ids, topk_weights, num_experts, num_local_experts, block_e=128,
+            num_tokens=None, workspace=None, status=None, row_weights=True, out=None):
+    """Copy every token's row to the rows of its kept slots in the compact layout,
+    unquantised: out[src2dst[t,k]] = x[t] (bfloat16, float16 or float32; padding
+    rows of `out` are not written). row_weights: True, False or the [bound]
+    float32 tensor to fill. Returns a dict: xs and the layout tensors of
+    dispatch_compact."""
+    dtype = _elem(x, FLOATS, "x")
+    ldx = _rows(x, "x")
+    T, H = x.shape
+    K, L, dev = topk_ids.shape[1], num_local_experts, x.device
+    _vec(topk_ids, T * K, "topk_ids", torch.int32)
+    _vec(topk_weights, T * K, "topk_weights")
+    bound = moe_compact_bound(T * K, L, block_e)
+    i32 = dict(dtype=torch.int32, device=dev)
+    if row_weights is True:
+        row_weights = torch.empty(bound, dtype=torch.float32, device=dev)
+    o = dict(xs=_like(out, (bound, H), dtype, dev, "out"), bound=bound,
+             m_indices=torch.empty(bound, **i32), src2dst=torch.empty((T, K), **i32),
+             counts=torch.empty(L, **i32), starts=torch.empty(L, **i32), psum=torch.empty(L, **i32),
+             total=torch.empty(1, **i32),
+             row_weights=None if row_weights is False else _vec(row_weights, bound, "row_weights"))
+    ws = workspace if workspace is not None else Workspace(T, K, L, dev)
+    st = status if status is not None else torch.zeros(1, **i32)
+    _check(moe_permute(x, ldx, dtype, T, num_tokens, H, topk_ids, topk_weights, K, num_experts, L,
+                       block_e, o["xs"], o["m_indices"], bound, o["src2dst"], o["counts"],
+                       o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, ws.nbytes, st),
+           "moe_permute")
+    o["status"] = st
+    return o
+
+
+def permute_grad(dxs, src2dst, num_tokens=None, status=None, out=None):
+    """Gradient of permute: dx[t] = sum over kept k of dxs[src2dst[t,k]]."""
+    dtype = _elem(dxs, FLOATS, "dxs")
+    ld = _rows(dxs, "dxs")
+    T, K = src2dst.shape
+    R, H = dxs.shape
+    _vec(src2dst, T * K, "src2dst", torch.int32)
+    out = _like(out, (T, H), dtype, dxs.device, "out")
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dxs.device)
+    _check(moe_combine_ex(dxs, ld, dtype, R, src2dst, None, T, num_tokens, K, H, out, st),
+           "moe_combine_ex")
+    return out
+
+
+def combine_grad(dout, y, src2dst, weights=None, num_tokens=None, status=None, dy=None,
+                 need_dy=True, need_dweights=True):
+    """Gradients of combine(y, src2dst, weights) for the output gradient dout:
+    dy[src2dst[t,k]] = w[t,k] * dout[t] (rows without a kept slot are not
+    written) and dweights[t,k] = <dout[t], y[src2dst[t,k]]> in float32. Returns
+    a dict (dy, dweights, status)."""
+    dtype = _elem(dout, FLOATS, "dout")
+    T, K = src2dst.shape
+    R, H = y.shape
+    ldd, ldy = _rows(dout, "dout", (T, H)), _rows(y, "y", None, dtype)
+    _vec(src2dst, T * K, "src2dst", torch.int32)
+    _vec(weights, T * K, "weights")
+    dev = dout.device
+    dy = _like(dy, (R, H), dtype, dev, "dy") if need_dy else None
+    dw = torch.empty((T, K), dtype=torch.float32, device=dev) if need_dweights else None
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+    _check(moe_combine_grad(dout, ldd, y, ldy, dtype, R, src2dst, weights, T, num_tokens, K, H, dy,
+                            H, dw, st), "moe_combine_grad")
+    return dict(dy=dy, dweights=dw, status=st)
+
+
+class NormWorkspace:
+    """Workspace of block_norm_grad for up to T tokens of H elements, reusable
+    across calls on one stream; needs no initialisation."""
+
+    def __init__(self, T: int, H: int, device):
+        self.nbytes = moe_block_norm_workspace_bytes(T, H)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+
+def _gate_mode(gate, T, H, name="gate"):
+    """none / channel / token by the gate's shape: [H] or [1, H] is per channel, [T] or
+    [T, 1] per token (a 1-D gate of T = H elements is per channel)."""
+    if gate is None:
+        return "none"
+    shape = tuple(gate.shape)
+    if shape in ((H,), (1, H)):
+        mode = "channel"
+    elif shape in ((T,), (T, 1)):
+        mode = "token"
+    else:
+        raise ValueError(f"moeperm: {name} must have shape [{H}] or [{T}], not {shape}")
+    _vec(gate, gate.numel(), name)
+    return mode
+
+
+def block_norm(x, y=None, w_post=None, gate=None, scale=1.0, w_pre=None, eps=1e-6,
+               save_rstd=False):
+    """The step between two blocks: x' = x + scale * gate * (rms(y) * w_post) and
+    h = rms(x') * w_pre, rms(v) = v / sqrt(mean(v^2) + eps). y: the last block's
+    output (None: x' = x); w_post None: y is added unnormalised; w_pre None: no
+    h. gate [H] or [T]. Returns a dict: x (x'), h, and with save_rstd rstd_post
+    and rstd_pre for block_norm_grad."""
+    dtype = _elem(x, FLOATS, "x")
+    ldx = _rows(x, "x")
+    T, H = x.shape
+    dev = x.device
+    ldy = _rows(y, "y", (T, H), dtype) if y is not None else 0
+    mode = _gate_mode(gate, T, H)
+    _vec(w_post, H, "w_post")
+    _vec(w_pre, H, "w_pre")
+    new = lambda on: torch.empty((T, H), dtype=dtype, device=dev) if on else None
+    rstd = lambda on: torch.empty(T, dtype=torch.float32, device=dev) if on and save_rstd else None
+    o = dict(x=new(y is not None), h=new(w_pre is not None), rstd_post=rstd(w_post is not None),
+             rstd_pre=rstd(w_pre is not None))
+    _check(moe_block_norm(x, ldx, y, ldy, dtype, T, H, w_post, gate, mode, scale, w_pre, eps, o["x"],
+                          o["h"], o["rstd_post"], o["rstd_pre"]), "moe_block_norm")
+    if y is None:
+        o["x"] = x
+    return o
+
+
+def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0, w_pre=None,
+                    rstd_pre=None, rstd_post=None, workspace=None):
+    """Gradients of block_norm for dx_out (None: zeros) and dh. x_out is the stream
+    after the sum (x itself without y), the rstds are the forward call's. Returns
+    a dict: dx, dy, dw_post, dgate, dw_pre (None where there is none)."""
+    dtype = _elem(x_out, FLOATS, "x_out")
+    ldx = _rows(x_out, "x_out")
+    T, H = x_out.shape
+    dev = x_out.device
+    ld = lambda t, name: _rows(t, name, (T, H), dtype) if t is not None else 0
+    ldo, ldh, ldy = ld(dx_out, "dx_out"), ld(dh, "dh"), ld(y, "y")
+    mode = _gate_mode(gate, T, H)
+    _vec(w_post, H, "w_post")
+    _vec(w_pre, H, "w_pre")
+    _vec(rstd_pre, T, "rstd_pre")
+    _vec(rstd_post, T, "rstd_post")
+    f32 = dict(dtype=torch.float32, device=dev)
+    o = dict(dx=torch.empty((T, H), dtype=dtype, device=dev),
+             dy=torch.empty((T, H), dtype=dtype, device=dev) if y is not None else None,
+             dw_post=torch.empty(H, **f32) if w_post is not None else None,
+             dgate=torch.empty(gate.shape, **f32) if gate is not None else None,
+             dw_pre=torch.empty(H, **f32) if w_pre is not None else None)
+    ws = workspace if workspace is not None else NormWorkspace(T, H, dev)
+    _check(moe_block_norm_grad(dx_out, ldo, dh, ldh, x_out, ldx, y, ldy, dtype, T, H, w_post, gate,
+                               mode, scale, w_pre, rstd_post, rstd_pre, o["dx"], o["dy"],
+                               o["dw_post"], o["dgate"], o["dw_pre"], ws.buf, ws.nbytes),
+           "moe_block_norm_grad")
+    return o
 
 
 def expand_to_slab(exp, psum, num_local_experts, cap, align=128, exp_scales=None, ld_es=0,

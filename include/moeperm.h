@@ -68,13 +68,18 @@ typedef enum {
   MOE_ERR_OVERFLOW = 2,      /* an expert received more rows than its slab capacity */
   MOE_ERR_LIVE_OVERFLOW = 3, /* device live-row count larger than the buffer's rows */
   MOE_ERR_BAD_LAYOUT = 4,    /* prefix sums / row indices inconsistent with the buffers */
-  MOE_ERR_CUDA = 5           /* a CUDA runtime call or launch failed */
+  MOE_ERR_CUDA = 5,          /* a CUDA runtime call or launch failed */
+  MOE_ERR_TIMEOUT = 6        /* a bounded wait inside a kernel ran out (see MOE_STATUS_TIMEOUT) */
 } moe_status_t;
 
 /* Bits ORed into the caller's device status word. */
 #define MOE_STATUS_OVERFLOW 0x1
 #define MOE_STATUS_LIVE_OVERFLOW 0x2
 #define MOE_STATUS_BAD_LAYOUT 0x4
+/* A kernel that waits for its own asynchronous copies or tensor-core work
+ * (moe_permute, moe_expert_matmul, moe_expert_matmul_grad) gives up after
+ * about two seconds and sets this bit; the call's outputs are then incomplete. */
+#define MOE_STATUS_TIMEOUT 0x8
 
 /*
  * Scale layouts ([P3 实现拆解 items 3-4: Blackwell column-major packed UE8M0 vs
@@ -312,6 +317,116 @@ moe_status_t moe_combine(
     int32_t* d_status, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* Rows sorted by expert and back, unquantised, and their gradients     */
+/* ------------------------------------------------------------------ */
+
+/* Element types of the calls below (an e4m3 row holds raw OCP E4M3 bytes). */
+typedef enum {
+  MOE_BF16 = 0,
+  MOE_F16 = 1,
+  MOE_F32 = 2,
+  MOE_E4M3 = 3
+} moe_elem_t;
+
+/*
+ * moe_permute -- the compact dispatch without quantisation, for training and
+ * for experts that run in 16 or 32 bits: every kept slot (t, k) gets a copy of
+ * its token's row, xs[src2dst[t,k]] = x[t]. Inputs, layout outputs, row order,
+ * limits, workspace and errors are those of moe_dispatch_compact.
+ *   x [T, ldx], xs [bound, H]    elements of `type` (BF16, F16 or F32); H and ldx
+ *                                times the element size are multiples of 16 bytes
+ * Launches: 1 for T*K <= 2048 slots, otherwise 2.
+ */
+moe_status_t moe_permute(
+    const void* x, int64_t ldx, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t H,
+    const int32_t* topk_ids, const float* topk_weights, int32_t K, int32_t E, int32_t L,
+    int32_t block_e, void* xs, int32_t* m_indices, int64_t bound, int32_t* src2dst,
+    int32_t* counts, int32_t* starts, int32_t* psum, int32_t* total, float* row_weights,
+    void* workspace, size_t workspace_bytes, int32_t* d_status, moe_stream_t stream);
+
+/*
+ * moe_combine_ex -- moe_combine for every element type (with MOE_BF16 the same
+ * call and the same results). With w = NULL it is also the gradient of
+ * moe_permute: dx[t] = sum over kept k of dxs[src2dst[t,k]].
+ *   y [R, ldy], out [T, H]       BF16, F16 or F32; rows a multiple of 16 bytes
+ * Launches: 1.
+ */
+moe_status_t moe_combine_ex(
+    const void* y, int64_t ldy, moe_elem_t type, int64_t R, const int32_t* src2dst, const float* w,
+    int32_t T, const int32_t* d_num_tokens, int32_t K, int32_t H, void* out, int32_t* d_status,
+    moe_stream_t stream);
+
+/*
+ * moe_combine_grad -- gradients of out[t] = sum_k w[t,k] * y[src2dst[t,k]] for the
+ * output gradient dout:
+ *   dy[src2dst[t,k]] = w[t,k] * dout[t]            (rounded once to `type`)
+ *   dw[t,k]          = sum_h dout[t,h] * y[src2dst[t,k],h]   (fp32; 0 for a dropped slot)
+ *   dout [T, ldd], y [R, ldy], dy [R, lddy]        BF16, F16 or F32
+ *   w [T, K] f32                 (optional; NULL means every weight is 1)
+ *   dy, dw                       either may be NULL (not both); y is needed for dw only
+ * Rows of dy that no kept slot owns, and rows of dw of tokens that are not
+ * live, are not written. The rows of src2dst are distinct (as every dispatch
+ * makes them); an index >= R sets MOE_STATUS_BAD_LAYOUT and is skipped (dw = 0).
+ * Deterministic. Launches: 1.
+ */
+moe_status_t moe_combine_grad(
+    const void* dout, int64_t ldd, const void* y, int64_t ldy, moe_elem_t type, int64_t R,
+    const int32_t* src2dst, const float* w, int32_t T, const int32_t* d_num_tokens, int32_t K,
+    int32_t H, void* dy, int64_t lddy, float* dw, int32_t* d_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Norms before and after a block                                      */
+/* ------------------------------------------------------------------ */
+
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1, /* gate [H] */
+  MOE_GATE_TOKEN = 2    /* gate [T] */
+} moe_gate_t;
+
+/*
+ * moe_block_norm -- what stands between two blocks, in one pass over the rows:
+ *   n     = rms(y) * w_post          rms(v) = v * rstd(v), rstd(v) = (mean_h v^2 + eps)^(-1/2)
+ *   x_out = x + scale * gate * n     the residual stream after the block
+ *   h     = rms(x_out) * w_pre       the next block's input
+ * Without y, x_out is x itself and is not written (gate_mode is then
+ * MOE_GATE_NONE); without w_post, n = y; without w_pre, no h. At least one of
+ * y and w_pre is given. Sums are in fp32; h is computed from x_out before its
+ * rounding to `type`.
+ *   x [T, ldx], y [T, ldy], x_out [T, H], h [T, H]   BF16, F16 or F32, rows a multiple
+ *                                of 16 bytes, at most 2048 16-byte vectors each
+ *   w_post [H], gate, w_pre [H]  f32, 16-byte aligned
+ *   rstd_post [T], rstd_pre [T]  f32, (optional) kept for the backward pass
+ * Launches: 1.
+ */
+moe_status_t moe_block_norm(
+    const void* x, int64_t ldx, const void* y, int64_t ldy, moe_elem_t type, int32_t T, int32_t H,
+    const float* w_post, const float* gate, moe_gate_t gate_mode, float scale, const float* w_pre,
+    float eps, void* x_out, void* h, float* rstd_post, float* rstd_pre, moe_stream_t stream);
+
+/* Bytes of device workspace moe_block_norm_grad needs (no initialisation; not
+ * to be used by two calls that can run at once). 0 for T < 0 or H < 1. */
+size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H);
+
+/*
+ * moe_block_norm_grad -- gradients of moe_block_norm for dx_out (optional: NULL
+ * means zeros) and dh (with w_pre). `x_out` is the stream after the sum (x
+ * itself without y); rstd_post / rstd_pre are the forward call's.
+ *   dx [T, H]                    gradient of x
+ *   dy [T, H]                    gradient of y (with y)
+ *   dw_post [H], dw_pre [H] f32  sums over the tokens (with w_post, w_pre)
+ *   dgate f32                    [H] or [T] by gate_mode
+ * The sums over tokens are formed in a fixed order (deterministic) and written
+ * in full, also for T = 0. Launches: 1 or 2.
+ */
+moe_status_t moe_block_norm_grad(
+    const void* dx_out, int64_t ld_dxo, const void* dh, int64_t ld_dh, const void* x_out,
+    int64_t ldx, const void* y, int64_t ldy, moe_elem_t type, int32_t T, int32_t H,
+    const float* w_post, const float* gate, moe_gate_t gate_mode, float scale, const float* w_pre,
+    const float* rstd_post, const float* rstd_pre, void* dx, void* dy, float* dw_post, float* dgate,
+    float* dw_pre, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Expanded (psum) layout <-> masked slab repack                        */
 /* ------------------------------------------------------------------ */
 
@@ -401,7 +516,7 @@ moe_status_t fp8_requant_per_tensor_ex(
 /* ------------------------------------------------------------------ */
 
 /* Waits for `stream`, reads the device status word and returns MOE_OK or the
- * most severe error it holds: MOE_ERR_BAD_LAYOUT, then MOE_ERR_LIVE_OVERFLOW,
+ * most severe error it holds: MOE_ERR_TIMEOUT, MOE_ERR_BAD_LAYOUT, then MOE_ERR_LIVE_OVERFLOW,
  * then MOE_ERR_OVERFLOW (MOE_ERR_CUDA if the wait or copy fails). The non-graph
  * "fail fast" check of [P3 风险与影响 item 1]. */
 moe_status_t moe_status_sync(const int32_t* d_status, moe_stream_t stream);
