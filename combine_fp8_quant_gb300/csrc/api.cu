@@ -26,6 +26,8 @@ std::mutex g_cache_mu;
 struct OccEntry { const void* kernel; int threads; size_t smem; int dev; int value; };
 OccEntry g_occ[256];
 int g_nocc = 0;
+OccEntry g_cl[32];  // resident clusters; `threads` holds the CTAs per cluster
+int g_ncl = 0;
 struct SmemEntry { const void* kernel; unsigned long long ctx; size_t dyn; };
 SmemEntry g_smem[128];
 int g_nsmem = 0;
@@ -87,6 +89,27 @@ cudaError_t occupancy_cached(const void* kernel, int threads, size_t smem, int* 
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> g(g_cache_mu);
   if (g_nocc < 256) g_occ[g_nocc++] = OccEntry{kernel, threads, smem, dev, *per_sm};
+  return cudaSuccess;
+}
+
+cudaError_t max_clusters_cached(const void* kernel, const cudaLaunchConfig_t& cfg, int cl, int* clusters) {
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  {
+    std::lock_guard<std::mutex> g(g_cache_mu);
+    for (int i = 0; i < g_ncl; ++i) {
+      const OccEntry& e = g_cl[i];
+      if (e.kernel == kernel && e.threads == cl && e.smem == cfg.dynamicSmemBytes && e.dev == dev) {
+        *clusters = e.value;
+        return cudaSuccess;
+      }
+    }
+  }
+  err = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
+  if (err != cudaSuccess) return err;
+  std::lock_guard<std::mutex> g(g_cache_mu);
+  if (g_ncl < 32) g_cl[g_ncl++] = OccEntry{kernel, cl, cfg.dynamicSmemBytes, dev, *clusters};
   return cudaSuccess;
 }
 

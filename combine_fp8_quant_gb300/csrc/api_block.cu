@@ -26,6 +26,22 @@ bool norm_shape_ok(int32_t T, int32_t H, int es) {
   return es != 0 && T >= 0 && H > 0 && (int64_t)H * es % 16 == 0 && (int64_t)H * es <= 2048 * 16;
 }
 
+// Where the rows of the experts are: segments, slabs or one dense matrix.
+bool segments_ok(int64_t R, int32_t L, const int32_t* begin, const int32_t* end, int32_t cap) {
+  if (L < 1 || L > kMaxL || R < 0 || R >= (int64_t(1) << 31) || cap < 0) return false;
+  if (cap > 0) return begin == nullptr && end != nullptr && R == (int64_t)L * cap;
+  if ((begin == nullptr) != (end == nullptr)) return false;
+  return begin != nullptr || L == 1;
+}
+bool act_ok(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU; }
+// Output features, and weight rows within 32 bits.
+bool feats_ok(int32_t N, int32_t L, int32_t gated) {
+  if (N < 1 || N % (gated ? 16 : 8) || (gated != 0 && gated != 1)) return false;
+  return (int64_t)L * N * (gated ? 2 : 1) < (int64_t(1) << 31);
+}
+
+size_t dpre_bytes(int64_t R, int32_t Nw) { return ((size_t)R * Nw * 2 + 255) / 256 * 256; }
+
 }  // namespace
 
 extern "C" {
@@ -177,6 +193,104 @@ moe_status_t moe_block_norm_grad(const void* dx_out, int64_t ld_dxo, const void*
   a.dw_post = dw_post; a.dgate = dgate; a.dw_pre = dw_pre; a.ws = static_cast<float*>(workspace);
   a.parts = T < 1 ? 1 : T < kNormParts ? T : kNormParts;
   return cuda_status(launch_block_norm_grad(a, (int)type, sms, cu(stream)));
+}
+
+moe_status_t moe_expert_matmul(const void* x, int64_t ldx, moe_elem_t type, const void* x_scales,
+                               int64_t ld_xs, int64_t R, int32_t K, const void* w, const void* w_scales,
+                               int64_t ld_ws, int32_t L, int32_t N, int32_t gated, moe_act_t act,
+                               const float* bias, const int32_t* seg_begin, const int32_t* seg_end,
+                               int32_t cap, const void* residual, int64_t ld_res, void* out, int64_t ldo,
+                               moe_elem_t out_type, void* pre, int64_t ld_pre, int32_t* d_status,
+                               moe_stream_t stream) {
+  const bool fp8 = type == MOE_E4M3;
+  const int es = fp8 ? 1 : 2;
+  if (type != MOE_BF16 && type != MOE_F16 && !fp8) return MOE_ERR_INVALID_ARG;
+  if (out_type != MOE_BF16 && out_type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (!fp8 && out_type != type) return MOE_ERR_INVALID_ARG;
+  if (!segments_ok(R, L, seg_begin, seg_end, cap) || !feats_ok(N, L, gated) || !act_ok(act))
+    return MOE_ERR_INVALID_ARG;
+  if (K < 1 || K % (fp8 ? 128 : 8) || (fp8 && pre)) return MOE_ERR_INVALID_ARG;
+  if (!w || !aligned16(w)) return MOE_ERR_INVALID_ARG;
+  const int32_t Nw = gated ? 2 * N : N;
+  if (fp8 && (!w_scales || !aligned16(w_scales) || ld_ws < (int64_t)L * Nw || ld_ws % 4)) return MOE_ERR_INVALID_ARG;
+  if (R == 0) return MOE_OK;
+  if (!rows_ok(x, ldx, K, es) || !out || ldo < N || (residual && ld_res < N) || (pre && ld_pre < Nw))
+    return MOE_ERR_INVALID_ARG;
+  if (fp8 && (!x_scales || !aligned16(x_scales) || ld_xs < (cap > 0 ? cap : R) || ld_xs % 4))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  MatmulArgs m{};
+  m.x = x; m.ldx = ldx; m.w = w; m.R = R; m.K = K; m.L = L; m.N = N; m.type = (int)type;
+  m.out_type = (int)out_type; m.gated = gated; m.act = (int)act; m.seg_begin = seg_begin;
+  m.seg_end = seg_end; m.cap = cap; m.bias = bias; m.residual = residual; m.ld_res = ld_res;
+  m.out = out; m.ldo = ldo; m.pre = pre; m.ld_pre = ld_pre;
+  m.xs = static_cast<const uint32_t*>(x_scales); m.ld_xs = ld_xs;
+  m.ws = static_cast<const uint32_t*>(w_scales); m.ld_ws = ld_ws; m.status = d_status;
+  return cuda_status(launch_matmul(m, sms, cu(stream)));
+}
+
+size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw) {
+  if (R < 0 || L < 1 || Nw < 1) return 0;
+  // the split count depends on N; a gated N is half of Nw and gives the larger one
+  const int splits = act_grad_splits(R, L, Nw < 2 ? 1 : Nw / 2);
+  return dpre_bytes(R, Nw) + (splits > 1 ? (size_t)splits * L * Nw * sizeof(float) : 0);
+}
+
+moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x, int64_t ldx,
+                                    moe_elem_t type, int64_t R, int32_t K, const void* w, int32_t L,
+                                    int32_t N, int32_t gated, moe_act_t act, const void* pre, int64_t ld_pre,
+                                    const int32_t* seg_begin, const int32_t* seg_end, int32_t cap, void* dx,
+                                    int64_t ld_dx, void* dw, moe_elem_t dw_type, float* dbias,
+                                    void* workspace, size_t workspace_bytes, int32_t* d_status,
+                                    moe_stream_t stream) {
+  if (type != MOE_BF16 && type != MOE_F16) return MOE_ERR_INVALID_ARG;
+  if (!segments_ok(R, L, seg_begin, seg_end, cap) || !feats_ok(N, L, gated) || !act_ok(act))
+    return MOE_ERR_INVALID_ARG;
+  if (K < 1 || K % 8 || (!dx && !dw && !dbias)) return MOE_ERR_INVALID_ARG;
+  if (dw && (dw_type != type && dw_type != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  const int32_t Nw = gated ? 2 * N : N;
+  const size_t dw_bytes = (size_t)L * Nw * K * (dw_type == MOE_F32 ? 4 : 2);
+  cudaStream_t s = cu(stream);
+  if (R == 0) {  // no rows: the sums are zero
+    if (dw && cudaMemsetAsync(dw, 0, dw_bytes, s) != cudaSuccess) return MOE_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, (size_t)L * Nw * 4, s) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const bool has_act = act != MOE_ACT_NONE || gated;
+  if (!rows_ok(dout, ldd, N, 2)) return MOE_ERR_INVALID_ARG;
+  if (has_act && !rows_ok(pre, ld_pre, Nw, 2)) return MOE_ERR_INVALID_ARG;
+  if (dw && !rows_ok(x, ldx, K, 2)) return MOE_ERR_INVALID_ARG;
+  if (dx && (!w || !aligned16(w) || ld_dx < K)) return MOE_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < moe_expert_matmul_grad_workspace_bytes(R, L, Nw))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms_cached();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  if (has_act || dbias) {
+    ActGradArgs a{};
+    a.dout = dout; a.ldd = ldd; a.pre = pre; a.ld_pre = ld_pre; a.R = R; a.L = L; a.N = N; a.gated = gated;
+    a.act = (int)act; a.seg_begin = seg_begin; a.seg_end = seg_end; a.cap = cap;
+    a.dpre = has_act ? workspace : nullptr;
+    a.dbias = dbias;
+    a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, Nw));
+    a.splits = act_grad_splits(R, L, N);
+    a.status = d_status;
+    if (launch_act_grad(a, (int)type, s) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  MatmulArgs m{};
+  m.x = x; m.ldx = ldx; m.g = has_act ? workspace : dout; m.ldg = has_act ? Nw : ldd; m.w = w; m.R = R;
+  m.K = K; m.L = L; m.N = N; m.type = (int)type; m.gated = gated; m.seg_begin = seg_begin;
+  m.seg_end = seg_end; m.cap = cap; m.status = d_status;
+  if (dx) {
+    m.out = dx; m.ldo = ld_dx; m.out_type = (int)type;
+    if (launch_matmul_grad_x(m, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  if (dw) {
+    m.out = dw; m.ldo = K; m.out_type = (int)dw_type;
+    if (launch_matmul_grad_w(m, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -293,6 +293,8 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 // memory. Without the opt-in a CTA is limited to 48 KiB of dynamic plus static
 // shared memory; the static arrays of these kernels stay under 1 KiB.
 cudaError_t occupancy_cached(const void* kernel, int threads, size_t smem, int* per_sm);
+// Resident clusters of `cl` CTAs on the whole device for a launch configuration.
+cudaError_t max_clusters_cached(const void* kernel, const cudaLaunchConfig_t& cfg, int cl, int* clusters);
 // Unique id of the CUDA context current on this thread (0 when none is).
 cudaError_t current_context_id(unsigned long long* id);
 cudaError_t opt_in_smem_cached(const void* kernel, size_t dyn);

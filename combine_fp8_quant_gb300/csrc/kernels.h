@@ -153,6 +153,60 @@ struct CombineGradArgs {
 cudaError_t launch_combine_grad(const CombineGradArgs& a, int type, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// Experts' products and their gradients
+// ---------------------------------------------------------------------------
+constexpr int kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3;
+struct MatmulArgs {
+  const void* x;               // [R, ldx] rows (forward, weight gradient)
+  int64_t ldx;
+  const void* g;               // [R, ldg] gradient of the pre-activations (both gradients)
+  int64_t ldg;
+  const void* w;               // [L, N or 2N, K]
+  int64_t R;
+  int32_t K, L, N;             // N: output features (half the weight rows when gated)
+  int32_t type, out_type;
+  int32_t gated, act;
+  const int32_t* seg_begin;    // segments, or slabs of `cap` rows with seg_end = rows per expert
+  const int32_t* seg_end;
+  int32_t cap;
+  const float* bias;
+  const void* residual;
+  int64_t ld_res;
+  void* out;                   // forward: out; gradients: dx or dW
+  int64_t ldo;
+  void* pre;                   // optional
+  int64_t ld_pre;
+  const uint32_t* xs;          // e4m3: packed scale words
+  int64_t ld_xs;
+  const uint32_t* ws;
+  int64_t ld_ws;
+  int32_t* status;
+};
+cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_matmul_grad_x(const MatmulArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_matmul_grad_w(const MatmulArgs& a, int num_sms, cudaStream_t s);
+
+struct ActGradArgs {
+  const void* dout;
+  int64_t ldd;
+  const void* pre;             // with dpre
+  int64_t ld_pre;
+  int64_t R;
+  int32_t L, N, gated, act;
+  const int32_t* seg_begin;
+  const int32_t* seg_end;
+  int32_t cap;
+  void* dpre;                  // [R, N or 2N]; nullptr: the sums of dout alone
+  float* dbias;                // optional [L, N or 2N]
+  float* ws;                   // [splits, L, N or 2N] when splits > 1
+  int32_t splits;
+  int32_t* status;
+};
+constexpr int kActGradSplits = 64;
+int act_grad_splits(int64_t R, int32_t L, int32_t N);
+cudaError_t launch_act_grad(const ActGradArgs& a, int type, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Norms around a block
 // ---------------------------------------------------------------------------
 constexpr int kGateNone = 0, kGateChannel = 1, kGateToken = 2;

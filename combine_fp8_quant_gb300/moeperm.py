@@ -29,6 +29,7 @@ STATUS_OVERFLOW, STATUS_LIVE_OVERFLOW, STATUS_BAD_LAYOUT, STATUS_TIMEOUT = 1, 2,
 FMT = {"u8": 0, "packed": 1, "f32pow2": 2, "f32": 3, "mx": 4}
 
 ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 GATE = {"none": 0, "channel": 1, "token": 2}
 
 _lock = threading.Lock()
@@ -91,6 +92,11 @@ def _declare(L):
         "moe_block_norm_workspace_bytes": (sz, [i32, i32]),
         "moe_block_norm_grad": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, i32, i32, i32, vp, vp, i32,
                                       f32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_expert_matmul": (i32, [vp, i64, i32, vp, i64, i64, i32, vp, vp, i64, i32, i32, i32, i32,
+                                    vp, vp, vp, i32, vp, i64, vp, i64, i32, vp, i64, vp, vp]),
+        "moe_expert_matmul_grad_workspace_bytes": (sz, [i64, i32, i32]),
+        "moe_expert_matmul_grad": (i32, [vp, i64, vp, i64, i32, i64, i32, vp, i32, i32, i32, i32, vp,
+                                         i64, vp, vp, i32, vp, i64, vp, i32, vp, vp, sz, vp, vp]),
         "moe_status_sync": (i32, [vp, vp]),
         "moe_status_string": (C.c_char_p, [i32]),
         "moe_version": (C.c_char_p, []),
@@ -282,6 +288,30 @@ def moe_block_norm_grad(dx_out, ld_dxo, dh, ld_dh, x_out, ldx, y, ldy, dtype, T,
         _ptr(w_post), _ptr(gate), GATE[gate_mode], scale, _ptr(w_pre), _ptr(rstd_post),
         _ptr(rstd_pre), _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
         _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_expert_matmul(x, ldx, dtype, x_scales, ld_xs, R, K, w, w_scales, ld_ws, L, N, gated, act,
+                      bias, seg_begin, seg_end, cap, residual, ld_res, out, ldo, out_dtype, pre,
+                      ld_pre, d_status, stream=None) -> int:
+    return int(lib().moe_expert_matmul(
+        _ptr(x), ldx, ELEM[dtype], _ptr(x_scales), ld_xs, R, K, _ptr(w), _ptr(w_scales), ld_ws, L, N,
+        int(gated), ACT[act], _ptr(bias), _ptr(seg_begin), _ptr(seg_end), cap, _ptr(residual),
+        ld_res, _ptr(out), ldo, ELEM[out_dtype], _ptr(pre), ld_pre, _ptr(d_status),
+        _stream(stream)))
+
+
+def moe_expert_matmul_grad_workspace_bytes(R: int, L: int, Nw: int) -> int:
+    return int(lib().moe_expert_matmul_grad_workspace_bytes(R, L, Nw))
+
+
+def moe_expert_matmul_grad(dout, ldd, x, ldx, dtype, R, K, w, L, N, gated, act, pre, ld_pre,
+                           seg_begin, seg_end, cap, dx, ld_dx, dw, dw_dtype, dbias, workspace,
+                           workspace_bytes, d_status, stream=None) -> int:
+    return int(lib().moe_expert_matmul_grad(
+        _ptr(dout), ldd, _ptr(x), ldx, ELEM[dtype], R, K, _ptr(w), L, N, int(gated), ACT[act],
+        _ptr(pre), ld_pre, _ptr(seg_begin), _ptr(seg_end), cap, _ptr(dx), ld_dx, _ptr(dw),
+        ELEM[dw_dtype], _ptr(dbias), _ptr(workspace), workspace_bytes, _ptr(d_status),
+        _stream(stream)))
 
 
 def moe_status_sync(d_status, stream=None) -> int:
@@ -521,6 +551,150 @@ def combine_grad(dout, y, src2dst, weights=None, num_tokens=None, status=None, d
     _check(moe_combine_grad(dout, ldd, y, ldy, dtype, R, src2dst, weights, T, num_tokens, K, H, dy,
                             H, dw, st), "moe_combine_grad")
     return dict(dy=dy, dweights=dw, status=st)
+
+
+def _segments(starts, psum, masked_m, L):
+    """Checks where the experts' rows are: (seg_begin, seg_end)."""
+    if masked_m is not None:
+        if starts is not None or psum is not None:
+            raise ValueError("moeperm: give starts and psum, or masked_m, not both")
+        return None, _vec(masked_m, L, "masked_m", torch.int32)
+    if (starts is None) != (psum is None) or (starts is None and L != 1):
+        raise ValueError("moeperm: the experts' rows need starts and psum, or masked_m (a single "
+                         "expert may have all rows)")
+    return _vec(starts, L, "starts", torch.int32), _vec(psum, L, "psum", torch.int32)
+
+
+def _expert_rows(t, masked, L, name):
+    """Rows [R, width] of a compact tensor or of slabs [L, cap, width]: (2-D tensor, cap)."""
+    if not masked:
+        return t, 0
+    if t.dim() != 3 or t.shape[0] != L or not t.is_contiguous():
+        raise ValueError(f"moeperm: with masked_m, {name} must be contiguous slabs [{L}, cap, width]")
+    return t.view(-1, t.shape[2]), t.shape[1]
+
+
+def _expert_weights(w, gated):
+    """[L, N (gated: 2N), K] from [.., .., K]: (L, N, K)."""
+    if w.dim() not in (2, 3) or not w.is_contiguous():
+        raise ValueError("moeperm: w must be contiguous, [L, N, K] or [N, K] (gated: 2N)")
+    Nw, K = w.shape[-2:]
+    if gated and Nw % 2:
+        raise ValueError("moeperm: gated weights hold gate and up rows: [.., 2N, K]")
+    return (w.shape[0] if w.dim() == 3 else 1), (Nw // 2 if gated else Nw), K
+
+
+def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=False, residual=None,
+                  masked_m=None, x_scales=None, ld_xs=0, w_scales=None, ld_ws=0, out=None, pre=None,
+                  out_dtype=torch.bfloat16, status=None):
+    """Every expert's product over its rows: P = x w_e^T + bias_e, out = act(P)
+    [+ residual], or gated act(P[:, :N]) * P[:, N:] [+ residual].
+
+    x [R, K] with the segments starts / psum of dispatch_compact or permute, or
+    slabs [L, cap, K] with masked_m of dispatch_masked, or all rows of one
+    expert. w [L, N, K] (gated [L, 2N, K]: gate rows, then up rows); bias
+    [L, N or 2N] float32. bfloat16, float16, or e4m3 (uint8 or float8_e4m3fn)
+    with the packed scales of the dispatch (x_scales, ld_xs) and of
+    quant_group(w.view(-1, K)) (w_scales, ld_ws) and an output of out_dtype. act:
+    none, relu, silu or gelu. `pre` receives P for expert_matmul_grad. Rows of
+    no expert are not written. Returns out."""
+    fp8 = x.element_size() == 1
+    dtype = torch.float8_e4m3fn if fp8 else _elem(x, FLOATS[:2], "x")
+    L, N, K = _expert_weights(w, gated)
+    if w.element_size() != x.element_size() or (not fp8 and w.dtype != dtype):
+        raise ValueError(f"moeperm: w must have the type of x ({dtype}), not {w.dtype}")
+    if fp8 and (x_scales is None or w_scales is None):
+        raise ValueError("moeperm: e4m3 rows and weights need x_scales and w_scales")
+    if act not in ACT:
+        raise ValueError(f"moeperm: act must be one of {sorted(ACT)}, not {act!r}")
+    masked = masked_m is not None
+    begin, end = _segments(starts, psum, masked_m, L)
+    shape3 = x.shape
+    x, cap = _expert_rows(x, masked, L, "x")
+    ldx = _rows(x, "x", (x.shape[0], K))
+    R = x.shape[0]
+    Nw = 2 * N if gated else N
+    odt = out_dtype if fp8 else dtype
+    if odt not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"moeperm: out_dtype must be bfloat16 or float16, not {odt}")
+    _vec(bias, L * Nw, "bias")
+    full = (*shape3[:-1], N)
+    if out is None:
+        out = torch.empty(full, dtype=odt, device=x.device)
+    elif tuple(out.shape) != full:
+        raise ValueError(f"moeperm: out must have shape {full}")
+    o2 = _expert_rows(out, masked, L, "out")[0]
+    ldo = _rows(o2, "out", (R, N), odt)
+    res, ld_res = None, 0
+    if residual is not None:
+        res = _expert_rows(residual, masked, L, "residual")[0]
+        ld_res = _rows(res, "residual", (R, N), odt)
+    p2, ld_pre = None, 0
+    if pre is not None:
+        p2 = _expert_rows(pre, masked, L, "pre")[0]
+        ld_pre = _rows(p2, "pre", (R, Nw), dtype)
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=x.device)
+    _check(moe_expert_matmul(x, ldx, dtype, x_scales, ld_xs, R, K, w, w_scales, ld_ws, L, N, gated,
+                             act, bias, begin, end, cap, res, ld_res, o2, ldo, odt, p2, ld_pre, st),
+           "moe_expert_matmul")
+    return out
+
+
+class GradWorkspace:
+    """Workspace of expert_matmul_grad for R rows, L experts and Nw weight rows per
+    expert (gated: 2N), reusable across calls on one stream; needs no
+    initialisation."""
+
+    def __init__(self, R: int, L: int, Nw: int, dtype, device):
+        _ = dtype  # 16 bits for both types
+        self.nbytes = moe_expert_matmul_grad_workspace_bytes(R, L, Nw)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+
+def expert_matmul_grad(dout, x, w, starts=None, psum=None, pre=None, act="none", gated=False,
+                       masked_m=None, need=("dx", "dw"), dx=None, dw=None, dbias=None,
+                       dw_dtype=None, workspace=None, status=None):
+    """Gradients of expert_matmul for the output gradient dout: those of dx, dw and
+    dbias that `need` names or that a tensor is given for, from the kept `pre` (not needed without act and gate). dw
+    [as w] in dw_dtype (w's type, or float32), dbias [L, N or 2N] float32; both
+    are written in full, dx on the experts' rows. The residual's gradient is
+    dout. Returns a dict (dx, dw, dbias, status)."""
+    dtype = _elem(x, FLOATS[:2], "x")
+    L, N, K = _expert_weights(w, gated)
+    if w.dtype != dtype:
+        raise ValueError(f"moeperm: w must have the type of x ({dtype}), not {w.dtype}")
+    if act not in ACT:
+        raise ValueError(f"moeperm: act must be one of {sorted(ACT)}, not {act!r}")
+    masked = masked_m is not None
+    begin, end = _segments(starts, psum, masked_m, L)
+    dev, shape3 = x.device, x.shape
+    x2, cap = _expert_rows(x, masked, L, "x")
+    ldx = _rows(x2, "x", (x2.shape[0], K))
+    R, Nw = x2.shape[0], (2 * N if gated else N)
+    d2 = _expert_rows(dout, masked, L, "dout")[0]
+    ldd = _rows(d2, "dout", (R, N), dtype)
+    p2, ld_pre = None, 0
+    if act != "none" or gated:
+        if pre is None:
+            raise ValueError("moeperm: the gradient through an activation needs pre")
+        p2 = _expert_rows(pre, masked, L, "pre")[0]
+        ld_pre = _rows(p2, "pre", (R, Nw), dtype)
+    x_out, w_out, b_out = None, None, None
+    dwt = dw.dtype if dw is not None else (dw_dtype or dtype)
+    if "dx" in need or dx is not None:
+        x_out = _like(dx, tuple(shape3), dtype, dev, "dx")
+    if "dw" in need or dw is not None:
+        w_out = _like(dw, tuple(w.shape), dwt, dev, "dw")
+    if "dbias" in need or dbias is not None:
+        b_out = _vec(dbias, L * Nw, "dbias")
+        if b_out is None:
+            b_out = torch.empty((L, Nw), dtype=torch.float32, device=dev)
+    ws = workspace if workspace is not None else GradWorkspace(R, L, Nw, dtype, dev)
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+    _check(moe_expert_matmul_grad(d2, ldd, x2, ldx, dtype, R, K, w, L, N, gated, act, p2, ld_pre,
+                                  begin, end, cap, x_out, K, w_out, dwt, b_out, ws.buf, ws.nbytes,
+                                  st), "moe_expert_matmul_grad")
+    return dict(dx=x_out, dw=w_out, dbias=b_out, status=st)
 
 
 class NormWorkspace:

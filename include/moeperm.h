@@ -375,6 +375,82 @@ moe_status_t moe_combine_grad(
     int32_t H, void* dy, int64_t lddy, float* dw, int32_t* d_status, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* The experts' matrix products and their gradients                    */
+/* ------------------------------------------------------------------ */
+
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2, /* v / (1 + exp(-v)) */
+  MOE_ACT_GELU = 3  /* v * Phi(v), Phi the normal distribution function */
+} moe_act_t;
+
+/*
+ * moe_expert_matmul -- one product per expert over the rows of a layout, with bias,
+ * activation, gate and residual in its epilogue. For a row r of expert e:
+ *   P[r, f]   = sum_k x[r, k] * w[e, f, k] + bias[e, f]
+ *   out[r, f] = act(P[r, f]) + residual[r, f]                      f < N
+ *   gated:      act(P[r, f]) * P[r, N + f] + residual[r, f]        (w holds 2N rows: gate, up)
+ * accumulated in fp32 on the tensor cores and rounded once.
+ *
+ * The rows of expert e:
+ *   compact / expanded layout    seg_begin[e] .. seg_end[e] (the dispatch's starts and psum)
+ *   masked slabs                 seg_begin NULL, cap > 0: e*cap .. e*cap + seg_end[e]
+ *                                (seg_end = masked_m; R = L*cap)
+ *   dense                        both NULL, cap 0, L = 1: all R rows
+ * Rows of no expert are not written and may hold anything. Segments outside
+ * [0, R] set MOE_STATUS_BAD_LAYOUT and count as empty.
+ *   x [R, ldx]                   BF16, F16 (K % 8 == 0) or E4M3 (K % 128 == 0); rows
+ *                                16-byte aligned
+ *   x_scales, ld_xs              E4M3: packed UE8M0 words of the rows in groups of 128, as
+ *                                the dispatches write them (one block for the compact
+ *                                layout, one of cap rows per expert for slabs)
+ *   w [L, N or 2N, K]            the type of x, dense, 16-byte aligned
+ *   w_scales, ld_ws              E4M3: packed words of the L*N (or L*2N) weight rows, as
+ *                                moe_quant_group writes them
+ *   N                            N % 8 == 0 (gated: N % 16 == 0)
+ *   bias [L, N or 2N] f32, residual [R, ld_res]      (optional)
+ *   out [R, ldo]                 out_type: BF16 or F16 (the type of x unless it is E4M3);
+ *                                the residual has the same type
+ *   pre [R, ld_pre]              (optional; not for E4M3) P in the type of x, for
+ *                                moe_expert_matmul_grad
+ * L <= 1024, R < 2^31. Launches: 1.
+ */
+moe_status_t moe_expert_matmul(
+    const void* x, int64_t ldx, moe_elem_t type, const void* x_scales, int64_t ld_xs, int64_t R,
+    int32_t K, const void* w, const void* w_scales, int64_t ld_ws, int32_t L, int32_t N,
+    int32_t gated, moe_act_t act, const float* bias, const int32_t* seg_begin,
+    const int32_t* seg_end, int32_t cap, const void* residual, int64_t ld_res, void* out,
+    int64_t ldo, moe_elem_t out_type, void* pre, int64_t ld_pre, int32_t* d_status,
+    moe_stream_t stream);
+
+/* Bytes of device workspace moe_expert_matmul_grad needs for R rows, L experts
+ * and Nw = N (gated: 2N) weight rows: the gradient of P in 16 bits and partial
+ * sums of the bias gradient. No initialisation; not to be used by two calls
+ * that can run at once. 0 for negative or zero sizes (R = 0 is allowed). */
+size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
+
+/*
+ * moe_expert_matmul_grad -- gradients of moe_expert_matmul for the output gradient
+ * dout (the residual's gradient is dout itself). With dP the gradient of P,
+ * formed in fp32 from dout and the kept P and rounded once to `type`:
+ *   dx[r]  = sum_n dP[r, n] * w[e, n]        rows of no expert are not written
+ *   dw[e]  = sum over the rows of e of dP[r]^T x[r]     (written in full: 0 without rows)
+ *   dbias[e] = sum over the rows of e of dP[r]   (f32, written in full)
+ *   dout [R, ldd], x [R, ldx], w, pre [R, ld_pre]   BF16 or F16, as in the forward call
+ *                                (pre is not needed without activation and gate)
+ *   dx [R, ld_dx], dw [L, N or 2N, K] of dw_type (`type` or F32), dbias   each optional
+ * Rows of no expert may hold anything, NaN included. Sums are in fp32 and in
+ * a fixed order (deterministic). Launches: up to 4.
+ */
+moe_status_t moe_expert_matmul_grad(
+    const void* dout, int64_t ldd, const void* x, int64_t ldx, moe_elem_t type, int64_t R,
+    int32_t K, const void* w, int32_t L, int32_t N, int32_t gated, moe_act_t act, const void* pre,
+    int64_t ld_pre, const int32_t* seg_begin, const int32_t* seg_end, int32_t cap, void* dx,
+    int64_t ld_dx, void* dw, moe_elem_t dw_type, float* dbias, void* workspace,
+    size_t workspace_bytes, int32_t* d_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Norms before and after a block                                      */
 /* ------------------------------------------------------------------ */
 

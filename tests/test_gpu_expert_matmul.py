@@ -1,0 +1,343 @@
+"""The experts' products with bias, activation, gate and residual, and their
+gradients, against the formulas in 64 bits.
+
+Bounds, with v = 2^-23 (one step of a 32-bit accumulation, twice the half step,
+as tensor cores may truncate): a sum of K products is off by (K + 2) v times the
+sum of magnitudes; the activations' slopes are below 1.13 and their own error
+(__expf to about 2 + 1.2 |x| ulp, normcdff 5 ulp) below 2^-17 relative to the
+magnitudes that enter; the rounding to 16 bits adds half a step, and 2^-25 covers
+fp16's smallest numbers. Gradients carry one more half step for the rounding of
+the pre-activations' gradient."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+V, TINY, ACT_ERR = 2.0 ** -23, 2.0 ** -25, 2.0 ** -17
+
+
+def rand(seed, *shape, dtype=torch.float32, gain=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return (torch.randn(*shape, device=DEV, generator=g) * gain).to(dtype)
+
+
+def phi(name, v):
+    """(activation, slope) in 64 bits."""
+    if name == "silu":
+        s = torch.sigmoid(v)
+        return v * s, s + v * s * (1 - s)
+    if name == "gelu":
+        c = 0.5 * torch.erfc(-v / math.sqrt(2.0))
+        return v * c, c + v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    if name == "relu":
+        return v.clamp_min(0), (v > 0).double()
+    return v, torch.ones_like(v)
+
+
+def segments(counts, align, gap=0):
+    """Segment starts and ends of rows padded to `align` (and `gap` rows between), and R."""
+    starts, ends, at = [], [], 0
+    for c in counts:
+        starts.append(at)
+        ends.append(at + c)
+        at += -(-c // align) * align + gap
+    return starts, ends, max(at, 1)
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def quant(x):
+    """e4m3 codes, packed scale words, leading dimension and the values they stand for."""
+    R, K = x.shape
+    v = x.reshape(R, K // 128, 128)
+    m, e = torch.frexp(v.abs().amax(2).clamp_min(1e-10))
+    e = torch.where(m <= 0.875, e - 9, e - 8)
+    q = (v * torch.exp2(-e.float())[:, :, None]).to(torch.float8_e4m3fn)
+    val = (q.double() * torch.exp2(e.double())[:, :, None]).reshape(R, K)
+    G = K // 128
+    G4, ld = (G + 3) // 4, (R + 3) // 4 * 4
+    b = torch.full((ld, G4 * 4), 0xFF, dtype=torch.uint8, device=DEV)   # bytes past the last group are never used
+    b[:R, :G] = (e + 127).to(torch.uint8)
+    return q.reshape(R, K), b.view(torch.int32).t().contiguous(), ld, val
+
+
+SHAPES = [  # counts per expert, align, K, N
+    ([1], 1, 64, 64), ([1], 1, 8, 8), ([5], 1, 72, 136), ([16, 1], 16, 128, 128), ([0, 3, 0, 17], 8, 200, 264),
+    ([256, 255, 257], 1, 136, 128), ([0, 0, 0], 8, 64, 64), ([700], 128, 2048, 1408), ([31, 600, 0, 129, 64], 16, 512, 384),
+    ([40] * 33, 8, 256, 72),
+]
+EPI = [  # act, gated, bias, residual, pre
+    ("none", False, False, False, False), ("relu", False, True, True, True), ("silu", True, True, False, True),
+    ("gelu", False, True, False, False), ("gelu", True, False, True, False), ("silu", False, False, False, True),
+    ("relu", True, True, True, True),
+]
+
+
+def check_forward(out, pre, xv, wv, bias, res, seg, N, act, gated, dtype):
+    """Every real row within the bound; every other row as it was (9)."""
+    hs = torch.finfo(dtype).eps / 2
+    K = xv.shape[1]
+    real = torch.zeros(out.shape[0], dtype=torch.bool, device=DEV)
+    for e, (lo, hi) in enumerate(seg):
+        if hi <= lo:
+            continue
+        real[lo:hi] = True
+        P = xv[lo:hi] @ wv[e].t()
+        err = (K + 2) * V * (xv[lo:hi].abs() @ wv[e].abs().t())
+        if bias is not None:
+            P = P + bias[e].double()
+            err = err + V * P.abs()
+        if pre is not None:
+            assert ((pre[lo:hi].double() - P).abs() <= hs * P.abs() + err * (1 + hs) + TINY).all()
+        a, _ = phi(act, P[:, :N])
+        ea = 1.13 * err[:, :N] + ACT_ERR * (a.abs() + err[:, :N]) * (act != "none")
+        if gated:
+            u, eu = P[:, N:], err[:, N:]
+            want, bound = a * u, ea * u.abs() + a.abs() * eu + ea * eu + V * (a * u).abs()
+        else:
+            want, bound = a, ea
+        if res is not None:
+            want = want + res[lo:hi].double()
+            bound = bound + V * want.abs()
+        assert ((out[lo:hi].double() - want).abs() <= hs * want.abs() + bound * (1 + hs) + TINY).all()
+    assert (out[~real] == 9).all() and (pre is None or (pre[~real] == 9).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("epi", range(len(EPI)))
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_forward(dev, shape, epi, dtype):
+    counts, align, K, N = SHAPES[shape]
+    act, gated, has_b, has_r, has_p = EPI[epi]
+    if gated:
+        N = max(16, N // 16 * 16)
+    starts, ends, R = segments(counts, align, gap=shape % 3)
+    L, Nw = len(counts), 2 * N if gated else N
+    x = rand(1, R, K + 8, dtype=dtype)[:, :K]
+    w = rand(2, L, Nw, K, dtype=dtype, gain=K ** -0.5)
+    bias = rand(3, L, Nw) if has_b else None
+    res = rand(4, R, N + 3, dtype=dtype)[:, :N] if has_r else None
+    seg = list(zip(starts, ends))
+    for lo in range(R):  # rows of no expert hold NaN
+        if not any(a <= lo < b for a, b in seg):
+            x[lo] = float("nan")
+    out = torch.full((R, N), 9.0, device=DEV, dtype=dtype)
+    pre = torch.full((R, Nw), 9.0, device=DEV, dtype=dtype) if has_p else None
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = lambda o: dev.expert_matmul(x, w, i32(starts), i32(ends), bias=bias, act=act, gated=gated, residual=res,
+                                       out=o, pre=pre, status=st)
+    call(out)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
+    check_forward(out, pre, x.double(), w.double(), bias, res, seg, N, act, gated, dtype)
+    again = call(torch.full_like(out, 9.0))
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("R", [1, 2, 15, 16, 17, 100, 300, 1000])
+@pytest.mark.parametrize("K,N", [(64, 8), (2048, 264), (136, 1024)])
+def test_forward_dense(dev, R, K, N):
+    x, w = rand(1, R, K, dtype=torch.bfloat16), rand(2, N, K, dtype=torch.bfloat16, gain=K ** -0.5)
+    b, res = rand(3, N), rand(4, R, N, dtype=torch.bfloat16)
+    out = dev.expert_matmul(x, w, bias=b, residual=res)
+    check_forward(out, None, x.double(), w[None].double(), b[None], res, [(0, R)], N, "none", False, torch.bfloat16)
+
+
+FP8 = [  # counts, align, K, N, gated
+    ([1], 1, 128, 64, False), ([3, 0, 30], 4, 512, 128, True), ([225, 224], 1, 640, 136, False), ([449], 1, 1152, 64, True),
+    ([4] * 32, 128, 7168, 256, True), ([100, 0, 300], 128, 2048, 384, True),
+]
+
+
+@pytest.mark.parametrize("odt", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts,align,K,N,gated", FP8)
+def test_forward_e4m3(dev, counts, align, K, N, gated, odt):
+    starts, ends, R = segments(counts, align)
+    L, Nw = len(counts), 2 * N if gated else N
+    q, sc, ld, xv = quant(rand(1, R, K) * torch.exp2(torch.randint(-6, 7, (R, 1), device=DEV).float()))
+    wq, wsc, ldw, wv = quant(rand(2, L * Nw, K, gain=K ** -0.5))
+    bias = rand(3, L, Nw)
+    seg = list(zip(starts, ends))
+    for lo in range(R):
+        if not any(a <= lo < b for a, b in seg):
+            q.view(torch.uint8)[lo] = 0x7F
+            sc[:, lo] = -1
+    out = torch.full((R, N), 9.0, device=DEV, dtype=odt)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dev.expert_matmul(q, wq.view(L, Nw, K), i32(starts), i32(ends), bias=bias, act="silu" if gated else "none", gated=gated,
+                      x_scales=sc, ld_xs=ld, w_scales=wsc, ld_ws=ldw, out=out, out_dtype=odt, status=st)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
+    check_forward(out, None, xv, wv.view(L, Nw, K), bias, None, seg, N, "silu" if gated else "none", gated, odt)
+
+
+def test_forward_on_a_dispatch(dev):
+    """e4m3 rows of both dispatch layouts through the same product: equal rows, equal results."""
+    T, H, E, L, K, N = 64, 512, 16, 8, 4, 128
+    x = rand(1, T, H, dtype=torch.bfloat16)
+    rng = np.random.default_rng(0)
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:K] for _ in range(T)]).astype(np.int32)).to(DEV)
+    tw = torch.softmax(rand(2, T, K), 1)
+    w = rand(3, L * 2 * N, H, dtype=torch.bfloat16, gain=H ** -0.5)
+    wq = dev.quant_group(w)
+    kw = dict(act="silu", gated=True, w_scales=wq["scales"], ld_ws=wq["ld_s"])
+    c = dev.dispatch_compact(x, ids, tw, E, L, block_e=128)
+    m = dev.dispatch_masked(x, ids, tw, E, L, T)
+    w3 = wq["xq"].view(L, 2 * N, H)
+    yc = dev.expert_matmul(c["xq"], w3, c["starts"], c["psum"], x_scales=c["scales"], ld_xs=c["ld_s"], **kw)
+    ym = dev.expert_matmul(m["xq"], w3, masked_m=m["masked_m"], x_scales=m["scales"], ld_xs=m["ld_s"], **kw)
+    a = dev.combine(yc, c["src2dst"], tw)
+    b = dev.combine(ym.view(-1, N), m["src2dst"], tw)
+    assert torch.equal(a, b) and torch.isfinite(a.float()).all() and (a != 0).any()
+
+
+@pytest.mark.parametrize("begin,end", [([0, 10], [4, 21]), ([-1, 4], [3, 8]), ([0, 6], [4, 5])])
+def test_bad_segments_are_flagged(dev, begin, end):
+    """A segment outside the rows counts as empty and is flagged; the others are computed."""
+    x, w = rand(1, 20, 64, dtype=torch.bfloat16), rand(2, 2, 64, 64, dtype=torch.bfloat16)
+    out = torch.full((20, 64), 9.0, device=DEV, dtype=torch.bfloat16)
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dev.expert_matmul(x, w, i32(begin), i32(end), out=out, status=st)
+    assert dev.moe_status_sync(st) == dev.MOE_ERR_BAD_LAYOUT
+    for e, (lo, hi) in enumerate(zip(begin, end)):
+        if 0 <= lo <= hi <= 20:
+            want = (x[lo:hi].double() @ w[e].double().t()).bfloat16()
+            assert (out[lo:hi].double() - want.double()).abs().max() <= 0.05 * want.double().abs().max()
+    assert (out[8 if begin[0] < 0 else 4:] == 9).all() or begin[0] < 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("act,gated", [("none", False), ("silu", True), ("gelu", False), ("relu", True), ("gelu", True)])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_gradients(dev, shape, act, gated, dtype):
+    counts, align, K, N = SHAPES[shape]
+    if gated:
+        N = max(16, N // 16 * 16)
+    starts, ends, R = segments(counts, align, gap=shape % 3)
+    L, Nw = len(counts), 2 * N if gated else N
+    seg = list(zip(starts, ends))
+    x, dout = rand(1, R, K + 8, dtype=dtype)[:, :K], rand(2, R, N + 8, dtype=dtype)[:, :N]
+    w = rand(3, L, Nw, K, dtype=dtype, gain=K ** -0.5)
+    pre = rand(4, R, Nw, dtype=dtype)
+    for r in range(R):
+        if not any(a <= r < b for a, b in seg):
+            x[r] = dout[r] = pre[r] = float("nan")
+    dx = torch.full((R, K), 9.0, device=DEV, dtype=dtype)
+    dwt = torch.float32 if shape % 2 else dtype
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    call = lambda d: dev.expert_matmul_grad(dout, x, w, i32(starts), i32(ends), pre=pre, act=act, gated=gated, dx=d,
+                                            need=("dx", "dw", "dbias"), dw_dtype=dwt, status=st)
+    o = call(dx)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
+    hs, hw = torch.finfo(dtype).eps / 2, torch.finfo(dwt).eps / 2
+    real = torch.zeros(R, dtype=torch.bool, device=DEV)
+    for e, (lo, hi) in enumerate(seg):
+        if hi <= lo:
+            assert (o["dw"][e] == 0).all() and (o["dbias"][e] == 0).all()
+            continue
+        real[lo:hi] = True
+        g, p, n = dout[lo:hi].double(), pre[lo:hi].double(), hi - lo
+        a, d = phi(act, p[:, :N])
+        dP = torch.cat([g * d * p[:, N:], g * a], 1) if gated else g * d
+        # the 32-bit gradient of P (slopes are below 1.13, relative error as above), then its rounding
+        if act == "none" and not gated:
+            e32, e16 = torch.zeros_like(dP), torch.zeros_like(dP)
+        else:
+            m = torch.cat([(g * p[:, N:]).abs() * 1.13, (g * p[:, :N]).abs()], 1) if gated else g.abs() * 1.13
+            e32 = ACT_ERR * m
+            e16 = e32 + hs * (dP.abs() + e32) + TINY
+        for got, A, B, eA, h, steps in (
+                (o["dx"][lo:hi], dP, w[e].double(), e16, hs, Nw),
+                (o["dw"][e], dP.t(), x[lo:hi].double(), e16.t(), hw, n)):
+            want, mag = A @ B, A.abs() @ B.abs()
+            bound = eA @ B.abs() + (steps + 2) * V * (mag + eA @ B.abs())
+            assert ((got.double() - want).abs() <= h * want.abs() + bound * (1 + h) + TINY).all()
+        bound = e32.sum(0) + (n + 2) * V * (dP.abs() + e32).sum(0)
+        assert ((o["dbias"][e].double() - dP.sum(0)).abs() <= bound).all()
+    assert (dx[~real] == 9).all()
+    again = call(torch.full_like(dx, 9.0))
+    for k in ("dx", "dw", "dbias"):
+        assert torch.equal(o[k], again[k]), k
+
+
+def test_gradients_of_slabs_equal_those_of_segments(dev):
+    L, cap, K, N = 5, 48, 128, 64
+    m = [0, 48, 17, 1, 30]
+    x, dout = rand(1, L, cap, K, dtype=torch.bfloat16), rand(2, L, cap, N, dtype=torch.bfloat16)
+    pre, w = rand(3, L, cap, N, dtype=torch.bfloat16), rand(4, L, N, K, dtype=torch.bfloat16)
+    starts = [e * cap for e in range(L)]
+    ends = [s + c for s, c in zip(starts, m)]
+    kw = dict(act="silu", need=("dx", "dw", "dbias"))
+    z = lambda *s: torch.zeros(*s, device=DEV, dtype=torch.bfloat16)
+    a = dev.expert_matmul_grad(dout, x, w, masked_m=i32(m), pre=pre, dx=z(L, cap, K), **kw)
+    b = dev.expert_matmul_grad(dout.view(-1, N), x.view(-1, K), w, i32(starts), i32(ends), pre=pre.view(-1, N),
+                               dx=z(L * cap, K), **kw)
+    for k in ("dx", "dw", "dbias"):
+        assert torch.equal(a[k].reshape(b[k].shape), b[k]), k
+
+
+def test_gradients_against_differences(dev):
+    """<c, out> by central differences in 64 bits along one direction of x, w and bias."""
+    counts, K, N = [7, 0, 20], 64, 32
+    starts, ends, R = segments(counts, 8)
+    x, w = rand(1, R, K, dtype=torch.float16), rand(2, 3, 2 * N, K, dtype=torch.float16, gain=0.125)
+    b, c = rand(3, 3, 2 * N), rand(4, R, N, dtype=torch.float16)
+    dirs = [rand(5, R, K, dtype=torch.float64), rand(6, 3, 2 * N, K, dtype=torch.float64), rand(7, 3, 2 * N, dtype=torch.float64)]
+
+    def f(h):
+        xx, ww, bb = (v.double() + h * d for v, d in zip((x, w, b), dirs))
+        total = 0
+        for e, (lo, hi) in enumerate(zip(starts, ends)):
+            P = xx[lo:hi] @ ww[e].t() + bb[e]
+            total = total + (c[lo:hi].double() * phi("gelu", P[:, :N])[0] * P[:, N:]).sum()
+        return total
+
+    h = 1e-4
+    want = (8 * (f(h) - f(-h)) - (f(2 * h) - f(-2 * h))) / (12 * h)
+    pre = torch.zeros(R, 2 * N, device=DEV, dtype=torch.float16)
+    kw = dict(act="gelu", gated=True)
+    dev.expert_matmul(x, w, i32(starts), i32(ends), bias=b, pre=pre, **kw)
+    g = dev.expert_matmul_grad(c, x, w, i32(starts), i32(ends), pre=pre, dx=torch.zeros_like(x), dw_dtype=torch.float32,
+                               need=("dx", "dw", "dbias"), **kw)
+    parts = [(g[k].double() * d) for k, d in zip(("dx", "dw", "dbias"), dirs)]
+    got, mag = sum(p.sum() for p in parts), sum(p.abs().sum() for p in parts)
+    # roundings of pre, dP and dx to fp16 (2^-11 each): at most four of them on any path
+    assert (got - want).abs() <= 4 * 2.0 ** -11 * mag
+
+
+def test_graph_replay_with_other_counts(dev):
+    """Captured once, replayed with other segment ends: the tile list is formed on the device."""
+    L, K, N, R = 6, 256, 192, 600
+    x, w = rand(1, R, K, dtype=torch.bfloat16), rand(2, L, N, K, dtype=torch.bfloat16, gain=0.06)
+    starts = i32([0, 100, 200, 300, 400, 500])
+    ends = i32([10, 100, 300, 301, 433, 600])
+    out, st = torch.zeros(R, N, device=DEV, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32, device=DEV)
+    pre, dw = torch.zeros_like(out), torch.zeros_like(w)
+    ws = dev.GradWorkspace(R, L, N, torch.bfloat16, DEV)
+
+    def step():
+        dev.expert_matmul(x, w, starts, ends, act="silu", out=out, pre=pre, status=st)
+        return dev.expert_matmul_grad(out, x, w, starts, ends, pre=pre, act="silu", dw=dw, need=("dw",), workspace=ws,
+                                      status=st)
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for e in ([0, 100, 200, 300, 400, 500], [100, 200, 300, 400, 500, 600], [1, 180, 216, 400, 499, 501]):
+        ends.copy_(i32(e))
+        out.zero_(), pre.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        a, b = out.clone(), dw.clone()
+        out.zero_(), pre.zero_()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(a, out) and torch.equal(b, dw)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
