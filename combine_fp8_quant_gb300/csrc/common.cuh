@@ -279,6 +279,14 @@ __device__ __forceinline__ void cp_async16(void* sdst, const void* gsrc) {
                ::"r"((uint32_t)__cvta_generic_to_shared(sdst)), "l"(gsrc)
                : "memory");
 }
+// Asynchronous 4-byte copy, and an arrival on an mbarrier (counted in its
+// initial count) once this thread's copies issued so far have landed.
+__device__ __forceinline__ void cp_async4(uint32_t sdst, const void* gsrc) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(sdst), "l"(gsrc) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t mbar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(mbar) : "memory");
+}
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }

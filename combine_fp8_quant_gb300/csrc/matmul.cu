@@ -13,26 +13,31 @@
 //    steps of 16: a tile of 40 rows costs 48 columns, not 128 (experts of a
 //    prefill hold a few hundred rows, of a decode batch a few), and the rows of
 //    an expert are cut into equal tiles of at most 256;
-//  - a warp's 32 lanes hold neighbouring output elements, so the epilogue
-//    stores straight from registers in full 32-byte sectors.
+//  - the epilogue reads tensor memory as 8x8 fragments, transposes them through
+//    a small staging area (stmatrix) and stores 16-byte pieces of output rows.
 // With a gated activation a tile of 128 weight rows is 64 gate and 64 up rows
 // interleaved by 16 (one 5-D tensor map does it), so gate and up of a feature
-// are 16 lanes apart in one warp and meet through one shuffle.
+// are 16 lanes apart and arrive in the same register position of one thread.
 //
-// A CTA is one of a cluster of two with neighbouring feature blocks and the
-// same rows; each loads half of the row tile and multicasts it to both, so a
-// 128 x 256 tile costs L2 32 KB per 128 bytes of reduction instead of 48 KB.
-// Warp roles: 0 loads (TMA), 1 issues the products, 2 lays out the e4m3 scales,
-// 4-7 the epilogue, one warp per 32 lanes of tensor memory; two accumulators
-// (columns 0.. and kRows..) let the epilogue of a tile overlap the products of
-// the next. The grid is persistent; the tile list is formed on the device from
-// the segment ends, so a captured graph can be replayed with other counts.
+// Two CTAs with neighbouring feature blocks form a pair (cta_group::2): each
+// holds its own 128 weight rows and half of the tile's rows, and the pair's
+// products read both halves. With one CTA per product the shared-memory port
+// was the bound: filling and reading 48 KB each per 128 bytes of reduction of a
+// 128 x 256 tile takes 768 cycles at 128 bytes a cycle where the products take
+// 512 (measured 727); a pair moves 32 KB.
+// Warp roles: 0 loads (TMA), 1 (of the pair's first CTA) issues the products, 2
+// and 3 lay out the e4m3 scales, or 2 zeroes the last lines of kGradW, 4-7 the
+// epilogue, one warp per 32 lanes of tensor memory; two accumulators (columns
+// 0.. and kRows..) let the epilogue of a tile overlap the products of the next.
+// The grid is persistent; the tile list is formed on the device from the
+// segment ends, so a captured graph can be replayed with other counts.
 //
 // Rows outside every segment are read at most as columns that are not stored.
 // In kGradW rows are the reduction: lines of the last block past the segment's
 // end are zeroed in shared memory before the product, so padding rows may hold
 // anything (NaN included).
 #include <cuda.h>
+#include <stddef.h>
 
 #include <mutex>
 
@@ -48,9 +53,15 @@ constexpr int kForward = 0, kGradX = 1, kGradW = 2;
 constexpr int kThreads = 256;
 constexpr int kMaxStages = 10;
 constexpr int kABytes = 16384;            // 128 rows x 128 bytes
+// Reduction blocks of 128 bytes per stage. Two halve the waits per block, which
+// the twice as fast e4m3 products need (prefill, 64 experts: 732 against 820 us);
+// 16-bit products have the time and want the finer ring (134 against 142 us).
+template <bool FP8>
+constexpr int kSubBlocks = FP8 ? 2 : 1;
 constexpr int kTmemCols = 512;
 constexpr int kScaleCols = 448;           // e4m3: scale words, 12 columns per buffer
 constexpr int kScaleBytes = 512 + 1024;   // of one buffer: 128 + 256 words
+constexpr int kScaleBufs = 8;             // in shared memory (two in tensor memory)
 constexpr int kBoxes = 7;                 // heights of the row boxes a CTA may load
 __host__ __device__ constexpr int box_rows(int i) {
   return i < 3 ? 8 << i : i < 5 ? 32 * (i - 1) : 16 * (i + 2);  // 8 16 32 64 96 112 128
@@ -75,7 +86,6 @@ struct Args {
   int32_t feats;             // features of an output row
   int32_t wrows;             // weight rows per expert (kGradW: output rows)
   int32_t gated, act, f16, out_f32;
-  int32_t cl;                // CTAs per cluster, 1 or 2
   int32_t ring_bytes;
   const float* bias;         // [L, wrows]
   const void* residual;
@@ -90,6 +100,10 @@ struct Args {
   int64_t ld_ws;
   int32_t G4;
   int32_t* status;
+};
+
+struct Bars {  // one barrier of each kind per stage
+  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
 };
 
 struct Tile {
@@ -126,11 +140,124 @@ __device__ __forceinline__ bool warp_wait_or_stop(uint32_t bar, uint32_t parity,
   return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop));
 }
 
-__device__ __forceinline__ uint16_t to_16bit(float v, bool f16) {
-  return (uint16_t)(f16 ? pack_f16x2(v, 0.0f) : pack_bf16x2(v, 0.0f));
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, bool f16) {
+  return f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
 }
-__device__ __forceinline__ float from_16bit(uint16_t v, bool f16) {
-  return f16 ? f16x2_to_float2(v).x : __uint_as_float((uint32_t)v << 16);
+__device__ __forceinline__ float2 unpack2(uint32_t w, bool f16) {
+  return f16 ? f16x2_to_float2(w) : make_float2(bf16_lo(w), bf16_hi(w));
+}
+
+// The epilogue's staging area: per warp 32 output rows of up to 32 features
+// (64 bytes), so that fragments of tensor memory (feature-major) leave as whole
+// 16-byte pieces of output rows. A pitch of 80 bytes puts the 8 rows of a block
+// into different banks.
+constexpr int kPitch = 80;
+constexpr int kStageBytes = 4 * 32 * kPitch;
+
+// Rows of 16-bit elements in global memory; `vec`: 16-byte pieces are aligned.
+struct Rows16 {
+  uint16_t* p;
+  int64_t ld;
+  bool vec;
+};
+__device__ __forceinline__ Rows16 rows16(const void* p, int64_t ld) {
+  return {static_cast<uint16_t*>(const_cast<void*>(p)), ld, ((reinterpret_cast<uintptr_t>(p) | (uint64_t)(ld * 2)) & 15) == 0};
+}
+__device__ __forceinline__ void put8(const Rows16& r, int64_t row, int col, const uint4& v) {
+  uint16_t* dst = r.p + row * r.ld + col;
+  if (r.vec) {
+    st_v4(dst, v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      dst[2 * i] = (uint16_t)w[i];
+      dst[2 * i + 1] = (uint16_t)(w[i] >> 16);
+    }
+  }
+}
+__device__ __forceinline__ uint4 get8(const Rows16& r, int64_t row, int col) {
+  const uint16_t* src = r.p + row * r.ld + col;
+  if (r.vec) return ld_nc_v4(src);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)__ldg(src + 2 * i) | ((uint32_t)__ldg(src + 2 * i + 1) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One warp: the 32 x 32 fragments a (features 0-15) and b (16-31) to the
+// staging area and from there to `nr` rows; a lane's 16-byte piece c = lane & 3
+// goes to column col[c >> 1] + 8 * (c & 1), if that is below lim[c >> 1].
+__device__ __forceinline__ void store_32x32(uint8_t* st, const float (&a)[16], const float (&b)[16], bool f16,
+                                            const Rows16& out, int64_t row, int nr, int col0, int col1, int lim0,
+                                            int lim1) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t sa = smem_addr(st) + (lane & 7) * kPitch + (lane >> 3) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    stmatrix_trans(sa + i * 8 * kPitch, pack2(a[4 * i], a[4 * i + 1], f16), pack2(a[4 * i + 2], a[4 * i + 3], f16),
+                   pack2(b[4 * i], b[4 * i + 1], f16), pack2(b[4 * i + 2], b[4 * i + 3], f16));
+  __syncwarp();
+  const int c = lane & 3;
+  const int col = (c >> 1 ? col1 : col0) + 8 * (c & 1);
+  const bool ok = col < (c >> 1 ? lim1 : lim0);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = (lane >> 2) + 8 * k;
+    if (ok && r < nr) put8(out, row + r, col, *reinterpret_cast<const uint4*>(st + r * kPitch + c * 16));
+  }
+  __syncwarp();
+}
+// The same for 16 features (fragments a).
+__device__ __forceinline__ void store_16x32(uint8_t* st, const float (&a)[16], bool f16, const Rows16& out,
+                                            int64_t row, int nr, int col0, int lim) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t sa = smem_addr(st) + ((lane & 7) + 8 * (lane >> 4)) * kPitch + ((lane >> 3) & 1) * 16;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    stmatrix_trans(sa + i * 8 * kPitch, pack2(a[4 * i], a[4 * i + 1], f16), pack2(a[4 * i + 2], a[4 * i + 3], f16),
+                   pack2(a[4 * i + 4], a[4 * i + 5], f16), pack2(a[4 * i + 6], a[4 * i + 7], f16));
+  __syncwarp();
+  const int col = col0 + 8 * (lane & 1);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (lane >> 1) + 16 * k;
+    if (col < lim && r < nr) put8(out, row + r, col, *reinterpret_cast<const uint4*>(st + r * kPitch + (lane & 1) * 16));
+  }
+  __syncwarp();
+}
+// Residual rows into fragments, added to a (features 0-15) and, with kWide, b.
+template <bool kWide>
+__device__ __forceinline__ void add_rows(uint8_t* st, float (&a)[16], float (&b)[16], bool f16, const Rows16& res,
+                                         int64_t row, int nr, int col0, int lim) {
+  const int lane = threadIdx.x & 31;
+  constexpr int kPieces = kWide ? 4 : 2, kPer = 32 / kPieces;  // 16-byte pieces a row, rows at once
+  const int c = lane % kPieces, col = col0 + 8 * c;
+#pragma unroll
+  for (int k = 0; k < 32 / kPer; ++k) {
+    const int r = lane / kPieces + kPer * k;
+    const uint4 v = col < lim && r < nr ? get8(res, row + r, col) : make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(st + r * kPitch + c * 16) = v;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; i += kWide ? 1 : 2) {
+    uint32_t w[4];
+    if constexpr (kWide) {
+      ldmatrix_trans(smem_addr(st) + ((lane & 7) + 8 * i) * kPitch + (lane >> 3) * 16, w);
+    } else {
+      ldmatrix_trans(smem_addr(st) + ((lane & 7) + 8 * (i + (lane >> 4))) * kPitch + ((lane >> 3) & 1) * 16, w);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float2 f = unpack2(w[m], f16);
+      float (&dst)[16] = (kWide && m >= 2) ? b : a;
+      const int at = kWide ? 4 * i + 2 * (m & 1) : 4 * (i + (m >> 1)) + 2 * (m & 1);
+      dst[at] += f.x;
+      dst[at + 1] += f.y;
+    }
+  }
+  __syncwarp();
 }
 
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
@@ -155,22 +282,23 @@ template <int MODE, bool FP8>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t dyn[];
-  __shared__ uint64_t s_full[kMaxStages], s_empty[kMaxStages];
-  __shared__ uint64_t s_tfull[2], s_tempty[2], s_sfull[2], s_sempty[2], s_drain;
+  __shared__ Bars s_bars;
+  uint64_t *s_full = s_bars.full, *s_empty = s_bars.empty, *s_ready = s_bars.ready;
+  __shared__ uint64_t s_tfull[2], s_tempty[2], s_sraw[kScaleBufs], s_sfull[kScaleBufs], s_sempty[kScaleBufs], s_drain;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_stop;
   __shared__ int s_max;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = p.cl > 1 ? (int)cluster_rank() : 0;
-  const int cluster = blockIdx.x / p.cl, nclusters = gridDim.x / p.cl;
-  const uint16_t mask = (uint16_t)((1 << p.cl) - 1);
-  constexpr int kTileRows = kRows<FP8>;
+  const int rank = (int)cluster_rank();  // 0 issues the pair's products
+  const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
+  constexpr int kTileRows = kRows<FP8>, kSub = kSubBlocks<FP8>;
   constexpr int kRedBlock = FP8 ? 128 : 64;  // reduction elements per stage
 
   uint8_t* ring = dyn + ((1024 - (smem_addr(dyn) & 1023)) & 1023);
-  uint8_t* s_scale = ring + p.ring_bytes;                                 // FP8: two buffers
-  int32_t* s_tiles = reinterpret_cast<int32_t*>(s_scale + (FP8 ? 2 * kScaleBytes : 0));  // [L + 1]
+  uint8_t* s_scale = ring + p.ring_bytes;                                 // FP8: kScaleBufs buffers
+  uint8_t* s_stage = s_scale + (FP8 ? kScaleBufs * kScaleBytes : 0);               // the epilogue's
+  int32_t* s_tiles = reinterpret_cast<int32_t*>(s_stage + kStageBytes);   // [L + 1]
   int32_t* s_begin = s_tiles + p.L + 1;
   int32_t* s_count = s_begin + p.L;
 
@@ -178,12 +306,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_addr(s_full + i), 1);
-      mbar_init(smem_addr(s_empty + i), p.cl);
+      mbar_init(smem_addr(s_empty + i), 1);
+      if (MODE == kGradW) mbar_init(smem_addr(s_ready + i), 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(s_tfull + i), 1);
-      mbar_init(smem_addr(s_tempty + i), 4);
-      mbar_init(smem_addr(s_sfull + i), 1);
+      mbar_init(smem_addr(s_tempty + i), 8);  // four epilogue warps of each CTA
+    }
+    for (int i = 0; i < kScaleBufs; ++i) {
+      mbar_init(smem_addr(s_sraw + i), 32);
+      mbar_init(smem_addr(s_sfull + i), 2);  // one of each CTA
       mbar_init(smem_addr(s_sempty + i), 1);
     }
     mbar_init(smem_addr(&s_drain), 1);
@@ -234,18 +366,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (p.cl > 1) cluster_sync();  // the peer's barriers are ready before anything arrives on them
+  cluster_sync();  // the other CTA's barriers are ready before anything arrives on them
   const uint32_t tmem = s_tmem;
 
-  // ---- tile list (the same for every role and both CTAs of the cluster)
+  // ---- tile list (the same for every role and both CTAs)
   const int fblk = p.gated && MODE == kForward ? 64 : 128;  // features per block
-  const int nfc = ((p.feats + fblk - 1) / fblk + p.cl - 1) / p.cl;  // clusters of blocks
+  const int nfp = (p.feats + 2 * fblk - 1) / (2 * fblk);    // pairs of blocks
   const int nnb = MODE == kGradW ? (p.wrows + 255) / 256 : 0;       // kGradW: row blocks per expert
-  const int total = MODE == kGradW ? p.L * nnb * nfc : s_tiles[p.L] * nfc;
+  const int total = MODE == kGradW ? p.L * nnb * nfp : s_tiles[p.L] * nfp;
   auto tile_at = [&](int w) {
     Tile t;
-    t.fb = (w % nfc) * p.cl + rank;
-    const int rb = w / nfc;
+    t.fb = (w % nfp) * 2 + rank;
+    const int rb = w / nfp;
     if constexpr (MODE == kGradW) {
       t.e = rb / nnb;
       t.row0 = (rb - t.e * nnb) * 256;
@@ -274,183 +406,237 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- ring geometry: as many stages as the largest row tile allows
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
-  const int b_bytes = MODE == kGradW ? min((p.wrows + 63) / 64, 4) * 8192
-                                     : 2 * box_rows(box_index(max_n / 2)) * 128;
-  const int stage_bytes = kABytes + b_bytes;
+  const int b_bytes = MODE == kGradW ? min((p.wrows + 127) / 128, 2) * 8192
+                                     : box_rows(box_index(max_n / 2)) * 128;
+  const int sub_bytes = kABytes + b_bytes, stage_bytes = kSub * sub_bytes;
   const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
   const uint32_t ring_s = smem_addr(ring);
 
   if (warp == 0) {
     // ------------------------------------------------------------------ loads
-    if (lane == 0) {
-      int it = 0;
+    // Each CTA loads its weight rows and its half of the tile's rows; the bytes
+    // of both count on the first CTA's barrier (kGradW: each on its own).
+    if (elect_one()) {
+      int s = 0, issued = 0;
+      uint32_t ph = 1;  // parity of the wait for a free stage
       bool ok = true;
-      for (int w = cluster; w < total && ok; w += nclusters) {
+      for (int w = pair; w < total && ok; w += npairs) {
         const Tile t = tile_at(w);
-        const int box = MODE == kGradW ? 0 : box_index(t.n / 2);
-        const int half = box_rows(box);
-        const int nbox = (t.n + 63) / 64;  // kGradW: 64-wide boxes of the row side
-        const uint32_t bytes = kABytes + (MODE == kGradW ? nbox * 8192 : 2 * half * 128);
-        for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-          const int s = it % stages;
-          if (!(ok = wait_or_stop(smem_addr(s_empty + s), ((it / stages) & 1) ^ 1, &s_stop))) break;
-          const uint32_t full = smem_addr(s_full + s);
-          const uint32_t a = ring_s + s * stage_bytes, b = a + kABytes;
-          mbar_expect_tx(full, bytes);
-          if constexpr (MODE == kForward) {
-            if (p.gated) tma_load_5d(a, &maps.a, full, kb * kRedBlock, 0, 0, t.fb * 4, t.e);
-            else tma_load_3d(a, &maps.a, full, kb * kRedBlock, t.fb * 128, t.e);
-          } else if constexpr (MODE == kGradX) {
-            tma_load_3d(a, &maps.a, full, t.fb * 128, kb * 64, t.e);
-            tma_load_3d(a + 8192, &maps.a, full, t.fb * 128 + 64, kb * 64, t.e);
-          } else {
-            tma_load_2d(a, &maps.a, full, t.fb * 128, t.red_row0 + kb * 64);
-            tma_load_2d(a + 8192, &maps.a, full, t.fb * 128 + 64, t.red_row0 + kb * 64);
-          }
+        const int half = t.n / 2;
+        const int box = MODE == kGradW ? 0 : box_index(half);
+        const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
+        const uint32_t bytes = kABytes + (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
+        const CUtensorMap* mb = &maps.b[box];
+        const int brow = t.row0 + rank * half;
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+          if (!(ok = wait_or_stop(smem_addr(s_empty + s), ph, &s_stop))) break;
+          const int nsub = min(kSub, t.nkb - kb0);
+          uint32_t full = smem_addr(s_full + s);
           if constexpr (MODE == kGradW) {
-            for (int i = rank; i < nbox; i += p.cl) {
-              if (p.cl > 1)
-                tma_load_2d_multi(b + i * 8192, &maps.b[0], full, t.row0 + i * 64, t.red_row0 + kb * 64, mask);
-              else
-                tma_load_2d(b + i * 8192, &maps.b[0], full, t.row0 + i * 64, t.red_row0 + kb * 64);
-            }
+            mbar_expect_tx(full, nsub * bytes);
           } else {
-            for (int h = rank; h < 2; h += p.cl) {
-              if (p.cl > 1)
-                tma_load_2d_multi(b + h * half * 128, &maps.b[box], full, kb * kRedBlock, t.row0 + h * half, mask);
-              else
-                tma_load_2d(b + h * half * 128, &maps.b[box], full, kb * kRedBlock, t.row0 + h * half);
+            if (rank == 0) mbar_expect_tx(full, nsub * 2 * bytes);
+            else full = map_to_rank(full, 0);
+          }
+#pragma unroll
+          for (int j = 0; j < kSub; ++j) {
+            if (j >= nsub) break;
+            const int kb = kb0 + j;
+            const uint32_t a = ring_s + s * stage_bytes + j * sub_bytes, b = a + kABytes;
+            if constexpr (MODE == kForward) {
+              if (p.gated) tma_load_5d(a, &maps.a, full, kb * kRedBlock, 0, 0, t.fb * 4, t.e);
+              else tma_load_3d(a, &maps.a, full, kb * kRedBlock, t.fb * 128, t.e);
+              tma_load_2d(b, mb, full, kb * kRedBlock, brow);
+            } else if constexpr (MODE == kGradX) {
+              tma_load_3d(a, &maps.a, full, t.fb * 128, kb * 64, t.e);
+              tma_load_3d(a + 8192, &maps.a, full, t.fb * 128 + 64, kb * 64, t.e);
+              tma_load_2d(b, mb, full, kb * kRedBlock, brow);
+            } else {
+              const int y = t.red_row0 + kb * 64;
+              tma_load_2d(a, &maps.a, full, t.fb * 128, y);
+              tma_load_2d(a + 8192, &maps.a, full, t.fb * 128 + 64, y);
+              for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * 8192, mb, full, brow + i * 64, y);
             }
+          }
+          ++issued;
+          if (++s == stages) {
+            s = 0;
+            ph ^= 1;
           }
         }
       }
-      if (!ok)  // let the copies in flight land, again with a limit
-        for (int i = it > stages ? it - stages : 0; i < it; ++i)
+      // a wait ran out: let the copies in flight land, again with a limit (they
+      // count on the first CTA's barriers, whose CTA stays until the end)
+      if (!ok && (MODE == kGradW || rank == 0))
+        for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
           mbar_wait(smem_addr(s_full + i % stages), (i / stages) & 1);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- products
-    // one lane issues; kGradW keeps the warp together to zero the last lines
-    int it = 0, acc_it = 0, sf_it = 0;
-    bool ok = MODE == kGradW || lane == 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      return MODE == kGradW ? warp_wait_or_stop(smem_addr(bar), parity, &s_stop)
-                            : wait_or_stop(smem_addr(bar), parity, &s_stop);
-    };
-    for (int w = cluster; w < total && ok; w += nclusters) {
-      const Tile t = tile_at(w);
-      if (t.nkb == 0) continue;  // kGradW: an expert without rows; the epilogue writes zeros
-      const int as = acc_it & 1;
-      if (!(ok = wait(s_tempty + as, ((acc_it >> 1) & 1) ^ 1))) break;
-      tc_fence_after();
-      const uint32_t d = tmem + as * kTileRows;
-      uint32_t idesc = idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
-      for (int kb = 0; kb < t.nkb; ++kb, ++it) {
-        const int s = it % stages;
-        if (!(ok = wait(s_full + s, (it / stages) & 1))) break;
-        if constexpr (FP8) {
-          if ((kb & 3) == 0 && !(ok = wait(s_sfull + (sf_it & 1), (sf_it >> 1) & 1))) break;
-        }
+    if (rank == 0 && elect_one()) {
+      int acc_it = 0, sf_it = 0;
+      // the stage's descriptor word and barrier, stepped rather than indexed: one
+      // thread issues alone, so every instruction of this loop counts
+      const uint32_t lo0 = desc_lo(ring_s, 0), bar0 = smem_addr(MODE == kGradW ? s_bars.ready : s_bars.full);
+      constexpr uint32_t kEmptyOffset = MODE == kGradW ? offsetof(Bars, empty) - offsetof(Bars, ready)
+                                                       : offsetof(Bars, empty) - offsetof(Bars, full);
+      uint32_t lo = lo0, bar = bar0, ph = 0;
+      int left = stages;
+      bool ok = true;
+      for (int w = pair; w < total && ok; w += npairs) {
+        const Tile t = tile_at(w);
+        if (t.nkb == 0) continue;  // kGradW: an expert without rows; the epilogue writes zeros
+        const int as = acc_it & 1;
+        if (!(ok = wait_or_stop(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
         tc_fence_after();
-        uint8_t* a = ring + s * stage_bytes;
-        if (MODE == kGradW && kb == t.nkb - 1 && t.tail < 64) {
-          // rows past the segment's end: zero lines in every 64-wide box
-          const int boxes = 2 + (t.n + 63) / 64;
+        const uint32_t d = tmem + as * kTileRows;
+        const uint32_t idesc = FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
+        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+          if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
+          if constexpr (FP8) {
+            if ((kb0 & 3) == 0 &&
+                !(ok = wait_or_stop(smem_addr(s_sfull + sf_it % kScaleBufs), (sf_it / kScaleBufs) & 1, &s_stop)))
+              break;
+          }
+          tc_fence_after();
+          const int nsub = min(kSub, t.nkb - kb0);
+          if constexpr (FP8) {
+            static_assert(kSub <= 4 && 4 % kSub == 0, "a scale word covers four blocks");
+            const uint32_t sfa = tmem + kScaleCols + 12 * (sf_it & 1), sfb = sfa + 4;
+            if ((kb0 & 3) == 0) {
+              const uint32_t sm = desc_lo(smem_addr(s_scale + sf_it % kScaleBufs * kScaleBytes), 0);
+              tmem_copy_scales(sfa, sm);
+              tmem_copy_scales(sfb, sm + (512 >> 4));
+              if (t.n > 128) tmem_copy_scales(sfb + 4, sm + (1024 >> 4));
+            }
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+              if (j >= nsub) break;
+              const uint32_t a = lo + j * (sub_bytes >> 4), b = a + (kABytes >> 4);
+              const uint32_t id = idesc + ((uint32_t)((kb0 + j) & 3) * ((1u << 4) | (1u << 29)));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, id, sfa, sfb, kb0 + j + k);
+            }
+            if (((kb0 + kSub) & 3) == 0 || kb0 + kSub >= t.nkb) {
+              mma_commit_pair(smem_addr(s_sempty + sf_it % kScaleBufs));
+              ++sf_it;
+            }
+          } else {
+            constexpr int ka = MODE == kForward ? 2 : 128, kb_step = MODE == kGradW ? 128 : 2;
+            constexpr uint32_t a_atom = MODE == kForward ? 0 : 8192, b_atom = MODE == kGradW ? 8192 : 0;
+#pragma unroll
+            for (int j = 0; j < kSub; ++j) {
+              if (j >= nsub) break;
+              const uint32_t a = lo + j * (sub_bytes >> 4) + ((a_atom >> 4) << 16);
+              const uint32_t b = lo + j * (sub_bytes >> 4) + (kABytes >> 4) + ((b_atom >> 4) << 16);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb0 + j + k);
+            }
+          }
+          mma_commit_pair(bar + kEmptyOffset);
+          if (kb0 + kSub >= t.nkb) mma_commit_pair(smem_addr(s_tfull + as));
+          lo += stage_bytes >> 4;
+          bar += 8;
+          if (--left == 0) {
+            left = stages;
+            lo = lo0;
+            bar = bar0;
+            ph ^= 1;
+          }
+        }
+        ++acc_it;
+      }
+      if (!ok) {  // products in flight end before tensor memory is freed
+        mma_commit_pair(smem_addr(&s_drain));
+        mbar_wait(smem_addr(&s_drain), 0);
+      }
+    }
+  } else if (MODE == kGradW && warp == 2) {
+    // ------------------------------------------- lines past the segment's end
+    // Every stage passes through here on its way to the products: the last
+    // block of a segment gets zero lines in each of its 64-wide boxes.
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int w = pair; w < total && ok; w += npairs) {
+      const Tile t = tile_at(w);
+      for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+        if (!(ok = warp_wait_or_stop(smem_addr(s_full + s), ph, &s_stop))) break;
+        if (kb0 + kSub >= t.nkb && t.tail < 64) {
+          uint8_t* a = ring + s * stage_bytes + (t.nkb - 1 - kb0) * sub_bytes;
+          const int boxes = 2 + (t.n / 2 + 63) / 64;
           for (int i = lane; i < boxes * (64 - t.tail) * 8; i += 32) {
             const int line = i >> 3, bx = line / (64 - t.tail), r = t.tail + line % (64 - t.tail);
             *reinterpret_cast<uint4*>(a + bx * 8192 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (lane == 0) {
-          const uint32_t as_ = smem_addr(a);
-          if constexpr (FP8) {
-            const int sb = sf_it & 1;
-            const uint32_t sfa = tmem + kScaleCols + 12 * sb, sfb = sfa + 4;
-            if ((kb & 3) == 0) {
-              const uint32_t sm = smem_addr(s_scale + sb * kScaleBytes);
-              tmem_copy_scales(sfa, desc_plain16(sm));
-              for (int i = 0; i * 128 < t.n; ++i) tmem_copy_scales(sfb + 4 * i, desc_plain16(sm + 512 + 512 * i));
-            }
-            idesc = idesc_e4m3(t.n, kb & 3);
-            const uint64_t da = desc_k_major(as_), db = desc_k_major(as_ + kABytes);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              mma_e4m3(d, da + 2 * k, db + 2 * k, idesc, sfa, sfb, kb > 0 || k > 0);
-            if ((kb & 3) == 3 || kb == t.nkb - 1) mma_commit(smem_addr(s_sempty + sb));
-          } else {
-            const uint64_t da = MODE == kForward ? desc_k_major(as_) : desc_mn_major(as_, 8192);
-            const uint64_t db = MODE == kGradW ? desc_mn_major(as_ + kABytes, 8192) : desc_k_major(as_ + kABytes);
-            constexpr int ka = MODE == kForward ? 2 : 128, kb_step = MODE == kGradW ? 128 : 2;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_16bit(d, da + ka * k, db + kb_step * k, idesc, kb > 0 || k > 0);
-          }
-          if (p.cl > 1) mma_commit_multi(smem_addr(s_empty + s), mask);
-          else mma_commit(smem_addr(s_empty + s));
-          if (kb == t.nkb - 1) mma_commit(smem_addr(s_tfull + as));
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_ready + s), 0));
+        if (++s == stages) {
+          s = 0;
+          ph ^= 1;
         }
-        if constexpr (MODE == kGradW) __syncwarp();
-        if (FP8 && ((kb & 3) == 3 || kb == t.nkb - 1)) ++sf_it;
       }
-      ++acc_it;
-    }
-    if (!ok && lane == 0) {  // products in flight end before tensor memory is freed
-      mma_commit(smem_addr(&s_drain));
-      mbar_wait(smem_addr(&s_drain), 0);
     }
   } else if (FP8 && warp == 2) {
     // ----------------------------------------------------------------- scales
     // Word w of a row holds the exponents of its reduction elements 512 w ..
     // 512 w + 511, one byte per 128. Tensor memory wants row r of a block of
-    // 128 at lane r % 32, column r / 32: lane l stores rows l, l + 32, l + 64
-    // and l + 96 as one 16-byte line.
-    const int Nw = p.wrows;
+    // 128 at lane r % 32, column r / 32: row r goes to byte 16 (r % 32) +
+    // 4 (r / 32) of its block's 512 bytes, by 4-byte asynchronous copies that
+    // run up to kScaleBufs words ahead of the products. (Loads through
+    // registers wait for the newest load in flight, not for the oldest: 1170
+    // cycles a word of a decode batch.) Both CTAs need the words of all rows
+    // and of their own weight rows.
     int sf_it = 0;
     bool ok = true;
-    for (int w = cluster; w < total && ok; w += nclusters) {
+    const int fstep = p.gated ? 16 : 32;
+    for (int w = pair; w < total && ok; w += npairs) {
       const Tile t = tile_at(w);
-      int64_t arow[4], brow[8];  // word offsets of this lane's rows (-1: none)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int f = t.fb * 128 + i * 32 + lane, wr = f;
-        if (p.gated) {
-          f = t.fb * 64 + i * 16 + (lane & 15);
-          wr = (lane & 16) ? p.feats + f : f;
-        }
-        arow[i] = f < p.feats ? (int64_t)t.e * Nw + wr : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 32 + lane;
-        const int64_t row = p.cap > 0 ? (int64_t)t.e * p.G4 * p.ld_xs + (t.row0 + r - t.e * p.cap) : t.row0 + r;
-        brow[i] = r < t.rows ? row : -1;
-      }
+      const int f = p.gated ? t.fb * 64 + (lane & 15) : t.fb * 128 + lane;  // this lane's first feature
+      const uint32_t* la = p.ws + (int64_t)t.e * p.wrows + (p.gated && (lane & 16) ? p.feats : 0) + f;
+      const uint32_t* lb =
+          p.xs + (p.cap > 0 ? (int64_t)t.e * p.G4 * p.ld_xs - (int64_t)t.e * p.cap : 0) + t.row0 + lane;
       for (int kb = 0; kb < t.nkb; kb += 4, ++sf_it) {
-        const int sb = sf_it & 1, word = kb >> 2;
-        uint32_t va[4], vb[8];
+        const int sb = sf_it % kScaleBufs;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kScaleBufs) & 1) ^ 1, &s_stop))) break;
+        const uint32_t dst = smem_addr(s_scale + sb * kScaleBytes + lane * 16);
+        const int64_t wa = (int64_t)(kb >> 2) * p.ld_ws, wb = (int64_t)(kb >> 2) * p.ld_xs;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          va[i] = arow[i] >= 0 ? __ldg(p.ws + (int64_t)word * p.ld_ws + arow[i]) : 0x7F7F7F7Fu;
+          if (f + i * fstep < p.feats) cp_async4(dst + 4 * i, la + wa + i * fstep);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          vb[i] = brow[i] >= 0 ? __ldg(p.xs + (int64_t)word * p.ld_xs + brow[i]) : 0x7F7F7F7Fu;
-        if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + sb), ((sf_it >> 1) & 1) ^ 1, &s_stop))) break;
-        uint8_t* dst = s_scale + sb * kScaleBytes + lane * 16;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(va[0], va[1], va[2], va[3]);
-        *reinterpret_cast<uint4*>(dst + 512) = make_uint4(vb[0], vb[1], vb[2], vb[3]);
-        *reinterpret_cast<uint4*>(dst + 1024) = make_uint4(vb[4], vb[5], vb[6], vb[7]);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(s_sfull + sb));
+          if (i * 32 + lane < t.rows) cp_async4(dst + 512 + (i >> 2) * 512 + 4 * (i & 3), lb + wb + i * 32);
+        cp_async_arrive(smem_addr(s_sraw + sb));  // when this lane's copies have landed
+      }
+    }
+    cp_async_wait_all();
+  } else if (FP8 && warp == 3) {
+    // Makes the words that have landed visible to the asynchronous proxy and hands
+    // them to the products. A warp of its own, because the fence waits for the loads
+    // its thread has in flight (in warp 2 it exposed their latency).
+    if (lane == 0) {
+      bool ok = true;
+      int sf_it = 0;
+      for (int w = pair; w < total && ok; w += npairs) {
+        const int words = (tile_at(w).nkb + 3) / 4;
+        for (int i = 0; i < words; ++i, ++sf_it) {
+          const int sb = sf_it % kScaleBufs;
+          if (!(ok = wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
+          fence_proxy_async_smem();
+          mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), 0));
+        }
       }
     }
   } else if (warp >= 4) {
     // --------------------------------------------------------------- epilogue
     const int q = warp & 3;  // this warp's 32 lanes of tensor memory
     const bool f16 = p.f16 != 0;
+    const Rows16 out = rows16(p.out, p.ldo), pre = rows16(p.pre, p.ld_pre), res = rows16(p.residual, p.ld_res);
     int acc_it = 0;
-    for (int w = cluster; w < total; w += nclusters) {
+    for (int w = pair; w < total; w += npairs) {
       const Tile t = tile_at(w);
       const int as = acc_it & 1;
       if (t.nkb > 0) {
@@ -458,101 +644,97 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t acc = tmem + as * kTileRows + ((uint32_t)(q * 32) << 16);
-      const bool gated = MODE == kForward && p.gated;
-      // this lane's feature (gated: lanes 0-15 gate, 16-31 up of the same 16)
-      const int f = gated ? t.fb * 64 + q * 16 + (lane & 15) : t.fb * 128 + q * 32 + lane;
-      const bool fok = f < p.feats;
-      const int wrow = gated && (lane & 16) ? p.feats + f : f;
-      float bias = 0.0f;
-      if (MODE == kForward && p.bias != nullptr && fok) bias = __ldg(p.bias + (int64_t)t.e * p.wrows + wrow);
       const int64_t orow = MODE == kGradW ? (int64_t)t.e * p.wrows + t.row0 : t.row0;
-      for (int c0 = 0; c0 < t.rows; c0 += 32) {
-        uint32_t raw[32];
-        __syncwarp();
-        if (t.nkb > 0) {
-          tmem_ld_x32(acc + c0, raw);
-          tmem_wait_ld();
-        } else {
+      if (MODE == kGradW && p.out_f32) {
+        // 32-bit outputs: a lane is a feature, a warp stores 128 bytes of a row
+        const int f = t.fb * 128 + q * 32 + lane;
+        for (int c0 = 0; c0 < t.rows; c0 += 32) {
+          uint32_t raw[32];
+          __syncwarp();
+          if (t.nkb > 0) {
+            tmem_ld_x32(acc + c0, raw);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) raw[j] = 0;
+            for (int j = 0; j < 32; ++j) raw[j] = 0;
+          }
+          float* dst = static_cast<float*>(p.out) + (orow + c0) * p.ldo + f;
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (f < p.feats && c0 + j < t.rows) dst[j * p.ldo] = __uint_as_float(raw[j]);
         }
-        const int nc = min(32, t.rows - c0);
-        if constexpr (MODE == kForward) {
-          float v[32];
+      } else {
+        // Fragments a and b: lanes 0-15 and 16-31 of this warp's quarter. Gated:
+        // gate and up of the same 16 features; else features 0-15 and 16-31.
+        const bool gated = MODE == kForward && p.gated;
+        const int f0 = gated ? t.fb * 64 + q * 16 : t.fb * 128 + q * 32;
+        uint8_t* st = s_stage + q * 32 * kPitch;
+        float ba[2] = {0.0f, 0.0f}, bb[2] = {0.0f, 0.0f};  // bias of features l / 4 + 8 g
+        if (MODE == kForward && p.bias != nullptr) {
+          const float* bias = p.bias + (int64_t)t.e * p.wrows;
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) + bias;
-          if (p.pre != nullptr && fok) {
-            uint16_t* dst = static_cast<uint16_t*>(p.pre) + (orow + c0) * p.ld_pre + wrow;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < nc) dst[j * p.ld_pre] = to_16bit(v[j], f16);
+          for (int g = 0; g < 2; ++g) {
+            const int f = f0 + (lane >> 2) + 8 * g, f2 = gated ? p.feats + f : f + 16;
+            if (f < p.feats) ba[g] = __ldg(bias + f);
+            if (gated ? f < p.feats : f2 < p.feats) bb[g] = __ldg(bias + f2);
           }
-          if (gated) {
-            // lanes 0-15 finish the even rows, 16-31 the odd ones: one exchange per pair
-            float g[16], u[16];
-            const bool upper = (lane & 16) != 0;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float give = upper ? v[2 * j] : v[2 * j + 1];
-              const float got = __shfl_xor_sync(0xffffffffu, give, 16);
-              g[j] = upper ? got : v[2 * j];
-              u[j] = upper ? v[2 * j + 1] : got;
-            }
-            activate(g, p.act);
-            const int odd = upper ? 1 : 0;
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + (orow + c0 + odd) * p.ldo + f;
-            const uint16_t* res = static_cast<const uint16_t*>(p.residual) + (orow + c0 + odd) * p.ld_res + f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (!fok || 2 * j + odd >= nc) continue;
-              float o = g[j] * u[j];
-              if (p.residual != nullptr) o += from_16bit(__ldg(res + 2 * j * p.ld_res), f16);
-              dst[2 * j * p.ldo] = to_16bit(o, f16);
-            }
+        }
+        for (int c0 = 0; c0 < t.rows; c0 += 32) {
+          uint32_t ra[16], rb[16];
+          __syncwarp();
+          if (t.nkb > 0) {
+            tmem_ld_16x32(acc + c0, ra);
+            tmem_ld_16x32(acc + c0 + (16u << 16), rb);
+            tmem_wait_ld();
           } else {
-            activate(v, p.act);
-            if (!fok) continue;
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + (orow + c0) * p.ldo + f;
-            const uint16_t* res = static_cast<const uint16_t*>(p.residual) + (orow + c0) * p.ld_res + f;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (j >= nc) continue;
-              if (p.residual != nullptr) v[j] += from_16bit(__ldg(res + j * p.ld_res), f16);
-              dst[j * p.ldo] = to_16bit(v[j], f16);
+            for (int j = 0; j < 16; ++j) ra[j] = rb[j] = 0;
+          }
+          float a[16], b[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            a[j] = __uint_as_float(ra[j]) + ba[(j >> 1) & 1];
+            b[j] = __uint_as_float(rb[j]) + bb[(j >> 1) & 1];
+          }
+          const int nr = min(32, t.rows - c0);
+          const int64_t row = orow + c0;
+          if constexpr (MODE == kForward) {
+            if (p.pre != nullptr) {
+              if (gated) store_32x32(st, a, b, f16, pre, row, nr, f0, p.feats + f0, p.feats, p.wrows);
+              else store_32x32(st, a, b, f16, pre, row, nr, f0, f0 + 16, p.feats, p.feats);
             }
-          }
-        } else {
-          if (!fok) continue;
-          if (p.out_f32) {
-            float* dst = static_cast<float*>(p.out) + (orow + c0) * p.ldo + f;
+            activate(a, p.act);
+            if (gated) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < nc) dst[j * p.ldo] = __uint_as_float(raw[j]);
-          } else {
-            uint16_t* dst = static_cast<uint16_t*>(p.out) + (orow + c0) * p.ldo + f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (j < nc) dst[j * p.ldo] = to_16bit(__uint_as_float(raw[j]), f16);
+              for (int j = 0; j < 16; ++j) a[j] *= b[j];
+              if (p.residual != nullptr) add_rows<false>(st, a, b, f16, res, row, nr, f0, p.feats);
+              store_16x32(st, a, f16, out, row, nr, f0, p.feats);
+              continue;
+            }
+            activate(b, p.act);
+            if (p.residual != nullptr) add_rows<true>(st, a, b, f16, res, row, nr, f0, p.feats);
           }
+          store_32x32(st, a, b, f16, out, row, nr, f0, f0 + 16, p.feats, p.feats);
         }
       }
       if (t.nkb > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(s_tempty + as));
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_tempty + as), 0));
         ++acc_it;
       }
     }
   }
 
-  // ---- the end: nothing of this CTA's peer may still arrive here
+  // ---- the end: the other CTA may still arrive on barriers or read this CTA's memory
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (tid == 0 && s_stop) set_status(p.status, kStTimeout);
-  if (p.cl > 1) cluster_sync();
+  cluster_sync();
   if (warp == 3) tmem_free(tmem, kTmemCols);
+  cluster_sync();  // the pair frees its tensor memory together
 }
 
 // ---------------------------------------------------------------------------
@@ -603,7 +785,7 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerBlockOptin, &optin);
   if (err != cudaSuccess) return err;
   const size_t smem = (size_t)optin - 1024;  // room for the static arrays
-  const size_t lists = (size_t)(3 * a.L + 1) * sizeof(int32_t) + (FP8 ? 2 * kScaleBytes : 0);
+  const size_t lists = (size_t)(3 * a.L + 1) * sizeof(int32_t) + kStageBytes + (FP8 ? kScaleBufs * kScaleBytes : 0);
   a.ring_bytes = (int32_t)((smem - 1024 - lists) / 1024 * 1024);
   err = opt_in_smem(matmul_kernel<MODE, FP8>, smem);
   if (err != cudaSuccess) return err;
@@ -613,19 +795,19 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)a.cl;
+  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // as many clusters as can be resident at once: one more would start late
-  cfg.gridDim = dim3((unsigned)(num_sms / a.cl * a.cl));
-  int clusters = 0;
-  err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, FP8>), cfg, a.cl, &clusters);
+  // as many pairs as can be resident at once: one more would start late
+  cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
+  int pairs = 0;
+  err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, FP8>), cfg, 2, &pairs);
   if (err != cudaSuccess) return err;
-  if (clusters < 1) return cudaErrorInvalidConfiguration;
-  if (clusters > num_sms / a.cl) clusters = num_sms / a.cl;
-  if (clusters > max_tiles) clusters = (int)max_tiles;
-  cfg.gridDim = dim3((unsigned)(clusters * a.cl));
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  if (pairs > num_sms / 2) pairs = num_sms / 2;
+  if (pairs > max_tiles) pairs = (int)max_tiles;
+  cfg.gridDim = dim3((unsigned)(pairs * 2));
   return cudaLaunchKernelEx(&cfg, matmul_kernel<MODE, FP8>, maps, a);
 }
 
@@ -656,8 +838,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, int num_sms, cudaStream_t s) {
   a.out = m.out; a.ldo = m.ldo; a.pre = m.pre; a.ld_pre = m.ld_pre;
   a.xs = m.xs; a.ld_xs = m.ld_xs; a.ws = m.ws; a.ld_ws = m.ld_ws; a.G4 = (m.K / 128 + 3) / 4;
   const int fblk = m.gated ? 64 : 128;
-  const int nfb = (m.N + fblk - 1) / fblk;
-  a.cl = nfb > 1 ? 2 : 1;
+  const int nfp = (m.N + 2 * fblk - 1) / (2 * fblk);
   Maps maps;
   const cuuint64_t row = (cuuint64_t)m.K * es;
   bool ok;
@@ -674,7 +855,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, int num_sms, cudaStream_t s) {
   }
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.x, m.K, m.R, m.ldx, span, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = max_row_tiles(m, fp8 ? kRows<true> : kRows<false>) * ((nfb + a.cl - 1) / a.cl);
+  const int64_t tiles = max_row_tiles(m, fp8 ? kRows<true> : kRows<false>) * nfp;
   return fp8 ? launch<kForward, true>(maps, a, tiles, num_sms, s) : launch<kForward, false>(maps, a, tiles, num_sms, s);
 }
 
@@ -684,8 +865,7 @@ cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t 
   Args a = common_args(m);
   a.wrows = m.gated ? 2 * m.N : m.N;
   a.red = a.wrows; a.feats = m.K; a.out = m.out; a.ldo = m.ldo;
-  const int nfb = (m.K + 127) / 128;
-  a.cl = nfb > 1 ? 2 : 1;
+  const int nfp = (m.K + 255) / 256;
   Maps maps;
   const cuuint64_t row = (cuuint64_t)m.K * 2;
   const cuuint64_t dims[3] = {(cuuint64_t)m.K, (cuuint64_t)a.wrows, (cuuint64_t)m.L};
@@ -694,7 +874,7 @@ cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t 
   bool ok = make_map(&maps.a, m.type, m.w, 3, dims, strides, box);
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.R, m.ldg, 64, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  return launch<kGradX, false>(maps, a, max_row_tiles(m, kRows<false>) * ((nfb + a.cl - 1) / a.cl), num_sms, s);
+  return launch<kGradX, false>(maps, a, max_row_tiles(m, kRows<false>) * nfp, num_sms, s);
 }
 
 cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t s) {
@@ -703,13 +883,12 @@ cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t 
   Args a = common_args(m);
   a.wrows = m.gated ? 2 * m.N : m.N;
   a.feats = m.K; a.out = m.out; a.ldo = m.ldo; a.out_f32 = m.out_type == kF32;
-  const int nfb = (m.K + 127) / 128;
-  a.cl = nfb > 1 ? 2 : 1;
+  const int nfp = (m.K + 255) / 256;
   Maps maps;
   bool ok = map_2d(&maps.a, m.type, m.x, m.K, m.R, m.ldx, 64, 64);
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.R, m.ldg, 64, 64);
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = (int64_t)m.L * ((a.wrows + 255) / 256) * ((nfb + a.cl - 1) / a.cl);
+  const int64_t tiles = (int64_t)m.L * ((a.wrows + 255) / 256) * nfp;
   return launch<kGradW, false>(maps, a, tiles, num_sms, s);
 }
 
