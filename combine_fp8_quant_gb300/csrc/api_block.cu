@@ -155,7 +155,7 @@ moe_status_t moe_block_norm(const void* x, int64_t ldx, const void* y, int64_t l
 size_t moe_block_norm_workspace_bytes(int32_t T, int32_t H) {
   if (T < 0 || H < 1) return 0;
   const int64_t parts = T < 1 ? 1 : T < kNormParts ? T : kNormParts;
-  return (size_t)3 * parts * H * sizeof(float);
+  return (size_t)2 * parts * H * sizeof(float);
 }
 
 moe_status_t moe_block_norm_grad(const void* dx_out, int64_t ld_dxo, const void* dh, int64_t ld_dh,

@@ -24,11 +24,12 @@ namespace {
 
 constexpr int kBatch = 4;    // rows in flight per thread and chunk
 constexpr int kMaxSlots = 32;
+constexpr int kMaxThreads = 256;
 
 template <int TYPE>
-__global__ void __launch_bounds__(512) combine_grad_kernel(CombineGradArgs p) {
+__global__ void __launch_bounds__(kMaxThreads, 4) combine_grad_kernel(CombineGradArgs p) {
   constexpr int N = Vec<TYPE>::kN;
-  __shared__ float s_part[2][kMaxSlots][17];  // [slot][warp], padded
+  __shared__ float s_part[2][kMaxSlots][kMaxThreads / 32 + 1];  // [slot][warp], padded
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, bd = blockDim.x, nw = bd >> 5;
   const int nch = p.H / N;
   const int n_live = live_count(p.d_num_tokens, p.T, p.status, blockIdx.x == 0 && tid == 0);
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(512) combine_grad_kernel(CombineGradArgs p) {
 template <int TYPE>
 cudaError_t launch_type(const CombineGradArgs& a, int num_sms, cudaStream_t s) {
   const int nch = a.H / Vec<TYPE>::kN;
-  const int per_thread = (nch + 511) / 512;  // chunks per thread, of equal count
+  const int per_thread = (nch + kMaxThreads - 1) / kMaxThreads;  // chunks per thread, of equal count
   int bd = ((nch + per_thread - 1) / per_thread + 31) / 32 * 32;
   int per_sm = 0;
   cudaError_t err = occupancy(combine_grad_kernel<TYPE>, bd, 0, &per_sm);

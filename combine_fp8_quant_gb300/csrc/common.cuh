@@ -279,6 +279,11 @@ __device__ __forceinline__ void cp_async16(void* sdst, const void* gsrc) {
                ::"r"((uint32_t)__cvta_generic_to_shared(sdst)), "l"(gsrc)
                : "memory");
 }
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // at most N of this thread's groups still in flight
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 // Asynchronous 4-byte copy, and an arrival on an mbarrier (counted in its
 // initial count) once this thread's copies issued so far have landed.
 __device__ __forceinline__ void cp_async4(uint32_t sdst, const void* gsrc) {

@@ -6,6 +6,30 @@
 
 namespace moeperm {
 
+// Pairs of floats for the packed 32-bit instructions of sm_100 and later (one
+// issue slot for two multiply-adds; each half rounds as the scalar one does).
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 halves(f32x2 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int TYPE>
 struct Vec {
   static constexpr int kBytes = TYPE == kF32 ? 4 : 2;
@@ -28,6 +52,23 @@ struct Vec {
         }
       }
     }
+  }
+  static constexpr int kP = kN / 2;  // pairs per vector
+  __device__ __forceinline__ static void unpack2(const uint4& v, f32x2 (&p)[kP]) {
+    float f[kN];
+    unpack(v, f);
+#pragma unroll
+    for (int i = 0; i < kP; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+  }
+  __device__ __forceinline__ static uint4 pack2(const f32x2 (&p)[kP]) {
+    float f[kN];
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      const float2 h = halves(p[i]);
+      f[2 * i] = h.x;
+      f[2 * i + 1] = h.y;
+    }
+    return pack(f);
   }
   __device__ __forceinline__ static uint4 pack(const float (&f)[kN]) {
     if constexpr (TYPE == kF32) {

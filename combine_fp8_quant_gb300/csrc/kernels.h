@@ -236,7 +236,7 @@ struct NormArgs {
   float* dw_post;
   float* dgate;
   float* dw_pre;
-  float* ws;                   // [3][parts][H] partial sums
+  float* ws;                   // [2][parts][H] partial sums
   int32_t parts;
 };
 // Rows of partial sums the backward pass may use (the grid's upper limit).

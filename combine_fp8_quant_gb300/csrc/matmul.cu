@@ -32,6 +32,12 @@
 // The grid is persistent; the tile list is formed on the device from the
 // segment ends, so a captured graph can be replayed with other counts.
 //
+// Few tiles (one dense matrix with few rows): the reduction is cut into up to
+// four runs, one pair of a larger cluster each. When its own products are done
+// the first pair lets the others write their accumulators into its ring (st.async
+// over distributed shared memory) and adds them in a fixed order; every cluster
+// then has one tile at most, so nothing has to be handed back.
+//
 // Rows outside every segment are read at most as columns that are not stored.
 // In kGradW rows are the reduction: lines of the last block past the segment's
 // end are zeroed in shared memory before the product, so padding rows may hold
@@ -51,15 +57,12 @@ namespace {
 
 constexpr int kForward = 0, kGradX = 1, kGradW = 2;
 constexpr int kThreads = 256;
+constexpr int kMaxSplits = 4;
 constexpr int kMaxStages = 10;
 constexpr int kABytes = 16384;            // 128 rows x 128 bytes
-// Reduction blocks of 128 bytes per stage. Two halve the waits per block, which
-// the twice as fast e4m3 products need (prefill, 64 experts: 732 against 820 us);
-// 16-bit products have the time and want the finer ring (134 against 142 us).
-template <bool FP8>
-constexpr int kSubBlocks = FP8 ? 2 : 1;
+
 constexpr int kTmemCols = 512;
-constexpr int kScaleCols = 448;           // e4m3: scale words, 12 columns per buffer
+constexpr int kScaleCols = 480;           // e4m3: scale words, 12 columns per buffer
 constexpr int kScaleBytes = 512 + 1024;   // of one buffer: 128 + 256 words
 constexpr int kScaleBufs = 8;             // in shared memory (two in tensor memory)
 constexpr int kBoxes = 7;                 // heights of the row boxes a CTA may load
@@ -70,7 +73,7 @@ __host__ __device__ constexpr int box_rows(int i) {
 // Rows of one tile (the N side): two accumulators fill tensor memory; e4m3
 // leaves room for the scale words.
 template <bool FP8>
-constexpr int kRows = FP8 ? 224 : 256;
+constexpr int kRows = FP8 ? 240 : 256;
 
 struct Maps {
   CUtensorMap a;
@@ -86,6 +89,7 @@ struct Args {
   int32_t feats;             // features of an output row
   int32_t wrows;             // weight rows per expert (kGradW: output rows)
   int32_t gated, act, f16, out_f32;
+  int32_t splits;            // pairs per cluster, each with a run of the reduction
   int32_t ring_bytes;
   const float* bias;         // [L, wrows]
   const void* residual;
@@ -110,7 +114,7 @@ struct Tile {
   int e, fb;        // expert, feature block of this CTA
   int row0, rows;   // first output row (kGradW: within the expert), rows of the tile
   int n;            // N of the products (rows rounded up to 16)
-  int nkb;          // reduction blocks
+  int kb0, nkb;     // this CTA's reduction blocks: first, count
   int red_row0;     // kGradW: first row of the segment
   int tail;         // kGradW: valid lines of the last block
 };
@@ -285,14 +289,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Bars s_bars;
   uint64_t *s_full = s_bars.full, *s_empty = s_bars.empty, *s_ready = s_bars.ready;
   __shared__ uint64_t s_tfull[2], s_tempty[2], s_sraw[kScaleBufs], s_sfull[kScaleBufs], s_sempty[kScaleBufs], s_drain;
+  __shared__ uint64_t s_go, s_recv;  // splits: the ring may be written; the accumulators have arrived
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_stop;
   __shared__ int s_max;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_rank();  // 0 issues the pair's products
-  const int pair = blockIdx.x / 2, npairs = gridDim.x / 2;
-  constexpr int kTileRows = kRows<FP8>, kSub = kSubBlocks<FP8>;
+  const int crank = (int)cluster_rank(), rank = crank & 1;  // rank 0 issues the pair's products
+  const int split = crank >> 1, leader = crank & ~1;        // cluster rank of the pair's first CTA
+  const uint16_t both = (uint16_t)(3 << leader);
+  const int pair = blockIdx.x / (2 * p.splits), npairs = gridDim.x / (2 * p.splits);  // (clusters)
+  constexpr int kTileRows = kRows<FP8>;
   constexpr int kRedBlock = FP8 ? 128 : 64;  // reduction elements per stage
 
   uint8_t* ring = dyn + ((1024 - (smem_addr(dyn) & 1023)) & 1023);
@@ -319,6 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(s_sempty + i), 1);
     }
     mbar_init(smem_addr(&s_drain), 1);
+    mbar_init(smem_addr(&s_go), 1);
+    mbar_init(smem_addr(&s_recv), 1);
     mbar_init_fence();
     s_stop = 0;
     s_max = 0;
@@ -383,6 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.row0 = (rb - t.e * nnb) * 256;
       t.rows = min(256, p.wrows - t.row0);
       t.red_row0 = s_begin[t.e];
+      t.kb0 = 0;
       t.nkb = (s_count[t.e] + 63) / 64;
       t.tail = s_count[t.e] - (t.nkb - 1) * 64;
     } else {
@@ -397,7 +407,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = rb - s_tiles[lo];
       t.row0 = s_begin[lo] + j * per;
       t.rows = min(per, cnt - j * per);
-      t.nkb = (p.red + kRedBlock - 1) / kRedBlock;
+      // runs of whole scale words (four blocks); the host gives every run some
+      const int all = (p.red + kRedBlock - 1) / kRedBlock;
+      t.kb0 = all * split / p.splits & ~3;
+      t.nkb = (split + 1 == p.splits ? all : all * (split + 1) / p.splits & ~3) - t.kb0;
       t.red_row0 = t.tail = 0;
     }
     t.n = (t.rows + 15) / 16 * 16;
@@ -408,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
   const int b_bytes = MODE == kGradW ? min((p.wrows + 127) / 128, 2) * 8192
                                      : box_rows(box_index(max_n / 2)) * 128;
-  const int sub_bytes = kABytes + b_bytes, stage_bytes = kSub * sub_bytes;
+  const int stage_bytes = kABytes + b_bytes;
   const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
   const uint32_t ring_s = smem_addr(ring);
 
@@ -428,35 +441,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t bytes = kABytes + (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
         const CUtensorMap* mb = &maps.b[box];
         const int brow = t.row0 + rank * half;
-        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+        for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait_or_stop(smem_addr(s_empty + s), ph, &s_stop))) break;
-          const int nsub = min(kSub, t.nkb - kb0);
           uint32_t full = smem_addr(s_full + s);
+          const uint32_t a = ring_s + s * stage_bytes, b = a + kABytes;
+          const int red = (t.kb0 + kb) * kRedBlock;
           if constexpr (MODE == kGradW) {
-            mbar_expect_tx(full, nsub * bytes);
+            mbar_expect_tx(full, bytes);
           } else {
-            if (rank == 0) mbar_expect_tx(full, nsub * 2 * bytes);
-            else full = map_to_rank(full, 0);
+            if (rank == 0) mbar_expect_tx(full, 2 * bytes);
+            else full = map_to_rank(full, leader);
           }
-#pragma unroll
-          for (int j = 0; j < kSub; ++j) {
-            if (j >= nsub) break;
-            const int kb = kb0 + j;
-            const uint32_t a = ring_s + s * stage_bytes + j * sub_bytes, b = a + kABytes;
-            if constexpr (MODE == kForward) {
-              if (p.gated) tma_load_5d(a, &maps.a, full, kb * kRedBlock, 0, 0, t.fb * 4, t.e);
-              else tma_load_3d(a, &maps.a, full, kb * kRedBlock, t.fb * 128, t.e);
-              tma_load_2d(b, mb, full, kb * kRedBlock, brow);
-            } else if constexpr (MODE == kGradX) {
-              tma_load_3d(a, &maps.a, full, t.fb * 128, kb * 64, t.e);
-              tma_load_3d(a + 8192, &maps.a, full, t.fb * 128 + 64, kb * 64, t.e);
-              tma_load_2d(b, mb, full, kb * kRedBlock, brow);
-            } else {
-              const int y = t.red_row0 + kb * 64;
-              tma_load_2d(a, &maps.a, full, t.fb * 128, y);
-              tma_load_2d(a + 8192, &maps.a, full, t.fb * 128 + 64, y);
-              for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * 8192, mb, full, brow + i * 64, y);
-            }
+          if constexpr (MODE == kForward) {
+            if (p.gated) tma_load_5d(a, &maps.a, full, red, 0, 0, t.fb * 4, t.e);
+            else tma_load_3d(a, &maps.a, full, red, t.fb * 128, t.e);
+            tma_load_2d(b, mb, full, red, brow);
+          } else if constexpr (MODE == kGradX) {
+            tma_load_3d(a, &maps.a, full, t.fb * 128, red, t.e);
+            tma_load_3d(a + 8192, &maps.a, full, t.fb * 128 + 64, red, t.e);
+            tma_load_2d(b, mb, full, red, brow);
+          } else {
+            const int y = t.red_row0 + red;
+            tma_load_2d(a, &maps.a, full, t.fb * 128, y);
+            tma_load_2d(a + 8192, &maps.a, full, t.fb * 128 + 64, y);
+            for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * 8192, mb, full, brow + i * 64, y);
           }
           ++issued;
           if (++s == stages) {
@@ -491,50 +499,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + as * kTileRows;
         const uint32_t idesc = FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
-        for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+        for (int kb = 0; kb < t.nkb; ++kb) {
           if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
           if constexpr (FP8) {
-            if ((kb0 & 3) == 0 &&
+            if ((kb & 3) == 0 &&
                 !(ok = wait_or_stop(smem_addr(s_sfull + sf_it % kScaleBufs), (sf_it / kScaleBufs) & 1, &s_stop)))
               break;
           }
           tc_fence_after();
-          const int nsub = min(kSub, t.nkb - kb0);
           if constexpr (FP8) {
-            static_assert(kSub <= 4 && 4 % kSub == 0, "a scale word covers four blocks");
             const uint32_t sfa = tmem + kScaleCols + 12 * (sf_it & 1), sfb = sfa + 4;
-            if ((kb0 & 3) == 0) {
+            if ((kb & 3) == 0) {
               const uint32_t sm = desc_lo(smem_addr(s_scale + sf_it % kScaleBufs * kScaleBytes), 0);
               tmem_copy_scales(sfa, sm);
               tmem_copy_scales(sfb, sm + (512 >> 4));
               if (t.n > 128) tmem_copy_scales(sfb + 4, sm + (1024 >> 4));
             }
+            const uint32_t a = lo, b = lo + (kABytes >> 4);
+            const uint32_t id = idesc + ((uint32_t)(kb & 3) * ((1u << 4) | (1u << 29)));
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) {
-              if (j >= nsub) break;
-              const uint32_t a = lo + j * (sub_bytes >> 4), b = a + (kABytes >> 4);
-              const uint32_t id = idesc + ((uint32_t)((kb0 + j) & 3) * ((1u << 4) | (1u << 29)));
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, id, sfa, sfb, kb0 + j + k);
-            }
-            if (((kb0 + kSub) & 3) == 0 || kb0 + kSub >= t.nkb) {
-              mma_commit_pair(smem_addr(s_sempty + sf_it % kScaleBufs));
+            for (int k = 0; k < 4; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, id, sfa, sfb, kb + k);
+            if ((kb & 3) == 3 || kb == t.nkb - 1) {
+              mma_commit_pair(smem_addr(s_sempty + sf_it % kScaleBufs), both);
               ++sf_it;
             }
           } else {
             constexpr int ka = MODE == kForward ? 2 : 128, kb_step = MODE == kGradW ? 128 : 2;
             constexpr uint32_t a_atom = MODE == kForward ? 0 : 8192, b_atom = MODE == kGradW ? 8192 : 0;
+            const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
 #pragma unroll
-            for (int j = 0; j < kSub; ++j) {
-              if (j >= nsub) break;
-              const uint32_t a = lo + j * (sub_bytes >> 4) + ((a_atom >> 4) << 16);
-              const uint32_t b = lo + j * (sub_bytes >> 4) + (kABytes >> 4) + ((b_atom >> 4) << 16);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb0 + j + k);
-            }
+            for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb + k);
           }
-          mma_commit_pair(bar + kEmptyOffset);
-          if (kb0 + kSub >= t.nkb) mma_commit_pair(smem_addr(s_tfull + as));
+          mma_commit_pair(bar + kEmptyOffset, both);
+          if (kb == t.nkb - 1) mma_commit_pair(smem_addr(s_tfull + as), both);
           lo += stage_bytes >> 4;
           bar += 8;
           if (--left == 0) {
@@ -547,7 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++acc_it;
       }
       if (!ok) {  // products in flight end before tensor memory is freed
-        mma_commit_pair(smem_addr(&s_drain));
+        mma_commit_pair(smem_addr(&s_drain), both);
         mbar_wait(smem_addr(&s_drain), 0);
       }
     }
@@ -560,10 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int w = pair; w < total && ok; w += npairs) {
       const Tile t = tile_at(w);
-      for (int kb0 = 0; kb0 < t.nkb; kb0 += kSub) {
+      for (int kb = 0; kb < t.nkb; ++kb) {
         if (!(ok = warp_wait_or_stop(smem_addr(s_full + s), ph, &s_stop))) break;
-        if (kb0 + kSub >= t.nkb && t.tail < 64) {
-          uint8_t* a = ring + s * stage_bytes + (t.nkb - 1 - kb0) * sub_bytes;
+        if (kb == t.nkb - 1 && t.tail < 64) {
+          uint8_t* a = ring + s * stage_bytes;
           const int boxes = 2 + (t.n / 2 + 63) / 64;
           for (int i = lane; i < boxes * (64 - t.tail) * 8; i += 32) {
             const int line = i >> 3, bx = line / (64 - t.tail), r = t.tail + line % (64 - t.tail);
@@ -572,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_ready + s), 0));
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_ready + s), leader));
         if (++s == stages) {
           s = 0;
           ph ^= 1;
@@ -602,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int sb = sf_it % kScaleBufs;
         if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kScaleBufs) & 1) ^ 1, &s_stop))) break;
         const uint32_t dst = smem_addr(s_scale + sb * kScaleBytes + lane * 16);
-        const int64_t wa = (int64_t)(kb >> 2) * p.ld_ws, wb = (int64_t)(kb >> 2) * p.ld_xs;
+        const int64_t word = (t.kb0 + kb) >> 2, wa = word * p.ld_ws, wb = word * p.ld_xs;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (f + i * fstep < p.feats) cp_async4(dst + 4 * i, la + wa + i * fstep);
@@ -626,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int sb = sf_it % kScaleBufs;
           if (!(ok = wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
           fence_proxy_async_smem();
-          mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), 0));
+          mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), leader));
         }
       }
     }
@@ -644,6 +641,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const uint32_t acc = tmem + as * kTileRows + ((uint32_t)(q * 32) << 16);
+      if (MODE != kGradW && p.splits > 1) {
+        // accumulators of the other runs, [run - 1][32 columns][warp][8][lane] in
+        // 16-byte pieces of the fragments, in the first pair's ring
+        const uint32_t run_bytes = (uint32_t)((t.rows + 31) / 32) * 16384;
+        if (split == 0) {
+          if (q == 0 && lane == 0) {
+            mbar_expect_tx(smem_addr(&s_recv), (p.splits - 1) * run_bytes);
+            for (int i = 1; i < p.splits; ++i) mbar_arrive_mapped(map_to_rank(smem_addr(&s_go), 2 * i + rank));
+          }
+          if (!warp_wait_or_stop(smem_addr(&s_recv), 0, &s_stop)) break;
+        } else {
+          if (!warp_wait_or_stop(smem_addr(&s_go), 0, &s_stop)) break;
+          const uint32_t to = map_to_rank(ring_s, rank) + (split - 1) * run_bytes + q * 4096 + lane * 16;
+          const uint32_t bar = map_to_rank(smem_addr(&s_recv), rank);
+          for (int c0 = 0; c0 < t.rows; c0 += 32) {
+            uint32_t ra[16], rb[16];
+            tmem_ld_16x32(acc + c0, ra);
+            tmem_ld_16x32(acc + c0 + (16u << 16), rb);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              store_async16(to + c0 * 512 + i * 512, ra[4 * i], ra[4 * i + 1], ra[4 * i + 2], ra[4 * i + 3], bar);
+              store_async16(to + c0 * 512 + (4 + i) * 512, rb[4 * i], rb[4 * i + 1], rb[4 * i + 2], rb[4 * i + 3], bar);
+            }
+          }
+          break;  // the cluster's only tile
+        }
+      }
       const int64_t orow = MODE == kGradW ? (int64_t)t.e * p.wrows + t.row0 : t.row0;
       if (MODE == kGradW && p.out_f32) {
         // 32-bit outputs: a lane is a feature, a warp stores 128 bytes of a row
@@ -693,8 +718,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           float a[16], b[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            a[j] = __uint_as_float(ra[j]) + ba[(j >> 1) & 1];
-            b[j] = __uint_as_float(rb[j]) + bb[(j >> 1) & 1];
+            a[j] = __uint_as_float(ra[j]);
+            b[j] = __uint_as_float(rb[j]);
+          }
+          if (MODE != kGradW && p.splits > 1) {
+            const uint4* from = reinterpret_cast<const uint4*>(ring) + (c0 / 32 * 4 + q) * 256 + lane;
+            for (int run = 1; run < p.splits; ++run, from += (t.rows + 31) / 32 * 1024)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint4 v = from[i * 32];
+                float* dst = (i < 4 ? a : b) + 4 * (i & 3);
+                dst[0] += __uint_as_float(v.x);
+                dst[1] += __uint_as_float(v.y);
+                dst[2] += __uint_as_float(v.z);
+                dst[3] += __uint_as_float(v.w);
+              }
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            a[j] += ba[(j >> 1) & 1];
+            b[j] += bb[(j >> 1) & 1];
           }
           const int nr = min(32, t.rows - c0);
           const int64_t row = orow + c0;
@@ -720,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (t.nkb > 0) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_tempty + as), 0));
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_tempty + as), leader));
         ++acc_it;
       }
     }
@@ -795,20 +838,30 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  // as many pairs as can be resident at once: one more would start late
-  cfg.gridDim = dim3((unsigned)(num_sms / 2 * 2));
-  int pairs = 0;
-  err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, FP8>), cfg, 2, &pairs);
-  if (err != cudaSuccess) return err;
-  if (pairs < 1) return cudaErrorInvalidConfiguration;
-  if (pairs > num_sms / 2) pairs = num_sms / 2;
-  if (pairs > max_tiles) pairs = (int)max_tiles;
-  cfg.gridDim = dim3((unsigned)(pairs * 2));
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<MODE, FP8>, maps, a);
+  // Runs of the reduction: as many as leave every tile a cluster of its own that
+  // is resident, at least eight blocks a run, and accumulators that fit the ring.
+  const int64_t blocks = (a.red + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
+  const int64_t tile_rows = a.R < kRows<FP8> ? a.R : kRows<FP8>;
+  for (int splits = MODE == kGradW ? 1 : kMaxSplits;; splits /= 2) {
+    const int cl = 2 * splits;
+    if (splits > 1 && (blocks < 8 * splits || (splits - 1) * ((tile_rows + 31) / 32) * 16384 > a.ring_bytes)) continue;
+    attr[0].val.clusterDim.x = (unsigned)cl;
+    cfg.gridDim = dim3((unsigned)(num_sms / cl * cl));
+    // no more clusters than can be resident at once: one more would start late
+    int clusters = 0;
+    err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, FP8>), cfg, cl, &clusters);
+    if (err != cudaSuccess) return err;
+    if (clusters > num_sms / cl) clusters = num_sms / cl;
+    if (splits > 1 && max_tiles > clusters) continue;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (clusters > max_tiles) clusters = (int)max_tiles;
+    a.splits = splits;
+    cfg.gridDim = dim3((unsigned)(clusters * cl));
+    return cudaLaunchKernelEx(&cfg, matmul_kernel<MODE, FP8>, maps, a);
+  }
 }
 
 Args common_args(const MatmulArgs& m) {

@@ -43,6 +43,15 @@ __device__ __forceinline__ void mbar_arrive_mapped(uint32_t mapped) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapped) : "memory");
 }
 
+// 16 bytes to another CTA's shared memory, counted on an mbarrier there (both
+// mapped addresses).
+__device__ __forceinline__ void store_async16(uint32_t mapped, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                              uint32_t mapped_bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];"
+               ::"r"(mapped), "r"(a), "r"(b), "r"(c), "r"(d), "r"(mapped_bar)
+               : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Tensor-map loads (global -> this CTA's shared memory). The mbarrier that
 // counts the bytes may be the pair's other CTA's (a mapped address).
@@ -177,10 +186,9 @@ __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t lo) {
                "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}" ::"r"(taddr), "r"(lo), "n"(kDescPlainHi)
                : "memory");
 }
-// Arrives on the mbarrier at this offset in both CTAs of the pair when this
-// thread's matrix work issued so far has completed.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  const uint16_t both = 3;
+// Arrives on the mbarrier at this offset in the CTAs of the mask (by cluster
+// rank) when this thread's matrix work issued so far has completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t both) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
                ::"r"(bar), "h"(both)
                : "memory");

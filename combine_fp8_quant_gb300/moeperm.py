@@ -436,20 +436,25 @@ def _like(t, shape, dtype, dev, name):
     """The caller's output tensor, checked, or a new one. Outputs are dense."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=dev)
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"moeperm: {name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return t
 
 
 def _rows(t, name, shape=None, dtype=None):
     """Row stride of a 2-D tensor whose rows are dense; checks shape and dtype when given."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    own = t.shape
+    if len(own) != 2:
         raise ValueError(f"moeperm: {name} must be 2-D with dense rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"moeperm: {name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if shape is not None and own != shape:
+        raise ValueError(f"moeperm: {name} must have shape {tuple(shape)}, not {tuple(own)}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"moeperm: {name} must be {dtype}, not {t.dtype}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    rows, width = own
+    ld, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"moeperm: {name} must be 2-D with dense rows")
+    return ld if rows > 1 else max(ld, width)
 
 
 def _vec(t, n, name, dtype=torch.float32):
@@ -500,16 +505,16 @@ def permute(x, topk_ids, topk_weights, num_experts, num_local_experts, block_e=1
     _vec(topk_ids, T * K, "topk_ids", torch.int32)
     _vec(topk_weights, T * K, "topk_weights")
     bound = moe_compact_bound(T * K, L, block_e)
-    i32 = dict(dtype=torch.int32, device=dev)
     if row_weights is True:
         row_weights = torch.empty(bound, dtype=torch.float32, device=dev)
+    i32 = dict(dtype=torch.int32, device=dev)
     o = dict(xs=_like(out, (bound, H), dtype, dev, "out"), bound=bound,
              m_indices=torch.empty(bound, **i32), src2dst=torch.empty((T, K), **i32),
              counts=torch.empty(L, **i32), starts=torch.empty(L, **i32), psum=torch.empty(L, **i32),
              total=torch.empty(1, **i32),
              row_weights=None if row_weights is False else _vec(row_weights, bound, "row_weights"))
     ws = workspace if workspace is not None else Workspace(T, K, L, dev)
-    st = status if status is not None else torch.zeros(1, **i32)
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
     _check(moe_permute(x, ldx, dtype, T, num_tokens, H, topk_ids, topk_weights, K, num_experts, L,
                        block_e, o["xs"], o["m_indices"], bound, o["src2dst"], o["counts"],
                        o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, ws.nbytes, st),
@@ -711,14 +716,14 @@ def _gate_mode(gate, T, H, name="gate"):
     [T, 1] per token (a 1-D gate of T = H elements is per channel)."""
     if gate is None:
         return "none"
-    shape = tuple(gate.shape)
-    if shape in ((H,), (1, H)):
-        mode = "channel"
-    elif shape in ((T,), (T, 1)):
-        mode = "token"
+    shape = gate.shape
+    if shape == (H,) or shape == (1, H):
+        mode, n = "channel", H
+    elif shape == (T,) or shape == (T, 1):
+        mode, n = "token", T
     else:
-        raise ValueError(f"moeperm: {name} must have shape [{H}] or [{T}], not {shape}")
-    _vec(gate, gate.numel(), name)
+        raise ValueError(f"moeperm: {name} must have shape [{H}] or [{T}], not {tuple(shape)}")
+    _vec(gate, n, name)
     return mode
 
 
@@ -737,15 +742,17 @@ def block_norm(x, y=None, w_post=None, gate=None, scale=1.0, w_pre=None, eps=1e-
     mode = _gate_mode(gate, T, H)
     _vec(w_post, H, "w_post")
     _vec(w_pre, H, "w_pre")
-    new = lambda on: torch.empty((T, H), dtype=dtype, device=dev) if on else None
-    rstd = lambda on: torch.empty(T, dtype=torch.float32, device=dev) if on and save_rstd else None
-    o = dict(x=new(y is not None), h=new(w_pre is not None), rstd_post=rstd(w_post is not None),
-             rstd_pre=rstd(w_pre is not None))
-    _check(moe_block_norm(x, ldx, y, ldy, dtype, T, H, w_post, gate, mode, scale, w_pre, eps, o["x"],
-                          o["h"], o["rstd_post"], o["rstd_pre"]), "moe_block_norm")
-    if y is None:
-        o["x"] = x
-    return o
+    xo = torch.empty((T, H), dtype=dtype, device=dev) if y is not None else None
+    h = torch.empty((T, H), dtype=dtype, device=dev) if w_pre is not None else None
+    r_post = r_pre = None
+    if save_rstd:
+        if w_post is not None:
+            r_post = torch.empty(T, dtype=torch.float32, device=dev)
+        if w_pre is not None:
+            r_pre = torch.empty(T, dtype=torch.float32, device=dev)
+    _check(moe_block_norm(x, ldx, y, ldy, dtype, T, H, w_post, gate, mode, scale, w_pre, eps, xo, h,
+                          r_post, r_pre), "moe_block_norm")
+    return dict(x=x if y is None else xo, h=h, rstd_post=r_post, rstd_pre=r_pre)
 
 
 def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0, w_pre=None,

@@ -147,6 +147,33 @@ def test_forward_dense(dev, R, K, N):
     check_forward(out, None, x.double(), w[None].double(), b[None], res, [(0, R)], N, "none", False, torch.bfloat16)
 
 
+@pytest.mark.parametrize("R", [1, 9, 33, 64, 130, 256, 300])
+@pytest.mark.parametrize("K,N", [(1024, 256), (7168, 1160), (2056, 64)])
+def test_few_tiles_split_the_reduction(dev, R, K, N):
+    """One dense matrix with few rows: runs of the reduction on several pairs, joined in a fixed order."""
+    x, w = rand(1, R, K, dtype=torch.bfloat16), rand(2, N, K, dtype=torch.bfloat16, gain=K ** -0.5)
+    b = rand(3, N)
+    pre = torch.full((R, N), 9.0, device=DEV, dtype=torch.bfloat16)
+    out = dev.expert_matmul(x, w, bias=b, act="gelu", pre=pre)
+    check_forward(out, pre, x.double(), w[None].double(), b[None], None, [(0, R)], N, "gelu", False, torch.bfloat16)
+    assert torch.equal(out, dev.expert_matmul(x, w, bias=b, act="gelu", pre=pre))
+    dout = rand(4, R, N, dtype=torch.bfloat16)
+    dx = dev.expert_matmul_grad(dout, x, w, need=("dx",))["dx"].double()
+    want = dout.double() @ w.double()
+    mag = dout.double().abs() @ w.double().abs()
+    assert ((dx - want).abs() <= 2.0 ** -8 * want.abs() + (N + 4) * V * mag).all()
+
+
+@pytest.mark.parametrize("R", [1, 40, 200])
+@pytest.mark.parametrize("K,N,gated", [(2048, 512, False), (7168, 128, True), (2176, 64, False)])
+def test_few_tiles_split_the_reduction_e4m3(dev, R, K, N, gated):
+    Nw = 2 * N if gated else N
+    q, sc, ld, xv = quant(rand(1, R, K))
+    wq, wsc, ldw, wv = quant(rand(2, Nw, K, gain=K ** -0.5))
+    out = dev.expert_matmul(q, wq, act="silu", gated=gated, x_scales=sc, ld_xs=ld, w_scales=wsc, ld_ws=ldw)
+    check_forward(out, None, xv, wv[None], None, None, [(0, R)], N, "silu", gated, torch.bfloat16)
+
+
 FP8 = [  # counts, align, K, N, gated
     ([1], 1, 128, 64, False), ([3, 0, 30], 4, 512, 128, True), ([225, 224], 1, 640, 136, False), ([449], 1, 1152, 64, True),
     ([4] * 32, 128, 7168, 256, True), ([100, 0, 300], 128, 2048, 384, True),
