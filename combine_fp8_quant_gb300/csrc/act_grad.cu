@@ -21,7 +21,7 @@ namespace moeperm {
 
 namespace {
 
-constexpr int kThreads = 256, kStrip = 128, kRowLanes = kThreads / 16;
+constexpr int kThreads = 256, kStrip = 128, kRowLanes = kThreads / 16, kRows = 2;
 
 // (act(v), act'(v))
 __device__ __forceinline__ float2 act_and_slope(float v, int act) {
@@ -61,35 +61,44 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradArgs p) {
   float s0[8], s1[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.0f;
-  if (col < p.N)
-    for (int64_t r = lo + rl; r < hi; r += kRowLanes) {
+  // kRows rows at once, their loads issued before the arithmetic
+  for (int64_t r0 = lo + rl; r0 < hi && col < p.N; r0 += kRows * kRowLanes) {
+    uint4 dv[kRows], pv[kRows], uv[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + i * kRowLanes;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const bool in = r < hi;
+      dv[i] = in ? ld_nc_v4(dout + r * p.ldd + col) : zero;
+      pv[i] = in && dpre != nullptr ? ld_nc_v4(pre + r * p.ld_pre + col) : zero;
+      uv[i] = in && p.gated ? ld_nc_v4(pre + r * p.ld_pre + p.N + col) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int64_t r = r0 + i * kRowLanes;
+      if (r >= hi) break;
       float d[8];
-      const uint4 dv = ld_nc_v4(dout + r * p.ldd + col);
+      Vec<TYPE>::unpack(dv[i], d);
       if (dpre == nullptr) {
-        Vec<TYPE>::unpack(dv, d);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s0[j] += d[j];
         continue;
       }
       float v[8], u[8];
-      const uint4 pv = ld_nc_v4(pre + r * p.ld_pre + col);
-      if (p.gated) Vec<TYPE>::unpack(ld_nc_v4(pre + r * p.ld_pre + p.N + col), u);
-      Vec<TYPE>::unpack(dv, d);
-      Vec<TYPE>::unpack(pv, v);
+      Vec<TYPE>::unpack(pv[i], v);
+      Vec<TYPE>::unpack(uv[i], u);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 a = act_and_slope(v[j], p.act);
         v[j] = p.gated ? d[j] * u[j] * a.y : d[j] * a.y;
         u[j] = d[j] * a.x;
-      }
-      st_v4(dpre + r * Nw + col, Vec<TYPE>::pack(v));
-      if (p.gated) st_v4(dpre + r * Nw + p.N + col, Vec<TYPE>::pack(u));
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
         s0[j] += v[j];
         s1[j] += u[j];
       }
+      st_v4(dpre + r * Nw + col, Vec<TYPE>::pack(v));
+      if (p.gated) st_v4(dpre + r * Nw + p.N + col, Vec<TYPE>::pack(u));
     }
+  }
   if (p.dbias == nullptr) return;  // uniform over the grid
   float* dst = (p.splits > 1 ? p.ws + (int64_t)blockIdx.z * p.L * Nw : p.dbias) + (int64_t)e * Nw;
   for (int half = 0; half < (p.gated ? 2 : 1); ++half) {

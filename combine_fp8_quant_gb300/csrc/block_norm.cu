@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(MAXT) norm_grad_kernel(NormArgs p, int slots) 
   if (post || p.gate_mode == kGateChannel) put(1, a_q);
 }
 
-constexpr int kSumCols = 32, kSumRows = 8;  // columns per CTA, row groups per column
+constexpr int kSumCols = 32, kSumRows = 16;  // columns per CTA, row groups per column
 
 // Column sums of the partial rows in a fixed order. blockIdx.y = 0: dw_pre;
 // 1: Q, which gives dw_post and the gate's gradient per channel.
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kSumCols * kSumRows) norm_sum_kernel(NormArgs 
   const float* src = p.ws + (int64_t)blockIdx.y * p.parts * p.H + h;
   float acc = 0.0f;
   if (h < p.H)
-#pragma unroll 8
+#pragma unroll 10
     for (int r = grp; r < used; r += kSumRows) acc += __ldcg(src + (int64_t)r * p.H);
   s[grp][col] = acc;
   __syncthreads();

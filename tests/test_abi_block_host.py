@@ -1,0 +1,181 @@
+"""Host-side checks of the calls around the dispatch (no GPU work): every
+argument error is refused before any launch. Pointers are fake and never
+dereferenced."""
+import pytest
+import torch
+
+FAKE = 1 << 20
+ODD = FAKE + 4
+BF, FH, F32, E4 = torch.bfloat16, torch.float16, torch.float32, torch.float8_e4m3fn
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+S = _Stream()
+
+
+@pytest.fixture(scope="module")
+def mp():
+    from combine_fp8_quant_gb300 import build
+    build.build()
+    import combine_fp8_quant_gb300 as m
+    m.load()
+    return m
+
+
+def call(mp, name, args, over):
+    a = dict(args)
+    assert set(over) <= set(a), over
+    a.update(over)
+    return getattr(mp, name)(*a.values(), stream=S)
+
+
+PERMUTE = dict(x=FAKE, ldx=1024, dtype=BF, T=64, d_num_tokens=None, H=1024, topk_ids=FAKE, topk_weights=FAKE, K=8, E=256,
+               L=32, block_e=128, xs=FAKE, m_indices=FAKE, bound=1 << 20, src2dst=FAKE, counts=FAKE, starts=FAKE, psum=FAKE,
+               total=FAKE, row_weights=None, workspace=FAKE, workspace_bytes=1 << 20, d_status=FAKE)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(H=1020), dict(H=0), dict(H=32776, ldx=32776), dict(dtype=F32, H=1022), dict(ldx=1000), dict(ldx=1028),
+    dict(x=ODD), dict(x=None), dict(xs=ODD), dict(xs=None), dict(K=0), dict(K=33), dict(L=0), dict(L=1025, E=2000), dict(E=31),
+    dict(block_e=0), dict(T=-1), dict(T=1 << 18), dict(bound=100), dict(bound=1 << 31), dict(topk_ids=None),
+    dict(src2dst=None), dict(m_indices=None), dict(counts=None), dict(starts=None), dict(psum=None), dict(total=None),
+    dict(row_weights=FAKE, topk_weights=None), dict(workspace=None), dict(workspace=ODD), dict(workspace_bytes=64),
+])
+def test_permute_refuses(mp, over):
+    assert call(mp, "moe_permute", PERMUTE, over) == mp.MOE_ERR_INVALID_ARG
+
+
+COMBINE = dict(y=FAKE, ldy=1024, dtype=FH, R=100, src2dst=FAKE, w=FAKE, T=8, d_num_tokens=None, K=8, H=1024, out=FAKE,
+               d_status=FAKE)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(H=1020), dict(ldy=1000), dict(ldy=1028), dict(y=ODD), dict(y=None), dict(K=0), dict(K=33), dict(T=-1),
+    dict(R=-1), dict(src2dst=None), dict(out=None), dict(out=ODD),
+])
+def test_combine_refuses(mp, over):
+    assert call(mp, "moe_combine_ex", COMBINE, over) == mp.MOE_ERR_INVALID_ARG
+
+
+COMBINE_GRAD = dict(dout=FAKE, ldd=1024, y=FAKE, ldy=1024, dtype=BF, R=100, src2dst=FAKE, w=FAKE, T=8, d_num_tokens=None, K=8,
+                    H=1024, dy=FAKE, lddy=1024, dw=FAKE, d_status=FAKE)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(H=1020), dict(ldd=1000), dict(ldy=1028), dict(lddy=1004), dict(dout=None), dict(dout=ODD), dict(y=None),
+    dict(dy=ODD), dict(dy=None, dw=None), dict(K=33), dict(T=-1), dict(R=-1), dict(src2dst=None),
+])
+def test_combine_grad_refuses(mp, over):
+    assert call(mp, "moe_combine_grad", COMBINE_GRAD, over) == mp.MOE_ERR_INVALID_ARG
+
+
+NORM = dict(x=FAKE, ldx=1024, y=FAKE, ldy=1024, dtype=BF, T=8, H=1024, w_post=FAKE, gate=FAKE, gate_mode="channel", scale=1.0,
+            w_pre=FAKE, eps=1e-6, x_out=FAKE, h=FAKE, rstd_post=None, rstd_pre=None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(T=-1), dict(H=1020), dict(H=0), dict(H=16392, ldx=16392, ldy=16392), dict(dtype=F32, H=8196, ldx=8196),
+    dict(x=None), dict(x=ODD), dict(ldx=1000), dict(ldy=1004), dict(y=ODD), dict(y=None), dict(y=None, gate_mode="none"),
+    dict(y=None, w_post=None, gate_mode="none", w_pre=None), dict(gate=None), dict(gate=ODD), dict(w_post=ODD), dict(w_pre=ODD),
+    dict(x_out=None), dict(h=None), dict(eps=-1.0), dict(eps=float("nan")),
+])
+def test_block_norm_refuses(mp, over):
+    assert call(mp, "moe_block_norm", NORM, over) == mp.MOE_ERR_INVALID_ARG
+
+
+NORM_GRAD = dict(dx_out=FAKE, ld_dxo=1024, dh=FAKE, ld_dh=1024, x_out=FAKE, ldx=1024, y=FAKE, ldy=1024, dtype=BF, T=8, H=1024,
+                 w_post=FAKE, gate=FAKE, gate_mode="channel", scale=1.0, w_pre=FAKE, rstd_post=FAKE, rstd_pre=FAKE, dx=FAKE,
+                 dy=FAKE, dw_post=FAKE, dgate=FAKE, dw_pre=FAKE, workspace=FAKE, workspace_bytes=1 << 24)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(H=1020), dict(T=-1), dict(dx_out=ODD), dict(ld_dxo=1000), dict(dh=None), dict(ld_dh=1004), dict(x_out=None),
+    dict(y=ODD), dict(y=None), dict(rstd_post=None), dict(rstd_pre=None), dict(dx=None), dict(dy=None), dict(dw_post=None),
+    dict(dw_pre=None), dict(dgate=None), dict(gate_mode="token", dgate=None), dict(workspace=None), dict(workspace_bytes=100),
+    dict(gate=None),
+])
+def test_block_norm_grad_refuses(mp, over):
+    assert call(mp, "moe_block_norm_grad", NORM_GRAD, over) == mp.MOE_ERR_INVALID_ARG
+
+
+MATMUL = dict(x=FAKE, ldx=512, dtype=BF, x_scales=None, ld_xs=0, R=1024, K=512, w=FAKE, w_scales=None, ld_ws=0, L=4, N=256,
+              gated=True, act="silu", bias=None, seg_begin=FAKE, seg_end=FAKE, cap=0, residual=None, ld_res=0, out=FAKE, ldo=256,
+              out_dtype=BF, pre=None, ld_pre=0, d_status=FAKE)
+E4M3 = dict(dtype=E4, x_scales=FAKE, ld_xs=1024, w_scales=FAKE, ld_ws=2048)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=F32), dict(out_dtype=FH), dict(out_dtype=F32), dict(R=-1), dict(R=1 << 31), dict(L=0), dict(L=1025), dict(K=0),
+    dict(K=508), dict(N=0), dict(N=248), dict(gated=False, N=252), dict(N=1 << 29), dict(seg_begin=None), dict(seg_end=None),
+    dict(seg_begin=None, seg_end=None), dict(cap=256), dict(seg_begin=None, cap=100), dict(cap=-1), dict(x=None), dict(x=ODD),
+    dict(ldx=500), dict(ldx=516), dict(w=None), dict(w=ODD), dict(out=None), dict(ldo=200), dict(residual=FAKE, ld_res=100),
+    dict(pre=FAKE, ld_pre=256),
+    dict(E4M3, K=576, ldx=576), dict(E4M3, x_scales=None), dict(E4M3, w_scales=None), dict(E4M3, ld_xs=1000), dict(E4M3, ld_xs=1026),
+    dict(E4M3, ld_ws=2044), dict(E4M3, ld_ws=2050), dict(E4M3, pre=FAKE, ld_pre=512), dict(E4M3, out_dtype=F32), dict(E4M3, ldx=520),
+])
+def test_expert_matmul_refuses(mp, over):
+    assert call(mp, "moe_expert_matmul", MATMUL, over) == mp.MOE_ERR_INVALID_ARG
+
+
+GRAD = dict(dout=FAKE, ldd=256, x=FAKE, ldx=512, dtype=BF, R=1024, K=512, w=FAKE, L=4, N=256, gated=True, act="silu", pre=FAKE,
+            ld_pre=512, seg_begin=FAKE, seg_end=FAKE, cap=0, dx=FAKE, ld_dx=512, dw=FAKE, dw_dtype=BF, dbias=FAKE, workspace=FAKE,
+            workspace_bytes=1 << 30, d_status=FAKE)
+
+
+@pytest.mark.parametrize("over", [
+    dict(dtype=E4), dict(dtype=F32), dict(R=-1), dict(L=0), dict(K=508), dict(N=250), dict(dx=None, dw=None, dbias=None),
+    dict(dw_dtype=FH), dict(dw_dtype=E4), dict(dout=None), dict(dout=ODD), dict(ldd=200), dict(ldd=260), dict(pre=None),
+    dict(ld_pre=256), dict(x=None), dict(ldx=500), dict(w=None), dict(ld_dx=500), dict(workspace=None), dict(workspace_bytes=1000),
+    dict(seg_begin=None), dict(cap=256),
+])
+def test_expert_matmul_grad_refuses(mp, over):
+    assert call(mp, "moe_expert_matmul_grad", GRAD, over) == mp.MOE_ERR_INVALID_ARG
+
+
+def test_workspace_sizes(mp):
+    assert mp.moe_block_norm_workspace_bytes(0, 64) == 2 * 64 * 4
+    assert mp.moe_block_norm_workspace_bytes(100000, 64) == mp.moe_block_norm_workspace_bytes(304, 64)
+    assert mp.moe_block_norm_workspace_bytes(-1, 64) == 0
+    assert mp.moe_expert_matmul_grad_workspace_bytes(0, 4, 64) == 0
+    assert mp.moe_expert_matmul_grad_workspace_bytes(1000, 4, 64) >= 1000 * 64 * 2
+    assert mp.moe_expert_matmul_grad_workspace_bytes(-1, 4, 64) == 0
+
+
+def test_the_binding_refuses(mp):
+    """Wrong shapes, types, strides and devices raise before the library is called."""
+    x, w = torch.zeros(8, 64, dtype=BF), torch.zeros(2, 32, 64, dtype=BF)
+    seg = torch.zeros(2, dtype=torch.int32)
+    bad = [
+        lambda: mp.expert_matmul(x, w),                                            # two experts, no segments
+        lambda: mp.expert_matmul(x, w, seg),                                       # starts without psum
+        lambda: mp.expert_matmul(x, w, seg, seg, masked_m=seg),
+        lambda: mp.expert_matmul(x, w, seg.long(), seg.long()),
+        lambda: mp.expert_matmul(x, w, seg, seg, act="tanh"),
+        lambda: mp.expert_matmul(x, w.half(), seg, seg),
+        lambda: mp.expert_matmul(x.float(), w.float(), seg, seg),
+        lambda: mp.expert_matmul(x[:, :32], w, seg, seg),
+        lambda: mp.expert_matmul(x.t(), w, seg, seg),
+        lambda: mp.expert_matmul(x, w, seg, seg, bias=torch.zeros(2, 31)),
+        lambda: mp.expert_matmul(x, w, seg, seg, out=torch.zeros(8, 31, dtype=BF)),
+        lambda: mp.expert_matmul(x, w, masked_m=seg),                              # slabs are 3-D
+        lambda: mp.expert_matmul(x.to(E4), w.to(E4), seg, seg),                    # no scales
+        lambda: mp.expert_matmul(x, w, seg, seg),                                  # all well, but on the CPU
+        lambda: mp.expert_matmul_grad(x[:, :32], x, w, seg, seg, act="silu"),      # no pre
+        lambda: mp.expert_matmul_grad(x, x, w, seg, seg),                          # dout is [8, 32]
+        lambda: mp.permute(x.to(E4), seg.view(2, 1), torch.zeros(2, 1), 4, 4),
+        lambda: mp.permute(x, torch.zeros(8, 2), torch.zeros(8, 2), 4, 4),
+        lambda: mp.combine_grad(x, x[:4].float(), seg.view(2, 1)),
+        lambda: mp.permute_grad(x.t(), seg.view(2, 1)),
+        lambda: mp.block_norm(x, x[:4]),
+        lambda: mp.block_norm(x, x, gate=torch.zeros(5)),
+        lambda: mp.block_norm(x, x, w_post=torch.zeros(64, dtype=BF)),
+        lambda: mp.block_norm(x, w_pre=torch.zeros(64)),                           # all well, but on the CPU
+        lambda: mp.block_norm_grad(x, x, x[:, :32], w_pre=torch.zeros(32)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i} was accepted")
