@@ -21,7 +21,8 @@ namespace moeperm {
 
 namespace {
 
-constexpr int kThreads = 256, kStrip = 128, kRowLanes = kThreads / 16, kRows = 2;
+constexpr int kThreads = 256, kStrip = 128, kCols = kStrip / 8, kRowLanes = kThreads / kCols;
+constexpr int kSlots = 3;  // rows of a thread in flight and in work
 
 // (act(v), act'(v))
 __device__ __forceinline__ float2 act_and_slope(float v, int act) {
@@ -38,9 +39,10 @@ __device__ __forceinline__ float2 act_and_slope(float v, int act) {
 }
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradArgs p) {
+__global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
+  __shared__ uint4 s_ring[kSlots][3][kThreads];
   __shared__ float s_sum[kRowLanes][kStrip + 4];
-  const int tid = threadIdx.x, rl = tid >> 4, col = blockIdx.x * kStrip + (tid & 15) * 8;
+  const int tid = threadIdx.x, rl = tid / kCols, col = blockIdx.x * kStrip + (tid % kCols) * 8;
   const int e = blockIdx.y, Nw = p.gated ? 2 * p.N : p.N;
   int64_t b = 0, c = p.R;
   if (p.cap > 0) {
@@ -61,42 +63,46 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradArgs p) {
   float s0[8], s1[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.0f;
-  // kRows rows at once, their loads issued before the arithmetic
-  for (int64_t r0 = lo + rl; r0 < hi && col < p.N; r0 += kRows * kRowLanes) {
-    uint4 dv[kRows], pv[kRows], uv[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int64_t r = r0 + i * kRowLanes;
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      const bool in = r < hi;
-      dv[i] = in ? ld_nc_v4(dout + r * p.ldd + col) : zero;
-      pv[i] = in && dpre != nullptr ? ld_nc_v4(pre + r * p.ld_pre + col) : zero;
-      uv[i] = in && p.gated ? ld_nc_v4(pre + r * p.ld_pre + p.N + col) : zero;
+  // this thread's vectors of the next kSlots - 1 rows are in flight while it works
+  // on one (the slots are private to the thread: no barrier)
+  const bool has_act = dpre != nullptr;
+  auto fetch = [&](int64_t r, int slot) {
+    if (r < hi) {
+      cp_async16(&s_ring[slot][0][tid], dout + r * p.ldd + col);
+      if (has_act) cp_async16(&s_ring[slot][1][tid], pre + r * p.ld_pre + col);
+      if (p.gated) cp_async16(&s_ring[slot][2][tid], pre + r * p.ld_pre + p.N + col);
     }
+    cp_async_commit();
+  };
+  if (col < p.N) {
+    int64_t r = lo + rl;
+    int slot = 0;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int64_t r = r0 + i * kRowLanes;
-      if (r >= hi) break;
+    for (int i = 0; i + 1 < kSlots; ++i) fetch(r + i * kRowLanes, i);
+    for (; r < hi; r += kRowLanes) {
+      fetch(r + (kSlots - 1) * kRowLanes, slot == 0 ? kSlots - 1 : slot - 1);
+      cp_async_wait_group<kSlots - 1>();
       float d[8];
-      Vec<TYPE>::unpack(dv[i], d);
-      if (dpre == nullptr) {
+      Vec<TYPE>::unpack(s_ring[slot][0][tid], d);
+      if (!has_act) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) s0[j] += d[j];
-        continue;
-      }
-      float v[8], u[8];
-      Vec<TYPE>::unpack(pv[i], v);
-      Vec<TYPE>::unpack(uv[i], u);
+      } else {
+        float v[8], u[8];
+        Vec<TYPE>::unpack(s_ring[slot][1][tid], v);
+        if (p.gated) Vec<TYPE>::unpack(s_ring[slot][2][tid], u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float2 a = act_and_slope(v[j], p.act);
-        v[j] = p.gated ? d[j] * u[j] * a.y : d[j] * a.y;
-        u[j] = d[j] * a.x;
-        s0[j] += v[j];
-        s1[j] += u[j];
+        for (int j = 0; j < 8; ++j) {
+          const float2 a = act_and_slope(v[j], p.act);
+          v[j] = p.gated ? d[j] * u[j] * a.y : d[j] * a.y;
+          u[j] = d[j] * a.x;
+          s0[j] += v[j];
+          s1[j] += u[j];
+        }
+        st_v4(dpre + r * Nw + col, Vec<TYPE>::pack(v));
+        if (p.gated) st_v4(dpre + r * Nw + p.N + col, Vec<TYPE>::pack(u));
       }
-      st_v4(dpre + r * Nw + col, Vec<TYPE>::pack(v));
-      if (p.gated) st_v4(dpre + r * Nw + p.N + col, Vec<TYPE>::pack(u));
+      if (++slot == kSlots) slot = 0;
     }
   }
   if (p.dbias == nullptr) return;  // uniform over the grid
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kThreads) act_grad_kernel(ActGradArgs p) {
   for (int half = 0; half < (p.gated ? 2 : 1); ++half) {
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s_sum[rl][(tid & 15) * 8 + j] = half ? s1[j] : s0[j];
+    for (int j = 0; j < 8; ++j) s_sum[rl][(tid % kCols) * 8 + j] = half ? s1[j] : s0[j];
     __syncthreads();
     const int h = blockIdx.x * kStrip + tid;
     if (tid < kStrip && h < p.N) {

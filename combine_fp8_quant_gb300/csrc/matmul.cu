@@ -25,7 +25,7 @@
 // was the bound: filling and reading 48 KB each per 128 bytes of reduction of a
 // 128 x 256 tile takes 768 cycles at 128 bytes a cycle where the products take
 // 512 (measured 727); a pair moves 32 KB.
-// Warp roles: 0 loads (TMA), 1 (of the pair's first CTA) issues the products, 2
+// Warp roles: 0 and 8 load (TMA), 1 (of the pair's first CTA) issues the products, 2
 // and 3 lay out the e4m3 scales, or 2 zeroes the last lines of kGradW, 4-7 the
 // epilogue, one warp per 32 lanes of tensor memory; two accumulators (columns
 // 0.. and kRows..) let the epilogue of a tile overlap the products of the next.
@@ -56,7 +56,7 @@ namespace moeperm {
 namespace {
 
 constexpr int kForward = 0, kGradX = 1, kGradW = 2;
-constexpr int kThreads = 256;
+constexpr int kThreads = 288;
 constexpr int kMaxSplits = 4;
 constexpr int kMaxStages = 10;
 constexpr int kABytes = 16384;            // 128 rows x 128 bytes
@@ -107,7 +107,8 @@ struct Args {
 };
 
 struct Bars {  // one barrier of each kind per stage
-  uint64_t full[kMaxStages], ready[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t raw[kMaxStages];  // kGradW: the last block of a segment has landed in this CTA
 };
 
 struct Tile {
@@ -287,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t dyn[];
   __shared__ Bars s_bars;
-  uint64_t *s_full = s_bars.full, *s_empty = s_bars.empty, *s_ready = s_bars.ready;
+  uint64_t *s_full = s_bars.full, *s_empty = s_bars.empty, *s_raw = s_bars.raw;
   __shared__ uint64_t s_tfull[2], s_tempty[2], s_sraw[kScaleBufs], s_sfull[kScaleBufs], s_sempty[kScaleBufs], s_drain;
   __shared__ uint64_t s_go, s_recv;  // splits: the ring may be written; the accumulators have arrived
   __shared__ uint32_t s_tmem;
@@ -312,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(smem_addr(s_full + i), 1);
+      mbar_init(smem_addr(s_full + i), MODE == kGradW ? 2 : 1);
       mbar_init(smem_addr(s_empty + i), 1);
-      if (MODE == kGradW) mbar_init(smem_addr(s_ready + i), 2);
+      mbar_init(smem_addr(s_raw + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(s_tfull + i), 1);
@@ -425,57 +426,74 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
   const uint32_t ring_s = smem_addr(ring);
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 8) {
     // ------------------------------------------------------------------ loads
-    // Each CTA loads its weight rows and its half of the tile's rows; the bytes
-    // of both count on the first CTA's barrier (kGradW: each on its own).
+    // Warp 0 loads this CTA's weight rows (kGradW: its features of x), warp 8 its
+    // half of the tile's rows: issuing is serial in a thread (about 400 cycles a
+    // stage for both together, close to the products' 512), so two threads share
+    // it. The bytes of both CTAs count on the first CTA's barrier. In kGradW a
+    // block that ends inside counts on this CTA's own barrier and goes on through
+    // warp 2 (the first CTA's barrier then takes an arrival of each CTA's warp 2
+    // instead of the loads').
     if (elect_one()) {
-      int s = 0, issued = 0;
-      uint32_t ph = 1;  // parity of the wait for a free stage
+      const bool weights = warp == 0;
+      const uint32_t empty0 = smem_addr(s_empty), raw0 = smem_addr(s_raw);
+      const uint32_t full0 = map_to_rank(smem_addr(s_full), leader);
+      const uint32_t dst0 = ring_s + (weights ? 0 : kABytes);
+      uint32_t empty = empty0, full = full0, raw = raw0, dst = dst0, ph = 1;
+      int left = stages, issued = 0;
       bool ok = true;
       for (int w = pair; w < total && ok; w += npairs) {
         const Tile t = tile_at(w);
         const int half = t.n / 2;
         const int box = MODE == kGradW ? 0 : box_index(half);
         const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
-        const uint32_t bytes = kABytes + (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
+        const uint32_t b_tile = MODE == kGradW ? nbox * 8192 : box_rows(box) * 128;
         const CUtensorMap* mb = &maps.b[box];
-        const int brow = t.row0 + rank * half;
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!(ok = wait_or_stop(smem_addr(s_empty + s), ph, &s_stop))) break;
-          uint32_t full = smem_addr(s_full + s);
-          const uint32_t a = ring_s + s * stage_bytes, b = a + kABytes;
-          const int red = (t.kb0 + kb) * kRedBlock;
-          if constexpr (MODE == kGradW) {
-            mbar_expect_tx(full, bytes);
+        const int f = t.fb * 128, brow = t.row0 + rank * half;
+        int red = t.kb0 * kRedBlock;
+        for (int kb = 0; kb < t.nkb; ++kb, red += kRedBlock) {
+          if (!(ok = wait_or_stop(empty, ph, &s_stop))) break;
+          const bool tail = MODE == kGradW && kb == t.nkb - 1 && t.tail < 64;
+          const uint32_t bar = tail ? raw : full;
+          if (weights) {
+            // one arrival arms the barrier for all bytes that will count on it
+            if (tail) mbar_expect_tx(bar, kABytes + b_tile);
+            else if (rank == 0) mbar_expect_tx(smem_addr(s_full) + (full - full0), 2 * (kABytes + b_tile));
+            else if (MODE == kGradW) mbar_arrive_mapped(bar);
+            if constexpr (MODE == kForward) {
+              if (p.gated) tma_load_5d(dst, &maps.a, bar, red, 0, 0, t.fb * 4, t.e);
+              else tma_load_3d(dst, &maps.a, bar, red, f, t.e);
+            } else if constexpr (MODE == kGradX) {
+              tma_load_3d(dst, &maps.a, bar, f, red, t.e);
+              tma_load_3d(dst + 8192, &maps.a, bar, f + 64, red, t.e);
+            } else {
+              tma_load_2d(dst, &maps.a, bar, f, t.red_row0 + red);
+              tma_load_2d(dst + 8192, &maps.a, bar, f + 64, t.red_row0 + red);
+            }
+          } else if constexpr (MODE == kGradW) {
+            for (int i = 0; i < nbox; ++i) tma_load_2d(dst + i * 8192, mb, bar, brow + i * 64, t.red_row0 + red);
           } else {
-            if (rank == 0) mbar_expect_tx(full, 2 * bytes);
-            else full = map_to_rank(full, leader);
-          }
-          if constexpr (MODE == kForward) {
-            if (p.gated) tma_load_5d(a, &maps.a, full, red, 0, 0, t.fb * 4, t.e);
-            else tma_load_3d(a, &maps.a, full, red, t.fb * 128, t.e);
-            tma_load_2d(b, mb, full, red, brow);
-          } else if constexpr (MODE == kGradX) {
-            tma_load_3d(a, &maps.a, full, t.fb * 128, red, t.e);
-            tma_load_3d(a + 8192, &maps.a, full, t.fb * 128 + 64, red, t.e);
-            tma_load_2d(b, mb, full, red, brow);
-          } else {
-            const int y = t.red_row0 + red;
-            tma_load_2d(a, &maps.a, full, t.fb * 128, y);
-            tma_load_2d(a + 8192, &maps.a, full, t.fb * 128 + 64, y);
-            for (int i = 0; i < nbox; ++i) tma_load_2d(b + i * 8192, mb, full, brow + i * 64, y);
+            tma_load_2d(dst, mb, bar, red, brow);
           }
           ++issued;
-          if (++s == stages) {
-            s = 0;
+          dst += stage_bytes;
+          empty += 8;
+          full += 8;
+          raw += 8;
+          if (--left == 0) {
+            left = stages;
+            empty = empty0;
+            full = full0;
+            raw = raw0;
+            dst = dst0;
             ph ^= 1;
           }
         }
       }
       // a wait ran out: let the copies in flight land, again with a limit (they
       // count on the first CTA's barriers, whose CTA stays until the end)
-      if (!ok && (MODE == kGradW || rank == 0))
+      if (!ok && rank == 0 && weights)
         for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
           mbar_wait(smem_addr(s_full + i % stages), (i / stages) & 1);
     }
@@ -485,9 +503,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int acc_it = 0, sf_it = 0;
       // the stage's descriptor word and barrier, stepped rather than indexed: one
       // thread issues alone, so every instruction of this loop counts
-      const uint32_t lo0 = desc_lo(ring_s, 0), bar0 = smem_addr(MODE == kGradW ? s_bars.ready : s_bars.full);
-      constexpr uint32_t kEmptyOffset = MODE == kGradW ? offsetof(Bars, empty) - offsetof(Bars, ready)
-                                                       : offsetof(Bars, empty) - offsetof(Bars, full);
+      const uint32_t lo0 = desc_lo(ring_s, 0), bar0 = smem_addr(s_bars.full);
+      constexpr uint32_t kEmptyOffset = offsetof(Bars, empty) - offsetof(Bars, full);
       uint32_t lo = lo0, bar = bar0, ph = 0;
       int left = stages;
       bool ok = true;
@@ -550,31 +567,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (MODE == kGradW && warp == 2) {
     // ------------------------------------------- lines past the segment's end
-    // Every stage passes through here on its way to the products: the last
-    // block of a segment gets zero lines in each of its 64-wide boxes.
-    int s = 0;
-    uint32_t ph = 0;
+    // The last block of a segment gets zero lines in each of its 64-wide boxes on
+    // its way to the products; the others go straight there.
+    int at = 0;          // stage of the tile's first block
+    uint32_t phase = 0;  // bit s: parity of the next wait on s_raw[s]
     bool ok = true;
     for (int w = pair; w < total && ok; w += npairs) {
       const Tile t = tile_at(w);
-      for (int kb = 0; kb < t.nkb; ++kb) {
-        if (!(ok = warp_wait_or_stop(smem_addr(s_full + s), ph, &s_stop))) break;
-        if (kb == t.nkb - 1 && t.tail < 64) {
-          uint8_t* a = ring + s * stage_bytes;
-          const int boxes = 2 + (t.n / 2 + 63) / 64;
-          for (int i = lane; i < boxes * (64 - t.tail) * 8; i += 32) {
-            const int line = i >> 3, bx = line / (64 - t.tail), r = t.tail + line % (64 - t.tail);
-            *reinterpret_cast<uint4*>(a + bx * 8192 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
+      if (t.nkb > 0 && t.tail < 64) {
+        const int s = (at + t.nkb - 1) % stages;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_raw + s), (phase >> s) & 1, &s_stop))) break;
+        phase ^= 1u << s;
+        uint8_t* a = ring + s * stage_bytes;
+        const int boxes = 2 + (t.n / 2 + 63) / 64;
+        for (int i = lane; i < boxes * (64 - t.tail) * 8; i += 32) {
+          const int line = i >> 3, bx = line / (64 - t.tail), r = t.tail + line % (64 - t.tail);
+          *reinterpret_cast<uint4*>(a + bx * 8192 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
         }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_ready + s), leader));
-        if (++s == stages) {
-          s = 0;
-          ph ^= 1;
-        }
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s), leader));
       }
+      at = (at + t.nkb) % stages;
     }
   } else if (FP8 && warp == 2) {
     // ----------------------------------------------------------------- scales
@@ -627,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp >= 4) {
+  } else if (warp >= 4 && warp < 8) {
     // --------------------------------------------------------------- epilogue
     const int q = warp & 3;  // this warp's 32 lanes of tensor memory
     const bool f16 = p.f16 != 0;

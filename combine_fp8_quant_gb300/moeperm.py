@@ -125,6 +125,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _off_device(t):
+    raise ValueError(f"moeperm: tensor on {t.device}, but every tensor argument must be on a CUDA "
+                     "device")
+
+
+def _ptrs(*tensors):
+    """_ptr of several tensors (or None) at once: the helpers below go straight to
+    the library with these, which saves a small call a few microseconds."""
+    return [None if t is None else t.data_ptr() if t.is_cuda else _off_device(t) for t in tensors]
+
+
 # The current stream's raw handle without building a torch Stream object (the
 # public call costs microseconds per launch on small problems); the public
 # call is the fallback where these functions are absent.
@@ -444,22 +455,19 @@ def _like(t, shape, dtype, dev, name):
 def _rows(t, name, shape=None, dtype=None):
     """Row stride of a 2-D tensor whose rows are dense; checks shape and dtype when given."""
     own = t.shape
-    if len(own) != 2:
-        raise ValueError(f"moeperm: {name} must be 2-D with dense rows")
-    if shape is not None and own != shape:
-        raise ValueError(f"moeperm: {name} must have shape {tuple(shape)}, not {tuple(own)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"moeperm: {name} must be {dtype}, not {t.dtype}")
+    if len(own) != 2 or (shape is not None and own != shape) or (dtype is not None and t.dtype is not dtype):
+        raise ValueError(f"moeperm: {name} must be 2-D{'' if shape is None else f' of shape {tuple(shape)}'}"
+                         f"{'' if dtype is None else f' and {dtype}'}, not {t.dtype} of shape {tuple(own)}")
     rows, width = own
     ld, one = t.stride()
     if one != 1 and width > 1:
-        raise ValueError(f"moeperm: {name} must be 2-D with dense rows")
-    return ld if rows > 1 else max(ld, width)
+        raise ValueError(f"moeperm: the rows of {name} must be dense")
+    return ld if rows > 1 or ld >= width else width
 
 
 def _vec(t, n, name, dtype=torch.float32):
     """A dense vector argument of n elements (or None)."""
-    if t is not None and (t.dtype != dtype or t.numel() != n or not t.is_contiguous()):
+    if t is not None and (t.dtype is not dtype or t.numel() != n or not t.is_contiguous()):
         raise ValueError(f"moeperm: {name} must be a contiguous {dtype} tensor of {n} elements")
     return t
 
@@ -515,9 +523,11 @@ def permute(x, topk_ids, topk_weights, num_experts, num_local_experts, block_e=1
              row_weights=None if row_weights is False else _vec(row_weights, bound, "row_weights"))
     ws = workspace if workspace is not None else Workspace(T, K, L, dev)
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
-    _check(moe_permute(x, ldx, dtype, T, num_tokens, H, topk_ids, topk_weights, K, num_experts, L,
-                       block_e, o["xs"], o["m_indices"], bound, o["src2dst"], o["counts"],
-                       o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, ws.nbytes, st),
+    px, pn, pi, pw, *po, pws, pst = _ptrs(x, num_tokens, topk_ids, topk_weights, o["xs"],
+                                          o["m_indices"], o["src2dst"], o["counts"], o["starts"],
+                                          o["psum"], o["total"], o["row_weights"], ws.buf, st)
+    _check(lib().moe_permute(px, ldx, ELEM[dtype], T, pn, H, pi, pw, K, num_experts, L, block_e,
+                             po[0], po[1], bound, *po[2:], pws, ws.nbytes, pst, _stream()),
            "moe_permute")
     o["status"] = st
     return o
@@ -532,7 +542,8 @@ def permute_grad(dxs, src2dst, num_tokens=None, status=None, out=None):
     _vec(src2dst, T * K, "src2dst", torch.int32)
     out = _like(out, (T, H), dtype, dxs.device, "out")
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dxs.device)
-    _check(moe_combine_ex(dxs, ld, dtype, R, src2dst, None, T, num_tokens, K, H, out, st),
+    pd, ps, pn, po, pst = _ptrs(dxs, src2dst, num_tokens, out, st)
+    _check(lib().moe_combine_ex(pd, ld, ELEM[dtype], R, ps, None, T, pn, K, H, po, pst, _stream()),
            "moe_combine_ex")
     return out
 
@@ -553,8 +564,9 @@ def combine_grad(dout, y, src2dst, weights=None, num_tokens=None, status=None, d
     dy = _like(dy, (R, H), dtype, dev, "dy") if need_dy else None
     dw = torch.empty((T, K), dtype=torch.float32, device=dev) if need_dweights else None
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
-    _check(moe_combine_grad(dout, ldd, y, ldy, dtype, R, src2dst, weights, T, num_tokens, K, H, dy,
-                            H, dw, st), "moe_combine_grad")
+    pd, py, ps, pw, pn, pdy, pdw, pst = _ptrs(dout, y, src2dst, weights, num_tokens, dy, dw, st)
+    _check(lib().moe_combine_grad(pd, ldd, py, ldy, ELEM[dtype], R, ps, pw, T, pn, K, H, pdy, H, pdw,
+                                  pst, _stream()), "moe_combine_grad")
     return dict(dy=dy, dweights=dw, status=st)
 
 
@@ -639,9 +651,11 @@ def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=Fal
         p2 = _expert_rows(pre, masked, L, "pre")[0]
         ld_pre = _rows(p2, "pre", (R, Nw), dtype)
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=x.device)
-    _check(moe_expert_matmul(x, ldx, dtype, x_scales, ld_xs, R, K, w, w_scales, ld_ws, L, N, gated,
-                             act, bias, begin, end, cap, res, ld_res, o2, ldo, odt, p2, ld_pre, st),
-           "moe_expert_matmul")
+    px, pxs, pw, pws, pb, p0, p1, pr, po, pp, pst = _ptrs(x, x_scales, w, w_scales, bias, begin, end,
+                                                          res, o2, p2, st)
+    _check(lib().moe_expert_matmul(px, ldx, ELEM[dtype], pxs, ld_xs, R, K, pw, pws, ld_ws, L, N,
+                                   1 if gated else 0, ACT[act], pb, p0, p1, cap, pr, ld_res, po, ldo,
+                                   ELEM[odt], pp, ld_pre, pst, _stream()), "moe_expert_matmul")
     return out
 
 
@@ -750,8 +764,9 @@ def block_norm(x, y=None, w_post=None, gate=None, scale=1.0, w_pre=None, eps=1e-
             r_post = torch.empty(T, dtype=torch.float32, device=dev)
         if w_pre is not None:
             r_pre = torch.empty(T, dtype=torch.float32, device=dev)
-    _check(moe_block_norm(x, ldx, y, ldy, dtype, T, H, w_post, gate, mode, scale, w_pre, eps, xo, h,
-                          r_post, r_pre), "moe_block_norm")
+    px, py, pw, pg, pp, po, ph, pr0, pr1 = _ptrs(x, y, w_post, gate, w_pre, xo, h, r_post, r_pre)
+    _check(lib().moe_block_norm(px, ldx, py, ldy, ELEM[dtype], T, H, pw, pg, GATE[mode], scale, pp,
+                                eps, po, ph, pr0, pr1, _stream()), "moe_block_norm")
     return dict(x=x if y is None else xo, h=h, rstd_post=r_post, rstd_pre=r_pre)
 
 
