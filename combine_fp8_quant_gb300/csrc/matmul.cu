@@ -418,6 +418,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return t;
   };
 
+  auto first_tile = [&] { return pair < total ? tile_at(pair) : Tile{}; };
+  auto next_tile = [&](int w, const Tile& t) { return w + npairs < total ? tile_at(w + npairs) : t; };
+
   // ---- ring geometry: as many stages as the largest row tile allows
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
   const int b_bytes = MODE == kGradW ? min((p.wrows + 127) / 128, 2) * 8192
@@ -443,8 +446,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t empty = empty0, full = full0, raw = raw0, dst = dst0, ph = 1;
       int left = stages, issued = 0;
       bool ok = true;
+      // the next tile is looked up while this one's first blocks are under way
+      // (its divisions and search cost about 600 cycles between tiles)
+      Tile t = first_tile();
       for (int w = pair; w < total && ok; w += npairs) {
-        const Tile t = tile_at(w);
+        Tile nt = t;
         const int half = t.n / 2;
         const int box = MODE == kGradW ? 0 : box_index(half);
         const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
@@ -489,7 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst = dst0;
             ph ^= 1;
           }
+          if (kb == 0) nt = next_tile(w, t);
         }
+        t = t.nkb > 0 ? nt : next_tile(w, t);
       }
       // a wait ran out: let the copies in flight land, again with a limit (they
       // count on the first CTA's barriers, whose CTA stays until the end)
@@ -508,9 +516,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t lo = lo0, bar = bar0, ph = 0;
       int left = stages;
       bool ok = true;
+      Tile t = first_tile();
       for (int w = pair; w < total && ok; w += npairs) {
-        const Tile t = tile_at(w);
-        if (t.nkb == 0) continue;  // kGradW: an expert without rows; the epilogue writes zeros
+        if (t.nkb == 0) {  // kGradW: an expert without rows; the epilogue writes zeros
+          t = next_tile(w, t);
+          continue;
+        }
+        Tile nt = t;
         const int as = acc_it & 1;
         if (!(ok = wait_or_stop(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
         tc_fence_after();
@@ -557,7 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = bar0;
             ph ^= 1;
           }
+          if (kb == 0) nt = next_tile(w, t);
         }
+        t = nt;
         ++acc_it;
       }
       if (!ok) {  // products in flight end before tensor memory is freed
@@ -578,12 +592,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (at + t.nkb - 1) % stages;
         if (!(ok = warp_wait_or_stop(smem_addr(s_raw + s), (phase >> s) & 1, &s_stop))) break;
         phase ^= 1u << s;
-        uint8_t* a = ring + s * stage_bytes;
-        const int boxes = 2 + (t.n / 2 + 63) / 64;
-        for (int i = lane; i < boxes * (64 - t.tail) * 8; i += 32) {
-          const int line = i >> 3, bx = line / (64 - t.tail), r = t.tail + line % (64 - t.tail);
-          *reinterpret_cast<uint4*>(a + bx * 8192 + r * 128 + (i & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        // four lines at a time, eight lanes each
+        uint8_t* a = ring + s * stage_bytes + (t.tail + (lane >> 3)) * 128 + (lane & 7) * 16;
+        const int boxes = 2 + (t.n / 2 + 63) / 64, lines = 64 - t.tail - (lane >> 3);
+        for (int bx = 0; bx < boxes; ++bx, a += 8192)
+          for (int r = 0; r < lines; r += 4) *reinterpret_cast<uint4*>(a + r * 128) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s), leader));
