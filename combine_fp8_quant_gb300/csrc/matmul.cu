@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t* s_tiles = reinterpret_cast<int32_t*>(s_stage + kStageBytes);   // [L + 1]
   int32_t* s_begin = s_tiles + p.L + 1;
   int32_t* s_count = s_begin + p.L;
+  int32_t* s_per = s_count + p.L;  // rows of an expert's tiles
 
   // ---- set-up
   if (tid == 0) {
@@ -368,7 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nb = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += nb;
       }
-      if (e < p.L) s_tiles[e] = base + incl - v;
+      if (e < p.L) {
+        s_tiles[e] = base + incl - v;
+        s_per[e] = v > 0 ? ((s_count[e] + v - 1) / v + 15) / 16 * 16 : 0;  // equal tiles
+      }
       base += __shfl_sync(0xffffffffu, incl, 31);
     }
     if (lane == 0) s_tiles[p.L] = base;
@@ -383,43 +387,65 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int fblk = p.gated && MODE == kForward ? 64 : 128;  // features per block
   const int nfp = (p.feats + 2 * fblk - 1) / (2 * fblk);    // pairs of blocks
   const int nnb = MODE == kGradW ? (p.wrows + 255) / 256 : 0;       // kGradW: row blocks per expert
-  const int total = MODE == kGradW ? p.L * nnb * nfp : s_tiles[p.L] * nfp;
-  auto tile_at = [&](int w) {
-    Tile t;
-    t.fb = (w % nfp) * 2 + rank;
-    const int rb = w / nfp;
+  // the run of the reduction this pair takes: whole scale words (four blocks); the
+  // host gives every run some
+  const int red_blocks = (p.red + kRedBlock - 1) / kRedBlock;
+  const int run_kb0 = red_blocks * split / p.splits & ~3;
+  const int run_nkb = (split + 1 == p.splits ? red_blocks : red_blocks * (split + 1) / p.splits & ~3) - run_kb0;
+  // A role's walk over its pair's tiles: tile w = rb * nfp + fp is followed by
+  // w + npairs. Steps add with carries and the expert only moves forward, so a
+  // step costs about 100 cycles (divisions and a search took 900, between tiles).
+  struct Walk {
+    int rb, fp, e;
+  };
+  const int d_rb = npairs / nfp, d_fp = npairs % nfp;
+  auto settle = [&](Walk& k) {  // kGradW: rb counts within expert e
     if constexpr (MODE == kGradW) {
-      t.e = rb / nnb;
-      t.row0 = (rb - t.e * nnb) * 256;
+      while (k.rb >= nnb) {
+        k.rb -= nnb;
+        ++k.e;
+      }
+    } else {
+      while (k.rb >= s_tiles[k.e + 1]) ++k.e;
+    }
+  };
+  auto more = [&](const Walk& k) { return MODE == kGradW ? k.e < p.L : k.rb < s_tiles[p.L]; };
+  auto first = [&] {
+    Walk k{pair / nfp, pair % nfp, 0};
+    if (MODE == kGradW || more(k)) settle(k);
+    return k;
+  };
+  auto step = [&](Walk& k) {
+    k.rb += d_rb;
+    k.fp += d_fp;
+    if (k.fp >= nfp) {
+      k.fp -= nfp;
+      ++k.rb;
+    }
+    if (MODE == kGradW || more(k)) settle(k);
+  };
+  auto tile_at = [&](const Walk& k) {
+    Tile t;
+    t.e = k.e;
+    t.fb = k.fp * 2 + rank;
+    if constexpr (MODE == kGradW) {
+      t.row0 = k.rb * 256;
       t.rows = min(256, p.wrows - t.row0);
       t.red_row0 = s_begin[t.e];
       t.kb0 = 0;
       t.nkb = (s_count[t.e] + 63) / 64;
       t.tail = s_count[t.e] - (t.nkb - 1) * 64;
     } else {
-      int lo = 0, hi = p.L - 1;  // the last expert whose tiles start at or before rb
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (s_tiles[mid] <= rb) lo = mid; else hi = mid - 1;
-      }
-      t.e = lo;
-      const int cnt = s_count[lo], nt = s_tiles[lo + 1] - s_tiles[lo];
-      const int per = ((cnt + nt - 1) / nt + 15) / 16 * 16;  // equal tiles
-      const int j = rb - s_tiles[lo];
-      t.row0 = s_begin[lo] + j * per;
-      t.rows = min(per, cnt - j * per);
-      // runs of whole scale words (four blocks); the host gives every run some
-      const int all = (p.red + kRedBlock - 1) / kRedBlock;
-      t.kb0 = all * split / p.splits & ~3;
-      t.nkb = (split + 1 == p.splits ? all : all * (split + 1) / p.splits & ~3) - t.kb0;
+      const int per = s_per[t.e], j = k.rb - s_tiles[t.e];
+      t.row0 = s_begin[t.e] + j * per;
+      t.rows = min(per, s_count[t.e] - j * per);
+      t.kb0 = run_kb0;
+      t.nkb = run_nkb;
       t.red_row0 = t.tail = 0;
     }
     t.n = (t.rows + 15) / 16 * 16;
     return t;
   };
-
-  auto first_tile = [&] { return pair < total ? tile_at(pair) : Tile{}; };
-  auto next_tile = [&](int w, const Tile& t) { return w + npairs < total ? tile_at(w + npairs) : t; };
 
   // ---- ring geometry: as many stages as the largest row tile allows
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
@@ -446,11 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t empty = empty0, full = full0, raw = raw0, dst = dst0, ph = 1;
       int left = stages, issued = 0;
       bool ok = true;
-      // the next tile is looked up while this one's first blocks are under way
-      // (its divisions and search cost about 600 cycles between tiles)
-      Tile t = first_tile();
-      for (int w = pair; w < total && ok; w += npairs) {
-        Tile nt = t;
+      for (Walk k = first(); ok && more(k); step(k)) {
+        const Tile t = tile_at(k);
         const int half = t.n / 2;
         const int box = MODE == kGradW ? 0 : box_index(half);
         const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
@@ -495,9 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             dst = dst0;
             ph ^= 1;
           }
-          if (kb == 0) nt = next_tile(w, t);
         }
-        t = t.nkb > 0 ? nt : next_tile(w, t);
       }
       // a wait ran out: let the copies in flight land, again with a limit (they
       // count on the first CTA's barriers, whose CTA stays until the end)
@@ -516,13 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t lo = lo0, bar = bar0, ph = 0;
       int left = stages;
       bool ok = true;
-      Tile t = first_tile();
-      for (int w = pair; w < total && ok; w += npairs) {
-        if (t.nkb == 0) {  // kGradW: an expert without rows; the epilogue writes zeros
-          t = next_tile(w, t);
-          continue;
-        }
-        Tile nt = t;
+      for (Walk k = first(); ok && more(k); step(k)) {
+        const Tile t = tile_at(k);
+        if (t.nkb == 0) continue;  // kGradW: an expert without rows; the epilogue writes zeros
         const int as = acc_it & 1;
         if (!(ok = wait_or_stop(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
         tc_fence_after();
@@ -569,9 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = bar0;
             ph ^= 1;
           }
-          if (kb == 0) nt = next_tile(w, t);
         }
-        t = nt;
         ++acc_it;
       }
       if (!ok) {  // products in flight end before tensor memory is freed
@@ -586,8 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int at = 0;          // stage of the tile's first block
     uint32_t phase = 0;  // bit s: parity of the next wait on s_raw[s]
     bool ok = true;
-    for (int w = pair; w < total && ok; w += npairs) {
-      const Tile t = tile_at(w);
+    for (Walk k = first(); ok && more(k); step(k)) {
+      const Tile t = tile_at(k);
       if (t.nkb > 0 && t.tail < 64) {
         const int s = (at + t.nkb - 1) % stages;
         if (!(ok = warp_wait_or_stop(smem_addr(s_raw + s), (phase >> s) & 1, &s_stop))) break;
@@ -616,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int sf_it = 0;
     bool ok = true;
     const int fstep = p.gated ? 16 : 32;
-    for (int w = pair; w < total && ok; w += npairs) {
-      const Tile t = tile_at(w);
+    for (Walk k = first(); ok && more(k); step(k)) {
+      const Tile t = tile_at(k);
       const int f = p.gated ? t.fb * 64 + (lane & 15) : t.fb * 128 + lane;  // this lane's first feature
       const uint32_t* la = p.ws + (int64_t)t.e * p.wrows + (p.gated && (lane & 16) ? p.feats : 0) + f;
       const uint32_t* lb =
@@ -644,8 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int sf_it = 0;
-      for (int w = pair; w < total && ok; w += npairs) {
-        const int words = (tile_at(w).nkb + 3) / 4;
+      for (Walk k = first(); ok && more(k); step(k)) {
+        const int words = (run_nkb + 3) / 4;
         for (int i = 0; i < words; ++i, ++sf_it) {
           const int sb = sf_it % kScaleBufs;
           if (!(ok = wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
@@ -660,8 +675,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool f16 = p.f16 != 0;
     const Rows16 out = rows16(p.out, p.ldo), pre = rows16(p.pre, p.ld_pre), res = rows16(p.residual, p.ld_res);
     int acc_it = 0;
-    for (int w = pair; w < total; w += npairs) {
-      const Tile t = tile_at(w);
+    for (Walk k = first(); more(k); step(k)) {
+      const Tile t = tile_at(k);
       const int as = acc_it & 1;
       if (t.nkb > 0) {
         if (!warp_wait_or_stop(smem_addr(s_tfull + as), (acc_it >> 1) & 1, &s_stop)) break;
@@ -855,7 +870,7 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerBlockOptin, &optin);
   if (err != cudaSuccess) return err;
   const size_t smem = (size_t)optin - 1024;  // room for the static arrays
-  const size_t lists = (size_t)(3 * a.L + 1) * sizeof(int32_t) + kStageBytes + (FP8 ? kScaleBufs * kScaleBytes : 0);
+  const size_t lists = (size_t)(4 * a.L + 1) * sizeof(int32_t) + kStageBytes + (FP8 ? kScaleBufs * kScaleBytes : 0);
   a.ring_bytes = (int32_t)((smem - 1024 - lists) / 1024 * 1024);
   err = opt_in_smem(matmul_kernel<MODE, FP8>, smem);
   if (err != cudaSuccess) return err;
