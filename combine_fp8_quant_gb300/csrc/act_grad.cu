@@ -12,7 +12,9 @@
 // splits > 1 the partial sums go to the workspace and a second launch adds them
 // in a fixed order. dP is rounded to the rows' 16-bit type because the two
 // products that follow take 16-bit operands. Bound by HBM (reads dout and P,
-// writes dP). Without an activation dP = dout and only the sums are formed.
+// writes dP): 16382 rows of 1408 gated features, 230 MB in 40 us, 5.8 TB/s (52 us
+// with loads straight to registers). Without an activation dP = dout and only the
+// sums are formed.
 #include "common.cuh"
 #include "elem.cuh"
 #include "kernels.h"

@@ -216,6 +216,8 @@ moe_status_t moe_expert_matmul(const void* x, int64_t ldx, moe_elem_t type, cons
   if (R == 0) return MOE_OK;
   if (!rows_ok(x, ldx, K, es) || !out || ldo < N || (residual && ld_res < N) || (pre && ld_pre < Nw))
     return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(out, 2) || !aligned_to(residual, 2) || !aligned_to(pre, 2) || !aligned_to(bias, 4))
+    return MOE_ERR_INVALID_ARG;
   if (fp8 && (!x_scales || !aligned16(x_scales) || ld_xs < (cap > 0 ? cap : R) || ld_xs % 4))
     return MOE_ERR_INVALID_ARG;
   const int sms = num_sms_cached();
@@ -262,6 +264,8 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
   if (has_act && !rows_ok(pre, ld_pre, Nw, 2)) return MOE_ERR_INVALID_ARG;
   if (dw && !rows_ok(x, ldx, K, 2)) return MOE_ERR_INVALID_ARG;
   if (dx && (!w || !aligned16(w) || ld_dx < K)) return MOE_ERR_INVALID_ARG;
+  if (!aligned_to(dx, 2) || !aligned_to(dw, dw_type == MOE_F32 ? 4 : 2) || !aligned_to(dbias, 4))
+    return MOE_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) ||
       workspace_bytes < moe_expert_matmul_grad_workspace_bytes(R, L, Nw))
     return MOE_ERR_INVALID_ARG;

@@ -19,6 +19,9 @@ constexpr size_t kWsHeader = 256;  // reserved header before the chunk table
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// (NULL is aligned: whether it is allowed is another check)
+inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % (unsigned)n == 0; }
+
 inline int num_sms_cached() {
   int n = 0;
   return device_attr_cached(cudaDevAttrMultiProcessorCount, &n) == cudaSuccess ? n : 0;

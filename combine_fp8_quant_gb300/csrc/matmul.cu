@@ -38,6 +38,14 @@
 // over distributed shared memory) and adds them in a fixed order; every cluster
 // then has one tile at most, so nothing has to be handed back.
 //
+// Measured on GB300 (2 x features counted for gated weights): bf16, 16 experts,
+// 16382 rows, 2048 x 2816, P kept: 124 us, 1520 TFLOP/s; its dx 110 us (1710), dW
+// 115 us (1640); e4m3, 64 experts, 32768 rows, 7168 x 4096: 664 us (2900 TFLOP/s)
+// a single pass, 767 us at the 1400 W power limit (1470 MHz) pass after pass; e4m3
+// decode, 32 experts with 4 rows each, 7168 x 4096: 140 us, 6.6 TB/s of weights.
+// Large products are bound by the tensor cores and the shared-memory port (a tile
+// of 176 rows moves 55 KB per 352 cycles of products), decode by HBM.
+//
 // Rows outside every segment are read at most as columns that are not stored.
 // In kGradW rows are the reduction: lines of the last block past the segment's
 // end are zeroed in shared memory before the product, so padding rows may hold

@@ -479,6 +479,7 @@ def _elem(t, allowed, name):
 
 
 FLOATS = (torch.bfloat16, torch.float16, torch.float32)
+E4M3_BYTES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def combine(y, src2dst, weights=None, num_tokens=None, status=None, out=None):
@@ -615,10 +616,10 @@ def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=Fal
     quant_group(w.view(-1, K)) (w_scales, ld_ws) and an output of out_dtype. act:
     none, relu, silu or gelu. `pre` receives P for expert_matmul_grad. Rows of
     no expert are not written. Returns out."""
-    fp8 = x.element_size() == 1
+    fp8 = x.dtype in E4M3_BYTES
     dtype = torch.float8_e4m3fn if fp8 else _elem(x, FLOATS[:2], "x")
     L, N, K = _expert_weights(w, gated)
-    if w.element_size() != x.element_size() or (not fp8 and w.dtype != dtype):
+    if w.dtype != dtype and not (fp8 and w.dtype in E4M3_BYTES):
         raise ValueError(f"moeperm: w must have the type of x ({dtype}), not {w.dtype}")
     if fp8 and (x_scales is None or w_scales is None):
         raise ValueError("moeperm: e4m3 rows and weights need x_scales and w_scales")

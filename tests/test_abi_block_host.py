@@ -112,7 +112,8 @@ E4M3 = dict(dtype=E4, x_scales=FAKE, ld_xs=1024, w_scales=FAKE, ld_ws=2048)
     dict(K=508), dict(N=0), dict(N=248), dict(gated=False, N=252), dict(N=1 << 29), dict(seg_begin=None), dict(seg_end=None),
     dict(seg_begin=None, seg_end=None), dict(cap=256), dict(seg_begin=None, cap=100), dict(cap=-1), dict(x=None), dict(x=ODD),
     dict(ldx=500), dict(ldx=516), dict(w=None), dict(w=ODD), dict(out=None), dict(ldo=200), dict(residual=FAKE, ld_res=100),
-    dict(pre=FAKE, ld_pre=256),
+    dict(pre=FAKE, ld_pre=256), dict(out=FAKE + 1), dict(residual=FAKE + 1, ld_res=256), dict(pre=FAKE + 1, ld_pre=512),
+    dict(bias=FAKE + 2),
     dict(E4M3, K=576, ldx=576), dict(E4M3, x_scales=None), dict(E4M3, w_scales=None), dict(E4M3, ld_xs=1000), dict(E4M3, ld_xs=1026),
     dict(E4M3, ld_ws=2044), dict(E4M3, ld_ws=2050), dict(E4M3, pre=FAKE, ld_pre=512), dict(E4M3, out_dtype=F32), dict(E4M3, ldx=520),
 ])
@@ -129,7 +130,7 @@ GRAD = dict(dout=FAKE, ldd=256, x=FAKE, ldx=512, dtype=BF, R=1024, K=512, w=FAKE
     dict(dtype=E4), dict(dtype=F32), dict(R=-1), dict(L=0), dict(K=508), dict(N=250), dict(dx=None, dw=None, dbias=None),
     dict(dw_dtype=FH), dict(dw_dtype=E4), dict(dout=None), dict(dout=ODD), dict(ldd=200), dict(ldd=260), dict(pre=None),
     dict(ld_pre=256), dict(x=None), dict(ldx=500), dict(w=None), dict(ld_dx=500), dict(workspace=None), dict(workspace_bytes=1000),
-    dict(seg_begin=None), dict(cap=256),
+    dict(seg_begin=None), dict(cap=256), dict(dx=FAKE + 1), dict(dw=FAKE + 1), dict(dw=FAKE + 2, dw_dtype=F32), dict(dbias=FAKE + 2),
 ])
 def test_expert_matmul_grad_refuses(mp, over):
     assert call(mp, "moe_expert_matmul_grad", GRAD, over) == mp.MOE_ERR_INVALID_ARG
@@ -156,6 +157,7 @@ def test_the_binding_refuses(mp):
         lambda: mp.expert_matmul(x, w, seg, seg, act="tanh"),
         lambda: mp.expert_matmul(x, w.half(), seg, seg),
         lambda: mp.expert_matmul(x.float(), w.float(), seg, seg),
+        lambda: mp.expert_matmul(x.to(torch.int8), w.to(torch.int8), seg, seg),
         lambda: mp.expert_matmul(x[:, :32], w, seg, seg),
         lambda: mp.expert_matmul(x.t(), w, seg, seg),
         lambda: mp.expert_matmul(x, w, seg, seg, bias=torch.zeros(2, 31)),

@@ -221,6 +221,30 @@ def test_forward_on_a_dispatch(dev):
     assert torch.equal(a, b) and torch.isfinite(a.float()).all() and (a != 0).any()
 
 
+def test_offsets_past_32_bits(dev):
+    """Rows whose element offsets pass 2^31 (2.6e9 elements of output, of the gradient and of sorted rows)."""
+    R, K, N = 640_000, 64, 4096
+    x, w = rand(1, R, K, dtype=torch.bfloat16), rand(2, N, K, dtype=torch.bfloat16, gain=0.125)
+    out = dev.expert_matmul(x, w)
+    dx = dev.expert_matmul_grad(out, x, w, need=("dx",))["dx"]
+    for lo in (0, 524_288 - 8, R - 16):       # the first rows, around element 2^31, the last rows
+        sl = slice(lo, lo + 16)
+        want = x[sl].double() @ w.double().t()
+        err = (K + 2) * V * (x[sl].double().abs() @ w.double().abs().t())
+        assert ((out[sl].double() - want).abs() <= 2.0 ** -8 * want.abs() + err * 1.01).all()
+        want, mag = out[sl].double() @ w.double(), out[sl].double().abs() @ w.double().abs()
+        assert ((dx[sl].double() - want).abs() <= 2.0 ** -8 * want.abs() + (N + 2) * V * mag).all()
+    del out, dx
+    T, H, k = 40_000, 8192, 8
+    x = rand(3, T, H, dtype=torch.bfloat16)
+    ids = torch.arange(T * k, device=DEV, dtype=torch.int32).reshape(T, k) % k
+    p = dev.permute(x, ids, torch.ones(T, k, device=DEV), k, k, block_e=1)
+    for t in (0, 20_000, T - 1):
+        assert all(torch.equal(p["xs"][r], x[t]) for r in p["src2dst"][t].tolist())
+    back = dev.permute_grad(p["xs"], p["src2dst"])
+    assert torch.equal(back, (x.float() * k).bfloat16())
+
+
 @pytest.mark.parametrize("begin,end", [([0, 10], [4, 21]), ([-1, 4], [3, 8]), ([0, 6], [4, 5])])
 def test_bad_segments_are_flagged(dev, begin, end):
     """A segment outside the rows counts as empty and is flagged; the others are computed."""
