@@ -553,39 +553,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + as * kTileRows;
         const uint32_t idesc = FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
-        for (int kb = 0; kb < t.nkb; ++kb) {
-          if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
-          if constexpr (FP8) {
-            if ((kb & 3) == 0 &&
-                !(ok = wait_or_stop(smem_addr(s_sfull + sf_it % kScaleBufs), (sf_it / kScaleBufs) & 1, &s_stop)))
-              break;
-          }
-          tc_fence_after();
-          if constexpr (FP8) {
-            const uint32_t sfa = tmem + kScaleCols + 12 * (sf_it & 1), sfb = sfa + 4;
-            if ((kb & 3) == 0) {
-              const uint32_t sm = desc_lo(smem_addr(s_scale + sf_it % kScaleBufs * kScaleBytes), 0);
-              tmem_copy_scales(sfa, sm);
-              tmem_copy_scales(sfb, sm + (512 >> 4));
-              if (t.n > 128) tmem_copy_scales(sfb + 4, sm + (1024 >> 4));
-            }
-            const uint32_t a = lo, b = lo + (kABytes >> 4);
-            const uint32_t id = idesc + ((uint32_t)(kb & 3) * ((1u << 4) | (1u << 29)));
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, id, sfa, sfb, kb + k);
-            if ((kb & 3) == 3 || kb == t.nkb - 1) {
-              mma_commit_pair(smem_addr(s_sempty + sf_it % kScaleBufs), both);
-              ++sf_it;
-            }
-          } else {
-            constexpr int ka = MODE == kForward ? 2 : 128, kb_step = MODE == kGradW ? 128 : 2;
-            constexpr uint32_t a_atom = MODE == kForward ? 0 : 8192, b_atom = MODE == kGradW ? 8192 : 0;
-            const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb + k);
-          }
+        auto advance = [&] {  // hand the stage back and move on to the next
           mma_commit_pair(bar + kEmptyOffset, both);
-          if (kb == t.nkb - 1) mma_commit_pair(smem_addr(s_tfull + as), both);
           lo += stage_bytes >> 4;
           bar += 8;
           if (--left == 0) {
@@ -594,7 +563,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             bar = bar0;
             ph ^= 1;
           }
+        };
+        if constexpr (FP8) {
+          // four blocks share a scale word, each its own byte of it
+          for (int kb = 0; kb < t.nkb && ok; kb += 4, ++sf_it) {
+            const int sb = sf_it % kScaleBufs;
+            if (!(ok = wait_or_stop(smem_addr(s_sfull + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
+            const uint32_t sfa = tmem + kScaleCols + 12 * (sf_it & 1), sfb = sfa + 4;
+            const uint32_t sm = desc_lo(smem_addr(s_scale + sb * kScaleBytes), 0);
+            tmem_copy_scales(sfa, sm);
+            tmem_copy_scales(sfb, sm + (512 >> 4));
+            if (t.n > 128) tmem_copy_scales(sfb + 4, sm + (1024 >> 4));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (kb + j >= t.nkb || !ok) break;
+              if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_e4m3(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc + j * ((1u << 4) | (1u << 29)), sfa, sfb,
+                         kb + j + k);
+              advance();
+            }
+            mma_commit_pair(smem_addr(s_sempty + sb), both);
+          }
+        } else {
+          constexpr int ka = MODE == kForward ? 2 : 128, kb_step = MODE == kGradW ? 128 : 2;
+          constexpr uint32_t a_atom = MODE == kForward ? 0 : 8192, b_atom = MODE == kGradW ? 8192 : 0;
+          for (int kb = 0; kb < t.nkb; ++kb) {
+            if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
+            const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb + k);
+            advance();
+          }
         }
+        mma_commit_pair(smem_addr(s_tfull + as), both);
         ++acc_it;
       }
       if (!ok) {  // products in flight end before tensor memory is freed
