@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int k = 0; k < 4; ++k)
                 mma_e4m3(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc + j * ((1u << 4) | (1u << 29)), sfa, sfb,
-                         kb + j + k);
+                         j + k > 0 ? 1u : (uint32_t)kb);
               advance();
             }
             mma_commit_pair(smem_addr(s_sempty + sb), both);
@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
             const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, kb + k);
+            for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, k > 0 ? 1u : (uint32_t)kb);
             advance();
           }
         }
