@@ -40,7 +40,9 @@ bool feats_ok(int32_t N, int32_t L, int32_t gated) {
   return (int64_t)L * N * (gated ? 2 : 1) < (int64_t(1) << 31);
 }
 
-size_t dpre_bytes(int64_t R, int32_t Nw) { return ((size_t)R * Nw * 2 + 255) / 256 * 256; }
+size_t dpre_bytes(int64_t R, int32_t L, int32_t Nw) {
+  return ((size_t)grad_terms(R, L) * R * Nw * 2 + 255) / 256 * 256;
+}
 
 }  // namespace
 
@@ -223,7 +225,7 @@ moe_status_t moe_expert_matmul(const void* x, int64_t ldx, moe_elem_t type, cons
   const int sms = num_sms_cached();
   if (sms <= 0) return MOE_ERR_CUDA;
   MatmulArgs m{};
-  m.x = x; m.ldx = ldx; m.w = w; m.R = R; m.K = K; m.L = L; m.N = N; m.type = (int)type;
+  m.x = x; m.ldx = ldx; m.terms = 1; m.w = w; m.R = R; m.K = K; m.L = L; m.N = N; m.type = (int)type;
   m.out_type = (int)out_type; m.gated = gated; m.act = (int)act; m.seg_begin = seg_begin;
   m.seg_end = seg_end; m.cap = cap; m.bias = bias; m.residual = residual; m.ld_res = ld_res;
   m.out = out; m.ldo = ldo; m.pre = pre; m.ld_pre = ld_pre;
@@ -236,7 +238,7 @@ size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw) 
   if (R < 0 || L < 1 || Nw < 1) return 0;
   // the split count depends on N; a gated N is half of Nw and gives the larger one
   const int splits = act_grad_splits(R, L, Nw < 2 ? 1 : Nw / 2);
-  return dpre_bytes(R, Nw) + (splits > 1 ? (size_t)splits * L * Nw * sizeof(float) : 0);
+  return dpre_bytes(R, L, Nw) + (splits > 1 ? (size_t)splits * L * Nw * sizeof(float) : 0);
 }
 
 moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x, int64_t ldx,
@@ -276,16 +278,18 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     a.dout = dout; a.ldd = ldd; a.pre = pre; a.ld_pre = ld_pre; a.R = R; a.L = L; a.N = N; a.gated = gated;
     a.act = (int)act; a.seg_begin = seg_begin; a.seg_end = seg_end; a.cap = cap;
     a.dpre = has_act ? workspace : nullptr;
+    a.terms = grad_terms(R, L);
     a.dbias = dbias;
-    a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, Nw));
+    a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, L, Nw));
     a.splits = act_grad_splits(R, L, N);
     a.status = d_status;
     if (launch_act_grad(a, (int)type, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
   MatmulArgs m{};
-  m.x = x; m.ldx = ldx; m.g = has_act ? workspace : dout; m.ldg = has_act ? Nw : ldd; m.w = w; m.R = R;
-  m.K = K; m.L = L; m.N = N; m.type = (int)type; m.gated = gated; m.seg_begin = seg_begin;
-  m.seg_end = seg_end; m.cap = cap; m.status = d_status;
+  m.x = x; m.ldx = ldx; m.g = has_act ? workspace : dout; m.ldg = has_act ? Nw : ldd;
+  m.terms = has_act ? grad_terms(R, L) : 1;
+  m.w = w; m.R = R; m.K = K; m.L = L; m.N = N; m.type = (int)type; m.gated = gated;
+  m.seg_begin = seg_begin; m.seg_end = seg_end; m.cap = cap; m.status = d_status;
   if (dx) {
     m.out = dx; m.ldo = ld_dx; m.out_type = (int)type;
     if (launch_matmul_grad_x(m, sms, s) != cudaSuccess) return MOE_ERR_CUDA;

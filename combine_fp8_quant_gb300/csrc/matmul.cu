@@ -46,6 +46,11 @@
 // Large products are bound by the tensor cores and the shared-memory port (a tile
 // of 176 rows moves 55 KB per 352 cycles of products), decode by HBM.
 //
+// The gradient of the pre-activations enters both backward products in 16 bits. With
+// few rows it comes as two terms, its rounding and what that left over (`terms` = 2):
+// both are multiplied against the same staged weights (or rows), at next to no cost
+// where moving those is the bound.
+//
 // Rows outside every segment are read at most as columns that are not stored.
 // In kGradW rows are the reduction: lines of the last block past the segment's
 // end are zeroed in shared memory before the product, so padding rows may hold
@@ -98,6 +103,7 @@ struct Args {
   int32_t wrows;             // weight rows per expert (kGradW: output rows)
   int32_t gated, act, f16, out_f32;
   int32_t splits;            // pairs per cluster, each with a run of the reduction
+  int32_t terms;             // 2: the row operand is a sum of two tensors, R rows apart
   int32_t ring_bytes;
   const float* bias;         // [L, wrows]
   const void* residual;
@@ -459,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
   const int b_bytes = MODE == kGradW ? min((p.wrows + 127) / 128, 2) * 8192
                                      : box_rows(box_index(max_n / 2)) * 128;
-  const int stage_bytes = kABytes + b_bytes;
+  const int stage_bytes = kABytes + p.terms * b_bytes;
   const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
   const uint32_t ring_s = smem_addr(ring);
 
@@ -485,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = t.n / 2;
         const int box = MODE == kGradW ? 0 : box_index(half);
         const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
-        const uint32_t b_tile = MODE == kGradW ? nbox * 8192 : box_rows(box) * 128;
+        const uint32_t b_tile = p.terms * (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
         const CUtensorMap* mb = &maps.b[box];
         const int f = t.fb * 128, brow = t.row0 + rank * half;
         int red = t.kb0 * kRedBlock;
@@ -508,10 +514,16 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(dst, &maps.a, bar, f, t.red_row0 + red);
               tma_load_2d(dst + 8192, &maps.a, bar, f + 64, t.red_row0 + red);
             }
-          } else if constexpr (MODE == kGradW) {
-            for (int i = 0; i < nbox; ++i) tma_load_2d(dst + i * 8192, mb, bar, brow + i * 64, t.red_row0 + red);
           } else {
-            tma_load_2d(dst, mb, bar, red, brow);
+            for (int term = 0; term < p.terms; ++term) {
+              const uint32_t to = dst + term * b_bytes;
+              if constexpr (MODE == kGradW) {
+                for (int i = 0; i < nbox; ++i)
+                  tma_load_2d(to + i * 8192, mb, bar, brow + i * 64, t.red_row0 + red + term * p.R);
+              } else {
+                tma_load_2d(to, mb, bar, red, brow + term * p.R);
+              }
+            }
           }
           ++issued;
           dst += stage_bytes;
@@ -594,6 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, k > 0 ? 1u : (uint32_t)kb);
+            if (MODE != kForward && p.terms > 1) {
+              const uint32_t b2 = b + (b_bytes >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b2 + kb_step * k, idesc, 1u);
+            }
             advance();
           }
         }
@@ -620,9 +637,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         phase ^= 1u << s;
         // four lines at a time, eight lanes each
         uint8_t* a = ring + s * stage_bytes + (t.tail + (lane >> 3)) * 128 + (lane & 7) * 16;
-        const int boxes = 2 + (t.n / 2 + 63) / 64, lines = 64 - t.tail - (lane >> 3);
-        for (int bx = 0; bx < boxes; ++bx, a += 8192)
-          for (int r = 0; r < lines; r += 4) *reinterpret_cast<uint4*>(a + r * 128) = make_uint4(0, 0, 0, 0);
+        const int lines = 64 - t.tail - (lane >> 3), nbox = (t.n / 2 + 63) / 64;
+        auto clear = [&](uint8_t* box, int boxes) {
+          for (int bx = 0; bx < boxes; ++bx, box += 8192)
+            for (int r = 0; r < lines; r += 4) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
+        };
+        clear(a, 2);
+        for (int term = 0; term < p.terms; ++term) clear(a + kABytes + term * b_bytes, nbox);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s), leader));
@@ -921,6 +942,7 @@ Args common_args(const MatmulArgs& m) {
   Args a{};
   a.seg_begin = m.seg_begin; a.seg_end = m.seg_end; a.cap = m.cap;
   a.R = (int32_t)m.R; a.L = m.L; a.f16 = m.type == kF16 || (m.type == kE4M3 && m.out_type == kF16);
+  a.terms = m.terms;
   a.status = m.status;
   return a;
 }
@@ -978,7 +1000,7 @@ cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t 
   const cuuint64_t strides[2] = {row, row * a.wrows};
   const cuuint32_t box[3] = {64, 64, 1};
   bool ok = make_map(&maps.a, m.type, m.w, 3, dims, strides, box);
-  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.R, m.ldg, 64, box_rows(i));
+  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.terms * m.R, m.ldg, 64, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
   return launch<kGradX, false>(maps, a, max_row_tiles(m, kRows<false>) * nfp, num_sms, s);
 }
@@ -992,7 +1014,7 @@ cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t 
   const int nfp = (m.K + 255) / 256;
   Maps maps;
   bool ok = map_2d(&maps.a, m.type, m.x, m.K, m.R, m.ldx, 64, 64);
-  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.R, m.ldg, 64, 64);
+  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.terms * m.R, m.ldg, 64, 64);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)m.L * ((a.wrows + 255) / 256) * nfp;
   return launch<kGradW, false>(maps, a, tiles, num_sms, s);

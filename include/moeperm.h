@@ -425,7 +425,7 @@ moe_status_t moe_expert_matmul(
     moe_stream_t stream);
 
 /* Bytes of device workspace moe_expert_matmul_grad needs for R rows, L experts
- * and Nw = N (gated: 2N) weight rows: the gradient of P in 16 bits and partial
+ * and Nw = N (gated: 2N) weight rows: the gradient of P (16 bits a term) and partial
  * sums of the bias gradient. No initialisation; not to be used by two calls
  * that can run at once. 0 for negative or zero sizes (R = 0 is allowed). */
 size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
@@ -433,7 +433,8 @@ size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
 /*
  * moe_expert_matmul_grad -- gradients of moe_expert_matmul for the output gradient
  * dout (the residual's gradient is dout itself). With dP the gradient of P,
- * formed in fp32 from dout and the kept P and rounded once to `type`:
+ * formed in fp32 from dout and the kept P and rounded to `type` for the products
+ * (while R <= 128 L, together with the rounding of what that left over):
  *   dx[r]  = sum_n dP[r, n] * w[e, n]        rows of no expert are not written
  *   dw[e]  = sum over the rows of e of dP[r]^T x[r]     (written in full: 0 without rows)
  *   dbias[e] = sum over the rows of e of dP[r]   (f32, written in full)

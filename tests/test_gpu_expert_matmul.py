@@ -314,6 +314,33 @@ def test_gradients(dev, shape, act, gated, dtype):
         assert torch.equal(o[k], again[k]), k
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts,align,K,N", [([1], 1, 64, 64), ([3, 0, 40, 128], 8, 512, 128), ([70] * 9, 1, 136, 320)])
+def test_few_rows_keep_the_gradients_rounding(dev, counts, align, K, N, dtype):
+    """While R <= 128 L the rounding of the pre-activations' gradient is carried along: what is lost of it is its
+    second rounding (half a step squared), so dx and dw are off by little more than their own rounding."""
+    starts, ends, R = segments(counts, align)
+    assert R <= 128 * len(counts)
+    x, dout = rand(1, R, K, dtype=dtype), rand(2, R, N, dtype=dtype)
+    w, pre = rand(3, len(counts), 2 * N, K, dtype=dtype, gain=K ** -0.5), rand(4, R, 2 * N, dtype=dtype)
+    o = dev.expert_matmul_grad(dout, x, w, i32(starts), i32(ends), pre=pre, act="silu", gated=True,
+                               dx=torch.zeros_like(x))
+    hs = torch.finfo(dtype).eps / 2
+    for e, (lo, hi) in enumerate(zip(starts, ends)):
+        if hi <= lo:
+            continue
+        g, p = dout[lo:hi].double(), pre[lo:hi].double()
+        a, d = phi("silu", p[:, :N])
+        dP = torch.cat([g * d * p[:, N:], g * a], 1)
+        m = torch.cat([(g * p[:, N:]).abs() * 1.13, (g * p[:, :N]).abs()], 1)
+        err = ACT_ERR * m + hs * hs * dP.abs() + TINY
+        for got, A, B, eA, steps in ((o["dx"][lo:hi], dP, w[e].double(), err, 4 * N),
+                                     (o["dw"][e], dP.t(), x[lo:hi].double(), err.t(), 2 * (hi - lo))):
+            want, mag = A @ B, A.abs() @ B.abs()
+            bound = eA @ B.abs() + (steps + 2) * V * (mag + eA @ B.abs())
+            assert ((got.double() - want).abs() <= hs * want.abs() + bound * (1 + hs) + TINY).all()
+
+
 def test_gradients_of_slabs_equal_those_of_segments(dev):
     L, cap, K, N = 5, 48, 128, 64
     m = [0, 48, 17, 1, 30]
