@@ -726,35 +726,41 @@ class NormWorkspace:
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
 
 
-def _gate_mode(gate, T, H, name="gate"):
-    """none / channel / token by the gate's shape: [H] or [1, H] is per channel, [T] or
-    [T, 1] per token (a 1-D gate of T = H elements is per channel)."""
+def _gate_mode(gate, T, H, mode=None, name="gate"):
+    """none / channel / token: [H] or [1, H] is per channel, [T] or [T, 1] per token. A
+    1-D gate with T = H fits both: the caller has to name its mode, since a guess
+    would change a gate's meaning with the number of tokens in a batch."""
+    if mode not in (None, "channel", "token") and not (mode == "none" and gate is None):
+        raise ValueError(f"moeperm: gate_mode must be 'channel' or 'token', not {mode!r}")
     if gate is None:
         return "none"
-    shape = gate.shape
-    if shape == (H,) or shape == (1, H):
-        mode, n = "channel", H
-    elif shape == (T,) or shape == (T, 1):
-        mode, n = "token", T
-    else:
-        raise ValueError(f"moeperm: {name} must have shape [{H}] or [{T}], not {tuple(shape)}")
-    _vec(gate, n, name)
-    return mode
+    shape = tuple(gate.shape)
+    fits = [m for m, shapes in (("channel", ((H,), (1, H))), ("token", ((T,), (T, 1)))) if shape in shapes]
+    if mode is not None:
+        fits = [m for m in fits if m == mode]
+    if not fits:
+        want = {"channel": f"[{H}]", "token": f"[{T}]", None: f"[{H}] or [{T}]"}[mode]
+        raise ValueError(f"moeperm: {name} must have shape {want}, not {shape}")
+    if len(fits) > 1:
+        raise ValueError(f"moeperm: {name} {shape} fits both a gate per channel and one per token: name gate_mode")
+    _vec(gate, gate.numel(), name)
+    return fits[0]
 
 
 def block_norm(x, y=None, w_post=None, gate=None, scale=1.0, w_pre=None, eps=1e-6,
-               save_rstd=False):
+               save_rstd=False, gate_mode=None):
     """The step between two blocks: x' = x + scale * gate * (rms(y) * w_post) and
     h = rms(x') * w_pre, rms(v) = v / sqrt(mean(v^2) + eps). y: the last block's
     output (None: x' = x); w_post None: y is added unnormalised; w_pre None: no
-    h. gate [H] or [T]. Returns a dict: x (x'), h, and with save_rstd rstd_post
-    and rstd_pre for block_norm_grad."""
+    h. gate [H] (per channel) or [T] (per token); gate_mode "channel" or "token"
+    says which, and has to where T can equal H. Returns a dict: x (x'), h, and
+    with save_rstd rstd_post and rstd_pre for block_norm_grad."""
     dtype = _elem(x, FLOATS, "x")
     ldx = _rows(x, "x")
     T, H = x.shape
     dev = x.device
     ldy = _rows(y, "y", (T, H), dtype) if y is not None else 0
-    mode = _gate_mode(gate, T, H)
+    mode = _gate_mode(gate, T, H, gate_mode)
     _vec(w_post, H, "w_post")
     _vec(w_pre, H, "w_pre")
     xo = torch.empty((T, H), dtype=dtype, device=dev) if y is not None else None
@@ -772,7 +778,7 @@ def block_norm(x, y=None, w_post=None, gate=None, scale=1.0, w_pre=None, eps=1e-
 
 
 def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0, w_pre=None,
-                    rstd_pre=None, rstd_post=None, workspace=None):
+                    rstd_pre=None, rstd_post=None, workspace=None, gate_mode=None):
     """Gradients of block_norm for dx_out (None: zeros) and dh. x_out is the stream
     after the sum (x itself without y), the rstds are the forward call's. Returns
     a dict: dx, dy, dw_post, dgate, dw_pre (None where there is none)."""
@@ -782,7 +788,7 @@ def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0
     dev = x_out.device
     ld = lambda t, name: _rows(t, name, (T, H), dtype) if t is not None else 0
     ldo, ldh, ldy = ld(dx_out, "dx_out"), ld(dh, "dh"), ld(y, "y")
-    mode = _gate_mode(gate, T, H)
+    mode = _gate_mode(gate, T, H, gate_mode)
     _vec(w_post, H, "w_post")
     _vec(w_pre, H, "w_pre")
     _vec(rstd_pre, T, "rstd_pre")

@@ -85,7 +85,7 @@ class Serving:
         y = mp.expert_matmul(q["xq"], self.down, x_scales=q["scales"], ld_xs=q["ld_s"], w_scales=self.down_sc,
                              ld_ws=self.down_ld, **seg)
         out = mp.combine(y, d["src2dst"], tw, status=d["status"])
-        return mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, scale=w.scale)["x"]
+        return mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, gate_mode="channel", scale=w.scale)["x"]
 
 
 def forward(x, w: Weights, top_k):
@@ -100,7 +100,7 @@ def forward(x, w: Weights, top_k):
     a = mp.expert_matmul(p["xs"], w.up, bias=w.up_bias, act="silu", gated=True, pre=P, **seg)
     y = mp.expert_matmul(a, w.down, **seg)
     out = mp.combine(y, p["src2dst"], tw, status=p["status"])
-    post = mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, scale=w.scale, save_rstd=True)
+    post = mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, gate_mode="channel", scale=w.scale, save_rstd=True)
     saved = dict(x=x, h=h, ids=ids, tw=tw, xs=p["xs"], P=P, a=a, y=y, out=out, seg=seg, src2dst=p["src2dst"],
                  x_out=post["x"], rstd_in=pre_norm["rstd_pre"], rstd_out=post["rstd_post"])
     return post["x"], saved
@@ -108,8 +108,8 @@ def forward(x, w: Weights, top_k):
 
 def backward(dx_out, s, w: Weights):
     """Gradients of every parameter and of x for the gradient of x'."""
-    post = mp.block_norm_grad(dx_out, None, s["x_out"], s["out"], w_post=w.w_out, gate=w.gate, scale=w.scale,
-                              rstd_post=s["rstd_out"])
+    post = mp.block_norm_grad(dx_out, None, s["x_out"], s["out"], w_post=w.w_out, gate=w.gate,
+                              gate_mode="channel", scale=w.scale, rstd_post=s["rstd_out"])
     st = s["seg"]["status"]
     c = mp.combine_grad(post["dy"], s["y"], s["src2dst"], s["tw"], status=st)
     down = mp.expert_matmul_grad(c["dy"], s["a"], w.down, need=("dx", "dw"), **s["seg"])

@@ -181,3 +181,19 @@ def test_the_binding_refuses(mp):
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i} was accepted")
+
+
+def test_a_gate_that_fits_both_kinds_is_named(mp):
+    x, g = torch.zeros(8, 8), torch.ones(8)
+    for call in (lambda **k: mp.block_norm(x, x, gate=g, **k), lambda **k: mp.block_norm_grad(x, None, x, x, gate=g, **k)):
+        with pytest.raises(ValueError, match="gate_mode"):
+            call()
+        with pytest.raises(ValueError, match="gate_mode"):
+            call(gate_mode="row")
+    kind = mp.moeperm._gate_mode
+    assert kind(g, 8, 8, "token") == "token" and kind(g, 8, 8, "channel") == "channel"
+    assert kind(g[None], 8, 8) == "channel" and kind(g[:, None], 8, 8) == "token"
+    assert kind(g, 8, 16) == "token" and kind(g, 16, 8) == "channel" and kind(None, 8, 8) == "none"
+    for args in ((g, 8, 16, "channel"), (g, 16, 8, "token"), (g[None], 8, 8, "token"), (g, 4, 16)):
+        with pytest.raises(ValueError):
+            kind(*args)

@@ -198,3 +198,24 @@ def test_gradients_against_differences(dev):
         got = sum((g[names[k]].double() * dirs[k]).sum() for k in dirs)
         mag = sum((g[names[k]].double() * dirs[k]).abs().sum() for k in dirs)
         assert (got - want).abs() <= 1e-5 * mag, mode
+
+
+def test_as_many_tokens_as_channels(dev):
+    """T = H: a named mode, or a 2-D gate, gives its own result; [T, 1] is the form without a name."""
+    n, dtype = 96, torch.float32
+    s = make(n, n, dtype, "token", True, True)
+    for mode, two_d in (("token", s["gate"][:, None]), ("channel", s["gate"][None])):
+        kw = dict(w_post=s["w_post"], scale=0.37, w_pre=s["w_pre"])
+        call = lambda **k: dev.block_norm(s["x"], s["y"], eps=EPS, save_rstd=True, **kw, **k)
+        grad = lambda f, **k: dev.block_norm_grad(s["x"], f["h"], f["x"], s["y"], rstd_pre=f["rstd_pre"],
+                                                  rstd_post=f["rstd_post"], **kw, **k)
+        f, f2 = call(gate=s["gate"], gate_mode=mode), call(gate=two_d)
+        g, g2 = grad(f, gate=s["gate"], gate_mode=mode), grad(f, gate=two_d)
+        y, w = s["y"].double(), s["w_post"].double()
+        x = s["x"].double() + 0.37 * gate64(s, mode) * rms64(y) * y * w
+        bound = C * U * (s["x"].double().abs() + (x - s["x"].double()).abs()) + U * x.abs()
+        assert ((f["x"].double() - x).abs() <= bound).all()
+        for k in f:
+            assert torch.equal(f[k], f2[k]), k
+        for k in g:
+            assert torch.equal(g[k], g2[k].view_as(g[k])), k
