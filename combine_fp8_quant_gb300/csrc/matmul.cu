@@ -474,10 +474,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Warp 0 loads this CTA's weight rows (kGradW: its features of x), warp 8 its
     // half of the tile's rows: issuing is serial in a thread (about 400 cycles a
     // stage for both together, close to the products' 512), so two threads share
-    // it. The bytes of both CTAs count on the first CTA's barrier. In kGradW a
-    // block that ends inside counts on this CTA's own barrier and goes on through
-    // warp 2 (the first CTA's barrier then takes an arrival of each CTA's warp 2
-    // instead of the loads').
+    // it as a margin (one thread for both measured the same). The bytes of both
+    // CTAs count on the first CTA's barrier. In kGradW a block that ends inside
+    // counts on this CTA's own barrier and goes on through warp 2 (the first CTA's
+    // barrier then takes an arrival of each CTA's warp 2 instead of the loads').
     if (elect_one()) {
       const bool weights = warp == 0;
       const uint32_t empty0 = smem_addr(s_empty), raw0 = smem_addr(s_raw);
