@@ -29,7 +29,7 @@ constexpr int kSlots = 3;  // rows of a thread in flight and in work
 
 // (act(v), act'(v))
 __device__ __forceinline__ float2 act_and_slope(float v, int act) {
-  if (act == kActRelu) return v > 0.0f ? make_float2(v, 1.0f) : make_float2(0.0f, 0.0f);
+  if (act == kActRelu) return v <= 0.0f ? make_float2(0.0f, 0.0f) : make_float2(v, 1.0f);  // NaN: (NaN, 1)
   if (act == kActSilu) {
     const float s = __fdividef(1.0f, 1.0f + __expf(-v));
     return make_float2(v * s, s * (1.0f + v * (1.0f - s)));

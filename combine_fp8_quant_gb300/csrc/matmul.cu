@@ -287,7 +287,7 @@ template <int N>
 __device__ __forceinline__ void activate(float (&v)[N], int act) {
   if (act == kActRelu) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = v[j] > 0.0f ? v[j] : 0.0f;
+    for (int j = 0; j < N; ++j) v[j] = v[j] <= 0.0f ? 0.0f : v[j];  // NaN stays NaN
   } else if (act == kActSilu) {
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] = silu(v[j]);

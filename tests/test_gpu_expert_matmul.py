@@ -419,3 +419,47 @@ def test_graph_replay_with_other_counts(dev):
         torch.cuda.synchronize()
         assert torch.equal(a, out) and torch.equal(b, dw)
     assert dev.moe_status_sync(st) == dev.MOE_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("gated", [False, True], ids=["plain", "gated"])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu"])
+@pytest.mark.parametrize("R,K,N", [(5, 2048, 64), (300, 136, 128)])
+def test_nan_reaches_its_row_alone(dev, R, K, N, act, gated, dtype):
+    """A NaN in one row (or one expert's weight row) shows in what depends on it and
+    nowhere else; no activation turns it into a number."""
+    Nw, bad, feature = 2 * N if gated else N, R // 2, 3
+    x, w = rand(1, R, K, dtype=dtype), rand(2, 2, Nw, K, dtype=dtype, gain=K ** -0.5)
+    half = R // 2 + 1  # expert 0 owns the bad row
+    seg = (i32([0, half]), i32([half, R]))
+    call = lambda a, b: dev.expert_matmul(a, b, *seg, act=act, gated=gated).clone()
+    clean = call(x, w)
+    xb, wb = x.clone(), w.clone()
+    xb[bad, K - 1] = float("nan")
+    got = call(xb, w)
+    rows = torch.arange(R, device=DEV) == bad
+    assert got[rows].isnan().all() and torch.equal(got[~rows], clean[~rows])
+    wb[1, feature, 0] = float("nan")
+    got = call(x, wb)
+    hit = torch.zeros(R, N, dtype=torch.bool, device=DEV)
+    hit[half:, feature] = True
+    assert got[hit].isnan().all() and torch.equal(got[~hit], clean[~hit])
+    if act == "none" and not gated:
+        return
+    dout, pre = rand(3, R, N, dtype=dtype), rand(4, R, Nw, dtype=dtype)
+    grad = lambda p: dev.expert_matmul_grad(dout, x, w, *seg, pre=p, act=act, gated=gated)
+    g = grad(pre)
+    g = {k: g[k].clone() for k in ("dx", "dw")}
+    pb = pre.clone()
+    pb[bad, feature] = float("nan")
+    b = grad(pb)
+    if act == "relu" and not gated:  # the slope of relu is a number at NaN
+        return
+    assert b["dx"][rows].isnan().all() and torch.equal(b["dx"][~rows], g["dx"][~rows])
+    hit = torch.zeros(2, Nw, dtype=torch.bool, device=DEV)
+    hit[0, feature] = act in ("silu", "gelu")  # the others' slope at NaN is 1: dout * up
+    if gated:
+        hit[0, N + feature] = True
+    same = ~hit
+    same[0, feature] = False
+    assert b["dw"][hit].isnan().all() and torch.equal(b["dw"][same], g["dw"][same])
