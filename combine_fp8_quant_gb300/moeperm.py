@@ -480,23 +480,34 @@ def _elem(t, allowed, name):
 
 FLOATS = (torch.bfloat16, torch.float16, torch.float32)
 E4M3_BYTES = (torch.uint8, torch.float8_e4m3fn)
+BF16_BITS = (torch.int16, torch.uint16)
 
 
 def combine(y, src2dst, weights=None, num_tokens=None, status=None, out=None):
     """out[t] = sum_k w[t,k] * y[src2dst[t,k]] in fp32, rounded once to y's type
-    (bfloat16, float16 or float32)."""
+    (bfloat16, float16 or float32; 16-bit integers are taken for bfloat16 bits).
+    `out` may have more than T rows; the first T are written."""
+    ldy = _rows(y, "y")
     T, K = src2dst.shape
     R, H = y.shape
     dev = y.device
-    dtype = y.dtype if y.dtype in FLOATS else torch.bfloat16
-    out = torch.empty((T, H), dtype=dtype, device=dev) if out is None else out
+    dtype = torch.bfloat16 if y.dtype in BF16_BITS else _elem(y, FLOATS, "y")
+    _vec(src2dst, T * K, "src2dst", torch.int32)
+    if weights is not None and (weights.dtype is not torch.float32 or weights.numel() < T * K
+                                or not weights.is_contiguous()):
+        raise ValueError(f"moeperm: weights must be a contiguous float32 tensor of {T * K} elements")
+    if out is None:
+        out = torch.empty((T, H), dtype=dtype, device=dev)
+    elif ((out.dtype is not dtype and not (dtype is torch.bfloat16 and out.dtype in BF16_BITS))
+          or out.dim() != 2 or out.shape[0] < T or out.shape[1] != H or not out.is_contiguous()):
+        raise ValueError(f"moeperm: out must be a contiguous {dtype} tensor of shape [{T}, {H}], not "
+                         f"{out.dtype} of shape {tuple(out.shape)}")
     st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
-    if dtype == torch.bfloat16:
-        _check(moe_combine(y, y.stride(0), R, src2dst, weights, T, num_tokens, K, H, out, st),
-               "moe_combine")
+    if dtype is torch.bfloat16:
+        _check(moe_combine(y, ldy, R, src2dst, weights, T, num_tokens, K, H, out, st), "moe_combine")
     else:
-        _check(moe_combine_ex(y, y.stride(0), dtype, R, src2dst, weights, T, num_tokens, K, H, out,
-                              st), "moe_combine_ex")
+        _check(moe_combine_ex(y, ldy, dtype, R, src2dst, weights, T, num_tokens, K, H, out, st),
+               "moe_combine_ex")
     return out
 
 

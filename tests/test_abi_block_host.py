@@ -197,3 +197,37 @@ def test_a_gate_that_fits_both_kinds_is_named(mp):
     for args in ((g, 8, 16, "channel"), (g, 16, 8, "token"), (g[None], 8, 8, "token"), (g, 4, 16)):
         with pytest.raises(ValueError):
             kind(*args)
+
+
+def test_combine_refuses_what_does_not_fit(mp):
+    """The output is written in y's type: any other type, shape or layout would be written past or misread."""
+    T, K, R, H = 4, 2, 6, 64
+    y, row, w = torch.zeros(R, H), torch.zeros(T, K, dtype=torch.int32), torch.zeros(T, K)
+    bad = [
+        ("out", dict(out=torch.zeros(T, H, dtype=BF))),                       # half of what fp32 rows need
+        ("out", dict(y=y.half(), out=torch.zeros(T, H, dtype=BF))),
+        ("out", dict(y=y.half(), out=torch.zeros(T, H, dtype=torch.int16))),
+        ("out", dict(out=torch.zeros(T - 1, H))),
+        ("out", dict(out=torch.zeros(H, T))),
+        ("out", dict(out=torch.zeros(T * H))),
+        ("out", dict(out=torch.zeros(T, 2 * H)[:, :H])),
+        ("y", dict(y=y.double())),
+        ("y", dict(y=torch.zeros(R, H, dtype=torch.int32))),
+        ("y", dict(y=y.to(E4))),
+        ("y", dict(y=torch.zeros(H, R).t())),
+        ("y", dict(y=torch.zeros(R, 1, H))),
+        ("src2dst", dict(src2dst=row.long())),
+        ("src2dst", dict(src2dst=torch.zeros(K, T, dtype=torch.int32).t())),
+        ("weights", dict(weights=w.double())),
+        ("weights", dict(weights=w[:, :1])),
+        ("weights", dict(weights=w[:-1])),
+        ("weights", dict(weights=torch.zeros(K, T).t())),
+    ]
+    for what, over in bad:
+        with pytest.raises(ValueError, match=f"moeperm: (the rows of )?{what} must"):
+            mp.combine(**dict(dict(y=y, src2dst=row, weights=w), **over))
+    fits = [dict(), dict(y=y.to(BF)), dict(y=y.to(BF), out=torch.zeros(T + 3, H, dtype=BF)), dict(weights=torch.zeros(T + 1, K)),
+            dict(y=torch.zeros(R, H, dtype=torch.int16)), dict(y=y.to(BF), out=torch.zeros(T, H, dtype=torch.int16))]
+    for over in fits:  # all well, but on the CPU
+        with pytest.raises(ValueError, match="must be on a CUDA device"):
+            mp.combine(**dict(dict(y=y, src2dst=row, weights=w), **over))
