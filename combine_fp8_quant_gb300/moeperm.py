@@ -613,6 +613,19 @@ def _expert_weights(w, gated):
     return (w.shape[0] if w.dim() == 3 else 1), (Nw // 2 if gated else Nw), K
 
 
+def _scale_words(t, rows, ld, words, name, blocks=1):
+    """Packed scale words [blocks, words, ld] of `rows` rows in each block. Other scale
+    formats have the same bytes in another order, or fewer: their types are refused."""
+    need = (blocks * words - 1) * ld + rows
+    if t.dtype not in (torch.int32, torch.uint32):
+        raise ValueError(f"moeperm: {name} must be packed scale words (int32), not {t.dtype}")
+    if t.numel() < need or not t.is_contiguous():  # a part of a larger buffer may hold them too
+        held = t.untyped_storage().nbytes() // 4 - t.storage_offset()
+        if held < need or (t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1):
+            raise ValueError(f"moeperm: {name} must hold {blocks} x {words} x {ld} packed words of {rows} rows, "
+                             f"not {tuple(t.shape)}")
+
+
 def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=False, residual=None,
                   masked_m=None, x_scales=None, ld_xs=0, w_scales=None, ld_ws=0, out=None, pre=None,
                   out_dtype=torch.bfloat16, status=None):
@@ -643,6 +656,11 @@ def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=Fal
     ldx = _rows(x, "x", (x.shape[0], K))
     R = x.shape[0]
     Nw = 2 * N if gated else N
+    if fp8:
+        words = (K + 511) // 512
+        _scale_words(w_scales, L * Nw, ld_ws, words, "w_scales")
+        if R > 0:
+            _scale_words(x_scales, cap if masked else R, ld_xs, words, "x_scales", L if masked else 1)
     odt = out_dtype if fp8 else dtype
     if odt not in (torch.bfloat16, torch.float16):
         raise ValueError(f"moeperm: out_dtype must be bfloat16 or float16, not {odt}")

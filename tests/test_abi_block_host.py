@@ -231,3 +231,33 @@ def test_combine_refuses_what_does_not_fit(mp):
     for over in fits:  # all well, but on the CPU
         with pytest.raises(ValueError, match="must be on a CUDA device"):
             mp.combine(**dict(dict(y=y, src2dst=row, weights=w), **over))
+
+
+def test_expert_matmul_refuses_scales_that_do_not_hold_the_rows(mp):
+    """Packed words of every row and group: fewer would be read past their end, other formats misread."""
+    L, N, K, R, cap = 2, 32, 640, 10, 8  # five groups: two words a row
+    i32 = lambda *shape: torch.zeros(*shape, dtype=torch.int32)
+    x, w, seg = torch.zeros(R, K, dtype=torch.uint8), torch.zeros(L, N, K, dtype=torch.uint8), i32(L)
+    args = dict(x=x, w=w, starts=seg, psum=seg, x_scales=i32(1, 2, 12), ld_xs=12, w_scales=i32(2, 64), ld_ws=64)
+    slabs = dict(x=torch.zeros(L, cap, K, dtype=torch.uint8), starts=None, psum=None, masked_m=seg, x_scales=i32(L, 2, cap),
+                 ld_xs=cap)
+    bad = [
+        ("x_scales", dict(x_scales=i32(1, 1, 12))),                         # one word a row
+        ("x_scales", dict(x_scales=i32(1, 2, 12)[:, :, :8].contiguous())),  # eight rows
+        ("x_scales", dict(ld_xs=16)),
+        ("x_scales", dict(x_scales=torch.zeros(R, 5, dtype=torch.uint8), ld_xs=12)),
+        ("x_scales", dict(x_scales=torch.zeros(R, 5), ld_xs=12)),
+        ("x_scales", dict(x_scales=i32(12, 2).t())),                        # a word's rows are not neighbours
+        ("w_scales", dict(w_scales=i32(1, 64))),
+        ("w_scales", dict(w_scales=i32(2, 32), ld_ws=64)),
+        ("w_scales", dict(w_scales=torch.zeros(64, 5, dtype=torch.uint8))),
+        ("x_scales", dict(slabs, x_scales=i32(1, 2, cap))),                 # one expert's block
+        ("x_scales", dict(slabs, x_scales=i32(L, 1, cap))),
+    ]
+    for what, over in bad:
+        with pytest.raises(ValueError, match=f"moeperm: {what} must"):
+            mp.expert_matmul(**dict(args, **over))
+    fits = [dict(), slabs, dict(x_scales=i32(2, 12)[:, :R]), dict(x_scales=i32(30)), dict(x_scales=i32(4, 12))]
+    for over in fits:  # all well, but on the CPU
+        with pytest.raises(ValueError, match="must be on a CUDA device"):
+            mp.expert_matmul(**dict(args, **over))
