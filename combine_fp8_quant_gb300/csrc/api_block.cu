@@ -12,13 +12,17 @@ namespace {
 cudaStream_t cu(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Which parts a norm call has: a block output or a pre norm, and a post norm or
-// a gate only with a block output (whose pointer may be NULL without rows).
+// a gate only with a block output. Without rows the block output and a gate per
+// token may be NULL (they are empty); a gate per channel may not, since the
+// gradient still reads it for its sums over no tokens. Kernels read a gate per
+// channel in vectors, one per token a float at a time.
 bool norm_parts_ok(int32_t T, const void* y, const float* w_post, const float* gate, int mode,
                    const float* w_pre) {
   if (mode != MOE_GATE_NONE && mode != MOE_GATE_CHANNEL && mode != MOE_GATE_TOKEN) return false;
+  if (mode == MOE_GATE_CHANNEL && (!gate || !aligned16(gate))) return false;
   if (T <= 0) return true;
   if (!y && (!w_pre || w_post || mode != MOE_GATE_NONE)) return false;
-  return mode == MOE_GATE_NONE || (gate && aligned16(gate));
+  return mode != MOE_GATE_TOKEN || (gate && aligned_to(gate, 4));
 }
 
 // Rows of a norm: at most 2048 16-byte vectors.

@@ -472,7 +472,8 @@ typedef enum {
  * rounding to `type`.
  *   x [T, ldx], y [T, ldy], x_out [T, H], h [T, H]   BF16, F16 or F32, rows a multiple
  *                                of 16 bytes, at most 2048 16-byte vectors each
- *   w_post [H], gate, w_pre [H]  f32, 16-byte aligned
+ *   w_post [H], gate [H], w_pre [H]  f32, 16-byte aligned, also for T = 0; a gate [T]
+ *                                needs no more than a float's alignment
  *   rstd_post [T], rstd_pre [T]  f32, (optional) kept for the backward pass
  * Launches: 1.
  */

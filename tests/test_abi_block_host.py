@@ -261,3 +261,13 @@ def test_expert_matmul_refuses_scales_that_do_not_hold_the_rows(mp):
     for over in fits:  # all well, but on the CPU
         with pytest.raises(ValueError, match="must be on a CUDA device"):
             mp.expert_matmul(**dict(args, **over))
+
+
+@pytest.mark.parametrize("over", [
+    dict(T=0, gate=None), dict(T=0, gate=ODD), dict(T=0, y=None, gate=None), dict(T=0, w_post=ODD), dict(T=0, w_pre=ODD),
+    dict(T=0, gate=FAKE + 2, gate_mode="channel"), dict(gate=FAKE + 2, gate_mode="token"),
+])
+def test_block_norms_refuse_a_gate_that_is_read_without_tokens(mp, over):
+    """The gradient launches for T = 0 too (its sums are zeros) and reads a gate per channel."""
+    for name, args in (("moe_block_norm", NORM), ("moe_block_norm_grad", NORM_GRAD)):
+        assert call(mp, name, args, over) == mp.MOE_ERR_INVALID_ARG, name

@@ -219,3 +219,26 @@ def test_as_many_tokens_as_channels(dev):
             assert torch.equal(f[k], f2[k]), k
         for k in g:
             assert torch.equal(g[k], g2[k].view_as(g[k])), k
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_a_gate_per_token_may_start_at_any_float(dev, dtype):
+    """A batch's part of a longer gate: the same results as from a copy of it, also without tokens."""
+    T, H = 21, 136
+    s = make(T, H, dtype, "token", True, True)
+    longer = torch.cat([rand(9, 3), s["gate"], rand(10, 2)])
+    kw = dict(w_post=s["w_post"], scale=0.37, w_pre=s["w_pre"])
+    for first in (1, 2, 3):
+        longer[first:first + T] = s["gate"]
+        part = longer[first:first + T]
+        assert part.data_ptr() % 16 != 0
+        a, b = (dev.block_norm(s["x"], s["y"], gate=g, save_rstd=True, **kw) for g in (s["gate"], part))
+        c, d = (dev.block_norm_grad(s["x"], a["h"], a["x"], s["y"], gate=g, rstd_pre=a["rstd_pre"],
+                                    rstd_post=a["rstd_post"], **kw) for g in (s["gate"], part))
+        for u, v in ((a, b), (c, d)):
+            assert all(torch.equal(u[k], v[k]) for k in u)
+    e = make(0, H, dtype, "token", True, True)
+    z = torch.empty(0, device=DEV)
+    o = dev.block_norm_grad(e["x"], e["x"], e["x"], e["y"], gate=e["gate"], rstd_pre=z, rstd_post=z, **kw)
+    torch.cuda.synchronize()
+    assert all((o[k] == 0).all() for k in ("dw_pre", "dw_post")) and o["dgate"].shape == (0,)
