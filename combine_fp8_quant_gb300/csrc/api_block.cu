@@ -44,8 +44,12 @@ bool feats_ok(int32_t N, int32_t L, int32_t gated) {
   return (int64_t)L * N * (gated ? 2 : 1) < (int64_t(1) << 31);
 }
 
+// Room for the gradient of the pre-activations of any number of rows up to R: the
+// second term comes with few rows, so fewer rows than R may need more than R do.
 size_t dpre_bytes(int64_t R, int32_t L, int32_t Nw) {
-  return ((size_t)grad_terms(R, L) * R * Nw * 2 + 255) / 256 * 256;
+  const int64_t two = R < (int64_t)kTwoTermRows * L ? R : (int64_t)kTwoTermRows * L;
+  const int64_t rows = 2 * two > R ? 2 * two : R;
+  return ((size_t)rows * Nw * 2 + 255) / 256 * 256;
 }
 
 }  // namespace

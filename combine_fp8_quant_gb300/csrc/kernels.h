@@ -209,7 +209,8 @@ struct ActGradArgs {
 // product on staged data costs 2 to 3% (all gradients of 32 experts with 64 rows
 // each, 2048 x 2816: 241 against 236 us); it halves the error variance of dx and
 // dW. Above that the tensor cores are the bound and it would cost its full share.
-inline int grad_terms(int64_t R, int32_t L) { return R <= (int64_t)128 * L ? 2 : 1; }
+constexpr int kTwoTermRows = 128;  // per expert
+inline int grad_terms(int64_t R, int32_t L) { return R <= (int64_t)kTwoTermRows * L ? 2 : 1; }
 constexpr int kActGradSplits = 64;
 int act_grad_splits(int64_t R, int32_t L, int32_t N);
 cudaError_t launch_act_grad(const ActGradArgs& a, int type, cudaStream_t s);

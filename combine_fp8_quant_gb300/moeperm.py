@@ -690,12 +690,12 @@ def expert_matmul(x, w, starts=None, psum=None, bias=None, act="none", gated=Fal
 
 
 class GradWorkspace:
-    """Workspace of expert_matmul_grad for R rows, L experts and Nw weight rows per
-    expert (gated: 2N), reusable across calls on one stream; needs no
-    initialisation."""
+    """Workspace of expert_matmul_grad for up to R rows, L experts and Nw weight rows
+    per expert (gated: 2N), reusable across calls on one stream; needs no
+    initialisation. Its size is the same for both types."""
 
     def __init__(self, R: int, L: int, Nw: int, dtype, device):
-        _ = dtype  # 16 bits for both types
+        _ = dtype  # 16 bits for both types: the argument changes nothing
         self.nbytes = moe_expert_matmul_grad_workspace_bytes(R, L, Nw)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
 

@@ -424,10 +424,11 @@ moe_status_t moe_expert_matmul(
     int64_t ldo, moe_elem_t out_type, void* pre, int64_t ld_pre, int32_t* d_status,
     moe_stream_t stream);
 
-/* Bytes of device workspace moe_expert_matmul_grad needs for R rows, L experts
+/* Bytes of device workspace moe_expert_matmul_grad needs for up to R rows, L experts
  * and Nw = N (gated: 2N) weight rows: the gradient of P (16 bits a term) and partial
- * sums of the bias gradient. No initialisation; not to be used by two calls
- * that can run at once. 0 for negative or zero sizes (R = 0 is allowed). */
+ * sums of the bias gradient. A workspace for R rows serves every smaller number
+ * too. No initialisation; not to be used by two calls that can run at once. 0 for
+ * negative or zero sizes (R = 0 is allowed). */
 size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
 
 /*

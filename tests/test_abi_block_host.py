@@ -271,3 +271,13 @@ def test_block_norms_refuse_a_gate_that_is_read_without_tokens(mp, over):
     """The gradient launches for T = 0 too (its sums are zeros) and reads a gate per channel."""
     for name, args in (("moe_block_norm", NORM), ("moe_block_norm_grad", NORM_GRAD)):
         assert call(mp, name, args, over) == mp.MOE_ERR_INVALID_ARG, name
+
+
+@pytest.mark.parametrize("L,Nw", [(1, 64), (4, 200), (16, 2816), (64, 2816), (1000, 16)])
+def test_a_gradient_workspace_serves_fewer_rows(mp, L, Nw):
+    """Sized for the largest batch, it is enough for every smaller one, on both sides of 128 rows an expert."""
+    edges = {0, 1, 63, 64, 65, 8000, 12000, 100_000, 1_000_000}
+    for m in (1, 32, 64, 127, 128, 129, 255, 256, 257, 1024, 8192):
+        edges |= {m * L - 1, m * L, m * L + 1}
+    sizes = [mp.moe_expert_matmul_grad_workspace_bytes(R, L, Nw) for R in sorted(edges)]
+    assert sizes == sorted(sizes)
