@@ -322,10 +322,12 @@ __global__ void __launch_bounds__(MAXT) norm_grad_kernel(NormArgs p, int slots) 
       block_sum<3>(s, s_sum, buf);
       buf ^= 1;
     }
-    const float k1 = rx * rx * rx * s[0] * inv_h;  // g = dx' + rx * t - k1 * x'
+    // The sums first, then one rstd after the other: rstd^3 alone leaves the range of
+    // fp32 for rows of 1e-13 and of 1e15, whose gradients are ordinary numbers.
+    const float k1 = rx * s[0] * inv_h * rx * rx;  // g = dx' + rx * t - k1 * x'
     const float dot = s[1] - k1 * s[2];            // sum of scale * gate_c * w_post * y * g
     if (gate_t && has_y && tid == 0) p.dgate[t] = dot * ry;
-    const float k2 = post ? gt * ry * ry * ry * dot * inv_h : 0.0f;  // dy = gt * ry * c * g - k2 * y
+    const float k2 = post ? ry * dot * inv_h * ry : 0.0f;  // dy = gt * ry * (c * g - k2 * y)
     const float gry = gt * ry, kq = p.scale * gry;
     const f32x2 nk1 = pair(-k1, -k1), nk2 = pair(-k2, -k2), gry2 = pair(gry, gry), kq2 = pair(kq, kq);
     const int64_t out0 = (t * nv + tid) * 16;
@@ -352,7 +354,7 @@ __global__ void __launch_bounds__(MAXT) norm_grad_kernel(NormArgs p, int slots) 
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         a_q[i][j] = fma2(mul2(kq2, g[j]), y[j], a_q[i][j]);
-        y[j] = fma2(mul2(gry2, cw[i][j]), g[j], mul2(nk2, y[j]));
+        y[j] = mul2(gry2, fma2(nk2, y[j], mul2(cw[i][j], g[j])));
       }
       st_v4(static_cast<uint8_t*>(p.dy) + out0 + (int64_t)i * bd * 16, V::pack2(y));
     }

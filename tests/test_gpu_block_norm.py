@@ -242,3 +242,24 @@ def test_a_gate_per_token_may_start_at_any_float(dev, dtype):
     o = dev.block_norm_grad(e["x"], e["x"], e["x"], e["y"], gate=e["gate"], rstd_pre=z, rstd_post=z, **kw)
     torch.cuda.synchronize()
     assert all((o[k] == 0).all() for k in ("dw_pre", "dw_post")) and o["dgate"].shape == (0,)
+
+
+@pytest.mark.parametrize("mode", ["none", "channel", "token"])
+@pytest.mark.parametrize("sx", [1e-13, 1.0, 1e15])
+@pytest.mark.parametrize("sy", [1e-13, 1.0, 1e15])
+def test_gradients_of_very_small_and_large_rows(dev, sx, sy, mode):
+    """Rows whose reciprocal root, cubed, is out of fp32's range; every gradient is an ordinary number. Small rows
+    come with eps = 0. The same bounds as at ordinary sizes."""
+    T, H = 19, 264
+    s = make(T, H, torch.float32, mode, True, True)
+    s["x"], s["y"] = s["x"] * sx, s["y"] * sy
+    dxo, dh = rand(7, T, H, gain=1.0 / sx), rand(8, T, H)
+    rx, ry = (torch.rsqrt((s[k].double() ** 2).mean(1)).float() for k in ("x", "y"))
+    o = dev.block_norm_grad(dxo, dh, s["x"], s["y"], w_post=s["w_post"], gate=s["gate"], scale=0.37, w_pre=s["w_pre"],
+                            rstd_pre=rx, rstd_post=ry)
+    torch.cuda.synchronize()
+    want = grads64(s, mode, 0.37, dxo, dh, rx, ry)
+    assert {k for k, v in o.items() if v is not None} == set(want)
+    for k, (v, mag) in want.items():
+        bound = (2 * C + T) * U * mag + (U * v.abs() if k in ("dx", "dy") else 0)
+        assert torch.isfinite(o[k]).all() and ((o[k].double() - v).abs() <= bound).all(), k
