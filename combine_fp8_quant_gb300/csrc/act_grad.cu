@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "elem.cuh"
 #include "kernels.h"
+#include "segments.cuh"
 
 namespace moeperm {
 
@@ -61,19 +62,10 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
   __shared__ float s_sum[kRowLanes][kStrip + 4];
   const int tid = threadIdx.x, rl = tid / kCols, col = blockIdx.x * kStrip + (tid % kCols) * 8;
   const int e = blockIdx.y, Nw = p.gated ? 2 * p.N : p.N;
-  int64_t b = 0, c = p.R;
-  if (p.cap > 0) {
-    b = (int64_t)e * p.cap;
-    c = __ldg(p.seg_end + e);
-  } else if (p.seg_begin != nullptr) {
-    b = __ldg(p.seg_begin + e);
-    c = (int64_t)__ldg(p.seg_end + e) - b;
-  }
-  if (b < 0 || c < 0 || b + c > p.R || (p.cap > 0 && c > p.cap)) {
-    if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) set_status(p.status, kStBadLayout);
-    b = c = 0;
-  }
-  const int64_t lo = b + c * blockIdx.z / p.splits, hi = b + c * (blockIdx.z + 1) / p.splits;
+  int64_t b, c;
+  bool bad = !segment(p, e, b, c);
+  const int64_t lo = b + c * blockIdx.z / p.splits;
+  int64_t hi = b + c * (blockIdx.z + 1) / p.splits;
   const uint16_t* dout = static_cast<const uint16_t*>(p.dout);
   const uint16_t* pre = static_cast<const uint16_t*>(p.pre);
   uint16_t* dpre = static_cast<uint16_t*>(p.dpre);
@@ -92,10 +84,28 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
     cp_async_commit();
   };
   if (col < p.N) {
+#pragma unroll
+    for (int i = 0; i + 1 < kSlots; ++i) fetch(lo + rl + i * kRowLanes, i);
+  }
+  // A segment that shares rows with an earlier one counts as empty, as it does for the
+  // products. Its rows' dP is the same from either, so only the sums need to know.
+  if (p.dbias != nullptr && p.seg_begin != nullptr) {
+    bool hit = false;
+    for (int f = tid; f < e; f += kThreads) {
+      int64_t bf, cf;
+      segment(p, f, bf, cf);
+      hit |= share_rows(b, c, bf, cf);
+    }
+    bad |= __syncthreads_or(hit) != 0;
+  }
+  if (bad) {
+    if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) set_status(p.status, kStBadLayout);
+    cp_async_wait_all();
+    hi = lo;
+  }
+  if (col < p.N) {
     int64_t r = lo + rl;
     int slot = 0;
-#pragma unroll
-    for (int i = 0; i + 1 < kSlots; ++i) fetch(r + i * kRowLanes, i);
     for (; r < hi; r += kRowLanes) {
       fetch(r + (kSlots - 1) * kRowLanes, slot == 0 ? kSlots - 1 : slot - 1);
       cp_async_wait_group<kSlots - 1>();

@@ -62,6 +62,7 @@
 
 #include "elem.cuh"
 #include "kernels.h"
+#include "segments.cuh"
 #include "tcgen05.cuh"
 
 namespace moeperm {
@@ -352,26 +353,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 3) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   __syncthreads();
   int mx = 0;
+  bool ascending = true;  // as every layout makes them: then no two share a row
   for (int e = tid; e < p.L; e += kThreads) {
-    int64_t b = 0, c = p.R;
-    if (p.cap > 0) {
-      b = (int64_t)e * p.cap;
-      c = __ldg(p.seg_end + e);
-    } else if (p.seg_begin != nullptr) {
-      b = __ldg(p.seg_begin + e);
-      c = (int64_t)__ldg(p.seg_end + e) - b;
-    }
-    const bool bad = b < 0 || c < 0 || b + c > p.R || (p.cap > 0 && c > p.cap);
-    if (bad) {  // nothing of it is read or written
-      if (blockIdx.x == 0) set_status(p.status, kStBadLayout);
-      b = c = 0;
-    }
+    int64_t b, c;
+    const bool ok = segment(p, e, b, c);
+    if (!ok && blockIdx.x == 0) set_status(p.status, kStBadLayout);
+    if (p.seg_begin != nullptr) ascending &= ok && (e + 1 == p.L || b + c <= __ldg(p.seg_begin + e + 1));
     s_begin[e] = (int)b;
     s_count[e] = (int)c;
     mx = max(mx, (int)c);
   }
   atomicMax(&s_max, mx);
-  __syncthreads();
+  if (!__syncthreads_and(ascending)) {
+    // Each against all before it. One that shares rows with an earlier one counts as
+    // empty: its rows are written once, and there are no more tiles than the host
+    // counted (with split reductions a cluster has one tile at most).
+    uint32_t hit = 0;  // bit i: this thread's i-th segment
+    for (int e = tid, i = 0; e < p.L; e += kThreads, ++i)
+      for (int f = 0; f < e; ++f)
+        if (share_rows(s_begin[e], s_count[e], s_begin[f], s_count[f])) hit |= 1u << i;
+    __syncthreads();
+    for (int e = tid, i = 0; e < p.L; e += kThreads, ++i)
+      if ((hit >> i) & 1u) {
+        s_count[e] = 0;
+        if (blockIdx.x == 0) set_status(p.status, kStBadLayout);
+      }
+    __syncthreads();
+  }
   if (warp == 0) {  // row tiles before each expert
     int base = 0;
     for (int e0 = 0; e0 < p.L; e0 += 32) {

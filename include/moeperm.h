@@ -398,8 +398,9 @@ typedef enum {
  *   masked slabs                 seg_begin NULL, cap > 0: e*cap .. e*cap + seg_end[e]
  *                                (seg_end = masked_m; R = L*cap)
  *   dense                        both NULL, cap 0, L = 1: all R rows
- * Rows of no expert are not written and may hold anything. Segments outside
- * [0, R] set MOE_STATUS_BAD_LAYOUT and count as empty.
+ * Rows of no expert are not written and may hold anything. Segments come in any order
+ * but share no rows. One outside [0, R], or with a row of an earlier one (of a smaller
+ * e, inside [0, R]), sets MOE_STATUS_BAD_LAYOUT and counts as empty.
  *   x [R, ldx]                   BF16, F16 (K % 8 == 0) or E4M3 (K % 128 == 0); rows
  *                                16-byte aligned
  *   x_scales, ld_xs              E4M3: packed UE8M0 words of the rows in groups of 128, as
@@ -442,7 +443,8 @@ size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
  *   dout [R, ldd], x [R, ldx], w, pre [R, ld_pre]   BF16 or F16, as in the forward call
  *                                (pre is not needed without activation and gate)
  *   dx [R, ld_dx], dw [L, N or 2N, K] of dw_type (`type` or F32), dbias   each optional
- * Rows of no expert may hold anything, NaN included. Sums are in fp32 and in
+ * Segments are those of the forward call, with its errors. Rows of no expert may hold
+ * anything, NaN included. Sums are in fp32 and in
  * a fixed order (deterministic). Launches: up to 4.
  */
 moe_status_t moe_expert_matmul_grad(

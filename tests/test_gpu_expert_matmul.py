@@ -463,3 +463,87 @@ def test_nan_reaches_its_row_alone(dev, R, K, N, act, gated, dtype):
     same = ~hit
     same[0, feature] = False
     assert b["dw"][hit].isnan().all() and torch.equal(b["dw"][same], g["dw"][same])
+
+
+def check_gradients(o, dout, pre, x, w, seg, N, act, gated, dw_dtype):
+    """dx, dw and dbias of every expert's rows within the bounds of test_gradients; rows of no expert as they were (9)."""
+    dtype, Nw = x.dtype, w.shape[1]
+    hs, hw = torch.finfo(dtype).eps / 2, torch.finfo(dw_dtype).eps / 2
+    real = torch.zeros(x.shape[0], dtype=torch.bool, device=DEV)
+    for e, (lo, hi) in enumerate(seg):
+        if hi <= lo:
+            assert all((o[k][e] == 0).all() for k in ("dw", "dbias") if o[k] is not None)
+            continue
+        real[lo:hi] = True
+        g, n = dout[lo:hi].double(), hi - lo
+        if act == "none" and not gated:
+            dP = g
+            e32 = e16 = torch.zeros_like(dP)
+        else:
+            p = pre[lo:hi].double()
+            a, d = phi(act, p[:, :N])
+            dP = torch.cat([g * d * p[:, N:], g * a], 1) if gated else g * d
+            m = torch.cat([(g * p[:, N:]).abs() * 1.13, (g * p[:, :N]).abs()], 1) if gated else g.abs() * 1.13
+            e32 = ACT_ERR * m
+            e16 = e32 + hs * (dP.abs() + e32) + TINY
+        for got, A, B, eA, h, steps in ((o["dx"], dP, w[e].double(), e16, hs, Nw),
+                                        (o["dw"], dP.t(), x[lo:hi].double(), e16.t(), hw, n)):
+            if got is None:
+                continue
+            got = got[lo:hi] if got is o["dx"] else got[e]
+            want, mag = A @ B, A.abs() @ B.abs()
+            bound = eA @ B.abs() + (steps + 2) * V * (mag + eA @ B.abs())
+            assert ((got.double() - want).abs() <= h * want.abs() + bound * (1 + h) + TINY).all(), e
+        if o["dbias"] is not None:
+            bound = e32.sum(0) + (n + 2) * V * (dP.abs() + e32).sum(0)
+            assert ((o["dbias"][e].double() - dP.sum(0)).abs() <= bound).all(), e
+    if o["dx"] is not None:
+        assert (o["dx"][~real] == 9).all()
+
+
+def valid_segments(begin, end, R):
+    """The segments that count: inside the rows, and without a row of an earlier one that is."""
+    inside = [0 <= lo <= hi <= R for lo, hi in zip(begin, end)]
+    seg, bad = [], False
+    for e, (lo, hi) in enumerate(zip(begin, end)):
+        shares = any(inside[f] and max(lo, begin[f]) < min(hi, end[f]) for f in range(e))
+        ok = inside[e] and not shares
+        bad |= not ok
+        seg.append((lo, hi) if ok else (0, 0))
+    return seg, bad
+
+
+LISTS = [  # begin, end, R, K, N
+    ([0, 10], [4, 21], 20, 64, 64), ([-1, 4], [3, 8], 20, 64, 64), ([0, 6], [4, 5], 20, 64, 64),    # outside the rows
+    ([10, 0], [20, 10], 20, 64, 64), ([7, 20, 3], [12, 20, 7], 20, 136, 64),                        # in another order
+    ([0, 5], [10, 15], 20, 64, 64), ([5, 0], [15, 10], 20, 64, 64), ([0, 4, 2], [8, 4, 12], 20, 64, 64),
+    ([0, 0, 0], [40, 40, 40], 40, 2048, 64), ([0] * 9, [300] * 9, 300, 1024, 128),                  # with split reductions
+    ([0, 8, 6, 12], [8, 9, 10, 20], 20, 128, 64), ([0, 0, 30], [0, 30, 300], 300, 64, 264),
+    (list(range(0, 1200, 3)), list(range(4, 1204, 3)), 1300, 64, 16),                               # each overlaps the next
+]
+
+
+@pytest.mark.parametrize("begin,end,R,K,N", LISTS)
+def test_segments_that_do_not_fit_count_as_empty(dev, begin, end, R, K, N):
+    """Segments outside the rows, or with rows of an earlier one, are flagged and nothing of them is read or written;
+    all others are computed, in any order."""
+    L, dtype = len(begin), torch.bfloat16
+    seg, bad = valid_segments(begin, end, R)
+    x, w = rand(1, R, K, dtype=dtype), rand(2, L, N, K, dtype=dtype, gain=K ** -0.5)
+    bias, dout = rand(3, L, N), rand(4, R, N, dtype=dtype)
+    out, pre = (torch.full((R, N), 9.0, device=DEV, dtype=dtype) for _ in range(2))
+    want = dev.MOE_ERR_BAD_LAYOUT if bad else dev.MOE_OK
+    st = torch.zeros(1, dtype=torch.int32, device=DEV)
+    dev.expert_matmul(x, w, i32(begin), i32(end), bias=bias, act="silu", out=out, pre=pre, status=st)
+    assert dev.moe_status_sync(st) == want
+    check_forward(out, pre, x.double(), w.double(), bias, None, seg, N, "silu", False, dtype)
+    for act in ("silu", "none"):
+        st.zero_()
+        dx = torch.full((R, K), 9.0, device=DEV, dtype=dtype)
+        o = dev.expert_matmul_grad(dout, x, w, i32(begin), i32(end), pre=pre, act=act, dx=dx, status=st,
+                                   need=("dx", "dw", "dbias"))
+        assert dev.moe_status_sync(st) == want
+        check_gradients(o, dout, pre, x, w, seg, N, act, False, dtype)
+        st.zero_()
+        alone = dev.expert_matmul_grad(dout, x, w, i32(begin), i32(end), pre=pre, act=act, status=st, need=("dbias",))
+        assert dev.moe_status_sync(st) == want and torch.equal(alone["dbias"], o["dbias"])
