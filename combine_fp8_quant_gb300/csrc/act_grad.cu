@@ -60,6 +60,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
   __shared__ uint4 s_ring[kSlots][3][kThreads];
   __shared__ float s_sum[kRowLanes][kStrip + 4];
+  __shared__ int s_held[kThreads / 32];
   const int tid = threadIdx.x, rl = tid / kCols, col = blockIdx.x * kStrip + (tid % kCols) * 8;
   const int e = blockIdx.y, Nw = p.gated ? 2 * p.N : p.N;
   int64_t b, c;
@@ -89,15 +90,28 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
   }
   // A segment that shares rows with an earlier one counts as empty, as it does for the
   // products. Its rows' dP is the same from either, so only the sums need to know.
-  if (p.dbias != nullptr && p.seg_begin != nullptr) {
+  const bool sums = p.dbias != nullptr && p.seg_begin != nullptr, count = p.terms == kTermsByRows;
+  int terms = p.terms;
+  if (sums || count) {
     bool hit = false;
-    for (int f = tid; f < e; f += kThreads) {
+    int held = 0;
+    for (int f = tid; f < (count ? p.L : e); f += kThreads) {
       int64_t bf, cf;
       segment(p, f, bf, cf);
-      hit |= share_rows(b, c, bf, cf);
+      held += rows_held(cf);
+      hit |= sums && f < e && share_rows(b, c, bf, cf);
     }
+    held = __reduce_add_sync(0xffffffffu, held);
+    if (tid % 32 == 0) s_held[tid / 32] = held;
     bad |= __syncthreads_or(hit) != 0;
+    if (count) {
+      held = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) held += s_held[i];
+      terms = terms_of(held, p.L);
+    }
   }
+  const int64_t rest = terms > 1 ? p.R * Nw : 0;
   if (bad) {
     if (tid == 0 && blockIdx.x == 0 && blockIdx.z == 0) set_status(p.status, kStBadLayout);
     cp_async_wait_all();
@@ -126,8 +140,8 @@ __global__ void __launch_bounds__(kThreads, 3) act_grad_kernel(ActGradArgs p) {
           s0[j] += v[j];
           s1[j] += u[j];
         }
-        put<TYPE>(dpre + r * Nw + col, v, p.terms > 1 ? p.R * Nw : 0);
-        if (p.gated) put<TYPE>(dpre + r * Nw + p.N + col, u, p.terms > 1 ? p.R * Nw : 0);
+        put<TYPE>(dpre + r * Nw + col, v, rest);
+        if (p.gated) put<TYPE>(dpre + r * Nw + p.N + col, u, rest);
       }
       if (++slot == kSlots) slot = 0;
     }

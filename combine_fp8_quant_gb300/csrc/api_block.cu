@@ -44,13 +44,9 @@ bool feats_ok(int32_t N, int32_t L, int32_t gated) {
   return (int64_t)L * N * (gated ? 2 : 1) < (int64_t(1) << 31);
 }
 
-// Room for the gradient of the pre-activations of any number of rows up to R: the
-// second term comes with few rows, so fewer rows than R may need more than R do.
-size_t dpre_bytes(int64_t R, int32_t L, int32_t Nw) {
-  const int64_t two = R < (int64_t)kTwoTermRows * L ? R : (int64_t)kTwoTermRows * L;
-  const int64_t rows = 2 * two > R ? 2 * two : R;
-  return ((size_t)rows * Nw * 2 + 255) / 256 * 256;
-}
+// Room for the gradient of the pre-activations in two terms: the rows held decide
+// whether both are used, and they may be few in any buffer.
+size_t dpre_bytes(int64_t R, int32_t Nw) { return ((size_t)2 * R * Nw * 2 + 255) / 256 * 256; }
 
 }  // namespace
 
@@ -246,7 +242,7 @@ size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw) 
   if (R < 0 || L < 1 || Nw < 1) return 0;
   // the split count depends on N; a gated N is half of Nw and gives the larger one
   const int splits = act_grad_splits(R, L, Nw < 2 ? 1 : Nw / 2);
-  return dpre_bytes(R, L, Nw) + (splits > 1 ? (size_t)splits * L * Nw * sizeof(float) : 0);
+  return dpre_bytes(R, Nw) + (splits > 1 ? (size_t)splits * L * Nw * sizeof(float) : 0);
 }
 
 moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x, int64_t ldx,
@@ -270,6 +266,7 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     return MOE_OK;
   }
   const bool has_act = act != MOE_ACT_NONE || gated;
+  const int terms = grad_terms(R, L, /*dense=*/seg_end == nullptr);
   if (!rows_ok(dout, ldd, N, 2)) return MOE_ERR_INVALID_ARG;
   if (has_act && !rows_ok(pre, ld_pre, Nw, 2)) return MOE_ERR_INVALID_ARG;
   if (dw && !rows_ok(x, ldx, K, 2)) return MOE_ERR_INVALID_ARG;
@@ -286,16 +283,16 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     a.dout = dout; a.ldd = ldd; a.pre = pre; a.ld_pre = ld_pre; a.R = R; a.L = L; a.N = N; a.gated = gated;
     a.act = (int)act; a.seg_begin = seg_begin; a.seg_end = seg_end; a.cap = cap;
     a.dpre = has_act ? workspace : nullptr;
-    a.terms = grad_terms(R, L);
+    a.terms = terms;
     a.dbias = dbias;
-    a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, L, Nw));
+    a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, Nw));
     a.splits = act_grad_splits(R, L, N);
     a.status = d_status;
     if (launch_act_grad(a, (int)type, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
   MatmulArgs m{};
   m.x = x; m.ldx = ldx; m.g = has_act ? workspace : dout; m.ldg = has_act ? Nw : ldd;
-  m.terms = has_act ? grad_terms(R, L) : 1;
+  m.terms = has_act ? terms : 1;
   m.w = w; m.R = R; m.K = K; m.L = L; m.N = N; m.type = (int)type; m.gated = gated;
   m.seg_begin = seg_begin; m.seg_end = seg_end; m.cap = cap; m.status = d_status;
   if (dx) {

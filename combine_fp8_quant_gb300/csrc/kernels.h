@@ -161,7 +161,7 @@ struct MatmulArgs {
   int64_t ldx;
   const void* g;               // [R, ldg] gradient of the pre-activations (both gradients)
   int64_t ldg;
-  int32_t terms;               // 1, or 2: g is the sum of rows [0, R) and [R, 2R)
+  int32_t terms;               // 1; 2: g is the sum of rows [0, R) and [R, 2R); or kTermsByRows
   const void* w;               // [L, N or 2N, K]
   int64_t R;
   int32_t K, L, N;             // N: output features (half the weight rows when gated)
@@ -197,20 +197,26 @@ struct ActGradArgs {
   const int32_t* seg_begin;
   const int32_t* seg_end;
   int32_t cap;
-  void* dpre;                  // [terms, R, N or 2N]; nullptr: the sums of dout alone
-  int32_t terms;               // 2: dpre rounded, then what the rounding left over
+  void* dpre;                  // [2, R, N or 2N]; nullptr: the sums of dout alone
+  int32_t terms;               // 2: dpre rounded, then what the rounding left over; or kTermsByRows
   float* dbias;                // optional [L, N or 2N]
   float* ws;                   // [splits, L, N or 2N] when splits > 1
   int32_t splits;
   int32_t* status;
 };
-// Terms of the pre-activations' gradient: two while the experts hold at most 128
-// rows on average. There moving the weights bounds the two products, and a second
-// product on staged data costs 2 to 3% (all gradients of 32 experts with 64 rows
-// each, 2048 x 2816: 241 against 236 us); it halves the error variance of dx and
-// dW. Above that the tensor cores are the bound and it would cost its full share.
+// Terms of the pre-activations' gradient: two while the experts hold at most 128 rows
+// on average. There the products wait for their operands and the epilogue, and a
+// second product on staged data costs 2 to 3% (all gradients of 32 experts with 64
+// rows each, 2048 x 2816: 241 against 236 us); it halves the error variance of dx
+// and dW. Above that the tensor cores are the bound and it would cost its full share.
+// The rows held decide, not the room for them: a batch's gradients are the same in a
+// larger buffer. kTermsByRows leaves it to the kernels, which count them; the host
+// knows where R rows are few enough, or one dense matrix holds them all.
 constexpr int kTwoTermRows = 128;  // per expert
-inline int grad_terms(int64_t R, int32_t L) { return R <= (int64_t)kTwoTermRows * L ? 2 : 1; }
+constexpr int kTermsByRows = 0;
+inline int grad_terms(int64_t R, int32_t L, bool dense) {
+  return R <= (int64_t)kTwoTermRows * L ? 2 : dense ? 1 : kTermsByRows;
+}
 constexpr int kActGradSplits = 64;
 int act_grad_splits(int64_t R, int32_t L, int32_t N);
 cudaError_t launch_act_grad(const ActGradArgs& a, int type, cudaStream_t s);

@@ -46,10 +46,10 @@
 // Large products are bound by the tensor cores and the shared-memory port (a tile
 // of 176 rows moves 55 KB per 352 cycles of products), decode by HBM.
 //
-// The gradient of the pre-activations enters both backward products in 16 bits. With
-// few rows it comes as two terms, its rounding and what that left over (`terms` = 2):
-// both are multiplied against the same staged weights (or rows), at next to no cost
-// where moving those is the bound.
+// The gradient of the pre-activations enters both backward products in 16 bits. While
+// the experts hold few rows it comes as two terms, its rounding and what that left
+// over: both are multiplied against the same staged weights (or rows), at next to no
+// cost while the tensor cores are not the bound.
 //
 // Rows outside every segment are read at most as columns that are not stored.
 // In kGradW rows are the reduction: lines of the last block past the segment's
@@ -104,7 +104,7 @@ struct Args {
   int32_t wrows;             // weight rows per expert (kGradW: output rows)
   int32_t gated, act, f16, out_f32;
   int32_t splits;            // pairs per cluster, each with a run of the reduction
-  int32_t terms;             // 2: the row operand is a sum of two tensors, R rows apart
+  int32_t terms;             // 2: the row operand is a sum of two tensors; or kTermsByRows
   int32_t ring_bytes;
   const float* bias;         // [L, wrows]
   const void* residual;
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint64_t s_go, s_recv;  // splits: the ring may be written; the accumulators have arrived
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_stop;
-  __shared__ int s_max;
+  __shared__ int s_max, s_held;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int crank = (int)cluster_rank(), rank = crank & 1;  // rank 0 issues the pair's products
@@ -347,12 +347,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_addr(&s_recv), 1);
     mbar_init_fence();
     s_stop = 0;
-    s_max = 0;
+    s_max = s_held = 0;
     prefetch_map(&maps.a);
   }
   if (warp == 3) tmem_alloc(smem_addr(&s_tmem), kTmemCols);
   __syncthreads();
-  int mx = 0;
+  int mx = 0, held = 0;
   bool ascending = true;  // as every layout makes them: then no two share a row
   for (int e = tid; e < p.L; e += kThreads) {
     int64_t b, c;
@@ -362,8 +362,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     s_begin[e] = (int)b;
     s_count[e] = (int)c;
     mx = max(mx, (int)c);
+    held += rows_held(c);
   }
   atomicMax(&s_max, mx);
+  if (MODE != kForward && p.terms == kTermsByRows) {
+    held = __reduce_add_sync(0xffffffffu, held);
+    if (lane == 0) atomicAdd(&s_held, held);
+  }
   if (!__syncthreads_and(ascending)) {
     // Each against all before it. One that shares rows with an earlier one counts as
     // empty: its rows are written once, and there are no more tiles than the host
@@ -473,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int max_n = MODE == kGradW ? 256 : min(kTileRows, (s_max + 15) / 16 * 16);
   const int b_bytes = MODE == kGradW ? min((p.wrows + 127) / 128, 2) * 8192
                                      : box_rows(box_index(max_n / 2)) * 128;
-  const int stage_bytes = kABytes + p.terms * b_bytes;
+  const int terms = MODE == kForward ? 1 : p.terms == kTermsByRows ? terms_of(s_held, p.L) : p.terms;
+  const int stage_bytes = kABytes + terms * b_bytes;
   const int stages = min(kMaxStages, p.ring_bytes / stage_bytes);
   const uint32_t ring_s = smem_addr(ring);
 
@@ -499,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int half = t.n / 2;
         const int box = MODE == kGradW ? 0 : box_index(half);
         const int nbox = (half + 63) / 64;  // kGradW: 64-wide boxes of the row side
-        const uint32_t b_tile = p.terms * (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
+        const uint32_t b_tile = terms * (MODE == kGradW ? nbox * 8192 : box_rows(box) * 128);
         const CUtensorMap* mb = &maps.b[box];
         const int f = t.fb * 128, brow = t.row0 + rank * half;
         int red = t.kb0 * kRedBlock;
@@ -523,13 +529,17 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_2d(dst + 8192, &maps.a, bar, f + 64, t.red_row0 + red);
             }
           } else {
-            for (int term = 0; term < p.terms; ++term) {
-              const uint32_t to = dst + term * b_bytes;
-              if constexpr (MODE == kGradW) {
-                for (int i = 0; i < nbox; ++i)
-                  tma_load_2d(to + i * 8192, mb, bar, brow + i * 64, t.red_row0 + red + term * p.R);
-              } else {
-                tma_load_2d(to, mb, bar, red, brow + term * p.R);
+            if constexpr (MODE == kForward) {
+              tma_load_2d(dst, mb, bar, red, brow);
+            } else {
+              for (int term = 0; term < terms; ++term) {
+                const uint32_t to = dst + term * b_bytes;
+                if constexpr (MODE == kGradW) {
+                  for (int i = 0; i < nbox; ++i)
+                    tma_load_3d(to + i * 8192, mb, bar, brow + i * 64, t.red_row0 + red, term);
+                } else {
+                  tma_load_3d(to, mb, bar, red, brow, term);
+                }
               }
             }
           }
@@ -614,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t a = lo + ((a_atom >> 4) << 16), b = lo + (kABytes >> 4) + ((b_atom >> 4) << 16);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b + kb_step * k, idesc, k > 0 ? 1u : (uint32_t)kb);
-            if (MODE != kForward && p.terms > 1) {
+            if (MODE != kForward && terms > 1) {
               const uint32_t b2 = b + (b_bytes >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k) mma_16bit(d, a + ka * k, b2 + kb_step * k, idesc, 1u);
@@ -651,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = 0; r < lines; r += 4) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
         };
         clear(a, 2);
-        for (int term = 0; term < p.terms; ++term) clear(a + kABytes + term * b_bytes, nbox);
+        for (int term = 0; term < terms; ++term) clear(a + kABytes + term * b_bytes, nbox);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s), leader));
@@ -904,6 +914,14 @@ bool map_2d(CUtensorMap* m, int type, const void* base, int64_t cols, int64_t ro
   return make_map(m, type, base, 2, dims, strides, box);
 }
 
+// The gradient of the pre-activations: [term, R, cols], or one term of any row stride.
+bool map_terms(CUtensorMap* m, const MatmulArgs& a, int64_t cols, int box_rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)a.R, a.terms == 1 ? 1u : 2u};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.ldg * 2, (cuuint64_t)a.R * a.ldg * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+  return make_map(m, a.type, a.g, 3, dims, strides, box);
+}
+
 template <int MODE, bool FP8>
 cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cudaStream_t s) {
   int optin = 0;
@@ -1008,7 +1026,7 @@ cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t 
   const cuuint64_t strides[2] = {row, row * a.wrows};
   const cuuint32_t box[3] = {64, 64, 1};
   bool ok = make_map(&maps.a, m.type, m.w, 3, dims, strides, box);
-  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.terms * m.R, m.ldg, 64, box_rows(i));
+  for (int i = 0; i < kBoxes; ++i) ok = ok && map_terms(&maps.b[i], m, a.wrows, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
   return launch<kGradX, false>(maps, a, max_row_tiles(m, kRows<false>) * nfp, num_sms, s);
 }
@@ -1022,7 +1040,7 @@ cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t 
   const int nfp = (m.K + 255) / 256;
   Maps maps;
   bool ok = map_2d(&maps.a, m.type, m.x, m.K, m.R, m.ldx, 64, 64);
-  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.g, a.wrows, m.terms * m.R, m.ldg, 64, 64);
+  for (int i = 0; i < kBoxes; ++i) ok = ok && map_terms(&maps.b[i], m, a.wrows, 64);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)m.L * ((a.wrows + 255) / 256) * nfp;
   return launch<kGradW, false>(maps, a, tiles, num_sms, s);

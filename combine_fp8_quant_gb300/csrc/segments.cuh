@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "kernels.h"
 
 namespace moeperm {
 
@@ -23,6 +24,14 @@ __device__ __forceinline__ bool segment(const Args& p, int e, int64_t& b, int64_
   b = c = 0;
   return false;
 }
+
+// What a count adds to the rows held, in kTermsByRows: any above the limit of all
+// experts together decides alone, so a sum of 1024 stays within 32 bits.
+__device__ __forceinline__ int rows_held(int64_t c) {
+  constexpr int64_t kMost = (int64_t)kTwoTermRows * 1024 + 1;
+  return (int)(c < kMost ? c : kMost);
+}
+__device__ __forceinline__ int terms_of(int held, int L) { return held <= kTwoTermRows * L ? 2 : 1; }
 
 // Whether two segments have a row in common.
 __device__ __forceinline__ bool share_rows(int64_t b0, int64_t c0, int64_t b1, int64_t c1) {

@@ -465,8 +465,10 @@ def test_nan_reaches_its_row_alone(dev, R, K, N, act, gated, dtype):
     assert b["dw"][hit].isnan().all() and torch.equal(b["dw"][same], g["dw"][same])
 
 
-def check_gradients(o, dout, pre, x, w, seg, N, act, gated, dw_dtype):
-    """dx, dw and dbias of every expert's rows within the bounds of test_gradients; rows of no expert as they were (9)."""
+def check_gradients(o, dout, pre, x, w, seg, N, act, gated, dw_dtype, carried=()):
+    """dx, dw and dbias of every expert's rows within the bounds of test_gradients; rows of no expert as they were (9).
+    `carried`: those of dx and dw that carry the rounding of the pre-activations' gradient along, which is then off
+    by its second rounding (half a step squared) only."""
     dtype, Nw = x.dtype, w.shape[1]
     hs, hw = torch.finfo(dtype).eps / 2, torch.finfo(dw_dtype).eps / 2
     real = torch.zeros(x.shape[0], dtype=torch.bool, device=DEV)
@@ -486,13 +488,14 @@ def check_gradients(o, dout, pre, x, w, seg, N, act, gated, dw_dtype):
             m = torch.cat([(g * p[:, N:]).abs() * 1.13, (g * p[:, :N]).abs()], 1) if gated else g.abs() * 1.13
             e32 = ACT_ERR * m
             e16 = e32 + hs * (dP.abs() + e32) + TINY
-        for got, A, B, eA, h, steps in ((o["dx"], dP, w[e].double(), e16, hs, Nw),
-                                        (o["dw"], dP.t(), x[lo:hi].double(), e16.t(), hw, n)):
-            if got is None:
+        e48 = e32 + hs * hs * (dP.abs() + e32) + TINY
+        for k, A, B, h, steps in (("dx", dP, w[e].double(), hs, Nw), ("dw", dP.t(), x[lo:hi].double(), hw, n)):
+            if o[k] is None:
                 continue
-            got = got[lo:hi] if got is o["dx"] else got[e]
+            got, eA, terms = o[k][lo:hi] if k == "dx" else o[k][e], e48 if k in carried else e16, 2 if k in carried else 1
+            eA = eA.t() if k == "dw" else eA
             want, mag = A @ B, A.abs() @ B.abs()
-            bound = eA @ B.abs() + (steps + 2) * V * (mag + eA @ B.abs())
+            bound = eA @ B.abs() + (terms * steps + 2) * V * (mag + eA @ B.abs())
             assert ((got.double() - want).abs() <= h * want.abs() + bound * (1 + h) + TINY).all(), e
         if o["dbias"] is not None:
             bound = e32.sum(0) + (n + 2) * V * (dP.abs() + e32).sum(0)
@@ -547,3 +550,39 @@ def test_segments_that_do_not_fit_count_as_empty(dev, begin, end, R, K, N):
         st.zero_()
         alone = dev.expert_matmul_grad(dout, x, w, i32(begin), i32(end), pre=pre, act=act, status=st, need=("dbias",))
         assert dev.moe_status_sync(st) == want and torch.equal(alone["dbias"], o["dbias"])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("counts", [[100, 60, 0, 3], [512, 0, 0, 0], [128] * 4, [0, 0, 0, 0], [513, 0, 0, 0]])
+def test_gradients_do_not_depend_on_the_buffer(dev, counts, dtype):
+    """The rows held decide how exact dx and dw are: the same batch in a larger buffer, or in slabs, gives equal bits,
+    and up to 128 rows an expert the rounding of the pre-activations' gradient is carried along in each."""
+    L, K, N = 4, 136, 64
+    tight, ends, R = segments(counts, 1)
+    rows = rand(1, R, K, dtype=dtype), rand(2, R, N, dtype=dtype), rand(3, R, 2 * N, dtype=dtype)
+    w = rand(4, L, 2 * N, K, dtype=dtype, gain=K ** -0.5)
+    got = []
+    for room in (R, 4 * 128, 4 * 128 + 1, 9000):  # rows of the buffer
+        if room < R:
+            continue
+        x, dout, pre = (torch.full((room, t.shape[1]), float("nan"), device=DEV, dtype=dtype) for t in rows)
+        for big, t in zip((x, dout, pre), rows):
+            big[:R] = t
+        dx = torch.full((room, K), 9.0, device=DEV, dtype=dtype)
+        o = dev.expert_matmul_grad(dout, x, w, i32(tight), i32(ends), pre=pre, act="silu", gated=True, dx=dx)
+        check_gradients(o, dout, pre, x, w, list(zip(tight, ends)), N, "silu", True, dtype,
+                        ("dx", "dw") if sum(counts) <= 128 * L else ())
+        got.append((o["dx"][:R], o["dw"]))
+    for cap in (max(max(counts), 1), 4000):
+        slabs = [torch.full((L, cap, t.shape[1]), float("nan"), device=DEV, dtype=dtype) for t in rows]
+        for e, (lo, hi) in enumerate(zip(tight, ends)):
+            for big, t in zip(slabs, rows):
+                big[e, :hi - lo] = t[lo:hi]
+        dx = torch.full((L, cap, K), 9.0, device=DEV, dtype=dtype)
+        o = dev.expert_matmul_grad(slabs[1], slabs[0], w, masked_m=i32(counts), pre=slabs[2], act="silu", gated=True, dx=dx)
+        flat = got[0][0].clone()
+        for e, (lo, hi) in enumerate(zip(tight, ends)):
+            flat[lo:hi] = o["dx"][e, :hi - lo]
+        got.append((flat, o["dw"]))
+    for dx, dw in got[1:]:
+        assert torch.equal(dx, got[0][0]) and torch.equal(dw, got[0][1])
