@@ -267,6 +267,7 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
   }
   const bool has_act = act != MOE_ACT_NONE || gated;
   const int terms = grad_terms(R, L, /*dense=*/seg_end == nullptr);
+  const int dw_terms = dw && dw_type == MOE_F32 ? 2 : terms;  // (dx does not depend on what dw is)
   if (!rows_ok(dout, ldd, N, 2)) return MOE_ERR_INVALID_ARG;
   if (has_act && !rows_ok(pre, ld_pre, Nw, 2)) return MOE_ERR_INVALID_ARG;
   if (dw && !rows_ok(x, ldx, K, 2)) return MOE_ERR_INVALID_ARG;
@@ -283,7 +284,7 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     a.dout = dout; a.ldd = ldd; a.pre = pre; a.ld_pre = ld_pre; a.R = R; a.L = L; a.N = N; a.gated = gated;
     a.act = (int)act; a.seg_begin = seg_begin; a.seg_end = seg_end; a.cap = cap;
     a.dpre = has_act ? workspace : nullptr;
-    a.terms = terms;
+    a.terms = dw_terms;
     a.dbias = dbias;
     a.ws = reinterpret_cast<float*>(static_cast<char*>(workspace) + dpre_bytes(R, Nw));
     a.splits = act_grad_splits(R, L, N);
@@ -300,7 +301,7 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     if (launch_matmul_grad_x(m, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
   if (dw) {
-    m.out = dw; m.ldo = K; m.out_type = (int)dw_type;
+    m.out = dw; m.ldo = K; m.out_type = (int)dw_type; m.terms = has_act ? dw_terms : 1;
     if (launch_matmul_grad_w(m, sms, s) != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;

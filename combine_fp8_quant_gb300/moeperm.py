@@ -704,9 +704,10 @@ def expert_matmul_grad(dout, x, w, starts=None, psum=None, pre=None, act="none",
                        masked_m=None, need=("dx", "dw"), dx=None, dw=None, dbias=None,
                        dw_dtype=None, workspace=None, status=None):
     """Gradients of expert_matmul for the output gradient dout: those of dx, dw and
-    dbias that `need` names or that a tensor is given for, from the kept `pre` (not needed without act and gate). dw
-    [as w] in dw_dtype (w's type, or float32), dbias [L, N or 2N] float32; both
-    are written in full, dx on the experts' rows. The residual's gradient is
+    dbias that `need` names or that a tensor is given for, from the kept `pre` (not
+    needed without act and gate). dw [as w] in dw_dtype: w's type, or float32, which
+    keeps the gradient of `pre` beyond its 16 bits too. dbias [L, N or 2N] float32;
+    both are written in full, dx on the experts' rows. The residual's gradient is
     dout. Returns a dict (dx, dw, dbias, status)."""
     dtype = _elem(x, FLOATS[:2], "x")
     L, N, K = _expert_weights(w, gated)

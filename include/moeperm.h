@@ -436,8 +436,8 @@ size_t moe_expert_matmul_grad_workspace_bytes(int64_t R, int32_t L, int32_t Nw);
  * moe_expert_matmul_grad -- gradients of moe_expert_matmul for the output gradient
  * dout (the residual's gradient is dout itself). With dP the gradient of P,
  * formed in fp32 from dout and the kept P and rounded to `type` for the products
- * (while the experts hold at most 128 rows on average, in a buffer of any size,
- * together with the rounding of what that left over):
+ * (together with the rounding of what that left over, while the experts hold at most
+ * 128 rows on average, in a buffer of any size, and always for dw in F32):
  *   dx[r]  = sum_n dP[r, n] * w[e, n]        rows of no expert are not written
  *   dw[e]  = sum over the rows of e of dP[r]^T x[r]     (written in full: 0 without rows)
  *   dbias[e] = sum over the rows of e of dP[r]   (f32, written in full)

@@ -586,3 +586,23 @@ def test_gradients_do_not_depend_on_the_buffer(dev, counts, dtype):
         got.append((flat, o["dw"]))
     for dx, dw in got[1:]:
         assert torch.equal(dx, got[0][0]) and torch.equal(dw, got[0][1])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("act,gated", [("silu", True), ("gelu", False)])
+@pytest.mark.parametrize("counts,K,N", [([300, 0, 170], 136, 128), ([700], 264, 64), ([257, 640], 64, 320)])
+def test_weight_gradients_in_fp32_carry_the_rounding(dev, counts, K, N, act, gated, dtype):
+    """With any number of rows: in 32 bits dw has no rounding of its own, so it is given none of the pre-activations'
+    gradient's either. dx is the same beside a dw of either type."""
+    starts, ends, R = segments(counts, 1)
+    L, Nw = len(counts), 2 * N if gated else N
+    x, dout, pre = rand(1, R, K, dtype=dtype), rand(2, R, N, dtype=dtype), rand(3, R, Nw, dtype=dtype)
+    w = rand(4, L, Nw, K, dtype=dtype, gain=K ** -0.5)
+    call = lambda t, **k: dev.expert_matmul_grad(dout, x, w, i32(starts), i32(ends), pre=pre, act=act, gated=gated,
+                                                 dw_dtype=t, **k)
+    o = call(torch.float32, need=("dx", "dw", "dbias"))
+    seg = list(zip(starts, ends))
+    check_gradients(o, dout, pre, x, w, seg, N, act, gated, torch.float32, ("dw",))
+    alone, half = call(torch.float32, need=("dw",)), call(dtype)
+    assert torch.equal(alone["dw"], o["dw"]) and torch.equal(half["dx"], o["dx"])
+    check_gradients(half, dout, pre, x, w, seg, N, act, gated, dtype)
