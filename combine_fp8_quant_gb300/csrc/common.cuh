@@ -234,9 +234,10 @@ __device__ __forceinline__ void bulk_store_s2g(void* gdst, uint32_t ssrc, uint32
 }
 
 // mbarriers (shared-memory addresses). Every wait is bounded: it gives up
-// after kWaitCycles of the SM clock (about two seconds, where the longest
-// legitimate wait is far below a millisecond) and the caller flags
-// kStTimeout instead of hanging the GPU.
+// after kWaitCycles of the SM clock (about two seconds) and the caller flags
+// kStTimeout instead of hanging the GPU. That is far above any wait for one
+// copy or one step; a wait for a whole reduction adds the time of its length
+// (limit_for in matmul.cu), since a reduction over 10^8 rows takes seconds.
 constexpr long long kWaitCycles = 4000000000ll;
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);

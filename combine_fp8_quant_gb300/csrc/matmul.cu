@@ -142,12 +142,13 @@ __device__ __forceinline__ int box_index(int half) {  // smallest box of at leas
 }
 
 // A bounded wait that other roles can cut short.
-__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop) {
+__device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop,
+                                             long long limit = kWaitCycles) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_try_wait(bar, parity)) {
     if (*stop) return false;
-    if (clock64() - t0 > kWaitCycles) {
+    if (clock64() - t0 > limit) {
       *stop = 1;
       return false;
     }
@@ -156,9 +157,14 @@ __device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, vola
 }
 
 // The same for a whole warp: every lane gets the same answer.
-__device__ __forceinline__ bool warp_wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop) {
-  return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop));
+__device__ __forceinline__ bool warp_wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop,
+                                                  long long limit = kWaitCycles) {
+  return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop, limit));
 }
+
+// The limit of a wait that lasts while `blocks` reduction blocks go through the
+// products: a block takes about 500 cycles, 2100 where all SMs wait for HBM.
+__device__ __forceinline__ long long limit_for(long long blocks) { return kWaitCycles + blocks * 8192; }
 
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, bool f16) {
   return f16 ? pack_f16x2(lo, hi) : pack_bf16x2(lo, hi);
@@ -646,12 +652,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // its way to the products; the others go straight there.
     int at = 0;          // stage of the tile's first block
     uint32_t phase = 0;  // bit s: parity of the next wait on s_raw[s]
+    long long blocks = 0;  // of the tiles since the last wait (64 more for each one's epilogue)
     bool ok = true;
     for (Walk k = first(); ok && more(k); step(k)) {
       const Tile t = tile_at(k);
+      blocks += t.nkb + 64;
       if (t.nkb > 0 && t.tail < 64) {
         const int s = (at + t.nkb - 1) % stages;
-        if (!(ok = warp_wait_or_stop(smem_addr(s_raw + s), (phase >> s) & 1, &s_stop))) break;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_raw + s), (phase >> s) & 1, &s_stop, limit_for(blocks)))) break;
+        blocks = 0;
         phase ^= 1u << s;
         // four lines at a time, eight lanes each
         uint8_t* a = ring + s * stage_bytes + (t.tail + (lane >> 3)) * 128 + (lane & 7) * 16;
@@ -729,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile t = tile_at(k);
       const int as = acc_it & 1;
       if (t.nkb > 0) {
-        if (!warp_wait_or_stop(smem_addr(s_tfull + as), (acc_it >> 1) & 1, &s_stop)) break;
+        if (!warp_wait_or_stop(smem_addr(s_tfull + as), (acc_it >> 1) & 1, &s_stop, limit_for(t.nkb))) break;
         tc_fence_after();
       }
       const uint32_t acc = tmem + as * kTileRows + ((uint32_t)(q * 32) << 16);
@@ -742,9 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_expect_tx(smem_addr(&s_recv), (p.splits - 1) * run_bytes);
             for (int i = 1; i < p.splits; ++i) mbar_arrive_mapped(map_to_rank(smem_addr(&s_go), 2 * i + rank));
           }
-          if (!warp_wait_or_stop(smem_addr(&s_recv), 0, &s_stop)) break;
+          if (!warp_wait_or_stop(smem_addr(&s_recv), 0, &s_stop, limit_for(t.nkb))) break;
         } else {
-          if (!warp_wait_or_stop(smem_addr(&s_go), 0, &s_stop)) break;
+          if (!warp_wait_or_stop(smem_addr(&s_go), 0, &s_stop, limit_for(t.nkb))) break;
           const uint32_t to = map_to_rank(ring_s, rank) + (split - 1) * run_bytes + q * 4096 + lane * 16;
           const uint32_t bar = map_to_rank(smem_addr(&s_recv), rank);
           for (int c0 = 0; c0 < t.rows; c0 += 32) {

@@ -77,8 +77,9 @@ typedef enum {
 #define MOE_STATUS_LIVE_OVERFLOW 0x2
 #define MOE_STATUS_BAD_LAYOUT 0x4
 /* A kernel that waits for its own asynchronous copies or tensor-core work
- * (moe_permute, moe_expert_matmul, moe_expert_matmul_grad) gives up after
- * about two seconds and sets this bit; the call's outputs are then incomplete. */
+ * (moe_permute, moe_expert_matmul, moe_expert_matmul_grad) gives up about two
+ * seconds after the longest that the wait can take, and sets this bit; the
+ * call's outputs are then incomplete. */
 #define MOE_STATUS_TIMEOUT 0x8
 
 /*

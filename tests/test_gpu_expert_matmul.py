@@ -606,3 +606,24 @@ def test_weight_gradients_in_fp32_carry_the_rounding(dev, counts, K, N, act, gat
     alone, half = call(torch.float32, need=("dw",)), call(dtype)
     assert torch.equal(alone["dw"], o["dw"]) and torch.equal(half["dx"], o["dx"])
     check_gradients(half, dout, pre, x, w, seg, N, act, gated, dtype)
+
+
+def test_a_reduction_of_seconds_is_waited_for(dev):
+    """dW over 1.2e9 rows: the epilogue waits longer than a single step may take. The few rows that are not zero hold
+    small whole numbers, so the sums are exact."""
+    R, K, N = 1_200_000_000, 8, 8
+    x, dout = (torch.zeros(R, 8, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    at = torch.tensor([0, 63, 64, 999_999_937, 1 << 30, R - 1], device=DEV)
+    vx, vd = (torch.randint(-3, 4, (at.numel(), 8), device=DEV).bfloat16() for _ in range(2))
+    x[at], dout[at] = vx, vd
+    w, st = torch.zeros(N, K, device=DEV, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32, device=DEV)
+    o = dev.expert_matmul_grad(dout, x, w, need=("dw",), dw_dtype=torch.float32, status=st)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
+    assert torch.equal(o["dw"], vd.float().t() @ vx.float())
+
+
+def test_a_wait_that_ran_out_is_the_gravest_status(dev):
+    """The status word's bits, set from the host: a timeout comes before a bad layout and the rest."""
+    for bits, want in ((8, dev.MOE_ERR_TIMEOUT), (15, dev.MOE_ERR_TIMEOUT), (12, dev.MOE_ERR_TIMEOUT), (7, dev.MOE_ERR_BAD_LAYOUT),
+                       (3, dev.MOE_ERR_LIVE_OVERFLOW), (1, dev.MOE_ERR_OVERFLOW), (0, dev.MOE_OK)):
+        assert dev.moe_status_sync(i32([bits])) == want
