@@ -263,3 +263,36 @@ def test_gradients_of_very_small_and_large_rows(dev, sx, sy, mode):
     for k, (v, mag) in want.items():
         bound = (2 * C + T) * U * mag + (U * v.abs() if k in ("dx", "dy") else 0)
         assert torch.isfinite(o[k]).all() and ((o[k].double() - v).abs() <= bound).all(), k
+
+
+# More rows than the grid holds: the second row of a pair, the walk over the rows and the ring's wrap. `H` in 16-byte
+# vectors: one per thread and up to 2048 (rings of three slots, of one, and 1024 threads).
+LONG = [  # T, vectors, gate, post, pre
+    (20011, 17, "token", True, True), (20011, 64, "channel", True, True), (3001, 155, "token", False, True),
+    (2501, 896, "channel", True, True), (1201, 897, "none", True, False), (1001, 1024, "token", True, True),
+    (999, 1025, "channel", True, True), (701, 2048, "token", True, True), (650, 2048, "channel", False, True),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,vectors,mode,post,pre", LONG)
+def test_more_rows_than_the_grid(dev, dtype, T, vectors, mode, post, pre):
+    H = vectors * 16 // torch.finfo(dtype).bits * 8
+    test_forward(dev, dtype, T, H, mode, post, pre)
+    test_gradients(dev, dtype, T, H, mode, post, pre)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("T,vectors", [(20011, 17), (2501, 896), (701, 2048)])
+def test_more_rows_than_the_grid_without_a_block_output(dev, dtype, T, vectors):
+    """One tensor a row in the ring, and two backward."""
+    H = vectors * 16 // torch.finfo(dtype).bits * 8
+    s = make(T, H, dtype, "none", False, True, y=False)
+    o = dev.block_norm(s["x"], w_pre=s["w_pre"], eps=EPS, save_rstd=True)
+    x, dh = s["x"].double(), rand(8, T, H, dtype=dtype)
+    h, hs = x * rms64(x) * s["w_pre"].double(), torch.finfo(dtype).eps / 2
+    assert ((o["h"].double() - h).abs() <= (hs + 2 * C * U) * h.abs() + TINY).all()
+    g = dev.block_norm_grad(None, dh, s["x"], w_pre=s["w_pre"], rstd_pre=o["rstd_pre"])
+    for k, (v, mag) in grads64(s, "none", 1.0, None, dh, o["rstd_pre"], None).items():
+        bound = hs * v.abs() + 2 * C * U * mag * (1 + hs) + TINY if k == "dx" else (2 * C + T) * U * mag
+        assert ((g[k].double() - v).abs() <= bound).all(), k
