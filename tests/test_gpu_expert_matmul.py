@@ -627,3 +627,80 @@ def test_a_wait_that_ran_out_is_the_gravest_status(dev):
     for bits, want in ((8, dev.MOE_ERR_TIMEOUT), (15, dev.MOE_ERR_TIMEOUT), (12, dev.MOE_ERR_TIMEOUT), (7, dev.MOE_ERR_BAD_LAYOUT),
                        (3, dev.MOE_ERR_LIVE_OVERFLOW), (1, dev.MOE_ERR_OVERFLOW), (0, dev.MOE_OK)):
         assert dev.moe_status_sync(i32([bits])) == want
+
+
+# Several hundred tiles, so that every pair of CTAs takes some one after the other: both accumulators and their hand-back,
+# the ring and the scale words going on from tile to tile, and tiles of every height beside each other.
+
+def ragged(seed, L, most):
+    """Counts per expert: none, whole blocks of 64 rows, and any other number up to `most`."""
+    rng = np.random.default_rng(seed)
+    c = rng.integers(0, most + 1, L)
+    c[::5] = 64 * rng.integers(0, most // 64 + 1, c[::5].size)
+    c[rng.integers(0, L, 2)] = 0
+    return c.tolist()
+
+
+def padded(R, seg):
+    """Whether a row is of no expert."""
+    pad = torch.ones(R, dtype=torch.bool, device=DEV)
+    for lo, hi in seg:
+        pad[lo:hi] = False
+    return pad
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("act,gated,residual", [("silu", True, False), ("gelu", False, True), ("relu", True, True)])
+def test_forward_of_many_tiles(dev, act, gated, residual, dtype):
+    L, K, N = 48, 200, 528
+    starts, ends, R = segments(ragged(1, L, 700), 8, gap=1)
+    seg, Nw = list(zip(starts, ends)), 2 * N if gated else N
+    x, w = rand(1, R, K, dtype=dtype), rand(2, L, Nw, K, dtype=dtype, gain=K ** -0.5)
+    bias, res = rand(3, L, Nw), rand(4, R, N, dtype=dtype) if residual else None
+    x[padded(R, seg)] = float("nan")
+    out, pre = torch.full((R, N), 9.0, device=DEV, dtype=dtype), torch.full((R, Nw), 9.0, device=DEV, dtype=dtype)
+    call = lambda o: dev.expert_matmul(x, w, i32(starts), i32(ends), bias=bias, act=act, gated=gated, residual=res, out=o, pre=pre)
+    call(out)
+    check_forward(out, pre, x.double(), w.double(), bias, res, seg, N, act, gated, dtype)
+    assert torch.equal(out, call(torch.full_like(out, 9.0)))
+
+
+@pytest.mark.parametrize("L,most,K,N,gated", [(40, 700, 1152, 272, True), (64, 480, 512, 392, False), (256, 12, 640, 128, True)])
+def test_forward_of_many_tiles_e4m3(dev, L, most, K, N, gated):
+    starts, ends, R = segments(ragged(2, L, max(most, 64)) if most >= 64 else [int(c) for c in np.arange(L) % (most + 1)], 4)
+    seg, Nw = list(zip(starts, ends)), 2 * N if gated else N
+    q, sc, ld, xv = quant(rand(1, R, K) * torch.exp2(torch.randint(-6, 7, (R, 1), device=DEV).float()))
+    wq, wsc, ldw, wv = quant(rand(2, L * Nw, K, gain=K ** -0.5))
+    pad = padded(R, seg)
+    q.view(torch.uint8)[pad] = 0x7F
+    sc[:, :R][:, pad] = -1
+    out = torch.full((R, N), 9.0, device=DEV, dtype=torch.bfloat16)
+    call = lambda o: dev.expert_matmul(q, wq.view(L, Nw, K), i32(starts), i32(ends), act="silu", gated=gated, x_scales=sc,
+                                       ld_xs=ld, w_scales=wsc, ld_ws=ldw, out=o)
+    call(out)
+    check_forward(out, None, xv, wv.view(L, Nw, K), None, None, seg, N, "silu", gated, torch.bfloat16)
+    assert torch.equal(out, call(torch.full_like(out, 9.0)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("L,most,K,N,act,gated", [(48, 600, 520, 264, "silu", True), (96, 128, 520, 264, "gelu", False),
+                                                  (96, 200, 520, 272, "silu", True), (48, 600, 520, 520, "none", False)])
+def test_gradients_of_many_tiles(dev, L, most, K, N, act, gated, dtype):
+    """With one term and with two (most <= 200: at most 128 rows an expert on average)."""
+    N = N // 16 * 16 if gated else N
+    counts = ragged(3, L, most)
+    starts, ends, R = segments(counts, 8, gap=3)
+    seg, Nw = list(zip(starts, ends)), 2 * N if gated else N
+    x, dout, pre = rand(1, R, K, dtype=dtype), rand(2, R, N, dtype=dtype), rand(3, R, Nw, dtype=dtype)
+    w = rand(4, L, Nw, K, dtype=dtype, gain=K ** -0.5)
+    for t in (x, dout, pre):
+        t[padded(R, seg)] = float("nan")
+    two = sum(counts) <= 128 * L
+    assert two == (most <= 200)
+    for dwt in (dtype, torch.float32):
+        call = lambda: dev.expert_matmul_grad(dout, x, w, i32(starts), i32(ends), pre=pre, act=act, gated=gated, dw_dtype=dwt,
+                                              dx=torch.full((R, K), 9.0, device=DEV, dtype=dtype), need=("dx", "dw", "dbias"))
+        o = call()
+        check_gradients(o, dout, pre, x, w, seg, N, act, gated, dwt, ("dx", "dw") if two else ("dw",) if dwt is torch.float32 else ())
+        again = call()
+        assert all(torch.equal(o[k], again[k]) for k in ("dx", "dw", "dbias"))
