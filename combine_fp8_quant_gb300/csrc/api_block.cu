@@ -69,6 +69,8 @@ moe_status_t moe_permute(const void* x, int64_t ldx, moe_elem_t type, int32_t T,
   if (T > 0 && (!rows_ok(x, ldx, H, es) || !topk_ids || !src2dst)) return MOE_ERR_INVALID_ARG;
   if (bound > 0 && (!m_indices || !xs || !aligned16(xs))) return MOE_ERR_INVALID_ARG;
   if (!counts || !starts || !psum || !total || (row_weights && !topk_weights)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({d_num_tokens, topk_ids, topk_weights, m_indices, src2dst, counts, starts, psum, total, row_weights, d_status}))
+    return MOE_ERR_INVALID_ARG;
   if (!workspace || !aligned16(workspace) || workspace_bytes < moe_workspace_bytes(T, K, L))
     return MOE_ERR_INVALID_ARG;
   const int sms = num_sms_cached();
@@ -108,6 +110,7 @@ moe_status_t moe_combine_ex(const void* y, int64_t ldy, moe_elem_t type, int64_t
     return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!src2dst || !out || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({src2dst, w, d_num_tokens, d_status})) return MOE_ERR_INVALID_ARG;
   if (R > 0 && !rows_ok(y, ldy, H, es)) return MOE_ERR_INVALID_ARG;
   const int sms = num_sms_cached();
   if (sms <= 0) return MOE_ERR_CUDA;
@@ -127,6 +130,7 @@ moe_status_t moe_combine_grad(const void* dout, int64_t ldd, const void* y, int6
   if (!dy && !dw) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!src2dst || !rows_ok(dout, ldd, H, es)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({src2dst, w, d_num_tokens, dw, d_status})) return MOE_ERR_INVALID_ARG;
   if (R > 0 && dw && !rows_ok(y, ldy, H, es)) return MOE_ERR_INVALID_ARG;
   if (R > 0 && dy && !rows_ok(dy, lddy, H, es)) return MOE_ERR_INVALID_ARG;
   const int sms = num_sms_cached();
@@ -145,6 +149,7 @@ moe_status_t moe_block_norm(const void* x, int64_t ldx, const void* y, int64_t l
   if (!norm_shape_ok(T, H, es) || !norm_parts_ok(T, y, w_post, gate, gate_mode, w_pre))
     return MOE_ERR_INVALID_ARG;
   if (!(eps >= 0.0f) || !aligned16(w_post) || !aligned16(w_pre)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({rstd_post, rstd_pre})) return MOE_ERR_INVALID_ARG;
   if (T == 0) return MOE_OK;
   if (!rows_ok(x, ldx, H, es) || (y && (!rows_ok(y, ldy, H, es) || !x_out || !aligned16(x_out))) ||
       (w_pre && (!h || !aligned16(h))))
@@ -175,6 +180,7 @@ moe_status_t moe_block_norm_grad(const void* dx_out, int64_t ld_dxo, const void*
   if (!norm_shape_ok(T, H, es) || !norm_parts_ok(T, y, w_post, gate, gate_mode, w_pre))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(w_post) || !aligned16(w_pre)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({rstd_post, rstd_pre, dw_post, dgate, dw_pre})) return MOE_ERR_INVALID_ARG;
   if ((w_post && !dw_post) || (w_pre && !dw_pre)) return MOE_ERR_INVALID_ARG;
   if (gate_mode == MOE_GATE_CHANNEL && !dgate) return MOE_ERR_INVALID_ARG;
   if ((w_post || w_pre || gate_mode == MOE_GATE_CHANNEL) &&
@@ -219,6 +225,7 @@ moe_status_t moe_expert_matmul(const void* x, int64_t ldx, moe_elem_t type, cons
   if (!w || !aligned16(w)) return MOE_ERR_INVALID_ARG;
   const int32_t Nw = gated ? 2 * N : N;
   if (fp8 && (!w_scales || !aligned16(w_scales) || ld_ws < (int64_t)L * Nw || ld_ws % 4)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({seg_begin, seg_end, d_status})) return MOE_ERR_INVALID_ARG;
   if (R == 0) return MOE_OK;
   if (!rows_ok(x, ldx, K, es) || !out || ldo < N || (residual && ld_res < N) || (pre && ld_pre < Nw))
     return MOE_ERR_INVALID_ARG;
@@ -257,6 +264,7 @@ moe_status_t moe_expert_matmul_grad(const void* dout, int64_t ldd, const void* x
     return MOE_ERR_INVALID_ARG;
   if (K < 1 || K % 8 || (!dx && !dw && !dbias)) return MOE_ERR_INVALID_ARG;
   if (dw && (dw_type != type && dw_type != MOE_F32)) return MOE_ERR_INVALID_ARG;
+  if (!words_ok({seg_begin, seg_end, d_status})) return MOE_ERR_INVALID_ARG;
   const int32_t Nw = gated ? 2 * N : N;
   const size_t dw_bytes = (size_t)L * Nw * K * (dw_type == MOE_F32 ? 4 : 2);
   cudaStream_t s = cu(stream);

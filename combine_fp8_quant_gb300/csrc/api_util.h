@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "../../include/moeperm.h"
 #include "common.cuh"
 
@@ -21,6 +23,13 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // (NULL is aligned: whether it is allowed is another check)
 inline bool aligned_to(const void* p, int n) { return reinterpret_cast<uintptr_t>(p) % (unsigned)n == 0; }
+
+// Vectors of 32-bit elements that kernels read or write one element at a time.
+inline bool words_ok(std::initializer_list<const void*> v) {
+  for (const void* p : v)
+    if (!aligned_to(p, 4)) return false;
+  return true;
+}
 
 inline int num_sms_cached() {
   int n = 0;

@@ -281,3 +281,20 @@ def test_a_gradient_workspace_serves_fewer_rows(mp, L, Nw):
         edges |= {m * L - 1, m * L, m * L + 1}
     sizes = [mp.moe_expert_matmul_grad_workspace_bytes(R, L, Nw) for R in sorted(edges)]
     assert sizes == sorted(sizes)
+
+
+WORDS = {  # 32-bit vectors of each call
+    "moe_permute": (PERMUTE, "d_num_tokens topk_ids topk_weights m_indices src2dst counts starts psum total row_weights d_status"),
+    "moe_combine_ex": (COMBINE, "src2dst w d_num_tokens d_status"),
+    "moe_combine_grad": (COMBINE_GRAD, "src2dst w d_num_tokens dw d_status"),
+    "moe_block_norm": (NORM, "rstd_post rstd_pre"),
+    "moe_block_norm_grad": (NORM_GRAD, "rstd_post rstd_pre dw_post dgate dw_pre"),
+    "moe_expert_matmul": (MATMUL, "seg_begin seg_end d_status bias"),
+    "moe_expert_matmul_grad": (GRAD, "seg_begin seg_end d_status dbias"),
+}
+
+
+@pytest.mark.parametrize("name,arg", [(n, a) for n, (_, args) in WORDS.items() for a in args.split()])
+def test_vectors_of_words_start_at_a_word(mp, name, arg):
+    """Kernels read and write them an element at a time, which faults at any other address."""
+    assert call(mp, name, WORDS[name][0], {arg: FAKE + 2}) == mp.MOE_ERR_INVALID_ARG
