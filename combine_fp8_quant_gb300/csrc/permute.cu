@@ -81,7 +81,6 @@ struct Mover {
     if (lit < ntok) load_next();
   }
   __device__ void run(const int* rows, int stride) {
-    if (issued < p.stages) refill(rows, stride);
     while (done < issued) {
       const int slot = done % p.stages;
       const bool landed = mbar_wait(smem_addr(bars + slot), (uint32_t)(done / p.stages) & 1u);
