@@ -455,12 +455,15 @@ cudaError_t launch_backward(const NormArgs& a, int num_sms, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// Elements per thread. Forward: 8, up to 896 threads (72 registers hold the
-// weights of 8 columns and two rows); backward: 16, up to 512 threads (128
-// registers, weights and sums of 16 columns): half the warps repeat the row's
-// reduction and scalars. Measured on 8192 x 7168 in bf16: forward 90.6 us with 8
-// and 94.7 with 16, backward 158 with 8 and 152 with 16. Longer rows take 16 and
-// up to 1024 threads.
+// Elements per thread. Forward: 8 while a CTA's threads can hold a row, compiled for
+// 896 threads (72 registers hold the weights of 8 columns and two rows) or for 1024
+// (64, which spill a little). Backward: 16, up to 512 threads (128 registers, weights
+// and sums of 16 columns): half the warps repeat the row's reduction and scalars.
+// Longer rows take 16 and up to 1024 threads. Measured in bf16 (us):
+//   forward, 8 elements, 896 / 1024 threads     16384 x 4096  86 / 96   40000 x 2048  119 / 121
+//                                               8192 x 7168 without y   41 / 47
+//   forward, 8 elements / 16, 1024 threads      8192 x 7176   88 / 142  8192 x 8192    89 / 147
+//   backward, 8 / 16 elements                   8192 x 7168  158 / 152
 template <int TYPE>
 cudaError_t launch_type(const NormArgs& a, bool grad, int num_sms, cudaStream_t s) {
   if (grad) {
@@ -468,6 +471,7 @@ cudaError_t launch_type(const NormArgs& a, bool grad, int num_sms, cudaStream_t 
     return launch_backward<TYPE, 16, 1024>(a, num_sms, s);
   }
   if (a.H <= 8 * 896) return launch_forward<TYPE, 8, 896>(a, num_sms, s);
+  if (a.H <= 8 * 1024) return launch_forward<TYPE, 8, 1024>(a, num_sms, s);
   return launch_forward<TYPE, 16, 1024>(a, num_sms, s);
 }
 
