@@ -13,9 +13,10 @@
 //   dgate = sum over t (or h) of scale * g * n;      dw_post = sum_t u * yh
 //   dy = rstd_post * (u * w_post - yh * mean(u * w_post * yh))     (no w_post: dy = u)
 //
-// Both kernels read every tensor once and are bound by HBM (8192 x 7168 in bf16:
-// forward 470 MB in 83 us, 5.7 TB/s; backward 705 MB in 143 us, 4.9 TB/s, where
-// issuing the arithmetic takes over half of the cycles). One CTA holds a row, 8
+// Both kernels read every tensor once. Forward is bound by HBM (8192 x 7168 in bf16:
+// 470 MB in 83 us, 5.7 TB/s); backward (705 MB in 136 us, 5.2 TB/s) HBM is busy 62% and
+// issue 45% of the time, and a row's reduction and barrier with one CTA on an SM are
+// what it waits for. One CTA holds a row, 8
 // (or 16) elements per thread, and walks rows strided by the grid. The rows to
 // come arrive by asynchronous copies in a ring of shared memory whose slots are
 // private to each thread (a thread copies and reads its own vectors), so loads

@@ -38,13 +38,15 @@
 // over distributed shared memory) and adds them in a fixed order; every cluster
 // then has one tile at most, so nothing has to be handed back.
 //
-// Measured on GB300 (2 x features counted for gated weights): bf16, 16 experts,
-// 16382 rows, 2048 x 2816, P kept: 124 us, 1520 TFLOP/s; its dx 110 us (1710), dW
-// 115 us (1640); e4m3, 64 experts, 32768 rows, 7168 x 4096: 664 us (2900 TFLOP/s)
-// a single pass, 767 us at the 1400 W power limit (1470 MHz) pass after pass; e4m3
-// decode, 32 experts with 4 rows each, 7168 x 4096: 140 us, 6.6 TB/s of weights.
-// Large products are bound by the tensor cores and the shared-memory port (a tile
-// of 176 rows moves 55 KB per 352 cycles of products), decode by HBM.
+// Measured on GB300 (2 x features counted for gated weights), single passes: bf16, 16
+// experts, 16382 rows, 2048 x 2816, P kept: 124 us, 1520 TFLOP/s, tensor cores 78% busy;
+// its dx 110 us (1710, 87%), dW 115 us (1640, 84%); e4m3, 64 experts, 32768 rows, 7168 x
+// 4096: 664 us (2900 TFLOP/s, 68%). Pass after pass the 1400 W power cap lowers the clock:
+// 140 to 145 us at 1600 to 1650 MHz, e4m3 721 to 737 us at 1250 to 1350 MHz. e4m3 decode,
+// 32 experts with 4 rows each, 7168 x 4096: 136 to 140 us, 6.7 TB/s of weights. Large
+// products are bound by the tensor cores and the shared-memory port (a tile of 176 rows
+// moves 55 KB per 352 cycles of products), decode by HBM, a weight gradient over few
+// rows by its epilogue.
 //
 // The gradient of the pre-activations enters both backward products in 16 bits. While
 // the experts hold few rows it comes as two terms, its rounding and what that left
@@ -286,6 +288,8 @@ __device__ __forceinline__ void add_rows(uint8_t* st, float (&a)[16], float (&b)
   __syncwarp();
 }
 
+// v / (1 + e^-v), to about 2 + 1.2 |v| ulp; below about -87, where e^-v leaves the range
+// of the quotient, it is 0 (the value is above -1.5e-36).
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 // v * (the normal distribution function): no cancellation for negative v
 __device__ __forceinline__ float gelu(float v) { return v * normcdff(v); }
