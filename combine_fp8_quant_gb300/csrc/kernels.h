@@ -265,6 +265,69 @@ cudaError_t launch_block_norm(const NormArgs& a, int type, int num_sms, cudaStre
 cudaError_t launch_block_norm_grad(const NormArgs& a, int type, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// Router: choice of experts, balance and z losses, gradient of the logits
+// ---------------------------------------------------------------------------
+constexpr int kMaxRouted = 1024;   // experts a router chooses from
+constexpr int kMaxGroups = 4096;   // groups of tokens of a balance loss
+struct RouteArgs {
+  const void* logits;          // [T, ld]
+  int64_t ld;
+  int32_t T;
+  const int32_t* d_num_tokens;
+  int32_t E, K;
+  int32_t sigmoid, renorm;
+  const float* bias;           // optional [E]
+  float scale;
+  int32_t* ids;                // [T, K]
+  float* weights;
+  int32_t* status;
+};
+cudaError_t launch_route(const RouteArgs& a, int type, int num_sms, cudaStream_t s);
+
+struct GroupArgs {
+  const int32_t* begin;        // [Q] (nullptr: one group of all live tokens)
+  const int32_t* end;
+  int32_t Q;
+};
+// CTAs of the losses' first launch at most (two to an SM).
+constexpr int kBalanceParts = 304;
+struct BalanceArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t T;
+  const int32_t* d_num_tokens;
+  int32_t E, K, sigmoid;
+  const int32_t* ids;
+  GroupArgs g;
+  float* loss;                 // [2]
+  int32_t* counts;             // [Q, E]
+  float* prob_sums;            // [Q, E]
+  float* ws;
+  int32_t* status;
+};
+size_t balance_ws_bytes(int E, int Q);
+cudaError_t launch_balance(const BalanceArgs& a, int type, int num_sms, cudaStream_t s);
+
+struct RouteGradArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t T;
+  const int32_t* d_num_tokens;
+  int32_t E, K;
+  int32_t sigmoid, renorm;
+  float scale;
+  const int32_t* ids;          // with dweights
+  const float* dweights;       // optional [T, K]
+  const float* dloss;          // optional [2]
+  const int32_t* counts;       // with dloss [Q, E]
+  GroupArgs g;
+  void* dlogits;
+  int64_t ldd;
+  int32_t* status;
+};
+cudaError_t launch_route_grad(const RouteGradArgs& a, int type, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Expanded <-> slab repack
 // ---------------------------------------------------------------------------
 struct RepackArgs {

@@ -1,0 +1,741 @@
+// router.cu -- the router of an MoE block: each token's experts and weights from
+// its logits, the batch's balance and z losses, and the gradient of the logits.
+//
+//   score     s_e = exp(l_e) / sum_j exp(l_j)   or   1 / (1 + exp(-l_e))
+//   choice    the K largest of l_e, or of s_e + b_e with a bias, lowest index first
+//             among equals; weights scale * s_k, or scale * s_k / sum over the chosen
+//   balance   over groups q of n_q tokens:  1/Q sum_q E / (K n_q^2) sum_e c[q,e] P[q,e],
+//             c the chosen slots, P the sums of p (the scores normalised over the experts)
+//   z         mean over the tokens of logsumexp(l)^2
+//
+// One warp works on a token; lane i holds the logits i, 32 + i, ... in registers,
+// so a row is read once and everything about it is a few warp reductions.
+#include <climits>
+#include <type_traits>
+
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moeperm {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr float kNegInf = -INFINITY;
+
+template <int TYPE>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
+  if constexpr (TYPE == kF32) {
+    return __ldg(static_cast<const float*>(p) + i);
+  } else {
+    const uint32_t w = __ldg(static_cast<const uint16_t*>(p) + i);
+    return TYPE == kBF16 ? __uint_as_float(w << 16) : f16x2_to_float2(w).x;
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
+  if constexpr (TYPE == kF32) {
+    static_cast<float*>(p)[i] = v;
+  } else {
+    static_cast<uint16_t*>(p)[i] = (uint16_t)(TYPE == kBF16 ? pack_bf16x2(v, 0.0f) : pack_f16x2(v, 0.0f));
+  }
+}
+
+// Logits of a token; -inf past the last expert.
+template <int TYPE, int N>
+__device__ __forceinline__ void load_row(float (&v)[N], const void* p, int64_t at, int E, int lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = i * 32 + lane < E ? load_elem<TYPE>(p, at + i * 32 + lane) : kNegInf;
+}
+
+// Floats as unsigned integers of the same order. 0: never chosen (NaN and -inf).
+__device__ __forceinline__ uint32_t ordered(float f) {
+  const uint32_t b = __float_as_uint(f + 0.0f);  // both zeros are one key
+  return f > kNegInf ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {  // a NaN is left out
+  return unordered(__reduce_max_sync(0xffffffffu, v > kNegInf ? ordered(v) : 0x007FFFFFu));
+}
+
+// 1 / (1 + e^-l) and 1 minus that, neither with cancellation.
+__device__ __forceinline__ float sigmoid(float l) {
+  const float x = __expf(-fabsf(l));
+  return __fdividef(l < 0.0f ? x : 1.0f, 1.0f + x);
+}
+__device__ __forceinline__ float sigmoid_rest(float l) {
+  const float x = __expf(-fabsf(l));
+  return __fdividef(l < 0.0f ? 1.0f : x, 1.0f + x);
+}
+
+// Where every logit of a set is below this, its sigmoids are exponentials (to
+// 2^-86) that may leave the range of a float, and their ratios are those of a softmax.
+constexpr float kFarBelow = -60.0f;
+
+// Normalised scores of a token over all experts: softmax, or sigmoids over their
+// sum. m: the largest logit (-inf: a row without any, whose scores are 0).
+template <int N>
+__device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, float (&p)[N]) {
+  if (m == kNegInf) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = isnan(l[i]) ? l[i] : 0.0f;
+    return;
+  }
+  float z = 0.0f;
+  const bool soft = !sig || m < kFarBelow;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    p[i] = soft ? __expf(l[i] - m) : sigmoid(l[i]);
+    z += p[i];
+  }
+  const float r = __fdividef(1.0f, warp_sum(z));
+#pragma unroll
+  for (int i = 0; i < N; ++i) p[i] *= r;
+}
+
+// ---------------------------------------------------------------------------
+// The choice of experts
+// ---------------------------------------------------------------------------
+
+// The choice again with keys in 64 bits, for a token with keys so near each other that
+// 32 bits may have them in the wrong order. Lane k gets the k-th id (-1: none).
+template <int TYPE, int N>
+__device__ __noinline__ int choose64(const RouteArgs& a, int64_t at, int lane) {
+  double key[N];
+  double z = 0.0, m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    key[i] = i * 32 + lane < a.E ? (double)load_elem<TYPE>(a.logits, at + i * 32 + lane) : -INFINITY;
+    m = fmax(m, key[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-key[i])) : exp(key[i] - m);
+    z += key[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = i * 32 + lane;
+    key[i] = e < a.E ? (a.sigmoid ? key[i] : key[i] / z) + (double)__ldg(a.bias + e) : -INFINITY;
+    if (e < a.E && !(load_elem<TYPE>(a.logits, at + e) > kNegInf)) key[i] = -INFINITY;
+  }
+  int mine = -1;
+  for (int k = 0; k < a.K; ++k) {
+    double best = -INFINITY;
+    int id = INT_MAX;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        id = i * 32 + lane;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const int oi = __shfl_xor_sync(0xffffffffu, id, o);
+      if (ob > best || (ob == best && oi < id)) {
+        best = ob;
+        id = oi;
+      }
+    }
+    if (id == INT_MAX) break;
+    if (lane == k) mine = id;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 + lane == id) key[i] = -INFINITY;
+  }
+  return mine;
+}
+
+template <int TYPE, int N>
+__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && threadIdx.x == 0);
+  int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  float next[N];
+  if (t < n_live) load_row<TYPE>(next, a.logits, t * a.ld, a.E, lane);
+  float bias[N];
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) bias[i] = i * 32 + lane < a.E ? __ldg(a.bias + i * 32 + lane) : 0.0f;
+  }
+  for (; t < n_live; t += nwarps) {
+    float l[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = next[i];
+    if (t + nwarps < n_live) load_row<TYPE>(next, a.logits, (t + nwarps) * a.ld, a.E, lane);
+    uint32_t key[N];
+    float m = kNegInf, z = 1.0f;
+    if (!a.sigmoid && (a.bias != nullptr || !a.renorm)) {  // the sum over all experts
+#pragma unroll
+      for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+      m = warp_max(m);
+      z = 0.0f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) z += __expf(l[i] - m);
+      z = warp_sum(z);
+    }
+    if (a.bias != nullptr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float s = a.sigmoid ? sigmoid(l[i]) : __fdividef(__expf(l[i] - m), z);
+        key[i] = l[i] > kNegInf ? ordered(s + bias[i]) : 0u;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = ordered(l[i]);
+    }
+    // lane k keeps the k-th largest key and its expert
+    const int rounds = a.bias != nullptr && a.K < 32 && a.K < a.E ? a.K + 1 : a.K;
+    uint32_t mykey = 0;
+    int id = -1;
+    for (int k = 0; k < rounds; ++k) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int i = 1; i < N; ++i) best = max(best, key[i]);
+      best = __reduce_max_sync(0xffffffffu, best);
+      if (best == 0) break;
+      int at = INT_MAX;
+#pragma unroll
+      for (int i = N - 1; i >= 0; --i)
+        if (key[i] == best) at = i * 32 + lane;
+      at = __reduce_min_sync(0xffffffffu, at);
+      if (lane == k) {
+        mykey = best;
+        id = at;
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * 32 + lane == at) key[i] = 0;
+    }
+    float lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+    if (a.bias != nullptr) {
+      // Keys in 32 bits are off by 2^-21 (sigmoid), or by (N + 12) 2^-24 (a sum of 32 N
+      // exponentials), and half a step of the sum with the bias. Two of them nearer than
+      // twice that, and not equal from equal parts, are decided in 64 bits.
+      const float bk = id >= 0 ? __ldg(a.bias + id) : 0.0f;
+      const uint32_t nk = __shfl_down_sync(0xffffffffu, mykey, 1);
+      const float nl = __shfl_down_sync(0xffffffffu, lk, 1), nb = __shfl_down_sync(0xffffffffu, bk, 1);
+      const float mine = unordered(mykey);
+      const float eps = (a.sigmoid ? 0x1p-19f : (N + 24) * 0x1p-23f) + fabsf(mine) * 0x1p-22f;
+      const bool near = lane < a.K && lane < 31 && mykey != 0 && nk != 0 && !(mine - unordered(nk) > eps) && !(lk == nl && bk == nb);
+      if (a.K >= 32 || __any_sync(0xffffffffu, near)) {  // (32 slots: no lane is left for the key after the last)
+        id = choose64<TYPE, N>(a, t * a.ld, lane);
+        lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+      }
+    }
+    if (lane >= a.K) {
+      id = -1;
+      lk = kNegInf;
+    }
+    float s;
+    if (a.renorm) {
+      const float mk = warp_max(lk);
+      const bool soft = !a.sigmoid || mk < kFarBelow;
+      s = id >= 0 ? (soft ? __expf(lk - mk) : sigmoid(lk)) : 0.0f;
+        const float sum = warp_sum(s);
+      s = id >= 0 ? __fdividef(s, sum) : 0.0f;
+    } else {
+      s = id >= 0 ? (a.sigmoid ? sigmoid(lk) : __fdividef(__expf(lk - m), z)) : 0.0f;
+    }
+    if (lane < a.K) {
+      a.ids[t * a.K + lane] = id;
+      a.weights[t * a.K + lane] = a.scale * s;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Groups of tokens
+// ---------------------------------------------------------------------------
+
+// Sizes and first flattened tokens of the groups in shared memory: cnt, st [Q] (and 33
+// ints of scratch). Groups lie one after the other inside the live tokens; if any does
+// not, the call has none (and flags it). Returns the tokens of all groups.
+__device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int32_t* cnt, int32_t* st, int32_t* scratch,
+                                           int32_t* status, int& nonempty) {
+  bool ok = true;
+  for (int q = threadIdx.x; q < g.Q; q += blockDim.x) {
+    const int b = g.begin != nullptr ? __ldg(g.begin + q) : 0, e = g.begin != nullptr ? __ldg(g.end + q) : n_live;
+    const int before = g.begin != nullptr && q > 0 ? __ldg(g.end + q - 1) : 0;
+    ok &= before <= b && b >= 0 && b <= e && e <= n_live;
+    cnt[q] = e - b;
+  }
+  int some = 0;
+  ok = __syncthreads_and(ok);
+  if (!ok && blockIdx.x == 0 && threadIdx.x == 0) set_status(status, kStBadLayout);
+  for (int q = threadIdx.x; q < g.Q; q += blockDim.x) {
+    if (!ok) cnt[q] = 0;
+    some += cnt[q] > 0;
+  }
+  __syncthreads();
+  const int total = aligned_starts(cnt, st, g.Q, 1, INT_MAX, scratch);
+  some = __reduce_add_sync(0xffffffffu, some);
+  if (threadIdx.x == 0) scratch[0] = 0;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0 && some > 0) atomicAdd(scratch, some);
+  __syncthreads();
+  nonempty = scratch[0];
+  return total;
+}
+
+// ---------------------------------------------------------------------------
+// The losses
+// ---------------------------------------------------------------------------
+
+// Workspace: sums of the parts [slots][E] and their counts [slots][E], z [slots], each
+// group's share of the losses, and what the second launch has to know. A CTA takes a
+// run of the flattened tokens; its part of group q has slot blockIdx.x + q, which no
+// other part has, since along the tokens the two only grow.
+struct BalanceWs {
+  float* P;
+  int32_t* c;
+  float* z;
+  float* share;      // [Q][slices] balance
+  float* zshare;     // [Q]
+  int32_t* meta;     // [Q][3]: first slot, slots, tokens; then groups with tokens, tokens, ticket
+};
+__host__ __device__ inline int64_t balance_slots(int Q) { return kBalanceParts + Q; }
+__device__ __forceinline__ BalanceWs balance_ws(const BalanceArgs& a) {
+  const int64_t slots = balance_slots(a.g.Q), slices = (a.E + 31) / 32;
+  BalanceWs w;
+  w.P = a.ws;
+  w.c = reinterpret_cast<int32_t*>(w.P + slots * a.E);
+  w.z = reinterpret_cast<float*>(w.c + slots * a.E);
+  w.share = w.z + slots;
+  w.zshare = w.share + a.g.Q * slices;
+  w.meta = reinterpret_cast<int32_t*>(w.zshare + a.g.Q);
+  return w;
+}
+
+// Sums over a run of tokens, one warp a token, two at a time; bound by HBM where the
+// batch is large, by its two launches where it is small.
+template <int TYPE, int N>
+__global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t s_scratch[33];
+  __shared__ float s_z[kWarps];
+  int32_t* cnt = sm;
+  int32_t* st = cnt + a.g.Q;
+  int32_t* hist = st + a.g.Q;                               // [E]
+  float* s_acc = reinterpret_cast<float*>(hist + a.E);      // [kWarps][E]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E;
+  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
+  int nonempty;
+  const int total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
+  const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
+  const BalanceWs w = balance_ws(a);
+  if (blockIdx.x == 0) {
+    for (int q = tid; q < a.g.Q; q += kThreads) {
+      const int b0 = cnt[q] > 0 ? st[q] / per : 0;
+      w.meta[3 * q] = b0 + q;
+      w.meta[3 * q + 1] = cnt[q] > 0 ? (st[q] + cnt[q] - 1) / per - b0 + 1 : 0;
+      w.meta[3 * q + 2] = cnt[q];
+    }
+    if (tid == 0) {
+      w.meta[3 * a.g.Q] = nonempty;
+      w.meta[3 * a.g.Q + 1] = total;
+      w.meta[3 * a.g.Q + 2] = 0;
+    }
+  }
+  int at = (int)min((int64_t)blockIdx.x * per, (int64_t)total);
+  const int stop = (int)min((int64_t)at + per, (int64_t)total);
+  if (at >= stop) return;
+  int q = 0;
+  for (int hi = a.g.Q - 1; q < hi;) {  // the last group that starts at or before `at`
+    const int mid = (q + hi + 1) >> 1;
+    if (st[mid] <= at) q = mid; else hi = mid - 1;
+  }
+  for (; at < stop; ++q) {
+    const int upto = min(stop, st[q] + cnt[q]);
+    if (upto <= at) continue;
+    for (int e = tid; e < E; e += kThreads) hist[e] = 0;
+    __syncthreads();
+    const int64_t first = (a.g.begin != nullptr ? __ldg(a.g.begin + q) : 0) + (at - st[q]);
+    const int n = upto - at;
+    for (int64_t i = tid; i < (int64_t)n * a.K; i += kThreads) {
+      const int id = __ldg(a.ids + first * a.K + i);
+      if (id >= 0 && id < E) atomicAdd(hist + id, 1);
+    }
+    float acc[N], z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    constexpr int kAhead = N <= 8 ? 4 : N <= 16 ? 2 : 1;  // tokens of a warp in flight
+    for (int j = warp; j < n; j += kAhead * kWarps) {
+      float l[kAhead][N];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (j + u * kWarps < n) load_row<TYPE>(l[u], a.logits, (first + j + u * kWarps) * a.ld, E, lane);
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (j + u * kWarps >= n) break;
+        float m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = fmaxf(m, l[u][i]);
+        m = warp_max(m);
+        float p[N], zs = 0.0f;
+        const bool apart = a.sigmoid && m != kNegInf;  // (the z loss is of the softmax's sum)
+        if (m != kNegInf) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            p[i] = __expf(l[u][i] - m);
+            zs += p[i];
+          }
+          zs = warp_sum(zs);
+          const float lse = m + __logf(zs);
+          z = fmaf(lse, lse, z);
+          const float r = __fdividef(1.0f, zs);
+#pragma unroll
+          for (int i = 0; i < N; ++i) p[i] *= r;
+        }
+        if (apart || m == kNegInf) scores(l[u], m, a.sigmoid, p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += p[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 + lane < E) s_acc[warp * E + i * 32 + lane] = acc[i];
+    if (lane == 0) s_z[warp] = z;
+    __syncthreads();
+    const int64_t slot = (int64_t)blockIdx.x + q;
+    for (int e = tid; e < E; e += kThreads) {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += s_acc[i * E + e];
+      w.P[slot * E + e] = v;
+      w.c[slot * E + e] = hist[e];
+    }
+    if (tid == 0) {
+      float v = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) v += s_z[i];
+      w.z[slot] = v;
+    }
+    __syncthreads();
+    at = upto;
+  }
+}
+
+// Joins the parts of group blockIdx.y for 32 experts; the last CTA joins the groups.
+__global__ void __launch_bounds__(1024) balance_join_kernel(BalanceArgs a) {
+  __shared__ float s_p[32][33];
+  __shared__ int32_t s_c[32][33];
+  __shared__ bool s_last;
+  pdl_wait_primary();
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, rows = blockDim.x >> 5;
+  const int q = blockIdx.y, e = blockIdx.x * 32 + lane, E = a.E;
+  const BalanceWs w = balance_ws(a);
+  const int first = __ldcg(w.meta + 3 * q), parts = __ldcg(w.meta + 3 * q + 1), n = __ldcg(w.meta + 3 * q + 2);
+  float p = 0.0f;
+  int c = 0;
+  if (e < E) {
+#pragma unroll 4
+    for (int i = row; i < parts; i += rows) {
+      p += __ldcg(w.P + (int64_t)(first + i) * E + e);
+      c += __ldcg(w.c + (int64_t)(first + i) * E + e);
+    }
+  }
+  s_p[row][lane] = p;
+  s_c[row][lane] = c;
+  __syncthreads();
+  if (row == 0) {
+    for (int i = 1; i < rows; ++i) {
+      p += s_p[i][lane];
+      c += s_c[i][lane];
+    }
+    if (e < E) {
+      a.counts[(int64_t)q * E + e] = c;
+      a.prob_sums[(int64_t)q * E + e] = p;
+    }
+    const float dot = warp_sum((float)c * p);
+    if (lane == 0) {
+      w.share[(int64_t)q * gridDim.x + blockIdx.x] = n > 0 ? dot / n / n * E / a.K : 0.0f;
+      if (blockIdx.x == 0) {
+        float z = 0.0f;
+        for (int i = 0; i < parts; ++i) z += __ldcg(w.z + first + i);
+        w.zshare[q] = z;
+      }
+      __threadfence();
+      s_last = atomicAdd(reinterpret_cast<unsigned*>(w.meta + 3 * a.g.Q + 2), 1u) == gridDim.x * gridDim.y - 1;
+    }
+  }
+  __syncthreads();
+  if (!s_last || row > 0) return;
+  __threadfence();
+  float b = 0.0f, z = 0.0f;
+  for (int64_t i = lane; i < (int64_t)gridDim.x * gridDim.y; i += 32) b += __ldcg(w.share + i);
+  for (int i = lane; i < a.g.Q; i += 32) z += __ldcg(w.zshare + i);
+  b = warp_sum(b);
+  z = warp_sum(z);
+  if (lane == 0) {
+    const int some = __ldcg(w.meta + 3 * a.g.Q), total = __ldcg(w.meta + 3 * a.g.Q + 1);
+    a.loss[0] = some > 0 ? b / some : 0.0f;
+    a.loss[1] = total > 0 ? z / total : 0.0f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The gradient of the logits
+// ---------------------------------------------------------------------------
+
+// One warp a token, a run of tokens each, so that the group's counts stay in registers.
+// What the chosen experts add is spread over the row through a line of shared memory.
+template <int TYPE, int N>
+__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t s_scratch[33];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E, K = a.K, Q = a.g.Q;
+  int32_t* cnt = sm;
+  int32_t* st = cnt + Q;
+  float* add = reinterpret_cast<float*>(st + Q) + warp * E;
+  for (int e = lane; e < E; e += 32) add[e] = 0.0f;
+  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
+  int nonempty = 0, total = 0;
+  float db = 0.0f, dz = 0.0f;
+  if (a.dloss != nullptr) {  // uniform over the grid
+    total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
+    if (nonempty > 0) {
+      db = __ldg(a.dloss) * (float)E / ((float)K * (float)nonempty);
+      dz = 2.0f * __ldg(a.dloss + 1) / (float)total;
+    }
+  }
+  __syncwarp();
+  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+  const int64_t per = (a.T + nwarps - 1) / nwarps;
+  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * per;
+  const int64_t stop = min(t + per, (int64_t)a.T);
+  int q = -1;                       // group that holds token t or comes next
+  int64_t gb = 0, ge = -1;          // its tokens
+  float g[N];                       // its gradient of the sums of p
+  float l[N], next[N], dw = 0.0f, ndw = 0.0f, lk = kNegInf;
+  int id = -1, nid = -1;
+  auto load = [&](int64_t at, float (&row)[N], int& i, float& d) {
+    load_row<TYPE>(row, a.logits, at * a.ld, E, lane);
+    i = -1;
+    d = 0.0f;
+    if (a.dweights != nullptr && lane < K) {
+      i = __ldg(a.ids + at * K + lane);
+      d = __ldg(a.dweights + at * K + lane);
+      if (i < 0 || i >= E) {
+        i = -1;
+        d = 0.0f;
+      }
+    }
+  };
+  if (t < stop && t < n_live) load(t, next, nid, ndw);
+  for (; t < stop; ++t) {
+    if (t >= n_live) {
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * 32 + lane < E) store_elem<TYPE>(a.dlogits, t * a.ldd + i * 32 + lane, 0.0f);
+      continue;
+    }
+    id = nid;
+    dw = ndw;
+#pragma unroll
+    for (int i = 0; i < N; ++i) l[i] = next[i];
+    lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+    if (t + 1 < stop && t + 1 < n_live) load(t + 1, next, nid, ndw);
+    float r[N], m = kNegInf;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      r[i] = 0.0f;
+      m = fmaxf(m, l[i]);
+    }
+    m = warp_max(m);
+    if (db != 0.0f || dz != 0.0f) {
+      if (t >= ge) {  // on to the group that ends behind t
+        if (q < 0 && a.g.begin != nullptr) {
+          q = 0;
+          for (int hi = Q; q < hi;) {
+            const int mid = (q + hi) >> 1;
+            if (__ldg(a.g.end + mid) <= t) q = mid + 1; else hi = mid;
+          }
+        }
+        if (a.g.begin == nullptr) {
+          q = 0;
+          ge = n_live;
+        } else {
+          while (q < Q && __ldg(a.g.end + q) <= t) ++q;
+          gb = q < Q ? __ldg(a.g.begin + q) : INT_MAX;
+          ge = q < Q ? __ldg(a.g.end + q) : INT_MAX;
+        }
+        if (q < Q) {
+          const float n = (float)cnt[q];
+          const float scale = n > 0.0f ? db / n / n : 0.0f;
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            g[i] = i * 32 + lane < E ? scale * (float)__ldg(a.counts + (int64_t)q * E + i * 32 + lane) : 0.0f;
+        }
+      }
+      if (t >= gb && q < Q) {
+        float p[N], dot = 0.0f;
+        scores(l, m, a.sigmoid, p);
+#pragma unroll
+        for (int i = 0; i < N; ++i) dot = fmaf(p[i], g[i], dot);
+        dot = warp_sum(dot);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          r[i] = p[i] * (g[i] - dot);
+          if (a.sigmoid) r[i] *= sigmoid_rest(l[i]);
+        }
+        if (dz != 0.0f && m != kNegInf) {
+          float z = 0.0f;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            p[i] = __expf(l[i] - m);
+            z += p[i];
+          }
+          z = warp_sum(z);
+          const float c = __fdividef(dz * (m + __logf(z)), z);
+#pragma unroll
+          for (int i = 0; i < N; ++i) r[i] = fmaf(c, p[i], r[i]);
+        }
+      }
+    }
+    if (a.dweights != nullptr) {
+      float dk;
+      if (a.renorm) {
+        const float mk = warp_max(lk);
+        const bool soft = !a.sigmoid || mk < kFarBelow;
+        const float s = id >= 0 && mk != kNegInf ? (soft ? __expf(lk - mk) : sigmoid(lk)) : 0.0f;
+        const float sum = warp_sum(s);
+        const float u = id >= 0 && mk != kNegInf ? __fdividef(s, sum) : 0.0f;
+        dk = a.scale * u * (dw - warp_sum(u * dw));
+        if (a.sigmoid) dk *= sigmoid_rest(lk);
+      } else if (a.sigmoid) {
+        dk = id >= 0 ? a.scale * dw * sigmoid(lk) * sigmoid_rest(lk) : 0.0f;
+      } else {
+        float z = 0.0f, p[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          p[i] = __expf(l[i] - m);
+          z += p[i];
+        }
+        z = warp_sum(z);
+        dk = id >= 0 && m != kNegInf ? a.scale * dw * __fdividef(__expf(lk - m), z) : 0.0f;
+        const float c = m == kNegInf ? 0.0f : __fdividef(warp_sum(dk), z);
+        if (m != kNegInf) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) r[i] = fmaf(-c, p[i], r[i]);
+        }
+      }
+      // an expert twice in a token: one after the other, in the order of the slots
+      const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
+      if (__any_sync(0xffffffffu, (same & (same - 1)) != 0)) {
+        for (int k = 0; k < K; ++k) {
+          if (lane == k && id >= 0) add[id] += dk;
+          __syncwarp();
+        }
+      } else if (id >= 0) {
+        add[id] = dk;
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (i * 32 + lane < E) r[i] += add[i * 32 + lane];
+      __syncwarp();
+      if (id >= 0) add[id] = 0.0f;
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 + lane < E) store_elem<TYPE>(a.dlogits, t * a.ldd + i * 32 + lane, r[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+// Calls f with the element type and the logits a lane holds as constants.
+template <typename F>
+cudaError_t by_shape(int type, int E, F f) {
+  auto by_n = [&](auto ty) -> cudaError_t {
+    if (E <= 32) return f(ty, std::integral_constant<int, 1>{});
+    if (E <= 64) return f(ty, std::integral_constant<int, 2>{});
+    if (E <= 128) return f(ty, std::integral_constant<int, 4>{});
+    if (E <= 256) return f(ty, std::integral_constant<int, 8>{});
+    if (E <= 512) return f(ty, std::integral_constant<int, 16>{});
+    return f(ty, std::integral_constant<int, 32>{});
+  };
+  if (type == kBF16) return by_n(std::integral_constant<int, kBF16>{});
+  if (type == kF16) return by_n(std::integral_constant<int, kF16>{});
+  return by_n(std::integral_constant<int, kF32>{});
+}
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs& a, int type, int num_sms, cudaStream_t s) {
+  return by_shape(type, a.E, [&](auto ty, auto n) {
+    auto kernel = route_kernel<decltype(ty)::value, decltype(n)::value>;
+    int per_sm = 0;
+    cudaError_t err = occupancy(kernel, kThreads, 0, &per_sm);
+    if (err != cudaSuccess) return err;
+    const int64_t need = ((int64_t)a.T + kWarps - 1) / kWarps, most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+    kernel<<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+size_t balance_ws_bytes(int E, int Q) {
+  const int64_t slots = balance_slots(Q), slices = (E + 31) / 32;
+  return (size_t)(slots * (2 * (int64_t)E + 1) + Q * (slices + 4) + 3) * 4;
+}
+
+cudaError_t launch_balance(const BalanceArgs& a, int type, int num_sms, cudaStream_t s) {
+  cudaError_t err = by_shape(type, a.E, [&](auto ty, auto n) {
+    auto kernel = balance_parts_kernel<decltype(ty)::value, decltype(n)::value>;
+    const size_t smem = (2 * (size_t)a.g.Q + (1 + kWarps) * (size_t)a.E) * 4;
+    cudaError_t e = opt_in_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    int64_t grid = (a.T + 2 * kWarps - 1) / (2 * kWarps);  // two tokens a warp at least
+    if (grid > kBalanceParts) grid = kBalanceParts;
+    if (grid < 1) grid = 1;
+    kernel<<<(unsigned)grid, kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  });
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.E + 31) / 32), (unsigned)a.g.Q);
+  cfg.blockDim = dim3(a.g.Q <= 8 ? 1024 : 128);  // a group of many has few parts
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a);
+}
+
+cudaError_t launch_route_grad(const RouteGradArgs& a, int type, int num_sms, cudaStream_t s) {
+  return by_shape(type, a.E, [&](auto ty, auto n) {
+    auto kernel = route_grad_kernel<decltype(ty)::value, decltype(n)::value>;
+    const size_t smem = (2 * (size_t)a.g.Q + kWarps * (size_t)a.E) * 4;
+    cudaError_t err = opt_in_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    int per_sm = 0;
+    err = occupancy(kernel, kThreads, smem, &per_sm);
+    if (err != cudaSuccess) return err;
+    const int64_t need = ((int64_t)a.T + kWarps - 1) / kWarps, most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+    kernel<<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(a);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace moeperm

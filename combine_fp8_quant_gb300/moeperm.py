@@ -31,6 +31,7 @@ FMT = {"u8": 0, "packed": 1, "f32pow2": 2, "f32": 3, "mx": 4}
 ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 GATE = {"none": 0, "channel": 1, "token": 2}
+SCORE = {"softmax": 0, "sigmoid": 1}
 
 _lock = threading.Lock()
 _lib = None
@@ -97,6 +98,12 @@ def _declare(L):
         "moe_expert_matmul_grad_workspace_bytes": (sz, [i64, i32, i32]),
         "moe_expert_matmul_grad": (i32, [vp, i64, vp, i64, i32, i64, i32, vp, i32, i32, i32, i32, vp,
                                          i64, vp, vp, i32, vp, i64, vp, i32, vp, vp, sz, vp, vp]),
+        "moe_route": (i32, [vp, i64, i32, i32, vp, i32, i32, i32, vp, i32, f32, vp, vp, vp, vp]),
+        "moe_balance_loss_workspace_bytes": (sz, [i32, i32]),
+        "moe_balance_loss": (i32, [vp, i64, i32, i32, vp, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp,
+                                   sz, vp, vp]),
+        "moe_route_grad": (i32, [vp, i64, i32, i32, vp, i32, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp,
+                                 i32, vp, i64, vp, vp]),
         "moe_status_sync": (i32, [vp, vp]),
         "moe_status_string": (C.c_char_p, [i32]),
         "moe_version": (C.c_char_p, []),
@@ -134,6 +141,25 @@ def _ptrs(*tensors):
     """_ptr of several tensors (or None) at once: the helpers below go straight to
     the library with these, which saves a small call a few microseconds."""
     return [None if t is None else t.data_ptr() if t.is_cuda else _off_device(t) for t in tensors]
+
+
+def _on_current(*tensors):
+    """_ptrs of tensors that all have to be on the current device, whose stream the call uses."""
+    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
+    out = []
+    for t in tensors:
+        if t is not None:
+            if not t.is_cuda:
+                _off_device(t)
+            if t.get_device() != cur:
+                raise ValueError(f"moeperm: tensor on {t.device}, but the current device is cuda:{cur}")
+        out.append(None if t is None else t.data_ptr())
+    return out
+
+
+def _status(status, needed, dev):
+    """The caller's status word, or a new one where the call can meet an error in its data."""
+    return status if status is not None or not needed else torch.zeros(1, dtype=torch.int32, device=dev)
 
 
 # The current stream's raw handle without building a torch Stream object (the
@@ -323,6 +349,33 @@ def moe_expert_matmul_grad(dout, ldd, x, ldx, dtype, R, K, w, L, N, gated, act, 
         _ptr(pre), ld_pre, _ptr(seg_begin), _ptr(seg_end), cap, _ptr(dx), ld_dx, _ptr(dw),
         ELEM[dw_dtype], _ptr(dbias), _ptr(workspace), workspace_bytes, _ptr(d_status),
         _stream(stream)))
+
+
+def moe_route(logits, ldl, dtype, T, d_num_tokens, E, K, score, bias, renorm, scale, topk_ids,
+              topk_weights, d_status, stream=None) -> int:
+    return int(lib().moe_route(_ptr(logits), ldl, ELEM[dtype], T, _ptr(d_num_tokens), E, K, SCORE[score],
+                               _ptr(bias), int(renorm), scale, _ptr(topk_ids), _ptr(topk_weights),
+                               _ptr(d_status), _stream(stream)))
+
+
+def moe_balance_loss_workspace_bytes(E: int, Q: int) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(E, Q))
+
+
+def moe_balance_loss(logits, ldl, dtype, T, d_num_tokens, E, topk_ids, K, score, seq_begin, seq_end, Q,
+                     loss, counts, prob_sums, workspace, workspace_bytes, d_status, stream=None) -> int:
+    return int(lib().moe_balance_loss(
+        _ptr(logits), ldl, ELEM[dtype], T, _ptr(d_num_tokens), E, _ptr(topk_ids), K, SCORE[score],
+        _ptr(seq_begin), _ptr(seq_end), Q, _ptr(loss), _ptr(counts), _ptr(prob_sums), _ptr(workspace),
+        workspace_bytes, _ptr(d_status), _stream(stream)))
+
+
+def moe_route_grad(logits, ldl, dtype, T, d_num_tokens, E, topk_ids, K, score, renorm, scale, dweights,
+                   dloss, counts, seq_begin, seq_end, Q, dlogits, ldd, d_status, stream=None) -> int:
+    return int(lib().moe_route_grad(
+        _ptr(logits), ldl, ELEM[dtype], T, _ptr(d_num_tokens), E, _ptr(topk_ids), K, SCORE[score],
+        int(renorm), scale, _ptr(dweights), _ptr(dloss), _ptr(counts), _ptr(seq_begin), _ptr(seq_end), Q,
+        _ptr(dlogits), ldd, _ptr(d_status), _stream(stream)))
 
 
 def moe_status_sync(d_status, stream=None) -> int:
@@ -835,6 +888,106 @@ def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0
                                o["dw_post"], o["dgate"], o["dw_pre"], ws.buf, ws.nbytes),
            "moe_block_norm_grad")
     return o
+
+
+def _score(score):
+    if score not in SCORE:
+        raise ValueError(f"moeperm: score must be one of {sorted(SCORE)}, not {score!r}")
+    return SCORE[score]
+
+
+def _groups(seq_begin, seq_end):
+    """Groups of tokens: how many."""
+    if seq_begin is None and seq_end is None:
+        return 1
+    if seq_begin is None or seq_end is None:
+        raise ValueError("moeperm: groups of tokens need seq_begin and seq_end")
+    Q = seq_begin.numel()
+    _vec(seq_begin, Q, "seq_begin", torch.int32)
+    _vec(seq_end, Q, "seq_end", torch.int32)
+    return Q
+
+
+def route(logits, top_k, bias=None, score="softmax", renorm=True, scale=1.0, num_tokens=None, status=None):
+    """The experts of each token and their weights from the router's logits [T, E]
+    (bfloat16, float16 or float32): the top_k largest logits or, with a bias [E]
+    float32 for the choice alone, scores plus bias; lowest index first among equals.
+    score "softmax" or "sigmoid"; renorm: weights sum to scale, else they are scale
+    times the scores. Experts masked by -inf are never chosen: where too few are left
+    the id is -1 (which the dispatches drop) and the weight 0. Returns a dict:
+    topk_ids [T, top_k] int32, topk_weights [T, top_k] float32, status."""
+    dtype = _elem(logits, FLOATS, "logits")
+    ldl = _rows(logits, "logits")
+    T, E = logits.shape
+    _vec(bias, E, "bias")
+    dev = logits.device
+    ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    st = _status(status, num_tokens is not None, dev)
+    pl, pn, pb, pi, pw, pst = _on_current(logits, num_tokens, bias, ids, w, st)
+    _check(lib().moe_route(pl, ldl, ELEM[dtype], T, pn, E, top_k, _score(score), pb, 1 if renorm else 0, scale,
+                           pi, pw, pst, _stream()), "moe_route")
+    return dict(topk_ids=ids, topk_weights=w, status=st)
+
+
+class BalanceWorkspace:
+    """Workspace of balance_loss for E experts and up to Q groups, for any number of
+    tokens, reusable across calls on one stream; needs no initialisation."""
+
+    def __init__(self, E: int, Q: int, device):
+        self.nbytes = moe_balance_loss_workspace_bytes(E, Q)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+
+def balance_loss(logits, topk_ids, seq_begin=None, seq_end=None, score="softmax", num_tokens=None,
+                 workspace=None, status=None):
+    """The router's losses over groups of tokens [seq_begin[q], seq_end[q]) (None: all
+    tokens one group; groups one after the other, rows between them belong to none).
+    Returns a dict: loss [2] float32, the balance loss (mean over the groups of
+    E / (K n^2) sum_e counts * prob_sums, 1 for even use) and the z loss (mean over
+    the tokens of logsumexp(logits)^2); counts [Q, E] int32, the slots of each expert;
+    prob_sums [Q, E] float32; status."""
+    dtype = _elem(logits, FLOATS, "logits")
+    ldl = _rows(logits, "logits")
+    T, E = logits.shape
+    K, Q, dev = topk_ids.shape[1], _groups(seq_begin, seq_end), logits.device
+    _vec(topk_ids, T * K, "topk_ids", torch.int32)
+    loss = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty((Q, E), dtype=torch.int32, device=dev)
+    sums = torch.empty((Q, E), dtype=torch.float32, device=dev)
+    ws = workspace if workspace is not None else BalanceWorkspace(E, Q, dev)
+    st = _status(status, num_tokens is not None or seq_begin is not None, dev)
+    pl, pn, pi, pb, pe, po, pc, ps, pw, pst = _on_current(logits, num_tokens, topk_ids, seq_begin, seq_end, loss, counts,
+                                                          sums, ws.buf, st)
+    _check(lib().moe_balance_loss(pl, ldl, ELEM[dtype], T, pn, E, pi, K, _score(score), pb, pe, Q, po, pc, ps, pw,
+                                  ws.nbytes, pst, _stream()), "moe_balance_loss")
+    return dict(loss=loss, counts=counts, prob_sums=sums, status=st)
+
+
+def route_grad(logits, topk_ids, dweights=None, dloss=None, counts=None, seq_begin=None, seq_end=None,
+               score="softmax", renorm=True, scale=1.0, num_tokens=None, status=None, out=None):
+    """Gradient of the logits through the weights of route (dweights [T, K]) and through
+    both losses of balance_loss (dloss [2], with its counts and groups), in logits'
+    type; 0 for tokens that are not live. score, renorm and scale as in the forward
+    calls."""
+    dtype = _elem(logits, FLOATS, "logits")
+    ldl = _rows(logits, "logits")
+    T, E = logits.shape
+    K, Q, dev = topk_ids.shape[1], _groups(seq_begin, seq_end), logits.device
+    _vec(topk_ids, T * K, "topk_ids", torch.int32)
+    _vec(dweights, T * K, "dweights")
+    _vec(dloss, 2, "dloss")
+    _vec(counts, Q * E, "counts", torch.int32)
+    if dweights is None and dloss is None:
+        raise ValueError("moeperm: route_grad needs dweights, dloss or both")
+    if dloss is not None and counts is None:
+        raise ValueError("moeperm: the gradient of the balance loss needs its counts")
+    out = _like(out, (T, E), dtype, dev, "out")
+    pl, pn, pi, pw, pd, pc, pb, pe, po, pst = _on_current(logits, num_tokens, topk_ids, dweights, dloss, counts,
+                                                          seq_begin, seq_end, out, status)
+    _check(lib().moe_route_grad(pl, ldl, ELEM[dtype], T, pn, E, pi, K, _score(score), 1 if renorm else 0, scale, pw,
+                                pd, pc, pb, pe, Q, po, E, pst, _stream()), "moe_route_grad")
+    return out
 
 
 def expand_to_slab(exp, psum, num_local_experts, cap, align=128, exp_scales=None, ld_es=0,

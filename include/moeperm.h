@@ -510,6 +510,83 @@ moe_status_t moe_block_norm_grad(
     float* dw_pre, void* workspace, size_t workspace_bytes, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ */
+/* The router: choice of experts, its losses and their gradients        */
+/* ------------------------------------------------------------------ */
+
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0, /* s_e = exp(l_e) / sum_j exp(l_j) */
+  MOE_SCORE_SIGMOID = 1  /* s_e = 1 / (1 + exp(-l_e)) */
+} moe_score_t;
+
+/*
+ * moe_route -- the experts of each token and their weights, as the dispatches take
+ * them. A token's experts are the K with the largest key, in descending order, the
+ * lowest index first among equal keys; the key is the logit itself or, with a bias
+ * (which steers the choice only), s_e + bias[e].
+ *   topk_weights[t, k] = scale * s_k             (renorm 0)
+ *                        scale * s_k / sum of the chosen s    (renorm 1)
+ * An expert whose key is NaN or -infinity is never chosen; where fewer than K are
+ * left, the last ids are -1 (which the dispatches drop) with weight 0. With SOFTMAX a
+ * logit of NaN or +infinity makes every s of its token NaN: weights with renorm 0, and
+ * with a bias no expert is chosen. Keys are compared as if computed in 64 bits: two that
+ * 32 bits cannot tell apart are computed again. Weights are computed in fp32.
+ *   logits [T, ldl]              BF16, F16 or F32, ldl >= E, any alignment of the type
+ *   d_num_tokens (optional)      live tokens n; rows t >= n of the outputs are not written
+ *   E (1..1024), K (1..32, <= E), bias [E] f32 (optional)
+ *   topk_ids [T, K] int32, topk_weights [T, K] f32
+ * Launches: 1.
+ */
+moe_status_t moe_route(
+    const void* logits, int64_t ldl, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t E,
+    int32_t K, moe_score_t score, const float* bias, int32_t renorm, float scale, int32_t* topk_ids,
+    float* topk_weights, int32_t* d_status, moe_stream_t stream);
+
+/* Bytes of device workspace moe_balance_loss needs, for any T (no initialisation; not
+ * to be used by two calls that can run at once). 0 for sizes out of range. */
+size_t moe_balance_loss_workspace_bytes(int32_t E, int32_t Q);
+
+/*
+ * moe_balance_loss -- the slots of each expert and two losses of the router, over
+ * groups of tokens (the sequences of a batch, or the whole batch):
+ *   counts[q, e]     slots of group q's tokens that hold e
+ *   prob_sums[q, e]  sum over its tokens of p[t, e], p the softmax, or the sigmoids over
+ *                    their sum
+ *   loss[0]          mean over the groups with tokens of
+ *                    E / (K n_q^2) * sum_e counts[q, e] * prob_sums[q, e]   (1 for even use)
+ *   loss[1]          mean over the tokens of the groups of logsumexp_e(logits[t])^2
+ * n_q: tokens of the group. Without tokens a loss is 0.
+ *   topk_ids [T, K] int32        ids outside [0, E) count nowhere
+ *   seq_begin, seq_end [Q]       group q is the tokens seq_begin[q] .. seq_end[q]; the groups
+ *                                lie one after the other among the live tokens, with any
+ *                                rows between them. If one does not, MOE_STATUS_BAD_LAYOUT is
+ *                                set and all count as empty. Both NULL: Q = 1, all live tokens
+ *   Q (1..4096), loss [2] f32, counts [Q, E] int32, prob_sums [Q, E] f32   written in full
+ * A token whose logits are all -infinity has p = 0 and no part in loss[1]'s sum. Sums are
+ * in fp32 and in a fixed order (deterministic). Launches: 2.
+ */
+moe_status_t moe_balance_loss(
+    const void* logits, int64_t ldl, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t E,
+    const int32_t* topk_ids, int32_t K, moe_score_t score, const int32_t* seq_begin, const int32_t* seq_end,
+    int32_t Q, float* loss, int32_t* counts, float* prob_sums, void* workspace, size_t workspace_bytes,
+    int32_t* d_status, moe_stream_t stream);
+
+/*
+ * moe_route_grad -- the gradient of the logits, through the weights of moe_route
+ * (dweights) and through both losses of moe_balance_loss (dloss), added in fp32 and
+ * rounded once. The choice and the counts are constants; the bias takes no gradient.
+ *   topk_ids, dweights [T, K]    (optional, together) ids outside [0, E) take none
+ *   dloss [2] f32 device, counts [Q, E]   (optional, together) counts as moe_balance_loss
+ *                                wrote them; groups as there, with its errors
+ *   dlogits [T, ldd]             of `type`, written in full: 0 for tokens that are not live
+ * score, renorm and scale as in the forward calls. Deterministic. Launches: 1.
+ */
+moe_status_t moe_route_grad(
+    const void* logits, int64_t ldl, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t E,
+    const int32_t* topk_ids, int32_t K, moe_score_t score, int32_t renorm, float scale, const float* dweights,
+    const float* dloss, const int32_t* counts, const int32_t* seq_begin, const int32_t* seq_end, int32_t Q,
+    void* dlogits, int64_t ldd, int32_t* d_status, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
 /* Expanded (psum) layout <-> masked slab repack                        */
 /* ------------------------------------------------------------------ */
 
