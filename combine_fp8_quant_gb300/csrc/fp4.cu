@@ -1,0 +1,358 @@
+// fp4.cu -- rows to four bits and back (format in fp4.cuh), in place order and as a
+// dispatch into the compact layout.
+//
+// All of it is bound by HBM: a bf16 row is read once (2 bytes an element) and leaves as
+// 0.5 bytes and its scales (1/16 or 1/32). A lane owns 16 elements, so that a group of
+// 16 needs no exchange and one of 32 a single one; a warp covers 512 elements of a row
+// at a time, whose scales are one or two whole pieces.
+#include "common.cuh"
+#include "fp4.cuh"
+#include "kernels.h"
+#include "layout.cuh"
+
+namespace moeperm {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+template <int TYPE>
+constexpr int kChunkBytes = 16 * (TYPE == kF32 ? 4 : 2);  // of 16 elements
+
+// Whether row r is one of those to work on.
+__device__ __forceinline__ bool has_row(const Fp4Args& p, int64_t r, int64_t live) {
+  if (p.row_ids != nullptr) return __ldg(p.row_ids + r) >= 0;
+  if (p.masked_m != nullptr) return (int)(r % p.cap) < __ldg(p.masked_m + r / p.cap);
+  return r < live;
+}
+__device__ __forceinline__ int64_t live_rows(const Fp4Args& p) {
+  if (p.d_num_live == nullptr) return p.R;
+  int64_t n = __ldg(p.d_num_live);
+  if (n > p.R) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, kStLiveOverflow);
+    n = p.R;
+  }
+  return n < 0 ? 0 : n;
+}
+__device__ __forceinline__ float tensor_scale(const Fp4Args& p, int64_t r) {
+  return p.tscale == nullptr ? 1.0f : __ldg(p.tscale + (p.nts == 1 ? 0 : r / (p.R / p.nts)));
+}
+
+// A warp takes kAhead slices of 512 elements of a row at a time.
+template <int TYPE>
+constexpr int kAhead = TYPE == kF32 ? 1 : 2;
+
+template <int TYPE, int FMT>
+__global__ void __launch_bounds__(kThreads) quant_fp4_kernel(Fp4Args p) {
+  constexpr int kSpan = 32 * kAhead<TYPE>;  // chunks of a unit
+  const int lane = threadIdx.x & 31;
+  const int nch = p.H / 16, nchp = fp4_pieces(p.H, FMT) * (FMT == kFp4NV ? 16 : 32);  // chunks that have scale bytes
+  const int upr = (nchp + kSpan - 1) / kSpan;  // units of a row
+  const int64_t live = live_rows(p);
+  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+  int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int64_t r = u / upr;
+  int s = (int)(u - r * upr);
+  const int64_t dr = nwarps / upr;
+  const int ds = (int)(nwarps - dr * upr);
+  for (; r < p.R; r += dr, s += ds) {
+    if (s >= upr) {
+      s -= upr;
+      if (++r >= p.R) break;
+    }
+    if (!has_row(p, r, live)) continue;
+    Chunk<TYPE> x[kAhead<TYPE>];
+    const int c0 = s * kSpan + lane;
+    const uint8_t* src = static_cast<const uint8_t*>(p.x) + r * p.ldx * (kChunkBytes<TYPE> / 16);
+#pragma unroll
+    for (int i = 0; i < kAhead<TYPE>; ++i) {
+      const int c = c0 + 32 * i;
+      x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+    }
+    const float ts = FMT == kFp4NV ? tensor_scale(p, r) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
+#pragma unroll
+    for (int i = 0; i < kAhead<TYPE>; ++i) {
+      const int c = c0 + 32 * i;
+      uint32_t byte;
+      const uint2 q = fp4_quant<TYPE, FMT>(x[i], ts, ts6, byte);
+      if (c < nch) *reinterpret_cast<uint2*>(p.q + r * (p.H / 2) + (int64_t)c * 8) = q;
+      const uint32_t word = fp4_scale_word<FMT>(c < nch ? byte : 0u);
+      if (fp4_word_lane<FMT>(lane) && c < nchp)
+        *reinterpret_cast<uint32_t*>(p.scales + ((int64_t)fp4_piece_of<FMT>(c) * p.ld + r) * 16 + fp4_byte_of<FMT>(c)) = word;
+    }
+  }
+}
+
+template <int TYPE, int FMT>
+__global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(Fp4Args p) {
+  constexpr int kUnit = 2;  // slices of 512 elements at a time
+  constexpr int kSpan = 32 * kUnit;
+  const int lane = threadIdx.x & 31;
+  const int nch = p.H / 16, upr = (nch + kSpan - 1) / kSpan;
+  const int64_t live = live_rows(p);
+  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+  int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  int64_t r = u / upr;
+  int s = (int)(u - r * upr);
+  const int64_t dr = nwarps / upr;
+  const int ds = (int)(nwarps - dr * upr);
+  for (; r < p.R; r += dr, s += ds) {
+    if (s >= upr) {
+      s -= upr;
+      if (++r >= p.R) break;
+    }
+    if (!has_row(p, r, live)) continue;
+    uint2 q[kUnit];
+    uint32_t byte[kUnit];
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const int c = s * kSpan + 32 * i + lane;
+      if (c < nch) {
+        q[i] = __ldg(reinterpret_cast<const uint2*>(p.q + r * (p.H / 2) + (int64_t)c * 8));
+        byte[i] = __ldg(p.scales + ((int64_t)fp4_piece_of<FMT>(c) * p.ld + r) * 16 + fp4_byte_of<FMT>(c));
+      }
+    }
+    const float ts = FMT == kFp4NV ? tensor_scale(p, r) : 1.0f;
+    uint8_t* dst = static_cast<uint8_t*>(const_cast<void*>(p.x)) + r * p.ldx * (kChunkBytes<TYPE> / 16);
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const int c = s * kSpan + 32 * i + lane;
+      if (c >= nch) break;
+      const float d = fp4_scale<FMT>(byte[i], ts);
+      const uint32_t half[2] = {q[i].x, q[i].y};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+        e2m1x8_to_floats(half[h], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], d);
+        constexpr int kN = Vec<TYPE>::kN;
+#pragma unroll
+        for (int j = 0; j < 8; j += kN) {
+          float g[kN];
+#pragma unroll
+          for (int k = 0; k < kN; ++k) g[k] = f[j + k];
+          st_v4(dst + (int64_t)c * kChunkBytes<TYPE> + (h * 8 + j) * (kChunkBytes<TYPE> / 16), Vec<TYPE>::pack(g));
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The dispatch
+// ---------------------------------------------------------------------------
+
+// Small problems, one launch: every CTA ranks all slots itself (layout.cuh), then
+// quantises its tokens with all its warps and stores every 8 bytes, and every word of
+// scales, to each of the token's rows.
+template <int TYPE, int FMT, int S>
+__global__ void __launch_bounds__(kThreads) dispatch_fp4_small_kernel(DispatchFp4Args p) {
+  extern __shared__ int32_t sm[];
+  __shared__ int32_t s_wsum[33];
+  static_assert(kWarps == kSmallWarps, "small_layout's threads");
+  const ScatterArgs& a = p.s;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int nch = a.H / 16, nchp = fp4_pieces(a.H, FMT) * (FMT == kFp4NV ? 16 : 32);
+  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x);
+  Chunk<TYPE> v;  // the first token's first elements load meanwhile
+  v.load(x + (int64_t)blockIdx.x * p.ldx_bytes + (int64_t)tid * kChunkBytes<TYPE>, (int)blockIdx.x < n_live && tid < nch);
+  const float ts = FMT == kFp4NV && p.tscale != nullptr ? __ldg(p.tscale) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
+  small_layout<S>(a, sm, s_wsum, n_live);
+  const int32_t* rows_all = small_rows(a, sm);
+  for (int t = blockIdx.x; t < n_live; t += gridDim.x) {
+    const int32_t* rows = rows_all + (int64_t)t * a.K;
+    for (int c = tid; c - lane < nchp; c += kThreads) {
+      if (t != (int)blockIdx.x || c >= kThreads)
+        v.load(x + (int64_t)t * p.ldx_bytes + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+      uint32_t byte;
+      const uint2 q = fp4_quant<TYPE, FMT>(v, ts, ts6, byte);
+      const uint32_t word = fp4_scale_word<FMT>(c < nch ? byte : 0u);
+      const bool has_word = fp4_word_lane<FMT>(lane) && c < nchp;
+      for (int k = 0; k < a.K; ++k) {
+        const int64_t row = rows[k];
+        if (row < 0) continue;
+        if (c < nch) *reinterpret_cast<uint2*>(a.xq + row * (a.H / 2) + (int64_t)c * 8) = q;
+        if (has_word)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.scales) +
+                                       ((int64_t)fp4_piece_of<FMT>(c) * a.ld_s + row) * 16 + fp4_byte_of<FMT>(c)) = word;
+      }
+    }
+  }
+}
+
+// After the route plan. Each warp works alone: it finds a token's rows, quantises the
+// token into its staging buffer, and copies the elements to every row with one bulk copy
+// each (lane k that of slot k) and the scales piece by piece.
+template <int TYPE, int FMT>
+__global__ void __launch_bounds__(kThreads) dispatch_fp4_kernel(DispatchFp4Args p) {
+  extern __shared__ __align__(128) int32_t sm[];
+  __shared__ int32_t s_wsum[33];
+  const ScatterArgs& a = p.s;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_live = live_count(a.d_num_tokens, a.T, nullptr, false);  // the route plan flags it
+  const int nch = a.H / 16, pieces = fp4_pieces(a.H, FMT), nchp = pieces * (FMT == kFp4NV ? 16 : 32);
+  const int row_bytes = a.H / 2, stage_bytes = row_bytes + pieces * 16;
+  int32_t* st = sm + a.nchunks * a.L;
+  int32_t* ps = st + a.L;
+  const size_t plan = (((size_t)a.nchunks * a.L + 2 * (size_t)a.L) * sizeof(int32_t) + 127) / 128 * 128;
+  uint8_t* stage = reinterpret_cast<uint8_t*>(sm) + plan + (size_t)warp * p.stages * stage_bytes;
+  const float ts = FMT == kFp4NV && p.tscale != nullptr ? __ldg(p.tscale) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
+  pdl_wait_primary();
+  layout_prologue(a, sm, st, ps, s_wsum);
+  const int nwarps = gridDim.x * kWarps;
+  int buf = 0;
+  for (int64_t t = (int64_t)warp * gridDim.x + blockIdx.x; t < n_live; t += nwarps) {
+    int row = -1;
+    if (lane < a.K) {
+      const int64_t slot = t * a.K + lane;
+      row = slot_row(a, sm, st, slot, __ldg(a.ids + slot), __ldcg(a.src2dst + slot));
+      a.src2dst[slot] = row;
+      if (row >= 0 && a.row_weights != nullptr) a.row_weights[row] = __ldg(a.w + slot);
+    }
+    if (!__any_sync(0xffffffffu, row >= 0)) continue;
+    uint8_t* out = stage + buf * stage_bytes;
+    // the copies that last read this buffer have left it
+    if (p.stages == 2) bulk_wait_read<1>(); else bulk_wait_read<0>();
+    __syncwarp();
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + t * p.ldx_bytes;
+    for (int c0 = 0; c0 < nchp; c0 += 32 * kAhead<TYPE>) {
+      Chunk<TYPE> x[kAhead<TYPE>];
+#pragma unroll
+      for (int i = 0; i < kAhead<TYPE>; ++i) {
+        const int c = c0 + 32 * i + lane;
+        x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead<TYPE>; ++i) {
+        const int c = c0 + 32 * i + lane;
+        uint32_t byte;
+        const uint2 q = fp4_quant<TYPE, FMT>(x[i], ts, ts6, byte);
+        if (c < nch) *reinterpret_cast<uint2*>(out + c * 8) = q;
+        const uint32_t word = fp4_scale_word<FMT>(c < nch ? byte : 0u);
+        if (fp4_word_lane<FMT>(lane) && c < nchp)
+          *reinterpret_cast<uint32_t*>(out + row_bytes + fp4_piece_of<FMT>(c) * 16 + fp4_byte_of<FMT>(c)) = word;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (row >= 0) bulk_store_s2g(a.xq + (int64_t)row * row_bytes, smem_addr(out), (uint32_t)row_bytes);
+    bulk_commit();
+    for (int k = 0; k < a.K; ++k) {
+      const int64_t to = __shfl_sync(0xffffffffu, row, k);
+      if (to < 0) continue;
+      for (int c = lane; c < pieces; c += 32)
+        st_v4(static_cast<uint8_t*>(a.scales) + ((int64_t)c * a.ld_s + to) * 16,
+              *reinterpret_cast<const uint4*>(out + row_bytes + c * 16));
+    }
+    buf = p.stages == 2 ? buf ^ 1 : 0;
+  }
+  // tokens past the live ones have no rows; the layout's m_indices while the copies drain
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid + (int64_t)n_live * a.K; i < (int64_t)a.T * a.K; i += (int64_t)gridDim.x * kThreads)
+    a.src2dst[i] = -1;
+  fill_m_indices(a, st, ps, tid, kThreads);
+  bulk_wait_all();
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+
+template <typename F>
+cudaError_t by_type(int type, int fmt, F f) {
+  auto by_fmt = [&](auto ty) -> cudaError_t {
+    if (fmt == kFp4NV) return f(ty, std::integral_constant<int, kFp4NV>{});
+    if (fmt == kFp4MX) return f(ty, std::integral_constant<int, kFp4MX>{});
+    return f(ty, std::integral_constant<int, kFp4E8M0>{});
+  };
+  if (type == kBF16) return by_fmt(std::integral_constant<int, kBF16>{});
+  if (type == kF16) return by_fmt(std::integral_constant<int, kF16>{});
+  return by_fmt(std::integral_constant<int, kF32>{});
+}
+
+template <typename Kern>
+cudaError_t launch_units(Kern kernel, const Fp4Args& a, int64_t units, int num_sms, cudaStream_t s) {
+  int per_sm = 0;
+  cudaError_t err = occupancy(kernel, kThreads, 0, &per_sm);
+  if (err != cudaSuccess) return err;
+  const int64_t need = (units + kWarps - 1) / kWarps, most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+  kernel<<<(unsigned)(need < most ? need : most), kThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_quant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, cudaStream_t s) {
+  return by_type(type, fmt, [&](auto ty, auto f) {
+    constexpr int kT = decltype(ty)::value, kF = decltype(f)::value;
+    const int nchp = fp4_pieces(a.H, kF) * (kF == kFp4NV ? 16 : 32), span = 32 * kAhead<kT>;
+    return launch_units(quant_fp4_kernel<kT, kF>, a, a.R * ((nchp + span - 1) / span), num_sms, s);
+  });
+}
+
+cudaError_t launch_dequant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, cudaStream_t s) {
+  return by_type(type, fmt, [&](auto ty, auto f) {
+    return launch_units(dequant_fp4_kernel<decltype(ty)::value, decltype(f)::value>, a, a.R * ((a.H / 16 + 63) / 64), num_sms, s);
+  });
+}
+
+cudaError_t launch_dispatch_fp4(const DispatchFp4Args& a0, int type, int fmt, int num_sms, bool after_route_plan,
+                                cudaStream_t s) {
+  return by_type(type, fmt, [&](auto ty, auto f) -> cudaError_t {
+    constexpr int kT = decltype(ty)::value, kF = decltype(f)::value;
+    DispatchFp4Args a = a0;
+    const int64_t A = (int64_t)a.s.T * a.s.K;
+    if (!after_route_plan) {
+      if (A > kSmallSlots) return cudaErrorInvalidValue;
+      const size_t smem = small_layout_bytes(a.s);
+      auto go = [&](auto kernel) -> cudaError_t {
+        cudaError_t err = opt_in_smem(kernel, smem);
+        if (err != cudaSuccess) return err;
+        int per_sm = 0;
+        err = occupancy(kernel, kThreads, smem, &per_sm);
+        if (err != cudaSuccess) return err;
+        int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+        if (grid > a.s.T) grid = a.s.T;
+        if (grid < 1) grid = 1;
+        kernel<<<(unsigned)grid, kThreads, smem, s>>>(a);
+        return cudaGetLastError();
+      };
+      if (A <= 256) return go(dispatch_fp4_small_kernel<kT, kF, 1>);
+      if (A <= 1024) return go(dispatch_fp4_small_kernel<kT, kF, 4>);
+      return go(dispatch_fp4_small_kernel<kT, kF, 8>);
+    }
+    const size_t plan = (((size_t)a.s.nchunks * a.s.L + 2 * (size_t)a.s.L) * sizeof(int32_t) + 127) / 128 * 128;
+    const size_t stage = (size_t)a.s.H / 2 + (size_t)fp4_pieces(a.s.H, kF) * 16;
+    int optin = 0;
+    cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerBlockOptin, &optin);
+    if (err != cudaSuccess) return err;
+    // two rows in flight a warp, one where shared memory is short (the widest rows
+    // with the largest chunk table: 64 KiB and 8 * 18 KiB fit)
+    a.stages = plan + 2 * kWarps * stage + 1024 <= (size_t)optin ? 2 : 1;
+    const size_t smem = plan + a.stages * kWarps * stage;
+    auto kernel = dispatch_fp4_kernel<kT, kF>;
+    err = opt_in_smem(kernel, smem);
+    if (err != cudaSuccess) return err;
+    int per_sm = 0;
+    err = occupancy(kernel, kThreads, smem, &per_sm);
+    if (err != cudaSuccess) return err;
+    int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+    const int64_t need = ((int64_t)a.s.T + kWarps - 1) / kWarps;
+    if (grid > need) grid = need;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+  });
+}
+
+}  // namespace moeperm

@@ -265,6 +265,40 @@ cudaError_t launch_block_norm(const NormArgs& a, int type, int num_sms, cudaStre
 cudaError_t launch_block_norm_grad(const NormArgs& a, int type, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// Four-bit rows (formats: same values as moe_fp4_t)
+// ---------------------------------------------------------------------------
+constexpr int kFp4E8M0 = 0, kFp4MX = 1, kFp4NV = 2;
+struct Fp4Args {
+  const void* x;               // quantise: [R, ldx]; dequantise: the output [R, ldx]
+  int64_t ldx;
+  int64_t R;
+  int32_t H;
+  const float* tscale;         // [nts] (nv; nullptr: 1): row r has tscale[r / (R / nts)]
+  int32_t nts;
+  const int32_t* d_num_live;   // which rows: a live prefix,
+  const int32_t* row_ids;      // those with row_ids[r] >= 0,
+  const int32_t* masked_m;     // or the first masked_m[e] of each slab of `cap` rows
+  int32_t cap;
+  uint8_t* q;                  // [R, H / 2]
+  uint8_t* scales;             // [pieces, ld, 16]
+  int64_t ld;
+  int32_t* status;
+};
+cudaError_t launch_quant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, cudaStream_t s);
+cudaError_t launch_dequant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, cudaStream_t s);
+
+// The dispatch into four-bit rows of the compact layout: s.x in `type`, s.xq and s.scales
+// the rows, s.ld_s the pieces' leading dimension.
+struct DispatchFp4Args {
+  ScatterArgs s;
+  int64_t ldx_bytes;
+  const float* tscale;         // [1] or nullptr
+  int32_t stages;              // rows in flight per warp (set at launch)
+};
+cudaError_t launch_dispatch_fp4(const DispatchFp4Args& a, int type, int fmt, int num_sms, bool after_route_plan,
+                                cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // Router: choice of experts, balance and z losses, gradient of the logits
 // ---------------------------------------------------------------------------
 constexpr int kMaxRouted = 1024;   // experts a router chooses from

@@ -105,6 +105,19 @@ __device__ __forceinline__ int slot_row(const ScatterArgs& p, const int32_t* tbl
   return j < p.cap ? e * p.cap + j : -1;
 }
 
+// m_indices over the whole bound, shared out over the grid (nthreads of each CTA).
+__device__ __forceinline__ void fill_m_indices(const ScatterArgs& s, const int32_t* st, const int32_t* ps,
+                                               int tid, int nthreads) {
+  for (int64_t r = (int64_t)blockIdx.x * nthreads + tid; r < s.bound; r += (int64_t)gridDim.x * nthreads) {
+    int lo = 0, hi = s.L - 1;  // largest e with start[e] <= r (start[0] = 0)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (st[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    s.m_indices[r] = (r < ps[lo]) ? lo : -1;
+  }
+}
+
 // Warps of a CTA that ranks all slots itself.
 constexpr int kSmallWarps = 8;
 

@@ -108,18 +108,6 @@ struct Mover {
   }
 };
 
-__device__ __forceinline__ void fill_m_indices(const ScatterArgs& s, const int32_t* st, const int32_t* ps,
-                                               int tid, int nthreads) {
-  for (int64_t r = (int64_t)blockIdx.x * nthreads + tid; r < s.bound; r += (int64_t)gridDim.x * nthreads) {
-    int lo = 0, hi = s.L - 1;  // largest e with start[e] <= r (start[0] = 0)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (st[mid] <= r) lo = mid; else hi = mid - 1;
-    }
-    s.m_indices[r] = (r < ps[lo]) ? lo : -1;
-  }
-}
-
 __host__ __device__ inline size_t plan_bytes(const ScatterArgs& s, int64_t ntok) {
   const size_t ints = (size_t)s.nchunks * s.L + 2 * (size_t)s.L + (size_t)ntok * s.K;
   return (ints * sizeof(int32_t) + 127) / 128 * 128;

@@ -8,8 +8,9 @@
 //             c the chosen slots, P the sums of p (the scores normalised over the experts)
 //   z         mean over the tokens of logsumexp(l)^2
 //
-// One warp works on a token; lane i holds the logits i, 32 + i, ... in registers,
-// so a row is read once and everything about it is a few warp reductions.
+// One warp works on a token with its logits in registers (lane i holds the vectors i,
+// 32 + i, ... of the row), so a row is read once and everything about it is a few warp
+// reductions.
 #include <climits>
 #include <type_traits>
 
@@ -42,11 +43,77 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v) {
   }
 }
 
-// Logits of a token; -inf past the last expert.
-template <int TYPE, int N>
+// Expert of a lane's i-th logit: vectors of V logits, the warp's 32 side by side.
+template <int V>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+  return (i / V) * 32 * V + lane * V + i % V;
+}
+// Logits of a token; -inf past the last expert. V > 1: the rows are whole aligned
+// vectors of V (two, four or eight to 16 bytes or less).
+template <int TYPE, int N, int V>
 __device__ __forceinline__ void load_row(float (&v)[N], const void* p, int64_t at, int E, int lane) {
+  if constexpr (V == 1) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = i * 32 + lane < E ? load_elem<TYPE>(p, at + i * 32 + lane) : kNegInf;
+    for (int i = 0; i < N; ++i) v[i] = i * 32 + lane < E ? load_elem<TYPE>(p, at + i * 32 + lane) : kNegInf;
+  } else {
+    constexpr int kBytes = V * (TYPE == kF32 ? 4 : 2), kWords = kBytes / 4;
+    const uint8_t* row = static_cast<const uint8_t*>(p) + at * (kBytes / V) + lane * kBytes;
+#pragma unroll
+    for (int j = 0; j < N / V; ++j) {
+      uint32_t w[kWords];
+      if (j * 32 * V + lane * V < E) {
+        const uint8_t* q = row + j * 32 * kBytes;
+        if constexpr (kWords == 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4*>(q));
+          w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+        } else if constexpr (kWords == 2) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2*>(q));
+          w[0] = x.x; w[1] = x.y;
+        } else {
+          w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
+        }
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+          if constexpr (TYPE == kF32) {
+            v[j * V + i] = __uint_as_float(w[i]);
+          } else {
+            const float2 f = TYPE == kBF16 ? make_float2(bf16_lo(w[i]), bf16_hi(w[i])) : f16x2_to_float2(w[i]);
+            v[j * V + 2 * i] = f.x;
+            v[j * V + 2 * i + 1] = f.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[j * V + i] = kNegInf;
+      }
+    }
+  }
+}
+// The same way back, rounded to the type.
+template <int TYPE, int N, int V>
+__device__ __forceinline__ void store_row(void* p, int64_t at, int E, int lane, const float (&v)[N]) {
+  if constexpr (V == 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (i * 32 + lane < E) store_elem<TYPE>(p, at + i * 32 + lane, v[i]);
+  } else {
+    constexpr int kBytes = V * (TYPE == kF32 ? 4 : 2), kWords = kBytes / 4;
+    uint8_t* row = static_cast<uint8_t*>(p) + at * (kBytes / V) + lane * kBytes;
+#pragma unroll
+    for (int j = 0; j < N / V; ++j) {
+      if (j * 32 * V + lane * V >= E) break;
+      uint32_t w[kWords];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i)
+        w[i] = TYPE == kF32 ? __float_as_uint(v[j * V + i])
+               : TYPE == kBF16 ? pack_bf16x2(v[j * V + 2 * i], v[j * V + 2 * i + 1])
+                               : pack_f16x2(v[j * V + 2 * i], v[j * V + 2 * i + 1]);
+      uint8_t* q = row + j * 32 * kBytes;
+      if constexpr (kWords == 4) *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+      else if constexpr (kWords == 2) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(q) = w[0];
+    }
+  }
 }
 
 // Floats as unsigned integers of the same order. 0: never chosen (NaN and -inf).
@@ -82,20 +149,34 @@ __device__ __forceinline__ float sigmoid_rest(float l) {
 constexpr float kFarBelow = -60.0f;
 
 // Normalised scores of a token over all experts: softmax, or sigmoids over their
-// sum. m: the largest logit (-inf: a row without any, whose scores are 0).
-template <int N>
-__device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, float (&p)[N]) {
+// sum. m: the largest logit (-inf: a row without any, whose scores are 0). rest: 1
+// minus the sigmoids, where they are asked for.
+template <bool kRest, int N>
+__device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, float (&p)[N], float (&rest)[N]) {
   if (m == kNegInf) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) p[i] = isnan(l[i]) ? l[i] : 0.0f;
+    for (int i = 0; i < N; ++i) {
+      p[i] = isnan(l[i]) ? l[i] : 0.0f;
+      if (kRest) rest[i] = 1.0f;
+    }
     return;
   }
   float z = 0.0f;
-  const bool soft = !sig || m < kFarBelow;
+  if (!sig || m < kFarBelow) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    p[i] = soft ? __expf(l[i] - m) : sigmoid(l[i]);
-    z += p[i];
+    for (int i = 0; i < N; ++i) {
+      p[i] = __expf(l[i] - m);
+      if (kRest) rest[i] = 1.0f;
+      z += p[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float x = __expf(-fabsf(l[i])), r = __fdividef(1.0f, 1.0f + x), xr = x * r;
+      p[i] = l[i] < 0.0f ? xr : r;
+      if (kRest) rest[i] = l[i] < 0.0f ? r : xr;
+      z += p[i];
+    }
   }
   const float r = __fdividef(1.0f, warp_sum(z));
 #pragma unroll
@@ -106,35 +187,42 @@ __device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, f
 // The choice of experts
 // ---------------------------------------------------------------------------
 
-// The choice again with keys in 64 bits, for a token with keys so near each other that
-// 32 bits may have them in the wrong order. Lane k gets the k-th id (-1: none).
-template <int TYPE, int N>
-__device__ __noinline__ int choose64(const RouteArgs& a, int64_t at, int lane) {
-  double key[N];
-  double z = 0.0, m = -INFINITY;
+// The choice by K rounds of the largest key left, for a token that the quick way does
+// not settle: keys of KEY (uint32_t: ordered logits; double: scores with bias in 64
+// bits). Lane k gets the k-th id (-1: none).
+template <typename KEY, int TYPE, int N>
+__device__ __noinline__ int choose_by_rounds(const RouteArgs& a, int64_t at, int lane) {
+  KEY key[N];
+  const KEY none = std::is_same<KEY, double>::value ? (KEY)-INFINITY : (KEY)0;
+  if constexpr (std::is_same<KEY, double>::value) {
+    double z = 0.0, m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    key[i] = i * 32 + lane < a.E ? (double)load_elem<TYPE>(a.logits, at + i * 32 + lane) : -INFINITY;
-    m = fmax(m, key[i]);
-  }
+    for (int i = 0; i < N; ++i) {
+      key[i] = i * 32 + lane < a.E ? (double)load_elem<TYPE>(a.logits, at + i * 32 + lane) : -INFINITY;
+      m = fmax(m, key[i]);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-key[i])) : exp(key[i] - m);
-    z += key[i];
-  }
+    for (int i = 0; i < N; ++i) {
+      key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-key[i])) : exp(key[i] - m);
+      z += key[i];
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = i * 32 + lane;
-    key[i] = e < a.E ? (a.sigmoid ? key[i] : key[i] / z) + (double)__ldg(a.bias + e) : -INFINITY;
-    if (e < a.E && !(load_elem<TYPE>(a.logits, at + e) > kNegInf)) key[i] = -INFINITY;
+    for (int i = 0; i < N; ++i) {
+      const int e = i * 32 + lane;
+      const bool may = e < a.E && load_elem<TYPE>(a.logits, at + (e < a.E ? e : 0)) > kNegInf;
+      key[i] = may ? (a.sigmoid ? key[i] : key[i] / z) + (double)__ldg(a.bias + e) : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = i * 32 + lane < a.E ? ordered(load_elem<TYPE>(a.logits, at + i * 32 + lane)) : 0u;
   }
   int mine = -1;
   for (int k = 0; k < a.K; ++k) {
-    double best = -INFINITY;
+    KEY best = none;
     int id = INT_MAX;
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -144,7 +232,7 @@ __device__ __noinline__ int choose64(const RouteArgs& a, int64_t at, int lane) {
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
-      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
+      const KEY ob = __shfl_xor_sync(0xffffffffu, best, o);
       const int oi = __shfl_xor_sync(0xffffffffu, id, o);
       if (ob > best || (ob == best && oi < id)) {
         best = ob;
@@ -155,32 +243,40 @@ __device__ __noinline__ int choose64(const RouteArgs& a, int64_t at, int lane) {
     if (lane == k) mine = id;
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i * 32 + lane == id) key[i] = -INFINITY;
+      if (i * 32 + lane == id) key[i] = none;
   }
   return mine;
 }
 
-template <int TYPE, int N>
+// The quick way: at least K + 2 keys are no less than the (K + 2)-th largest of the 32
+// lanes' largest, and seldom many more (ten or eleven of 256 for K = 8). They go to
+// shared memory, one for each lane, which counts those that come before its own.
+//
+// 16384 tokens, 256 experts, K = 8, sigmoid with bias: see launch_route.
+template <int TYPE, int N, int V>
 __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
+  __shared__ uint4 s_cand[kWarps][32];  // key, expert, logit, bias
   const int lane = threadIdx.x & 31;
+  uint4* cand = s_cand[threadIdx.x >> 5];
   const int64_t nwarps = (int64_t)gridDim.x * kWarps;
   const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && threadIdx.x == 0);
   int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   float next[N];
-  if (t < n_live) load_row<TYPE>(next, a.logits, t * a.ld, a.E, lane);
+  if (t < n_live) load_row<TYPE, N, V>(next, a.logits, t * a.ld, a.E, lane);
+  const bool biased = a.bias != nullptr;
   float bias[N];
-  if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) bias[i] = i * 32 + lane < a.E ? __ldg(a.bias + i * 32 + lane) : 0.0f;
+  for (int i = 0; i < N; ++i) {
+    const int e = expert_of<V>(i, lane);
+    bias[i] = biased && e < a.E ? __ldg(a.bias + e) : 0.0f;
   }
   for (; t < n_live; t += nwarps) {
     float l[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = next[i];
-    if (t + nwarps < n_live) load_row<TYPE>(next, a.logits, (t + nwarps) * a.ld, a.E, lane);
-    uint32_t key[N];
+    if (t + nwarps < n_live) load_row<TYPE, N, V>(next, a.logits, (t + nwarps) * a.ld, a.E, lane);
     float m = kNegInf, z = 1.0f;
-    if (!a.sigmoid && (a.bias != nullptr || !a.renorm)) {  // the sum over all experts
+    if (!a.sigmoid && (biased || !a.renorm)) {  // the sum over all experts
 #pragma unroll
       for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
       m = warp_max(m);
@@ -189,72 +285,118 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
       for (int i = 0; i < N; ++i) z += __expf(l[i] - m);
       z = warp_sum(z);
     }
-    if (a.bias != nullptr) {
+    uint32_t key[N];
+    if (biased) {
+      const float r = a.sigmoid ? 0.0f : __fdividef(1.0f, z);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        const float s = a.sigmoid ? sigmoid(l[i]) : __fdividef(__expf(l[i] - m), z);
+        const float s = a.sigmoid ? sigmoid(l[i]) : __expf(l[i] - m) * r;
         key[i] = l[i] > kNegInf ? ordered(s + bias[i]) : 0u;
       }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) key[i] = ordered(l[i]);
     }
-    // lane k keeps the k-th largest key and its expert
-    const int rounds = a.bias != nullptr && a.K < 32 && a.K < a.E ? a.K + 1 : a.K;
-    uint32_t mykey = 0;
-    int id = -1;
-    for (int k = 0; k < rounds; ++k) {
-      uint32_t best = key[0];
+    // a key that at least K + 2 reach (or all, where there are fewer)
+    uint32_t top = key[0], floor = 1;
 #pragma unroll
-      for (int i = 1; i < N; ++i) best = max(best, key[i]);
-      best = __reduce_max_sync(0xffffffffu, best);
-      if (best == 0) break;
-      int at = INT_MAX;
-#pragma unroll
-      for (int i = N - 1; i >= 0; --i)
-        if (key[i] == best) at = i * 32 + lane;
-      at = __reduce_min_sync(0xffffffffu, at);
-      if (lane == k) {
-        mykey = best;
-        id = at;
+    for (int i = 1; i < N; ++i) top = max(top, key[i]);
+    for (int have = 0; have < a.K + 2;) {
+      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
+      if (best == 0) {
+        floor = 1;
+        break;
       }
+      floor = best;
+      const bool is = top == best;
+      have += __popc(__ballot_sync(0xffffffffu, is));
+      if (is) top = 0;
+    }
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) mine += key[i] >= floor;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int below = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += below;
+    }
+    const int n = __shfl_sync(0xffffffffu, upto, 31);
+    int id = -1, rank = 32;
+    float lk = kNegInf;
+    bool settled = n <= 32;
+    if (settled) {
+      int at = upto - mine;
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i * 32 + lane == at) key[i] = 0;
-    }
-    float lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
-    if (a.bias != nullptr) {
-      // Keys in 32 bits are off by 2^-21 (sigmoid), or by (N + 12) 2^-24 (a sum of 32 N
-      // exponentials), and half a step of the sum with the bias. Two of them nearer than
-      // twice that, and not equal from equal parts, are decided in 64 bits.
-      const float bk = id >= 0 ? __ldg(a.bias + id) : 0.0f;
-      const uint32_t nk = __shfl_down_sync(0xffffffffu, mykey, 1);
-      const float nl = __shfl_down_sync(0xffffffffu, lk, 1), nb = __shfl_down_sync(0xffffffffu, bk, 1);
-      const float mine = unordered(mykey);
-      const float eps = (a.sigmoid ? 0x1p-19f : (N + 24) * 0x1p-23f) + fabsf(mine) * 0x1p-22f;
-      const bool near = lane < a.K && lane < 31 && mykey != 0 && nk != 0 && !(mine - unordered(nk) > eps) && !(lk == nl && bk == nb);
-      if (a.K >= 32 || __any_sync(0xffffffffu, near)) {  // (32 slots: no lane is left for the key after the last)
-        id = choose64<TYPE, N>(a, t * a.ld, lane);
-        lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+        if (key[i] >= floor) cand[at++] = make_uint4(key[i], (uint32_t)expert_of<V>(i, lane), __float_as_uint(l[i]), __float_as_uint(bias[i]));
+      __syncwarp();
+      uint4 c = make_uint4(0, 0, 0, 0);
+      if (lane < n) {
+        c = cand[lane];
+        id = (int)c.y;
+        lk = __uint_as_float(c.z);
+        rank = 0;
       }
+      if (biased) {
+        // Keys in 32 bits are off by 2^-21 (sigmoid), or by (N + 12) 2^-24 (a sum of 32 N
+        // exponentials), and half a step of the sum with the bias. Two of them nearer than
+        // twice that, and not equal from equal parts, are told apart in 64 bits.
+        const float k = unordered(c.x);
+        const float eps = (a.sigmoid ? 0x1p-19f : (N + 24) * 0x1p-23f) + fabsf(k) * 0x1p-22f;
+        bool near = false;
+        for (int j = 0; j < n; ++j) {
+          const uint4 o = cand[j];
+          rank += o.x > c.x || (o.x == c.x && o.y < c.y);
+          near |= !(fabsf(unordered(o.x) - k) > eps) && (o.z != c.z || o.w != c.w);
+        }
+        // A key that is no candidate may be as near to the last chosen one only if that
+        // one is as near to the least candidate.
+        const bool open = lane < n && rank < a.K && n >= a.K + 2 && floor > 1 && !(k - unordered(floor) > 2.0f * eps);
+        if (__any_sync(0xffffffffu, (lane < n && near && rank < a.K) || open)) {
+          settled = a.sigmoid && !__any_sync(0xffffffffu, open);
+          if (settled) {
+            const double k64 = lane < n ? 1.0 / (1.0 + exp(-(double)lk)) + (double)__uint_as_float(c.w) : 0.0;
+            rank = lane < n ? 0 : 32;
+            for (int j = 0; j < n; ++j) {
+              const double o = __shfl_sync(0xffffffffu, k64, j);
+              const int oid = __shfl_sync(0xffffffffu, id, j);
+              rank += o > k64 || (o == k64 && oid < id);
+            }
+          }
+        }
+      } else {
+        for (int j = 0; j < n; ++j) {
+          const uint2 o = *reinterpret_cast<const uint2*>(cand + j);
+          rank += o.x > c.x || (o.x == c.x && o.y < c.y);
+        }
+      }
+      __syncwarp();
     }
-    if (lane >= a.K) {
-      id = -1;
-      lk = kNegInf;
+    int got = min(n, a.K);
+    if (!settled) {
+      id = biased ? choose_by_rounds<double, TYPE, N>(a, t * a.ld, lane) : choose_by_rounds<uint32_t, TYPE, N>(a, t * a.ld, lane);
+      rank = id >= 0 ? lane : 32;
+      lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+      got = __popc(__ballot_sync(0xffffffffu, id >= 0));
     }
-    float s;
+    const bool chosen = rank < a.K;
+    float s = 0.0f;
     if (a.renorm) {
-      const float mk = warp_max(lk);
+      const float mk = warp_max(chosen ? lk : kNegInf);
       const bool soft = !a.sigmoid || mk < kFarBelow;
-      s = id >= 0 ? (soft ? __expf(lk - mk) : sigmoid(lk)) : 0.0f;
-        const float sum = warp_sum(s);
-      s = id >= 0 ? __fdividef(s, sum) : 0.0f;
-    } else {
-      s = id >= 0 ? (a.sigmoid ? sigmoid(lk) : __fdividef(__expf(lk - m), z)) : 0.0f;
+      if (chosen) s = soft ? __expf(lk - mk) : sigmoid(lk);
+      s = __fdividef(s, warp_sum(s));
+    } else if (chosen) {
+      s = a.sigmoid ? sigmoid(lk) : __fdividef(__expf(lk - m), z);
     }
-    if (lane < a.K) {
-      a.ids[t * a.K + lane] = id;
-      a.weights[t * a.K + lane] = a.scale * s;
+    if (chosen) {
+      a.ids[t * a.K + rank] = id;
+      a.weights[t * a.K + rank] = a.scale * s;
+    }
+    if (lane >= got && lane < a.K) {
+      a.ids[t * a.K + lane] = -1;
+      a.weights[t * a.K + lane] = 0.0f;
     }
   }
 }
@@ -324,7 +466,7 @@ __device__ __forceinline__ BalanceWs balance_ws(const BalanceArgs& a) {
 
 // Sums over a run of tokens, one warp a token, two at a time; bound by HBM where the
 // batch is large, by its two launches where it is small.
-template <int TYPE, int N>
+template <int TYPE, int N, int V>
 __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int32_t s_scratch[33];
@@ -379,7 +521,7 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
       float l[kAhead][N];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
-        if (j + u * kWarps < n) load_row<TYPE>(l[u], a.logits, (first + j + u * kWarps) * a.ld, E, lane);
+        if (j + u * kWarps < n) load_row<TYPE, N, V>(l[u], a.logits, (first + j + u * kWarps) * a.ld, E, lane);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         if (j + u * kWarps >= n) break;
@@ -402,14 +544,14 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
 #pragma unroll
           for (int i = 0; i < N; ++i) p[i] *= r;
         }
-        if (apart || m == kNegInf) scores(l[u], m, a.sigmoid, p);
+        if (apart || m == kNegInf) scores<false>(l[u], m, a.sigmoid, p, p);
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += p[i];
       }
     }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-      if (i * 32 + lane < E) s_acc[warp * E + i * 32 + lane] = acc[i];
+      if (expert_of<V>(i, lane) < E) s_acc[warp * E + expert_of<V>(i, lane)] = acc[i];
     if (lane == 0) s_z[warp] = z;
     __syncthreads();
     const int64_t slot = (int64_t)blockIdx.x + q;
@@ -495,7 +637,7 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(BalanceArgs a) {
 
 // One warp a token, a run of tokens each, so that the group's counts stay in registers.
 // What the chosen experts add is spread over the row through a line of shared memory.
-template <int TYPE, int N>
+template <int TYPE, int N, int V>
 __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int32_t s_scratch[33];
@@ -522,10 +664,10 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
   int q = -1;                       // group that holds token t or comes next
   int64_t gb = 0, ge = -1;          // its tokens
   float g[N];                       // its gradient of the sums of p
-  float l[N], next[N], dw = 0.0f, ndw = 0.0f, lk = kNegInf;
+  float l[N], next[N], dw = 0.0f, ndw = 0.0f, lk, nlk = kNegInf;
   int id = -1, nid = -1;
   auto load = [&](int64_t at, float (&row)[N], int& i, float& d) {
-    load_row<TYPE>(row, a.logits, at * a.ld, E, lane);
+    load_row<TYPE, N, V>(row, a.logits, at * a.ld, E, lane);
     i = -1;
     d = 0.0f;
     if (a.dweights != nullptr && lane < K) {
@@ -537,20 +679,24 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
       }
     }
   };
-  if (t < stop && t < n_live) load(t, next, nid, ndw);
+  if (t < stop && t < n_live) {
+    load(t, next, nid, ndw);
+    if (nid >= 0) nlk = load_elem<TYPE>(a.logits, t * a.ld + nid);
+  }
   for (; t < stop; ++t) {
     if (t >= n_live) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i * 32 + lane < E) store_elem<TYPE>(a.dlogits, t * a.ldd + i * 32 + lane, 0.0f);
+      for (int i = 0; i < N; ++i) l[i] = 0.0f;
+      store_row<TYPE, N, V>(a.dlogits, t * a.ldd, E, lane, l);
       continue;
     }
     id = nid;
     dw = ndw;
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = next[i];
-    lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
-    if (t + 1 < stop && t + 1 < n_live) load(t + 1, next, nid, ndw);
+    lk = nlk;
+    const bool more = t + 1 < stop && t + 1 < n_live;
+    if (more) load(t + 1, next, nid, ndw);
     float r[N], m = kNegInf;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -580,19 +726,19 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
           const float scale = n > 0.0f ? db / n / n : 0.0f;
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            g[i] = i * 32 + lane < E ? scale * (float)__ldg(a.counts + (int64_t)q * E + i * 32 + lane) : 0.0f;
+            g[i] = expert_of<V>(i, lane) < E ? scale * (float)__ldg(a.counts + (int64_t)q * E + expert_of<V>(i, lane)) : 0.0f;
         }
       }
       if (t >= gb && q < Q) {
-        float p[N], dot = 0.0f;
-        scores(l, m, a.sigmoid, p);
+        float p[N], rest[N], dot = 0.0f;
+        scores<true>(l, m, a.sigmoid, p, rest);
 #pragma unroll
         for (int i = 0; i < N; ++i) dot = fmaf(p[i], g[i], dot);
         dot = warp_sum(dot);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           r[i] = p[i] * (g[i] - dot);
-          if (a.sigmoid) r[i] *= sigmoid_rest(l[i]);
+          if (a.sigmoid) r[i] *= rest[i];
         }
         if (dz != 0.0f && m != kNegInf) {
           float z = 0.0f;
@@ -648,14 +794,13 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (i * 32 + lane < E) r[i] += add[i * 32 + lane];
+        if (expert_of<V>(i, lane) < E) r[i] += add[expert_of<V>(i, lane)];
       __syncwarp();
       if (id >= 0) add[id] = 0.0f;
       __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i * 32 + lane < E) store_elem<TYPE>(a.dlogits, t * a.ldd + i * 32 + lane, r[i]);
+    nlk = more && nid >= 0 ? load_elem<TYPE>(a.logits, (t + 1) * a.ld + nid) : kNegInf;
+    store_row<TYPE, N, V>(a.dlogits, t * a.ldd, E, lane, r);
   }
 }
 
@@ -663,27 +808,39 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
 // Launches
 // ---------------------------------------------------------------------------
 
-// Calls f with the element type and the logits a lane holds as constants.
+// Calls f with the element type, the logits a lane holds and its vectors' length as
+// constants. Vectors where every row is made of whole aligned ones, of 16 bytes or what
+// a lane holds.
 template <typename F>
-cudaError_t by_shape(int type, int E, F f) {
+cudaError_t by_shape(int type, int E, bool whole, F f) {
+  auto by_v = [&](auto ty, auto n) -> cudaError_t {
+    constexpr int kMost = decltype(ty)::value == kF32 ? 4 : 8, kN = decltype(n)::value, kV = kN < kMost ? kN : kMost;
+    if constexpr (kV > 1)
+      if (whole && E % kV == 0) return f(ty, n, std::integral_constant<int, kV>{});
+    return f(ty, n, std::integral_constant<int, 1>{});
+  };
   auto by_n = [&](auto ty) -> cudaError_t {
-    if (E <= 32) return f(ty, std::integral_constant<int, 1>{});
-    if (E <= 64) return f(ty, std::integral_constant<int, 2>{});
-    if (E <= 128) return f(ty, std::integral_constant<int, 4>{});
-    if (E <= 256) return f(ty, std::integral_constant<int, 8>{});
-    if (E <= 512) return f(ty, std::integral_constant<int, 16>{});
-    return f(ty, std::integral_constant<int, 32>{});
+    if (E <= 32) return by_v(ty, std::integral_constant<int, 1>{});
+    if (E <= 64) return by_v(ty, std::integral_constant<int, 2>{});
+    if (E <= 128) return by_v(ty, std::integral_constant<int, 4>{});
+    if (E <= 256) return by_v(ty, std::integral_constant<int, 8>{});
+    if (E <= 512) return by_v(ty, std::integral_constant<int, 16>{});
+    return by_v(ty, std::integral_constant<int, 32>{});
   };
   if (type == kBF16) return by_n(std::integral_constant<int, kBF16>{});
   if (type == kF16) return by_n(std::integral_constant<int, kF16>{});
   return by_n(std::integral_constant<int, kF32>{});
 }
+// Rows that start on 16 bytes each.
+bool whole_rows(const void* p, int64_t ld, int type) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * (type == kF32 ? 4 : 2) % 16 == 0;
+}
 
 }  // namespace
 
 cudaError_t launch_route(const RouteArgs& a, int type, int num_sms, cudaStream_t s) {
-  return by_shape(type, a.E, [&](auto ty, auto n) {
-    auto kernel = route_kernel<decltype(ty)::value, decltype(n)::value>;
+  return by_shape(type, a.E, whole_rows(a.logits, a.ld, type), [&](auto ty, auto n, auto v) {
+    auto kernel = route_kernel<decltype(ty)::value, decltype(n)::value, decltype(v)::value>;
     int per_sm = 0;
     cudaError_t err = occupancy(kernel, kThreads, 0, &per_sm);
     if (err != cudaSuccess) return err;
@@ -699,8 +856,8 @@ size_t balance_ws_bytes(int E, int Q) {
 }
 
 cudaError_t launch_balance(const BalanceArgs& a, int type, int num_sms, cudaStream_t s) {
-  cudaError_t err = by_shape(type, a.E, [&](auto ty, auto n) {
-    auto kernel = balance_parts_kernel<decltype(ty)::value, decltype(n)::value>;
+  cudaError_t err = by_shape(type, a.E, whole_rows(a.logits, a.ld, type), [&](auto ty, auto n, auto v) {
+    auto kernel = balance_parts_kernel<decltype(ty)::value, decltype(n)::value, decltype(v)::value>;
     const size_t smem = (2 * (size_t)a.g.Q + (1 + kWarps) * (size_t)a.E) * 4;
     cudaError_t e = opt_in_smem(kernel, smem);
     if (e != cudaSuccess) return e;
@@ -724,8 +881,9 @@ cudaError_t launch_balance(const BalanceArgs& a, int type, int num_sms, cudaStre
 }
 
 cudaError_t launch_route_grad(const RouteGradArgs& a, int type, int num_sms, cudaStream_t s) {
-  return by_shape(type, a.E, [&](auto ty, auto n) {
-    auto kernel = route_grad_kernel<decltype(ty)::value, decltype(n)::value>;
+  const bool whole = whole_rows(a.logits, a.ld, type) && whole_rows(a.dlogits, a.ldd, type);
+  return by_shape(type, a.E, whole, [&](auto ty, auto n, auto v) {
+    auto kernel = route_grad_kernel<decltype(ty)::value, decltype(n)::value, decltype(v)::value>;
     const size_t smem = (2 * (size_t)a.g.Q + kWarps * (size_t)a.E) * 4;
     cudaError_t err = opt_in_smem(kernel, smem);
     if (err != cudaSuccess) return err;
