@@ -249,9 +249,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_kernel(DispatchFp4Args 
     }
     buf = p.stages == 2 ? buf ^ 1 : 0;
   }
-  // tokens past the live ones have no rows; the layout's m_indices while the copies drain
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + tid + (int64_t)n_live * a.K; i < (int64_t)a.T * a.K; i += (int64_t)gridDim.x * kThreads)
-    a.src2dst[i] = -1;
+  // the layout's m_indices while the last copies drain
   fill_m_indices(a, st, ps, tid, kThreads);
   bulk_wait_all();
 }

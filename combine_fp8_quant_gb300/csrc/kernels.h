@@ -181,8 +181,12 @@ struct MatmulArgs {
   int64_t ld_xs;
   const uint32_t* ws;
   int64_t ld_ws;
+  const float* x_tscale;       // four bits: tensor scales of the rows [1] and the weights [L],
+  const float* w_tscale;       // optional
   int32_t* status;
 };
+// Element types of the products beyond moe_elem_t's: four bits, by their scales.
+constexpr int kE2M1MX = 16, kE2M1NV = 17;
 cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_matmul_grad_x(const MatmulArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_matmul_grad_w(const MatmulArgs& a, int num_sms, cudaStream_t s);

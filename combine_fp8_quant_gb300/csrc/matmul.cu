@@ -72,24 +72,38 @@ namespace moeperm {
 namespace {
 
 constexpr int kForward = 0, kGradX = 1, kGradW = 2;
+// Operands: 16 bits, e4m3 with a scale per 128, or e2m1 with a scale per 32 or per 16.
+constexpr int kHalf = 0, kFp8 = 1, kFp4Mx = 2, kFp4Nv = 3;
+constexpr bool is_fp4(int kind) { return kind >= kFp4Mx; }
 constexpr int kThreads = 288;
 constexpr int kMaxSplits = 4;
 constexpr int kMaxStages = 10;
 constexpr int kABytes = 16384;            // 128 rows x 128 bytes
 
 constexpr int kTmemCols = 512;
-constexpr int kScaleCols = 480;           // e4m3: scale words, 12 columns per buffer
-constexpr int kScaleBytes = 512 + 1024;   // of one buffer: 128 + 256 words
-constexpr int kScaleBufs = 8;             // in shared memory (two in tensor memory)
+// Scales go through buffers in shared memory (two in tensor memory). e4m3: a word of the
+// 128 weight rows and of up to 256 rows, 12 columns; e2m1: a piece of four words each.
+constexpr int kMaxScaleBufs = 8;
+template <int KIND>
+constexpr int kScaleBufs = is_fp4(KIND) ? 6 : kMaxScaleBufs;
+template <int KIND>
+constexpr int kScaleBytes = (is_fp4(KIND) ? 4 : 1) * (512 + 1024);
+template <int KIND>
+constexpr int kScaleWidth = is_fp4(KIND) ? 48 : 12;  // columns of a buffer
+template <int KIND>
+constexpr int kScaleCols = is_fp4(KIND) ? 416 : 480;
+// Reduction blocks (128 bytes of a row) that share a buffer of scales.
+template <int KIND>
+constexpr int kScaleBlocks = KIND == kFp4Nv ? 1 : KIND == kFp4Mx ? 2 : 4;
 constexpr int kBoxes = 7;                 // heights of the row boxes a CTA may load
 __host__ __device__ constexpr int box_rows(int i) {
   return i < 3 ? 8 << i : i < 5 ? 32 * (i - 1) : 16 * (i + 2);  // 8 16 32 64 96 112 128
 }
 
-// Rows of one tile (the N side): two accumulators fill tensor memory; e4m3
-// leaves room for the scale words.
-template <bool FP8>
-constexpr int kRows = FP8 ? 240 : 256;
+// Rows of one tile (the N side): two accumulators fill tensor memory, but for
+// the room that scale words take.
+template <int KIND>
+constexpr int kRows = KIND == kHalf ? 256 : KIND == kFp8 ? 240 : 208;
 
 struct Maps {
   CUtensorMap a;
@@ -120,6 +134,8 @@ struct Args {
   const uint32_t* ws;        // and of the weights
   int64_t ld_ws;
   int32_t G4;
+  const float* x_tscale;     // e2m1: tensor scales, or nullptr
+  const float* w_tscale;
   int32_t* status;
 };
 
@@ -308,13 +324,14 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
   }
 }
 
-template <int MODE, bool FP8>
+template <int MODE, int KIND>
 __global__ void __launch_bounds__(kThreads, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t dyn[];
   __shared__ Bars s_bars;
   uint64_t *s_full = s_bars.full, *s_empty = s_bars.empty, *s_raw = s_bars.raw;
-  __shared__ uint64_t s_tfull[2], s_tempty[2], s_sraw[kScaleBufs], s_sfull[kScaleBufs], s_sempty[kScaleBufs], s_drain;
+  __shared__ uint64_t s_tfull[2], s_tempty[2], s_sraw[kMaxScaleBufs], s_sfull[kMaxScaleBufs], s_sempty[kMaxScaleBufs],
+      s_drain;
   __shared__ uint64_t s_go, s_recv;  // splits: the ring may be written; the accumulators have arrived
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_stop;
@@ -325,12 +342,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = crank >> 1, leader = crank & ~1;        // cluster rank of the pair's first CTA
   const uint16_t both = (uint16_t)(3 << leader);
   const int pair = blockIdx.x / (2 * p.splits), npairs = gridDim.x / (2 * p.splits);  // (clusters)
-  constexpr int kTileRows = kRows<FP8>;
-  constexpr int kRedBlock = FP8 ? 128 : 64;  // reduction elements per stage
+  constexpr int kTileRows = kRows<KIND>;
+  constexpr bool kScaled = KIND != kHalf, FP8 = KIND == kFp8, FP4 = is_fp4(KIND);
+  constexpr int kBufs = kScaleBufs<KIND>, kBufBytes = kScaleBytes<KIND>, kPerBuf = kScaleBlocks<KIND>;
+  constexpr int kRedBlock = kScaled ? 128 : 64;  // reduction elements per stage (e2m1: pairs of them)
 
   uint8_t* ring = dyn + ((1024 - (smem_addr(dyn) & 1023)) & 1023);
-  uint8_t* s_scale = ring + p.ring_bytes;                                 // FP8: kScaleBufs buffers
-  uint8_t* s_stage = s_scale + (FP8 ? kScaleBufs * kScaleBytes : 0);               // the epilogue's
+  uint8_t* s_scale = ring + p.ring_bytes;                                 // kBufs buffers
+  uint8_t* s_stage = s_scale + (kScaled ? kBufs * kBufBytes : 0);                  // the epilogue's
   int32_t* s_tiles = reinterpret_cast<int32_t*>(s_stage + kStageBytes);   // [L + 1]
   int32_t* s_begin = s_tiles + p.L + 1;
   int32_t* s_count = s_begin + p.L;
@@ -347,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_addr(s_tfull + i), 1);
       mbar_init(smem_addr(s_tempty + i), 8);  // four epilogue warps of each CTA
     }
-    for (int i = 0; i < kScaleBufs; ++i) {
-      mbar_init(smem_addr(s_sraw + i), 32);
+    for (int i = 0; i < kBufs; ++i) {
+      mbar_init(smem_addr(s_sraw + i), FP4 ? 1 : 32);
       mbar_init(smem_addr(s_sfull + i), 2);  // one of each CTA
       mbar_init(smem_addr(s_sempty + i), 1);
     }
@@ -592,7 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_or_stop(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
         tc_fence_after();
         const uint32_t d = tmem + as * kTileRows;
-        const uint32_t idesc = FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
+        const uint32_t idesc = FP4 ? idesc_e2m1(t.n, KIND == kFp4Mx, 0)
+                               : FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
         auto advance = [&] {  // hand the stage back and move on to the next
           mma_commit_pair(bar + kEmptyOffset, both);
           lo += stage_bytes >> 4;
@@ -604,13 +624,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1;
           }
         };
-        if constexpr (FP8) {
+        if constexpr (FP4) {
+          // A piece of scales (four words a row) serves one block (a word per product) or
+          // two (a word per two products, the halves of it). The columns of the piece
+          // before the last are free once its products are done.
+          for (int kb = 0; kb < t.nkb && ok; kb += kPerBuf, ++sf_it) {
+            const int sb = sf_it % kBufs;
+            if (sf_it >= 2 && !(ok = wait_or_stop(smem_addr(s_sempty + (sf_it - 2) % kBufs), ((sf_it - 2) / kBufs) & 1, &s_stop)))
+              break;
+            if (!(ok = wait_or_stop(smem_addr(s_sfull + sb), (sf_it / kBufs) & 1, &s_stop))) break;
+            const uint32_t sfa = tmem + kScaleCols<KIND> + kScaleWidth<KIND> * (sf_it & 1), sfb = sfa + 16;
+            const uint32_t sm = desc_lo(smem_addr(s_scale + sb * kBufBytes), 0);
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              tmem_copy_scales(sfa + 4 * w, sm + w * (512 >> 4));
+              tmem_copy_scales(sfb + 8 * w, sm + (2048 >> 4) + w * (512 >> 4));
+              if (t.n > 128) tmem_copy_scales(sfb + 8 * w + 4, sm + (4096 >> 4) + w * (512 >> 4));
+            }
+#pragma unroll
+            for (int j = 0; j < kPerBuf; ++j) {
+              if (kb + j >= t.nkb || !ok) break;
+              if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
+              const int left_red = p.red - (t.kb0 + kb + j) * 128;  // bytes: 32 a product
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int w = KIND == kFp4Nv ? k : 2 * j + k / 2;
+                const uint32_t sf = KIND == kFp4Nv ? 0 : 2 * (k & 1);
+                if (k * 32 < left_red)
+                  mma_e2m1<KIND == kFp4Mx>(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc | (sf << 4) | (sf << 29),
+                                           sfa + 4 * w, sfb + 8 * w, j + k > 0 ? 1u : (uint32_t)kb);
+              }
+              advance();
+            }
+            mma_commit_pair(smem_addr(s_sempty + sb), both);
+          }
+        } else if constexpr (FP8) {
           // four blocks share a scale word, each its own byte of it
           for (int kb = 0; kb < t.nkb && ok; kb += 4, ++sf_it) {
-            const int sb = sf_it % kScaleBufs;
-            if (!(ok = wait_or_stop(smem_addr(s_sfull + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
-            const uint32_t sfa = tmem + kScaleCols + 12 * (sf_it & 1), sfb = sfa + 4;
-            const uint32_t sm = desc_lo(smem_addr(s_scale + sb * kScaleBytes), 0);
+            const int sb = sf_it % kBufs;
+            if (!(ok = wait_or_stop(smem_addr(s_sfull + sb), (sf_it / kBufs) & 1, &s_stop))) break;
+            const uint32_t sfa = tmem + kScaleCols<KIND> + kScaleWidth<KIND> * (sf_it & 1), sfb = sfa + 4;
+            const uint32_t sm = desc_lo(smem_addr(s_scale + sb * kBufBytes), 0);
             tmem_copy_scales(sfa, sm);
             tmem_copy_scales(sfb, sm + (512 >> 4));
             if (t.n > 128) tmem_copy_scales(sfb + 4, sm + (1024 >> 4));
@@ -701,9 +755,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t* lb =
           p.xs + (p.cap > 0 ? (int64_t)t.e * p.G4 * p.ld_xs - (int64_t)t.e * p.cap : 0) + t.row0 + lane;
       for (int kb = 0; kb < t.nkb; kb += 4, ++sf_it) {
-        const int sb = sf_it % kScaleBufs;
-        if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kScaleBufs) & 1) ^ 1, &s_stop))) break;
-        const uint32_t dst = smem_addr(s_scale + sb * kScaleBytes + lane * 16);
+        const int sb = sf_it % kBufs;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kBufs) & 1) ^ 1, &s_stop))) break;
+        const uint32_t dst = smem_addr(s_scale + sb * kBufBytes + lane * 16);
         const int64_t word = (t.kb0 + kb) >> 2, wa = word * p.ld_ws, wb = word * p.ld_xs;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -725,11 +779,72 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Walk k = first(); ok && more(k); step(k)) {
         const int words = (run_nkb + 3) / 4;
         for (int i = 0; i < words; ++i, ++sf_it) {
-          const int sb = sf_it % kScaleBufs;
-          if (!(ok = wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kScaleBufs) & 1, &s_stop))) break;
+          const int sb = sf_it % kBufs;
+          if (!(ok = wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kBufs) & 1, &s_stop))) break;
           fence_proxy_async_smem();
           mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), leader));
         }
+      }
+    }
+  } else if (FP4 && warp == 2) {
+    // A row's piece of scales is 16 bytes, and those of consecutive rows are
+    // contiguous: one bulk copy for the tile's rows and one for its weight rows (gated:
+    // one for each run of 16 gate or up rows), up to kBufs pieces ahead.
+    if (elect_one()) {
+      int sf_it = 0;
+      bool ok = true;
+      const uint8_t* ws = reinterpret_cast<const uint8_t*>(p.ws);
+      const uint8_t* xs = reinterpret_cast<const uint8_t*>(p.xs);
+      for (Walk k = first(); ok && more(k); step(k)) {
+        const Tile t = tile_at(k);
+        const int f0 = t.fb * fblk, nf = max(min(fblk, p.feats - f0), 0);  // features of the tile
+        const int64_t wrow = (int64_t)t.e * p.wrows + f0;
+        const uint32_t bytes = (uint32_t)(t.rows + (p.gated ? 2 : 1) * nf) * 16;
+        for (int kb = 0; kb < t.nkb; kb += kPerBuf, ++sf_it) {
+          const int sb = sf_it % kBufs;
+          if (!(ok = wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kBufs) & 1) ^ 1, &s_stop))) break;
+          const uint32_t dst = smem_addr(s_scale + sb * kBufBytes), bar = smem_addr(s_sraw + sb);
+          const int64_t piece = (t.kb0 + kb) / kPerBuf;
+          mbar_expect_tx(bar, bytes);
+          bulk_load_g2s(dst + 2048, xs + (piece * p.ld_xs + t.row0) * 16, (uint32_t)t.rows * 16, bar);
+          const uint8_t* w = ws + (piece * p.ld_ws + wrow) * 16;
+          if (!p.gated) {
+            if (nf > 0) bulk_load_g2s(dst, w, (uint32_t)nf * 16, bar);
+          } else {
+            for (int i = 0; i < nf; i += 16) {
+              bulk_load_g2s(dst + i * 32, w + i * 16, 256, bar);
+              bulk_load_g2s(dst + i * 32 + 256, w + ((int64_t)p.feats + i) * 16, 256, bar);
+            }
+          }
+        }
+      }
+      // whatever ended the walk, no copy outlives the CTA
+      for (int i = sf_it > kBufs ? sf_it - kBufs : 0; i < sf_it; ++i)
+        mbar_wait(smem_addr(s_sraw + i % kBufs), (i / kBufs) & 1);
+    }
+  } else if (FP4 && warp == 3) {
+    // Tensor memory wants word w of row r of a block of 128 at byte 16 (r % 32) + 4 (r / 32)
+    // of the word's 512 bytes; the copies left row r's four words at byte 16 r. Lane l
+    // transposes the 4 x 4 words of rows l, 32 + l, 64 + l and 96 + l where they are.
+    bool ok = true;
+    int sf_it = 0;
+    for (Walk k = first(); ok && more(k); step(k)) {
+      const Tile t = tile_at(k);
+      const int blocks = t.n > 128 ? 3 : 2;
+      for (int kb = 0; kb < t.nkb; kb += kPerBuf, ++sf_it) {
+        const int sb = sf_it % kBufs;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kBufs) & 1, &s_stop))) break;
+        uint4* at = reinterpret_cast<uint4*>(s_scale + sb * kBufBytes) + lane;
+        for (int b = 0; b < blocks; ++b, at += 128) {
+          const uint4 r0 = at[0], r1 = at[32], r2 = at[64], r3 = at[96];
+          at[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+          at[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+          at[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+          at[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), leader));
       }
     }
   } else if (warp >= 4 && warp < 8) {
@@ -799,6 +914,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool gated = MODE == kForward && p.gated;
         const int f0 = gated ? t.fb * 64 + q * 16 : t.fb * 128 + q * 32;
         uint8_t* st = s_stage + q * 32 * kPitch;
+        float tscale = 1.0f;
+        if constexpr (FP4) {
+          if (p.x_tscale != nullptr) tscale = __ldg(p.x_tscale);
+          if (p.w_tscale != nullptr) tscale *= __ldg(p.w_tscale + t.e);
+        }
         float ba[2] = {0.0f, 0.0f}, bb[2] = {0.0f, 0.0f};  // bias of features l / 4 + 8 g
         if (MODE == kForward && p.bias != nullptr) {
           const float* bias = p.bias + (int64_t)t.e * p.wrows;
@@ -838,6 +958,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dst[2] += __uint_as_float(v.z);
                 dst[3] += __uint_as_float(v.w);
               }
+          }
+          if constexpr (FP4) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              a[j] *= tscale;
+              b[j] *= tscale;
+            }
           }
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
@@ -910,7 +1037,7 @@ void find_encode() {
 bool make_map(CUtensorMap* m, int type, const void* base, int rank, const cuuint64_t* dims,
               const cuuint64_t* strides, const cuuint32_t* box) {
   const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
-  const CUtensorMapDataType dt = type == kE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+  const CUtensorMapDataType dt = type == kE4M3 || type >= kE2M1MX ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                  : type == kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return g_encode(m, dt, (cuuint32_t)rank, const_cast<void*>(base), dims, strides, box, ones,
@@ -920,7 +1047,7 @@ bool make_map(CUtensorMap* m, int type, const void* base, int rank, const cuuint
 
 bool map_2d(CUtensorMap* m, int type, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_cols,
             int box_rows) {
-  const int es = type == kE4M3 ? 1 : 2;
+  const int es = type == kE4M3 || type >= kE2M1MX ? 1 : 2;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)(ld * es)};
   const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
@@ -935,15 +1062,16 @@ bool map_terms(CUtensorMap* m, const MatmulArgs& a, int64_t cols, int box_rows) 
   return make_map(m, a.type, a.g, 3, dims, strides, box);
 }
 
-template <int MODE, bool FP8>
+template <int MODE, int KIND>
 cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cudaStream_t s) {
   int optin = 0;
   cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerBlockOptin, &optin);
   if (err != cudaSuccess) return err;
   const size_t smem = (size_t)optin - 1024;  // room for the static arrays
-  const size_t lists = (size_t)(4 * a.L + 1) * sizeof(int32_t) + kStageBytes + (FP8 ? kScaleBufs * kScaleBytes : 0);
+  const size_t lists = (size_t)(4 * a.L + 1) * sizeof(int32_t) + kStageBytes +
+                       (KIND != kHalf ? kScaleBufs<KIND> * kScaleBytes<KIND> : 0);
   a.ring_bytes = (int32_t)((smem - 1024 - lists) / 1024 * 1024);
-  err = opt_in_smem(matmul_kernel<MODE, FP8>, smem);
+  err = opt_in_smem(matmul_kernel<MODE, KIND>, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -956,8 +1084,8 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   cfg.numAttrs = 1;
   // Runs of the reduction: as many as leave every tile a cluster of its own that
   // is resident, at least eight blocks a run, and accumulators that fit the ring.
-  const int64_t blocks = (a.red + (FP8 ? 127 : 63)) / (FP8 ? 128 : 64);
-  const int64_t tile_rows = a.R < kRows<FP8> ? a.R : kRows<FP8>;
+  const int64_t blocks = (a.red + (KIND != kHalf ? 127 : 63)) / (KIND != kHalf ? 128 : 64);
+  const int64_t tile_rows = a.R < kRows<KIND> ? a.R : kRows<KIND>;
   for (int splits = MODE == kGradW ? 1 : kMaxSplits;; splits /= 2) {
     const int cl = 2 * splits;
     if (splits > 1 && (blocks < 8 * splits || (splits - 1) * ((tile_rows + 31) / 32) * 16384 > a.ring_bytes)) continue;
@@ -965,7 +1093,7 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
     cfg.gridDim = dim3((unsigned)(num_sms / cl * cl));
     // no more clusters than can be resident at once: one more would start late
     int clusters = 0;
-    err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, FP8>), cfg, cl, &clusters);
+    err = max_clusters_cached(reinterpret_cast<const void*>(matmul_kernel<MODE, KIND>), cfg, cl, &clusters);
     if (err != cudaSuccess) return err;
     if (clusters > num_sms / cl) clusters = num_sms / cl;
     if (splits > 1 && max_tiles > clusters) continue;
@@ -973,14 +1101,15 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
     if (clusters > max_tiles) clusters = (int)max_tiles;
     a.splits = splits;
     cfg.gridDim = dim3((unsigned)(clusters * cl));
-    return cudaLaunchKernelEx(&cfg, matmul_kernel<MODE, FP8>, maps, a);
+    return cudaLaunchKernelEx(&cfg, matmul_kernel<MODE, KIND>, maps, a);
   }
 }
 
 Args common_args(const MatmulArgs& m) {
   Args a{};
   a.seg_begin = m.seg_begin; a.seg_end = m.seg_end; a.cap = m.cap;
-  a.R = (int32_t)m.R; a.L = m.L; a.f16 = m.type == kF16 || (m.type == kE4M3 && m.out_type == kF16);
+  a.R = (int32_t)m.R; a.L = m.L; 
+  a.f16 = m.type == kF16 || (m.type != kBF16 && m.out_type == kF16);
   a.terms = m.terms;
   a.status = m.status;
   return a;
@@ -997,33 +1126,38 @@ int64_t max_row_tiles(const MatmulArgs& m, int tile_rows) {
 cudaError_t launch_matmul(const MatmulArgs& m, int num_sms, cudaStream_t s) {
   std::call_once(g_encode_once, find_encode);
   if (g_encode == nullptr) return cudaErrorNotSupported;
-  const bool fp8 = m.type == kE4M3;
-  const int es = fp8 ? 1 : 2, span = 128 / es;  // elements per 128-byte line
+  const bool fp8 = m.type == kE4M3, fp4 = m.type >= kE2M1MX;
+  const int es = fp8 || fp4 ? 1 : 2, span = 128 / es;  // elements (e2m1: pairs) per 128-byte line
+  const int K = fp4 ? m.K / 2 : m.K;
   Args a = common_args(m);
-  a.red = m.K; a.feats = m.N; a.wrows = m.gated ? 2 * m.N : m.N;
+  a.x_tscale = m.x_tscale; a.w_tscale = m.w_tscale;
+  a.red = K; a.feats = m.N; a.wrows = m.gated ? 2 * m.N : m.N;
   a.gated = m.gated; a.act = m.act; a.bias = m.bias; a.residual = m.residual; a.ld_res = m.ld_res;
   a.out = m.out; a.ldo = m.ldo; a.pre = m.pre; a.ld_pre = m.ld_pre;
   a.xs = m.xs; a.ld_xs = m.ld_xs; a.ws = m.ws; a.ld_ws = m.ld_ws; a.G4 = (m.K / 128 + 3) / 4;
   const int fblk = m.gated ? 64 : 128;
   const int nfp = (m.N + 2 * fblk - 1) / (2 * fblk);
   Maps maps;
-  const cuuint64_t row = (cuuint64_t)m.K * es;
+  const cuuint64_t row = (cuuint64_t)K * es;
   bool ok;
   if (m.gated) {  // (k, 16 features, gate | up, feature / 16, expert)
-    const cuuint64_t dims[5] = {(cuuint64_t)m.K, 16, 2, (cuuint64_t)m.N / 16, (cuuint64_t)m.L};
+    const cuuint64_t dims[5] = {(cuuint64_t)K, 16, 2, (cuuint64_t)m.N / 16, (cuuint64_t)m.L};
     const cuuint64_t strides[4] = {row, row * m.N, row * 16, row * 2 * m.N};
     const cuuint32_t box[5] = {(cuuint32_t)span, 16, 2, 4, 1};
     ok = make_map(&maps.a, m.type, m.w, 5, dims, strides, box);
   } else {
-    const cuuint64_t dims[3] = {(cuuint64_t)m.K, (cuuint64_t)m.N, (cuuint64_t)m.L};
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)m.N, (cuuint64_t)m.L};
     const cuuint64_t strides[2] = {row, row * m.N};
     const cuuint32_t box[3] = {(cuuint32_t)span, 128, 1};
     ok = make_map(&maps.a, m.type, m.w, 3, dims, strides, box);
   }
-  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.x, m.K, m.R, m.ldx, span, box_rows(i));
+  for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.x, K, m.R, m.ldx, span, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tiles = max_row_tiles(m, fp8 ? kRows<true> : kRows<false>) * nfp;
-  return fp8 ? launch<kForward, true>(maps, a, tiles, num_sms, s) : launch<kForward, false>(maps, a, tiles, num_sms, s);
+  const int64_t tile_rows = fp4 ? kRows<kFp4Mx> : fp8 ? kRows<kFp8> : kRows<kHalf>;
+  const int64_t tiles = max_row_tiles(m, (int)tile_rows) * nfp;
+  if (m.type == kE2M1MX) return launch<kForward, kFp4Mx>(maps, a, tiles, num_sms, s);
+  if (m.type == kE2M1NV) return launch<kForward, kFp4Nv>(maps, a, tiles, num_sms, s);
+  return fp8 ? launch<kForward, kFp8>(maps, a, tiles, num_sms, s) : launch<kForward, kHalf>(maps, a, tiles, num_sms, s);
 }
 
 cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t s) {
@@ -1041,7 +1175,7 @@ cudaError_t launch_matmul_grad_x(const MatmulArgs& m, int num_sms, cudaStream_t 
   bool ok = make_map(&maps.a, m.type, m.w, 3, dims, strides, box);
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_terms(&maps.b[i], m, a.wrows, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  return launch<kGradX, false>(maps, a, max_row_tiles(m, kRows<false>) * nfp, num_sms, s);
+  return launch<kGradX, kHalf>(maps, a, max_row_tiles(m, kRows<kHalf>) * nfp, num_sms, s);
 }
 
 cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t s) {
@@ -1056,7 +1190,7 @@ cudaError_t launch_matmul_grad_w(const MatmulArgs& m, int num_sms, cudaStream_t 
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_terms(&maps.b[i], m, a.wrows, 64);
   if (!ok) return cudaErrorInvalidValue;
   const int64_t tiles = (int64_t)m.L * ((a.wrows + 255) / 256) * nfp;
-  return launch<kGradW, false>(maps, a, tiles, num_sms, s);
+  return launch<kGradW, kHalf>(maps, a, tiles, num_sms, s);
 }
 
 }  // namespace moeperm

@@ -179,6 +179,28 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint32_t b, uin
                "\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
                : "memory");
 }
+// e2m1 operands, 64 reduction elements an instruction: one UE8M0 scale per 32 (bytes sf
+// and sf + 1 of the scale words, sf 0 or 2), or one UE4M3 scale per 16 (all four bytes).
+__device__ __forceinline__ uint32_t idesc_e2m1(int n, bool ue8m0, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((ue8m0 ? 1u : 0u) << 23) |
+         ((256u >> 4) << 24) | (sf << 29);
+}
+template <bool UE8M0>
+__device__ __forceinline__ void mma_e2m1(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate) {
+  if constexpr (UE8M0)
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                 "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+                 "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;"
+                 "\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
+                 : "memory");
+  else
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+                 "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %7};\n\t"
+                 "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], da, db, %3, [%4], [%5], p;"
+                 "\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
+                 : "memory");
+}
 // 32 rows of 16 bytes of shared memory to 4 tensor-memory columns, in all four
 // lane quarters; in both CTAs of the pair, each from its own shared memory.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t lo) {

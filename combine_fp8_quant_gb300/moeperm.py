@@ -32,6 +32,7 @@ ELEM = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3
 ACT = {"none": 0, "relu": 1, "silu": 2, "gelu": 3}
 GATE = {"none": 0, "channel": 1, "token": 2}
 SCORE = {"softmax": 0, "sigmoid": 1}
+FP4 = {"e8m0": 0, "mx": 1, "nv": 2}
 
 _lock = threading.Lock()
 _lib = None
@@ -98,6 +99,13 @@ def _declare(L):
         "moe_expert_matmul_grad_workspace_bytes": (sz, [i64, i32, i32]),
         "moe_expert_matmul_grad": (i32, [vp, i64, vp, i64, i32, i64, i32, vp, i32, i32, i32, i32, vp,
                                          i64, vp, vp, i32, vp, i64, vp, i32, vp, vp, sz, vp, vp]),
+        "moe_fp4_scale_bytes": (sz, [i64, i32, i32]),
+        "moe_quant_fp4": (i32, [vp, i64, i32, i64, i32, i32, vp, i32, vp, vp, vp, i32, vp, vp, i64, vp, vp]),
+        "moe_dequant_fp4": (i32, [vp, vp, i64, i64, i32, i32, vp, i32, vp, vp, vp, i32, vp, i64, i32, vp, vp]),
+        "moe_dispatch_fp4": (i32, [vp, i64, i32, i32, vp, i32, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, i64,
+                                   vp, i64, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]),
+        "moe_expert_matmul_fp4": (i32, [vp, i64, vp, i64, vp, i64, i32, vp, vp, i64, vp, i32, i32, i32, i32, i32,
+                                        vp, vp, vp, i32, vp, i64, vp, i64, i32, vp, vp]),
         "moe_route": (i32, [vp, i64, i32, i32, vp, i32, i32, i32, vp, i32, f32, vp, vp, vp, vp]),
         "moe_balance_loss_workspace_bytes": (sz, [i32, i32]),
         "moe_balance_loss": (i32, [vp, i64, i32, i32, vp, i32, vp, i32, i32, vp, vp, i32, vp, vp, vp, vp,
@@ -349,6 +357,43 @@ def moe_expert_matmul_grad(dout, ldd, x, ldx, dtype, R, K, w, L, N, gated, act, 
         _ptr(pre), ld_pre, _ptr(seg_begin), _ptr(seg_end), cap, _ptr(dx), ld_dx, _ptr(dw),
         ELEM[dw_dtype], _ptr(dbias), _ptr(workspace), workspace_bytes, _ptr(d_status),
         _stream(stream)))
+
+
+def moe_fp4_scale_bytes(ld: int, H: int, fmt: str) -> int:
+    return int(lib().moe_fp4_scale_bytes(ld, H, FP4[fmt]))
+
+
+def moe_quant_fp4(x, ldx, dtype, R, H, fmt, tensor_scale, n_scales, d_num_live, m_indices, masked_m, cap, xq,
+                  scales, ld_s, d_status, stream=None) -> int:
+    return int(lib().moe_quant_fp4(
+        _ptr(x), ldx, ELEM[dtype], R, H, FP4[fmt], _ptr(tensor_scale), n_scales, _ptr(d_num_live),
+        _ptr(m_indices), _ptr(masked_m), cap, _ptr(xq), _ptr(scales), ld_s, _ptr(d_status), _stream(stream)))
+
+
+def moe_dequant_fp4(xq, scales, ld_s, R, H, fmt, tensor_scale, n_scales, d_num_live, m_indices, masked_m, cap,
+                    x, ldx, dtype, d_status, stream=None) -> int:
+    return int(lib().moe_dequant_fp4(
+        _ptr(xq), _ptr(scales), ld_s, R, H, FP4[fmt], _ptr(tensor_scale), n_scales, _ptr(d_num_live),
+        _ptr(m_indices), _ptr(masked_m), cap, _ptr(x), ldx, ELEM[dtype], _ptr(d_status), _stream(stream)))
+
+
+def moe_dispatch_fp4(x, ldx, dtype, T, d_num_tokens, H, topk_ids, topk_weights, K, E, L, block_e, fmt,
+                     tensor_scale, xq, scales, ld_s, m_indices, bound, src2dst, counts, starts, psum, total,
+                     row_weights, workspace, workspace_bytes, d_status, stream=None) -> int:
+    return int(lib().moe_dispatch_fp4(
+        _ptr(x), ldx, ELEM[dtype], T, _ptr(d_num_tokens), H, _ptr(topk_ids), _ptr(topk_weights), K, E, L,
+        block_e, FP4[fmt], _ptr(tensor_scale), _ptr(xq), _ptr(scales), ld_s, _ptr(m_indices), bound,
+        _ptr(src2dst), _ptr(counts), _ptr(starts), _ptr(psum), _ptr(total), _ptr(row_weights),
+        _ptr(workspace), workspace_bytes, _ptr(d_status), _stream(stream)))
+
+
+def moe_expert_matmul_fp4(x, ldx, x_scales, ld_xs, x_tscale, R, K, w, w_scales, ld_ws, w_tscale, fmt, L, N,
+                          gated, act, bias, seg_begin, seg_end, cap, residual, ld_res, out, ldo, out_dtype,
+                          d_status, stream=None) -> int:
+    return int(lib().moe_expert_matmul_fp4(
+        _ptr(x), ldx, _ptr(x_scales), ld_xs, _ptr(x_tscale), R, K, _ptr(w), _ptr(w_scales), ld_ws,
+        _ptr(w_tscale), FP4[fmt], L, N, int(gated), ACT[act], _ptr(bias), _ptr(seg_begin), _ptr(seg_end), cap,
+        _ptr(residual), ld_res, _ptr(out), ldo, ELEM[out_dtype], _ptr(d_status), _stream(stream)))
 
 
 def moe_route(logits, ldl, dtype, T, d_num_tokens, E, K, score, bias, renorm, scale, topk_ids,
@@ -888,6 +933,198 @@ def block_norm_grad(dx_out, dh, x_out, y=None, w_post=None, gate=None, scale=1.0
                                o["dw_post"], o["dgate"], o["dw_pre"], ws.buf, ws.nbytes),
            "moe_block_norm_grad")
     return o
+
+
+FP4_BYTES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,) if hasattr(torch, "float4_e2m1fn_x2") else ())
+
+
+def _fp4(fmt):
+    if fmt not in FP4:
+        raise ValueError(f"moeperm: fmt must be one of {sorted(FP4)}, not {fmt!r}")
+    return FP4[fmt]
+
+
+def fp4_scale_tensor(rows: int, H: int, fmt: str, device, ld: int | None = None):
+    """Allocate the scale bytes [pieces, ld, 16] of `rows` four-bit rows of H elements
+    (ld: rows by default)."""
+    _fp4(fmt)
+    g = 16 if fmt == "nv" else 32
+    return torch.empty(((H // g + 15) // 16, rows if ld is None else ld, 16), dtype=torch.uint8, device=device)
+
+
+def _fp4_scales(t, rows, H, fmt, name):
+    """The leading dimension of a scale tensor that holds `rows` rows of H elements."""
+    pieces = (H // (16 if fmt == "nv" else 32) + 15) // 16
+    if t.dtype != torch.uint8 or t.dim() != 3 or t.shape[0] < pieces or t.shape[1] < rows or t.shape[2] != 16 \
+            or not t.is_contiguous():
+        raise ValueError(f"moeperm: {name} must be contiguous uint8 scales [{pieces}, >= {rows}, 16] ({fmt}), not "
+                         f"{t.dtype} of shape {tuple(t.shape)}")
+    return t.shape[1]
+
+
+def _tensor_scale(t, fmt, name, n=None):
+    """Float32 scales of a tensor ("nv" only): how many."""
+    if t is None:
+        return 1
+    if fmt != "nv":
+        raise ValueError(f"moeperm: {name} belongs to the nv format, not to {fmt}")
+    _vec(t, t.numel() if n is None else n, name)
+    return t.numel()
+
+
+def _fp4_rows(R, num_live, m_indices, masked_m):
+    """The rows to work on, named in one way at most: cap."""
+    if sum(v is not None for v in (num_live, m_indices, masked_m)) > 1:
+        raise ValueError("moeperm: give one of num_live, m_indices and masked_m")
+    _vec(num_live, 1, "num_live", torch.int32)
+    _vec(m_indices, R, "m_indices", torch.int32)
+    if masked_m is None:
+        return 0
+    L = masked_m.numel()
+    _vec(masked_m, L, "masked_m", torch.int32)
+    if L < 1 or R % L:
+        raise ValueError(f"moeperm: {R} rows are not slabs of {L} experts")
+    return R // L
+
+
+def quant_fp4(x, fmt="nv", tensor_scale=None, num_live=None, m_indices=None, masked_m=None, status=None):
+    """Rows to four bits (e2m1): x [R, H] (slabs [L, cap, H] with masked_m) in bfloat16,
+    float16 or float32, H a multiple of 64. fmt "nv": a float8 scale for each 16
+    elements and tensor_scale, float32 [1] or one for each of n equal blocks of rows
+    (amax / 2688 is a good one); "e8m0" and "mx": a power of two for each 32, the
+    smallest that saturates nothing, or OCP MX's. Only the first num_live rows, those
+    with m_indices >= 0 as a dispatch writes it, or the first masked_m of each slab,
+    where one is given. Returns a dict: xq uint8 [.., H / 2], scales uint8
+    [pieces, R, 16], ld_s, status."""
+    dtype = _elem(x, FLOATS, "x")
+    f = _fp4(fmt)
+    lead = tuple(x.shape[:-1])
+    if x.dim() == 3 and masked_m is not None:
+        if not x.is_contiguous() or masked_m.numel() != x.shape[0]:
+            raise ValueError("moeperm: with masked_m, x must be contiguous slabs [L, cap, H]")
+        x = x.view(-1, x.shape[2])
+    ldx = _rows(x, "x")
+    R, H = x.shape
+    cap = _fp4_rows(R, num_live, m_indices, masked_m)
+    nts = _tensor_scale(tensor_scale, fmt, "tensor_scale")
+    dev = x.device
+    xq = torch.empty((*lead, H // 2), dtype=torch.uint8, device=dev)
+    sc = fp4_scale_tensor(R, H, fmt, dev)
+    st = _status(status, num_live is not None, dev)
+    px, pt, pn, pi, pm, pq, ps, pst = _on_current(x, tensor_scale, num_live, m_indices, masked_m, xq, sc, st)
+    _check(lib().moe_quant_fp4(px, ldx, ELEM[dtype], R, H, f, pt, nts, pn, pi, pm, cap, pq, ps, R, pst, _stream()),
+           "moe_quant_fp4")
+    return dict(xq=xq, scales=sc, ld_s=R, status=st)
+
+
+def dequant_fp4(xq, scales, fmt="nv", tensor_scale=None, dtype=torch.bfloat16, num_live=None, m_indices=None,
+                masked_m=None, status=None, out=None):
+    """The values of four-bit rows xq [R, H / 2] (slabs [L, cap, H / 2] with masked_m) with
+    their scales, in dtype or into `out`; rows as for quant_fp4, others are not
+    written."""
+    f = _fp4(fmt)
+    if xq.dtype not in FP4_BYTES:
+        raise ValueError(f"moeperm: xq must be uint8 pairs of elements, not {xq.dtype}")
+    lead, H = tuple(xq.shape[:-1]), xq.shape[-1] * 2
+    if not xq.is_contiguous() or xq.dim() != (3 if xq.dim() == 3 and masked_m is not None else 2):
+        raise ValueError("moeperm: xq must be contiguous [R, H / 2] (with masked_m also [L, cap, H / 2])")
+    R = xq.numel() * 2 // H if H else 0
+    cap = _fp4_rows(R, num_live, m_indices, masked_m)
+    nts = _tensor_scale(tensor_scale, fmt, "tensor_scale")
+    ld = _fp4_scales(scales, R, H, fmt, "scales")
+    if out is None:
+        out = torch.empty((*lead, H), dtype=dtype, device=xq.device)
+    elif tuple(out.shape) != (*lead, H):
+        raise ValueError(f"moeperm: out must have shape {(*lead, H)}")
+    dtype = _elem(out, FLOATS, "out")
+    o2 = out.view(R, H) if out.dim() == 3 else out
+    ldx = _rows(o2, "out")
+    st = _status(status, num_live is not None, xq.device)
+    pq, ps, pt, pn, pi, pm, po, pst = _on_current(xq, scales, tensor_scale, num_live, m_indices, masked_m, o2, st)
+    _check(lib().moe_dequant_fp4(pq, ps, ld, R, H, f, pt, nts, pn, pi, pm, cap, po, ldx, ELEM[dtype], pst, _stream()),
+           "moe_dequant_fp4")
+    return out
+
+
+def dispatch_fp4(x, topk_ids, topk_weights, num_experts, num_local_experts, block_e=128, fmt="nv",
+                 tensor_scale=None, num_tokens=None, workspace=None, status=None, row_weights=True):
+    """Quantise to four bits and scatter into the compact layout: xq [bound, H / 2] and
+    scales [pieces, bound, 16] as quant_fp4 makes them, and the layout tensors of
+    dispatch_compact. x in bfloat16, float16 or float32. Returns a dict."""
+    dtype = _elem(x, FLOATS, "x")
+    f = _fp4(fmt)
+    ldx = _rows(x, "x")
+    T, H = x.shape
+    K, L, dev = topk_ids.shape[1], num_local_experts, x.device
+    _vec(topk_ids, T * K, "topk_ids", torch.int32)
+    _vec(topk_weights, T * K, "topk_weights")
+    _tensor_scale(tensor_scale, fmt, "tensor_scale", 1)
+    bound = moe_compact_bound(T * K, L, block_e)
+    i32 = dict(dtype=torch.int32, device=dev)
+    o = dict(xq=torch.empty((bound, H // 2), dtype=torch.uint8, device=dev),
+             scales=fp4_scale_tensor(bound, H, fmt, dev), ld_s=bound, bound=bound,
+             m_indices=torch.empty(bound, **i32), src2dst=torch.empty((T, K), **i32),
+             counts=torch.empty(L, **i32), starts=torch.empty(L, **i32), psum=torch.empty(L, **i32),
+             total=torch.empty(1, **i32),
+             row_weights=torch.empty(bound, dtype=torch.float32, device=dev) if row_weights else None)
+    ws = workspace if workspace is not None else Workspace(T, K, L, dev)
+    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+    px, pn, pi, pw, pt, *po, pws, pst = _on_current(
+        x, num_tokens, topk_ids, topk_weights, tensor_scale, o["xq"], o["scales"], o["m_indices"], o["src2dst"],
+        o["counts"], o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, st)
+    _check(lib().moe_dispatch_fp4(px, ldx, ELEM[dtype], T, pn, H, pi, pw, K, num_experts, L, block_e, f, pt, po[0],
+                                  po[1], bound, po[2], bound, *po[3:], pws, ws.nbytes, pst, _stream()),
+           "moe_dispatch_fp4")
+    o["status"] = st
+    return o
+
+
+def expert_matmul_fp4(x, w, x_scales, w_scales, fmt="nv", starts=None, psum=None, x_tscale=None, w_tscale=None,
+                      bias=None, act="none", gated=False, residual=None, masked_m=None, out=None,
+                      out_dtype=torch.bfloat16, status=None):
+    """expert_matmul with four-bit rows and weights of one format, as quant_fp4 and
+    dispatch_fp4 make them: x uint8 [R, K / 2] (slabs [L, cap, K / 2] with masked_m),
+    w uint8 [L, N, K / 2] (gated [L, 2N, K / 2]) with the scales of w.view(-1, K / 2),
+    x_tscale float32 [1] and w_tscale [L] ("nv" only). The rest as in expert_matmul, the
+    output in out_dtype (bfloat16 or float16). Returns out."""
+    f = _fp4(fmt)
+    if x.dtype not in FP4_BYTES or w.dtype not in FP4_BYTES:
+        raise ValueError(f"moeperm: x and w must be uint8 pairs of four-bit elements, not {x.dtype} and {w.dtype}")
+    L, N, K2 = _expert_weights(w, gated)
+    if act not in ACT:
+        raise ValueError(f"moeperm: act must be one of {sorted(ACT)}, not {act!r}")
+    if out_dtype not in FLOATS[:2]:
+        raise ValueError(f"moeperm: out_dtype must be bfloat16 or float16, not {out_dtype}")
+    masked = masked_m is not None
+    begin, end = _segments(starts, psum, masked_m, L)
+    shape3 = x.shape
+    x, cap = _expert_rows(x, masked, L, "x")
+    ldx = _rows(x, "x", (x.shape[0], K2))
+    R, Nw = x.shape[0], (2 * N if gated else N)
+    ld_xs = _fp4_scales(x_scales, R, 2 * K2, fmt, "x_scales")
+    ld_ws = _fp4_scales(w_scales, L * Nw, 2 * K2, fmt, "w_scales")
+    _tensor_scale(x_tscale, fmt, "x_tscale", 1)
+    _tensor_scale(w_tscale, fmt, "w_tscale", L)
+    _vec(bias, L * Nw, "bias")
+    full = (*shape3[:-1], N)
+    if out is None:
+        out = torch.empty(full, dtype=out_dtype, device=x.device)
+    elif tuple(out.shape) != full:
+        raise ValueError(f"moeperm: out must have shape {full}")
+    odt = _elem(out, FLOATS[:2], "out")
+    o2 = _expert_rows(out, masked, L, "out")[0]
+    ldo = _rows(o2, "out", (R, N), odt)
+    res, ld_res = None, 0
+    if residual is not None:
+        res = _expert_rows(residual, masked, L, "residual")[0]
+        ld_res = _rows(res, "residual", (R, N), odt)
+    st = _status(status, begin is not None or masked, x.device)
+    px, pxs, pxt, pw, pws, pwt, pb, p0, p1, pr, po, pst = _on_current(
+        x, x_scales, x_tscale, w, w_scales, w_tscale, bias, begin, end, res, o2, st)
+    _check(lib().moe_expert_matmul_fp4(px, ldx, pxs, ld_xs, pxt, R, 2 * K2, pw, pws, ld_ws, pwt, f, L, N,
+                                       1 if gated else 0, ACT[act], pb, p0, p1, cap, pr, ld_res, po, ldo, ELEM[odt],
+                                       pst, _stream()), "moe_expert_matmul_fp4")
+    return out
 
 
 def _score(score):

@@ -77,7 +77,7 @@ typedef enum {
 #define MOE_STATUS_LIVE_OVERFLOW 0x2
 #define MOE_STATUS_BAD_LAYOUT 0x4
 /* A kernel that waits for its own asynchronous copies or tensor-core work
- * (moe_permute, moe_expert_matmul, moe_expert_matmul_grad) gives up about two
+ * (moe_permute, moe_expert_matmul, moe_expert_matmul_grad, moe_expert_matmul_fp4) gives up about two
  * seconds after the longest that the wait can take, and sets this bit; the
  * call's outputs are then incomplete. */
 #define MOE_STATUS_TIMEOUT 0x8
@@ -508,6 +508,102 @@ moe_status_t moe_block_norm_grad(
     const float* w_post, const float* gate, moe_gate_t gate_mode, float scale, const float* w_pre,
     const float* rstd_post, const float* rstd_pre, void* dx, void* dy, float* dw_post, float* dgate,
     float* dw_pre, void* workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------------------------ */
+/* Four-bit rows and weights, and the experts' products of them         */
+/* ------------------------------------------------------------------ */
+
+/*
+ * Elements are e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign), two to a byte, element 2 i
+ * in the low half of byte i, with one scale byte for each group along a row:
+ *   MOE_FP4_E8M0  groups of 32, UE8M0 scale 2^(b - 127): the least power of two with
+ *                 6 * 2^e >= amax, e in [-127, 127]; q = RNE(x * 2^-e)
+ *   MOE_FP4_MX    groups of 32, the OCP MX rule e = floor(log2(amax)) - 2, at least -127
+ *                 (zero gives -127); elements above 6 saturate
+ *   MOE_FP4_NV    groups of 16, UE4M3 scale s = RNE_e4m3(fl32(amax / fl32(6 * ts))), at
+ *                 most 448, ts the float32 scale of the tensor (1 where there is none);
+ *                 with d = fl32(s * ts), q = RNE(fl32(x / d)), saturating; 0 where s is 0
+ * A value is its element times 2^(b - 127), or times d. A group that holds a NaN or an
+ * infinity gets the scale NaN (0xFF, 0x7F) and elements 0: it is read as NaN.
+ * Scales [pieces, ld, 16] bytes: the 16 bytes at (c * ld + r) * 16 are the scales of
+ * groups 16 c .. 16 c + 15 of row r (0 past the last group); pieces = ceil(groups / 16).
+ * Row lengths are multiples of 64. A good ts of a tensor is amax / (6 * 448).
+ */
+typedef enum {
+  MOE_FP4_E8M0 = 0,
+  MOE_FP4_MX = 1,
+  MOE_FP4_NV = 2
+} moe_fp4_t;
+
+/* Bytes of a scale tensor with leading dimension ld for rows of H elements (0: H or fmt
+ * out of range). */
+size_t moe_fp4_scale_bytes(int64_t ld, int32_t H, moe_fp4_t fmt);
+
+/*
+ * moe_quant_fp4 -- rows to four bits, in the same order. Which rows: all R, or (at most
+ * one of)
+ *   d_num_live                   the first *d_num_live (more than R is clamped and sets
+ *                                MOE_STATUS_LIVE_OVERFLOW)
+ *   m_indices [R]                those with m_indices[r] >= 0, as a dispatch writes it
+ *   masked_m [R / cap], cap      of each slab of cap rows, the first masked_m[e]
+ * Other rows are neither read nor written.
+ *   x [R, ldx]                   BF16, F16 or F32, rows 16-byte aligned
+ *   tensor_scale [n_scales] f32  (optional, NV only) row r has tensor_scale[r / (R / n_scales)]:
+ *                                one for all rows, or one for each expert's weight rows.
+ *                                Positive and finite
+ *   xq [R, H / 2], scales        dense rows; ld_s >= R; both 16-byte aligned
+ * R < 2^31. Launches: 1.
+ */
+moe_status_t moe_quant_fp4(
+    const void* x, int64_t ldx, moe_elem_t type, int64_t R, int32_t H, moe_fp4_t fmt,
+    const float* tensor_scale, int32_t n_scales, const int32_t* d_num_live, const int32_t* m_indices,
+    const int32_t* masked_m, int32_t cap, void* xq, void* scales, int64_t ld_s, int32_t* d_status,
+    moe_stream_t stream);
+
+/*
+ * moe_dequant_fp4 -- the values of four-bit rows, fl32(element * scale) rounded to
+ * `type`; rows and arguments as for moe_quant_fp4, x [R, ldx] the output. Launches: 1.
+ */
+moe_status_t moe_dequant_fp4(
+    const void* xq, const void* scales, int64_t ld_s, int64_t R, int32_t H, moe_fp4_t fmt,
+    const float* tensor_scale, int32_t n_scales, const int32_t* d_num_live, const int32_t* m_indices,
+    const int32_t* masked_m, int32_t cap, void* x, int64_t ldx, moe_elem_t type, int32_t* d_status,
+    moe_stream_t stream);
+
+/*
+ * moe_dispatch_fp4 -- moe_dispatch_compact into four-bit rows. Inputs, layout outputs,
+ * row order, limits, workspace and errors are those of moe_dispatch_compact.
+ *   x [T, ldx]                   BF16, F16 or F32; H % 64 == 0, H <= 32768
+ *   tensor_scale [1] f32         (optional, NV only)
+ *   xq [bound, H / 2], scales    ld_s >= bound; only valid rows are written
+ * Launches: 1 for T*K <= 2048 slots, otherwise 2.
+ */
+moe_status_t moe_dispatch_fp4(
+    const void* x, int64_t ldx, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t H,
+    const int32_t* topk_ids, const float* topk_weights, int32_t K, int32_t E, int32_t L,
+    int32_t block_e, moe_fp4_t fmt, const float* tensor_scale, void* xq, void* scales, int64_t ld_s,
+    int32_t* m_indices, int64_t bound, int32_t* src2dst, int32_t* counts, int32_t* starts, int32_t* psum,
+    int32_t* total, float* row_weights, void* workspace, size_t workspace_bytes, int32_t* d_status,
+    moe_stream_t stream);
+
+/*
+ * moe_expert_matmul_fp4 -- moe_expert_matmul with four-bit rows and weights of one format:
+ * P[r, f] = x_tscale * w_tscale[e] * sum_k x[r, k] * w[e, f, k] + bias[e, f], where x and w
+ * are elements times group scales, summed in fp32 on the tensor cores; epilogue, rows of
+ * the experts and errors as there.
+ *   x [R, ldx] bytes             ldx >= K / 2, rows 16-byte aligned; K % 64 == 0
+ *   x_scales, ld_xs              pieces of the rows (slabs: row e * cap + j), ld_xs >= R
+ *   w [L, N or 2N, K / 2]        dense; w_scales, ld_ws: pieces of the L*N (L*2N) weight rows
+ *   x_tscale [1], w_tscale [L]   (optional, NV only)
+ *   out [R, ldo], residual       BF16 or F16
+ * MOE_FP4_E8M0 and MOE_FP4_MX are the same to this call. Launches: 1.
+ */
+moe_status_t moe_expert_matmul_fp4(
+    const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs, const float* x_tscale, int64_t R,
+    int32_t K, const void* w, const void* w_scales, int64_t ld_ws, const float* w_tscale, moe_fp4_t fmt,
+    int32_t L, int32_t N, int32_t gated, moe_act_t act, const float* bias, const int32_t* seg_begin,
+    const int32_t* seg_end, int32_t cap, const void* residual, int64_t ld_res, void* out, int64_t ldo,
+    moe_elem_t out_type, int32_t* d_status, moe_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* The router: choice of experts, its losses and their gradients        */
