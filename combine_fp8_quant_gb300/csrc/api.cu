@@ -465,6 +465,11 @@ moe_status_t moe_status_sync(const int32_t* d_status, moe_stream_t stream) {
   return MOE_OK;
 }
 
+moe_status_t moe_status_clear(int32_t* d_status, moe_stream_t stream) {
+  if (!d_status || !aligned_to(d_status, 4)) return MOE_ERR_INVALID_ARG;
+  return cuda_status(cudaMemsetAsync(d_status, 0, sizeof(int32_t), reinterpret_cast<cudaStream_t>(stream)));
+}
+
 const char* moe_status_string(moe_status_t s) {
   switch (s) {
     case MOE_OK: return "ok";

@@ -19,6 +19,10 @@ constexpr int kThreads = kWarps * 32;
 
 template <int TYPE>
 constexpr int kChunkBytes = 16 * (TYPE == kF32 ? 4 : 2);  // of 16 elements
+// Rows that start on 32 bytes each.
+__device__ __forceinline__ bool wide_rows(const void* p, int64_t ld_bytes) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uint64_t)ld_bytes) & 31) == 0;
+}
 
 // Whether row r is one of those to work on.
 __device__ __forceinline__ bool has_row(const Fp4Args& p, int64_t r, int64_t live) {
@@ -56,6 +60,7 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(Fp4Args p) {
   int s = (int)(u - r * upr);
   const int64_t dr = nwarps / upr;
   const int ds = (int)(nwarps - dr * upr);
+  const bool wide = wide_rows(p.x, p.ldx * (kChunkBytes<TYPE> / 16));
   for (; r < p.R; r += dr, s += ds) {
     if (s >= upr) {
       s -= upr;
@@ -68,7 +73,7 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(Fp4Args p) {
 #pragma unroll
     for (int i = 0; i < kAhead<TYPE>; ++i) {
       const int c = c0 + 32 * i;
-      x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+      x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch, wide);
     }
     const float ts = FMT == kFp4NV ? tensor_scale(p, r) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
 #pragma unroll
@@ -84,12 +89,13 @@ __global__ void __launch_bounds__(kThreads) quant_fp4_kernel(Fp4Args p) {
   }
 }
 
+// A lane writes 8 elements at a time (one run of memory for the warp), kUnit times.
+constexpr int kUnit = 4;
 template <int TYPE, int FMT>
 __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(Fp4Args p) {
-  constexpr int kUnit = 2;  // slices of 512 elements at a time
-  constexpr int kSpan = 32 * kUnit;
+  constexpr int kSpan = 32 * kUnit, kBytes = kChunkBytes<TYPE> / 2;
   const int lane = threadIdx.x & 31;
-  const int nch = p.H / 16, upr = (nch + kSpan - 1) / kSpan;
+  const int n8 = p.H / 8, upr = (n8 + kSpan - 1) / kSpan;
   const int64_t live = live_rows(p);
   const int64_t nwarps = (int64_t)gridDim.x * kWarps;
   int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -97,20 +103,20 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(Fp4Args p) {
   int s = (int)(u - r * upr);
   const int64_t dr = nwarps / upr;
   const int ds = (int)(nwarps - dr * upr);
+  const bool wide = wide_rows(p.x, p.ldx * (kChunkBytes<TYPE> / 16));
   for (; r < p.R; r += dr, s += ds) {
     if (s >= upr) {
       s -= upr;
       if (++r >= p.R) break;
     }
     if (!has_row(p, r, live)) continue;
-    uint2 q[kUnit];
-    uint32_t byte[kUnit];
+    uint32_t q[kUnit], byte[kUnit];
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       const int c = s * kSpan + 32 * i + lane;
-      if (c < nch) {
-        q[i] = __ldg(reinterpret_cast<const uint2*>(p.q + r * (p.H / 2) + (int64_t)c * 8));
-        byte[i] = __ldg(p.scales + ((int64_t)fp4_piece_of<FMT>(c) * p.ld + r) * 16 + fp4_byte_of<FMT>(c));
+      if (c < n8) {
+        q[i] = __ldg(reinterpret_cast<const uint32_t*>(p.q + r * (p.H / 2)) + c);
+        byte[i] = __ldg(p.scales + ((int64_t)fp4_piece_of<FMT>(c / 2) * p.ld + r) * 16 + fp4_byte_of<FMT>(c / 2));
       }
     }
     const float ts = FMT == kFp4NV ? tensor_scale(p, r) : 1.0f;
@@ -118,23 +124,23 @@ __global__ void __launch_bounds__(kThreads) dequant_fp4_kernel(Fp4Args p) {
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       const int c = s * kSpan + 32 * i + lane;
-      if (c >= nch) break;
+      if (c >= n8) break;
       const float d = fp4_scale<FMT>(byte[i], ts);
-      const uint32_t half[2] = {q[i].x, q[i].y};
+      float f[8];
+      e2m1x8_to_floats(q[i], f);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float f[8];
-        e2m1x8_to_floats(half[h], f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], d);
-        constexpr int kN = Vec<TYPE>::kN;
-#pragma unroll
-        for (int j = 0; j < 8; j += kN) {
-          float g[kN];
-#pragma unroll
-          for (int k = 0; k < kN; ++k) g[k] = f[j + k];
-          st_v4(dst + (int64_t)c * kChunkBytes<TYPE> + (h * 8 + j) * (kChunkBytes<TYPE> / 16), Vec<TYPE>::pack(g));
+      for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], d);
+      uint8_t* to = dst + (int64_t)c * kBytes;
+      if constexpr (TYPE == kF32) {
+        const float lo[4] = {f[0], f[1], f[2], f[3]}, hi[4] = {f[4], f[5], f[6], f[7]};
+        if (wide) {
+          st_v8(to, Vec<TYPE>::pack(lo), Vec<TYPE>::pack(hi));
+        } else {
+          st_v4(to, Vec<TYPE>::pack(lo));
+          st_v4(to + 16, Vec<TYPE>::pack(hi));
         }
+      } else {
+        st_v4(to, Vec<TYPE>::pack(f));
       }
     }
   }
@@ -157,8 +163,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_small_kernel(DispatchFp
   const int nch = a.H / 16, nchp = fp4_pieces(a.H, FMT) * (FMT == kFp4NV ? 16 : 32);
   const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
   const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x);
+  const bool wide = wide_rows(x, p.ldx_bytes);
   Chunk<TYPE> v;  // the first token's first elements load meanwhile
-  v.load(x + (int64_t)blockIdx.x * p.ldx_bytes + (int64_t)tid * kChunkBytes<TYPE>, (int)blockIdx.x < n_live && tid < nch);
+  v.load(x + (int64_t)blockIdx.x * p.ldx_bytes + (int64_t)tid * kChunkBytes<TYPE>, (int)blockIdx.x < n_live && tid < nch, wide);
   const float ts = FMT == kFp4NV && p.tscale != nullptr ? __ldg(p.tscale) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
   small_layout<S>(a, sm, s_wsum, n_live);
   const int32_t* rows_all = small_rows(a, sm);
@@ -166,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_small_kernel(DispatchFp
     const int32_t* rows = rows_all + (int64_t)t * a.K;
     for (int c = tid; c - lane < nchp; c += kThreads) {
       if (t != (int)blockIdx.x || c >= kThreads)
-        v.load(x + (int64_t)t * p.ldx_bytes + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+        v.load(x + (int64_t)t * p.ldx_bytes + (int64_t)c * kChunkBytes<TYPE>, c < nch, wide);
       uint32_t byte;
       const uint2 q = fp4_quant<TYPE, FMT>(v, ts, ts6, byte);
       const uint32_t word = fp4_scale_word<FMT>(c < nch ? byte : 0u);
@@ -203,6 +210,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_kernel(DispatchFp4Args 
   pdl_wait_primary();
   layout_prologue(a, sm, st, ps, s_wsum);
   const int nwarps = gridDim.x * kWarps;
+  const bool wide = wide_rows(a.x, p.ldx_bytes);
   int buf = 0;
   for (int64_t t = (int64_t)warp * gridDim.x + blockIdx.x; t < n_live; t += nwarps) {
     int row = -1;
@@ -223,7 +231,7 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_kernel(DispatchFp4Args 
 #pragma unroll
       for (int i = 0; i < kAhead<TYPE>; ++i) {
         const int c = c0 + 32 * i + lane;
-        x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch);
+        x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch, wide);
       }
 #pragma unroll
       for (int i = 0; i < kAhead<TYPE>; ++i) {
@@ -292,7 +300,7 @@ cudaError_t launch_quant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, c
 
 cudaError_t launch_dequant_fp4(const Fp4Args& a, int type, int fmt, int num_sms, cudaStream_t s) {
   return by_type(type, fmt, [&](auto ty, auto f) {
-    return launch_units(dequant_fp4_kernel<decltype(ty)::value, decltype(f)::value>, a, a.R * ((a.H / 16 + 63) / 64), num_sms, s);
+    return launch_units(dequant_fp4_kernel<decltype(ty)::value, decltype(f)::value>, a, a.R * ((a.H / 8 + 32 * kUnit - 1) / (32 * kUnit)), num_sms, s);
   });
 }
 

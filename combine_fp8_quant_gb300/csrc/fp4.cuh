@@ -57,12 +57,32 @@ __device__ __forceinline__ float fp4_scale(uint32_t byte, float ts) {
   return byte == 0 ? 0x1p-127f : byte == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(byte << 23);
 }
 
-// A chunk of 16 elements as a lane holds it.
+// 32 bytes at once, so that the lanes of a warp read or write one run of memory.
+__device__ __forceinline__ void ld_nc_v8(const void* p, uint4& a, uint4& b) {
+  asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+      : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+      : "l"(p));
+}
+__device__ __forceinline__ void st_v8(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// A chunk of 16 elements as a lane holds it. `wide`: the address is a multiple of 32.
 template <int TYPE>
 struct Chunk {
   static constexpr int kVecs = TYPE == kF32 ? 4 : 2;
   uint4 v[kVecs];
-  __device__ __forceinline__ void load(const void* p, bool valid) {
+  __device__ __forceinline__ void load(const void* p, bool valid, bool wide) {
+    if (wide) {
+#pragma unroll
+      for (int i = 0; i < kVecs; i += 2) {
+        if (valid) ld_nc_v8(static_cast<const uint8_t*>(p) + 16 * i, v[i], v[i + 1]);
+        else v[i] = v[i + 1] = make_uint4(0, 0, 0, 0);
+      }
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
       v[i] = valid ? ld_nc_v4(static_cast<const uint8_t*>(p) + 16 * i) : make_uint4(0, 0, 0, 0);

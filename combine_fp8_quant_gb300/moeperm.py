@@ -113,6 +113,7 @@ def _declare(L):
         "moe_route_grad": (i32, [vp, i64, i32, i32, vp, i32, vp, i32, i32, i32, f32, vp, vp, vp, vp, vp,
                                  i32, vp, i64, vp, vp]),
         "moe_status_sync": (i32, [vp, vp]),
+        "moe_status_clear": (i32, [vp, vp]),
         "moe_status_string": (C.c_char_p, [i32]),
         "moe_version": (C.c_char_p, []),
     }
@@ -151,23 +152,31 @@ def _ptrs(*tensors):
     return [None if t is None else t.data_ptr() if t.is_cuda else _off_device(t) for t in tensors]
 
 
+def _elsewhere(t, cur):
+    if not t.is_cuda:
+        _off_device(t)
+    raise ValueError(f"moeperm: tensor on {t.device}, but the current device is cuda:{cur}")
+
+
 def _on_current(*tensors):
     """_ptrs of tensors that all have to be on the current device, whose stream the call uses."""
     cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
-    out = []
-    for t in tensors:
-        if t is not None:
-            if not t.is_cuda:
-                _off_device(t)
-            if t.get_device() != cur:
-                raise ValueError(f"moeperm: tensor on {t.device}, but the current device is cuda:{cur}")
-        out.append(None if t is None else t.data_ptr())
-    return out
+    return [None if t is None else t.data_ptr() if t.get_device() == cur else _elsewhere(t, cur) for t in tensors]
 
 
 def _status(status, needed, dev):
-    """The caller's status word, or a new one where the call can meet an error in its data."""
-    return status if status is not None or not needed else torch.zeros(1, dtype=torch.int32, device=dev)
+    """The caller's status word, or a new one where the call can meet an error in its data
+    (cleared by the library: a fill by torch takes 10 us of the host)."""
+    if status is not None or not needed:
+        return status
+    st = torch.empty(1, dtype=torch.int32, device=dev)
+    _check(lib().moe_status_clear(*_on_current(st), _stream()), "moe_status_clear")
+    return st
+
+
+def _words(dev, *sizes):
+    """int32 vectors of these sizes from one allocation."""
+    return torch.unsafe_split_with_sizes(torch.empty(sum(sizes), dtype=torch.int32, device=dev), sizes)
 
 
 # The current stream's raw handle without building a torch Stream object (the
@@ -425,6 +434,10 @@ def moe_route_grad(logits, ldl, dtype, T, d_num_tokens, E, topk_ids, K, score, r
 
 def moe_status_sync(d_status, stream=None) -> int:
     return int(lib().moe_status_sync(_ptr(d_status), _stream(stream)))
+
+
+def moe_status_clear(d_status, stream=None) -> int:
+    return int(lib().moe_status_clear(_ptr(d_status), _stream(stream)))
 
 
 def moe_version() -> str:
@@ -1060,15 +1073,13 @@ def dispatch_fp4(x, topk_ids, topk_weights, num_experts, num_local_experts, bloc
     _vec(topk_weights, T * K, "topk_weights")
     _tensor_scale(tensor_scale, fmt, "tensor_scale", 1)
     bound = moe_compact_bound(T * K, L, block_e)
-    i32 = dict(dtype=torch.int32, device=dev)
+    m_indices, counts, starts, psum, total = _words(dev, bound, L, L, L, 1)
     o = dict(xq=torch.empty((bound, H // 2), dtype=torch.uint8, device=dev),
-             scales=fp4_scale_tensor(bound, H, fmt, dev), ld_s=bound, bound=bound,
-             m_indices=torch.empty(bound, **i32), src2dst=torch.empty((T, K), **i32),
-             counts=torch.empty(L, **i32), starts=torch.empty(L, **i32), psum=torch.empty(L, **i32),
-             total=torch.empty(1, **i32),
-             row_weights=torch.empty(bound, dtype=torch.float32, device=dev) if row_weights else None)
+             scales=fp4_scale_tensor(bound, H, fmt, dev), ld_s=bound, bound=bound, m_indices=m_indices,
+             src2dst=torch.empty((T, K), dtype=torch.int32, device=dev), counts=counts, starts=starts, psum=psum,
+             total=total, row_weights=torch.empty(bound, dtype=torch.float32, device=dev) if row_weights else None)
     ws = workspace if workspace is not None else Workspace(T, K, L, dev)
-    st = status if status is not None else torch.zeros(1, dtype=torch.int32, device=dev)
+    st = _status(status, True, dev)
     px, pn, pi, pw, pt, *po, pws, pst = _on_current(
         x, num_tokens, topk_ids, topk_weights, tensor_scale, o["xq"], o["scales"], o["m_indices"], o["src2dst"],
         o["counts"], o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, st)
@@ -1118,9 +1129,8 @@ def expert_matmul_fp4(x, w, x_scales, w_scales, fmt="nv", starts=None, psum=None
     if residual is not None:
         res = _expert_rows(residual, masked, L, "residual")[0]
         ld_res = _rows(res, "residual", (R, N), odt)
-    st = _status(status, begin is not None or masked, x.device)
     px, pxs, pxt, pw, pws, pwt, pb, p0, p1, pr, po, pst = _on_current(
-        x, x_scales, x_tscale, w, w_scales, w_tscale, bias, begin, end, res, o2, st)
+        x, x_scales, x_tscale, w, w_scales, w_tscale, bias, begin, end, res, o2, status)
     _check(lib().moe_expert_matmul_fp4(px, ldx, pxs, ld_xs, pxt, R, 2 * K2, pw, pws, ld_ws, pwt, f, L, N,
                                        1 if gated else 0, ACT[act], pb, p0, p1, cap, pr, ld_res, po, ldo, ELEM[odt],
                                        pst, _stream()), "moe_expert_matmul_fp4")
@@ -1131,6 +1141,16 @@ def _score(score):
     if score not in SCORE:
         raise ValueError(f"moeperm: score must be one of {sorted(SCORE)}, not {score!r}")
     return SCORE[score]
+
+
+def _logits(t):
+    """Shape, row stride and element type of logits."""
+    code = ELEM.get(t.dtype, 3)
+    if code > 2 or t.dim() != 2:
+        _elem(t, FLOATS, "logits")
+    ld = _rows(t, "logits")
+    T, E = t.shape
+    return T, E, ld, code
 
 
 def _groups(seq_begin, seq_end):
@@ -1153,17 +1173,16 @@ def route(logits, top_k, bias=None, score="softmax", renorm=True, scale=1.0, num
     times the scores. Experts masked by -inf are never chosen: where too few are left
     the id is -1 (which the dispatches drop) and the weight 0. Returns a dict:
     topk_ids [T, top_k] int32, topk_weights [T, top_k] float32, status."""
-    dtype = _elem(logits, FLOATS, "logits")
-    ldl = _rows(logits, "logits")
-    T, E = logits.shape
-    _vec(bias, E, "bias")
+    T, E, ldl, code = _logits(logits)
+    if bias is not None:
+        _vec(bias, E, "bias")
     dev = logits.device
     ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
     w = torch.empty((T, top_k), dtype=torch.float32, device=dev)
     st = _status(status, num_tokens is not None, dev)
     pl, pn, pb, pi, pw, pst = _on_current(logits, num_tokens, bias, ids, w, st)
-    _check(lib().moe_route(pl, ldl, ELEM[dtype], T, pn, E, top_k, _score(score), pb, 1 if renorm else 0, scale,
-                           pi, pw, pst, _stream()), "moe_route")
+    _check(lib().moe_route(pl, ldl, code, T, pn, E, top_k, _score(score), pb, 1 if renorm else 0, scale, pi, pw,
+                           pst, _stream()), "moe_route")
     return dict(topk_ids=ids, topk_weights=w, status=st)
 
 
@@ -1184,9 +1203,7 @@ def balance_loss(logits, topk_ids, seq_begin=None, seq_end=None, score="softmax"
     E / (K n^2) sum_e counts * prob_sums, 1 for even use) and the z loss (mean over
     the tokens of logsumexp(logits)^2); counts [Q, E] int32, the slots of each expert;
     prob_sums [Q, E] float32; status."""
-    dtype = _elem(logits, FLOATS, "logits")
-    ldl = _rows(logits, "logits")
-    T, E = logits.shape
+    T, E, ldl, code = _logits(logits)
     K, Q, dev = topk_ids.shape[1], _groups(seq_begin, seq_end), logits.device
     _vec(topk_ids, T * K, "topk_ids", torch.int32)
     loss = torch.empty(2, dtype=torch.float32, device=dev)
@@ -1196,7 +1213,7 @@ def balance_loss(logits, topk_ids, seq_begin=None, seq_end=None, score="softmax"
     st = _status(status, num_tokens is not None or seq_begin is not None, dev)
     pl, pn, pi, pb, pe, po, pc, ps, pw, pst = _on_current(logits, num_tokens, topk_ids, seq_begin, seq_end, loss, counts,
                                                           sums, ws.buf, st)
-    _check(lib().moe_balance_loss(pl, ldl, ELEM[dtype], T, pn, E, pi, K, _score(score), pb, pe, Q, po, pc, ps, pw,
+    _check(lib().moe_balance_loss(pl, ldl, code, T, pn, E, pi, K, _score(score), pb, pe, Q, po, pc, ps, pw,
                                   ws.nbytes, pst, _stream()), "moe_balance_loss")
     return dict(loss=loss, counts=counts, prob_sums=sums, status=st)
 
@@ -1207,9 +1224,7 @@ def route_grad(logits, topk_ids, dweights=None, dloss=None, counts=None, seq_beg
     both losses of balance_loss (dloss [2], with its counts and groups), in logits'
     type; 0 for tokens that are not live. score, renorm and scale as in the forward
     calls."""
-    dtype = _elem(logits, FLOATS, "logits")
-    ldl = _rows(logits, "logits")
-    T, E = logits.shape
+    T, E, ldl, code = _logits(logits)
     K, Q, dev = topk_ids.shape[1], _groups(seq_begin, seq_end), logits.device
     _vec(topk_ids, T * K, "topk_ids", torch.int32)
     _vec(dweights, T * K, "dweights")
@@ -1219,10 +1234,10 @@ def route_grad(logits, topk_ids, dweights=None, dloss=None, counts=None, seq_beg
         raise ValueError("moeperm: route_grad needs dweights, dloss or both")
     if dloss is not None and counts is None:
         raise ValueError("moeperm: the gradient of the balance loss needs its counts")
-    out = _like(out, (T, E), dtype, dev, "out")
+    out = _like(out, (T, E), logits.dtype, dev, "out")
     pl, pn, pi, pw, pd, pc, pb, pe, po, pst = _on_current(logits, num_tokens, topk_ids, dweights, dloss, counts,
                                                           seq_begin, seq_end, out, status)
-    _check(lib().moe_route_grad(pl, ldl, ELEM[dtype], T, pn, E, pi, K, _score(score), 1 if renorm else 0, scale, pw,
+    _check(lib().moe_route_grad(pl, ldl, code, T, pn, E, pi, K, _score(score), 1 if renorm else 0, scale, pw,
                                 pd, pc, pb, pe, Q, po, E, pst, _stream()), "moe_route_grad")
     return out
 

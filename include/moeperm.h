@@ -777,6 +777,10 @@ moe_status_t fp8_requant_per_tensor_ex(
  * "fail fast" check of [P3 风险与影响 item 1]. */
 moe_status_t moe_status_sync(const int32_t* d_status, moe_stream_t stream);
 
+/* Clears the device status word on `stream` (a 4-byte memset, which a graph captures).
+ * MOE_ERR_INVALID_ARG for NULL or a misaligned word. */
+moe_status_t moe_status_clear(int32_t* d_status, moe_stream_t stream);
+
 /* Static description of a status code. */
 const char* moe_status_string(moe_status_t s);
 

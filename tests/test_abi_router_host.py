@@ -93,3 +93,8 @@ def test_binding_refuses(mp):
                 lambda: mp.route_grad(x, ids, dweights=w)):
         with pytest.raises((ValueError, AssertionError, RuntimeError)):
             bad()
+
+
+def test_status_clear_refuses(mp):
+    assert mp.moe_status_clear(None, stream=S) == mp.MOE_ERR_INVALID_ARG
+    assert mp.moe_status_clear(FAKE + 2, stream=S) == mp.MOE_ERR_INVALID_ARG
