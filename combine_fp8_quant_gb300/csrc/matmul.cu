@@ -75,13 +75,16 @@ constexpr int kForward = 0, kGradX = 1, kGradW = 2;
 // Operands: 16 bits, e4m3 with a scale per 128, or e2m1 with a scale per 32 or per 16.
 constexpr int kHalf = 0, kFp8 = 1, kFp4Mx = 2, kFp4Nv = 3;
 constexpr bool is_fp4(int kind) { return kind >= kFp4Mx; }
-constexpr int kThreads = 288;
+// Warps: nine, and two more that lay out the scales of e2m1 operands.
+constexpr int kTransposers = 3;
+template <int KIND>
+constexpr int kThreadsOf = 288 + (is_fp4(KIND) ? 32 * (kTransposers - 1) : 0);
 constexpr int kMaxSplits = 4;
 constexpr int kMaxStages = 10;
 constexpr int kABytes = 16384;            // 128 rows x 128 bytes
 
 constexpr int kTmemCols = 512;
-// Scales go through buffers in shared memory (two in tensor memory). e4m3: a word of the
+// Scales go through buffers in shared memory and two in tensor memory. e4m3: a word of the
 // 128 weight rows and of up to 256 rows, 12 columns; e2m1: a piece of four words each.
 constexpr int kMaxScaleBufs = 8;
 template <int KIND>
@@ -178,6 +181,13 @@ __device__ __forceinline__ bool wait_or_stop(uint32_t bar, uint32_t parity, vola
 __device__ __forceinline__ bool warp_wait_or_stop(uint32_t bar, uint32_t parity, volatile int* stop,
                                                   long long limit = kWaitCycles) {
   return __all_sync(0xffffffffu, wait_or_stop(bar, parity, stop, limit));
+}
+
+// The wait of a converged warp whose next steps are uniform: one vote where the phase is
+// over already.
+__device__ __forceinline__ bool warp_ready(uint32_t bar, uint32_t parity, volatile int* stop) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return warp_wait_or_stop(bar, parity, stop);
 }
 
 // The limit of a wait that lasts while `blocks` reduction blocks go through the
@@ -325,7 +335,7 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
 }
 
 template <int MODE, int KIND>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
     matmul_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Args p) {
   extern __shared__ uint8_t dyn[];
   __shared__ Bars s_bars;
@@ -342,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = crank >> 1, leader = crank & ~1;        // cluster rank of the pair's first CTA
   const uint16_t both = (uint16_t)(3 << leader);
   const int pair = blockIdx.x / (2 * p.splits), npairs = gridDim.x / (2 * p.splits);  // (clusters)
-  constexpr int kTileRows = kRows<KIND>;
+  constexpr int kTileRows = kRows<KIND>, kThreads = kThreadsOf<KIND>;
   constexpr bool kScaled = KIND != kHalf, FP8 = KIND == kFp8, FP4 = is_fp4(KIND);
   constexpr int kBufs = kScaleBufs<KIND>, kBufBytes = kScaleBytes<KIND>, kPerBuf = kScaleBlocks<KIND>;
   constexpr int kRedBlock = kScaled ? 128 : 64;  // reduction elements per stage (e2m1: pairs of them)
@@ -358,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // ---- set-up
   if (tid == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
-      mbar_init(smem_addr(s_full + i), MODE == kGradW ? 2 : 1);
+      mbar_init(smem_addr(s_full + i), MODE == kGradW ? 2 : FP4 ? 3 : 1);
       mbar_init(smem_addr(s_empty + i), 1);
       mbar_init(smem_addr(s_raw + i), 1);
     }
@@ -591,7 +601,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       // count on the first CTA's barriers, whose CTA stays until the end)
       if (!ok && rank == 0 && weights)
         for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-          mbar_wait(smem_addr(s_full + i % stages), (i / stages) & 1);
+          if (!mbar_wait(smem_addr(s_full + i % stages), (i / stages) & 1)) break;  // (all had that time)
+    }
+  } else if (FP4 && warp == 1) {
+    // --------------------------------------------------------- products, e2m1
+    // A block of 128 bytes is four products, as with the other types, but they take half
+    // the time (332 cycles for 176 rows), and copies of scales come on top: issuing them is
+    // the bound. The warp stays converged, so that operands stay in uniform registers (a
+    // thread alone moves each there first), and waits once a block: 4096 tokens x top-8 of
+    // 64 experts, 7168 x 4096, scales per 16: 478 us with a thread alone and three waits, 430
+    // converged, 369 with one wait and three copies a piece of scales; 394 us even without
+    // any load, copy or layout of scales in the first form.
+    if (uniform(rank) == 0) {
+      const uint32_t lead = elect_one(), tm = uniform(tmem), lo_step = uniform(stage_bytes >> 4);
+      const int nstages = (int)uniform(stages);
+      const uint32_t lo0 = desc_lo(ring_s, 0), bar0 = smem_addr(s_bars.full);
+      constexpr uint32_t kEmptyOffset = offsetof(Bars, empty) - offsetof(Bars, full);
+      const uint32_t sm0 = desc_lo(smem_addr(s_scale), 0), sempty0 = smem_addr(s_sempty);
+      const uint16_t mask = (uint16_t)uniform(both);
+      uint32_t lo = lo0, bar = bar0, ph = 0;
+      int left = nstages;
+      uint32_t buf = 0, cols = 0;  // of the next piece of scales
+      int acc_it = 0;
+      bool ok = true;
+      for (Walk k = first(); ok && __any_sync(0xffffffffu, more(k)); step(k)) {
+        const Tile t = tile_at(k);
+        const int n = (int)uniform(t.n), nkb = (int)uniform(t.nkb), kb0 = (int)uniform(t.kb0);
+        const int as = acc_it & 1;
+        if (!(ok = warp_ready(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
+        tc_fence_after();
+        const uint32_t d = tm + as * kTileRows;
+        const uint32_t idesc = idesc_e2m1(n, KIND == kFp4Mx, 0);
+        for (int kb = 0; kb < nkb; kb += kPerBuf) {
+          // A piece of scales (four words a row) serves one block (a word per product) or two
+          // (half a word). A wait costs about 100 cycles even if it passes at once, so there
+          // is one a block: the warps that lay out the scales arrive on its barrier too, and
+          // not before the columns that the piece takes are free.
+          const uint32_t sfa = tm + kScaleCols<KIND> + cols, sfb = sfa + 16, sm = sm0 + buf * (kBufBytes >> 4);
+#pragma unroll
+          for (int j = 0; j < kPerBuf; ++j) {
+            if (kb + j >= nkb) break;
+            if (!(ok = warp_ready(bar, ph, &s_stop))) break;
+            const int left_red = p.red - (kb0 + kb + j) * 128;  // bytes: 32 a product
+            const uint32_t acc = j > 0 ? 1u : (uint32_t)kb, empty = bar + kEmptyOffset;
+            if (lead) {
+              if (j == 0) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  tmem_copy_scales(sfa + 4 * w, sm + w * (512 >> 4));
+                  tmem_copy_scales(sfb + 8 * w, sm + (2048 >> 4) + w * (512 >> 4));
+                }
+                if (n > 128) {
+#pragma unroll
+                  for (int w = 0; w < 4; ++w) tmem_copy_scales(sfb + 8 * w + 4, sm + (4096 >> 4) + w * (512 >> 4));
+                }
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int w = KIND == kFp4Nv ? k : 2 * j + k / 2;
+                const uint32_t sf = KIND == kFp4Nv ? 0 : 2 * (k & 1);
+                if (k == 0 || k * 32 < left_red)
+                  mma_e2m1<KIND == kFp4Mx>(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc | (sf << 4) | (sf << 29),
+                                           sfa + 4 * w, sfb + 8 * w, k > 0 ? 1u : acc);
+              }
+              mma_commit_pair(empty, mask);
+              if (j == kPerBuf - 1 || kb + j + 1 >= nkb) mma_commit_pair(sempty0 + 8 * buf, mask);
+            }
+            __syncwarp();
+            lo += lo_step;
+            bar += 8;
+            if (--left == 0) {
+              left = nstages;
+              lo = lo0;
+              bar = bar0;
+              ph ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (++buf == kBufs) buf = 0;
+          cols = kScaleWidth<KIND> - cols;
+        }
+        if (lead) mma_commit_pair(smem_addr(s_tfull + as), mask);
+        __syncwarp();
+        ++acc_it;
+      }
+      if (!ok) {  // products in flight end before tensor memory is freed
+        if (lead) mma_commit_pair(smem_addr(&s_drain), mask);
+        __syncwarp();
+        mbar_wait(smem_addr(&s_drain), 0);
+      }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- products
@@ -611,8 +709,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_or_stop(smem_addr(s_tempty + as), ((acc_it >> 1) & 1) ^ 1, &s_stop))) break;
         tc_fence_after();
         const uint32_t d = tmem + as * kTileRows;
-        const uint32_t idesc = FP4 ? idesc_e2m1(t.n, KIND == kFp4Mx, 0)
-                               : FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
+        const uint32_t idesc = FP8 ? idesc_e4m3(t.n, 0) : idesc_16bit(!p.f16, MODE != kForward, MODE == kGradW, t.n);
         auto advance = [&] {  // hand the stage back and move on to the next
           mma_commit_pair(bar + kEmptyOffset, both);
           lo += stage_bytes >> 4;
@@ -624,41 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ph ^= 1;
           }
         };
-        if constexpr (FP4) {
-          // A piece of scales (four words a row) serves one block (a word per product) or
-          // two (a word per two products, the halves of it). The columns of the piece
-          // before the last are free once its products are done.
-          for (int kb = 0; kb < t.nkb && ok; kb += kPerBuf, ++sf_it) {
-            const int sb = sf_it % kBufs;
-            if (sf_it >= 2 && !(ok = wait_or_stop(smem_addr(s_sempty + (sf_it - 2) % kBufs), ((sf_it - 2) / kBufs) & 1, &s_stop)))
-              break;
-            if (!(ok = wait_or_stop(smem_addr(s_sfull + sb), (sf_it / kBufs) & 1, &s_stop))) break;
-            const uint32_t sfa = tmem + kScaleCols<KIND> + kScaleWidth<KIND> * (sf_it & 1), sfb = sfa + 16;
-            const uint32_t sm = desc_lo(smem_addr(s_scale + sb * kBufBytes), 0);
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              tmem_copy_scales(sfa + 4 * w, sm + w * (512 >> 4));
-              tmem_copy_scales(sfb + 8 * w, sm + (2048 >> 4) + w * (512 >> 4));
-              if (t.n > 128) tmem_copy_scales(sfb + 8 * w + 4, sm + (4096 >> 4) + w * (512 >> 4));
-            }
-#pragma unroll
-            for (int j = 0; j < kPerBuf; ++j) {
-              if (kb + j >= t.nkb || !ok) break;
-              if (!(ok = wait_or_stop(bar, ph, &s_stop))) break;
-              const int left_red = p.red - (t.kb0 + kb + j) * 128;  // bytes: 32 a product
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int w = KIND == kFp4Nv ? k : 2 * j + k / 2;
-                const uint32_t sf = KIND == kFp4Nv ? 0 : 2 * (k & 1);
-                if (k * 32 < left_red)
-                  mma_e2m1<KIND == kFp4Mx>(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc | (sf << 4) | (sf << 29),
-                                           sfa + 4 * w, sfb + 8 * w, j + k > 0 ? 1u : (uint32_t)kb);
-              }
-              advance();
-            }
-            mma_commit_pair(smem_addr(s_sempty + sb), both);
-          }
-        } else if constexpr (FP8) {
+        if constexpr (FP8) {
           // four blocks share a scale word, each its own byte of it
           for (int kb = 0; kb < t.nkb && ok; kb += 4, ++sf_it) {
             const int sb = sf_it % kBufs;
@@ -789,7 +852,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (FP4 && warp == 2) {
     // A row's piece of scales is 16 bytes, and those of consecutive rows are
     // contiguous: one bulk copy for the tile's rows and one for its weight rows (gated:
-    // one for each run of 16 gate or up rows), up to kBufs pieces ahead.
+    // the gate rows, then the up rows), up to kBufs pieces ahead. (A copy costs its
+    // thread about 60 cycles: the runs of 16 rows that a gated tile interleaves, one by
+    // one, took 650 a piece, and 900 from as many lanes.)
     if (elect_one()) {
       int sf_it = 0;
       bool ok = true;
@@ -798,53 +863,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (Walk k = first(); ok && more(k); step(k)) {
         const Tile t = tile_at(k);
         const int f0 = t.fb * fblk, nf = max(min(fblk, p.feats - f0), 0);  // features of the tile
-        const int64_t wrow = (int64_t)t.e * p.wrows + f0;
-        const uint32_t bytes = (uint32_t)(t.rows + (p.gated ? 2 : 1) * nf) * 16;
+        const uint32_t row_bytes = (uint32_t)t.rows * 16, w_bytes = (uint32_t)nf * 16;
+        const uint32_t bytes = row_bytes + (p.gated ? 2 : 1) * w_bytes;
+        const uint8_t* xrow = xs + (int64_t)t.row0 * 16;
+        const uint8_t* wrow = ws + ((int64_t)t.e * p.wrows + f0) * 16;
         for (int kb = 0; kb < t.nkb; kb += kPerBuf, ++sf_it) {
           const int sb = sf_it % kBufs;
           if (!(ok = wait_or_stop(smem_addr(s_sempty + sb), ((sf_it / kBufs) & 1) ^ 1, &s_stop))) break;
           const uint32_t dst = smem_addr(s_scale + sb * kBufBytes), bar = smem_addr(s_sraw + sb);
           const int64_t piece = (t.kb0 + kb) / kPerBuf;
           mbar_expect_tx(bar, bytes);
-          bulk_load_g2s(dst + 2048, xs + (piece * p.ld_xs + t.row0) * 16, (uint32_t)t.rows * 16, bar);
-          const uint8_t* w = ws + (piece * p.ld_ws + wrow) * 16;
-          if (!p.gated) {
-            if (nf > 0) bulk_load_g2s(dst, w, (uint32_t)nf * 16, bar);
-          } else {
-            for (int i = 0; i < nf; i += 16) {
-              bulk_load_g2s(dst + i * 32, w + i * 16, 256, bar);
-              bulk_load_g2s(dst + i * 32 + 256, w + ((int64_t)p.feats + i) * 16, 256, bar);
-            }
+          bulk_load_g2s(dst + 2048, xrow + piece * p.ld_xs * 16, row_bytes, bar);
+          if (nf > 0) {
+            const uint8_t* w = wrow + piece * p.ld_ws * 16;
+            bulk_load_g2s(dst, w, w_bytes, bar);
+            if (p.gated) bulk_load_g2s(dst + 1024, w + (int64_t)p.feats * 16, w_bytes, bar);
           }
         }
       }
       // whatever ended the walk, no copy outlives the CTA
       for (int i = sf_it > kBufs ? sf_it - kBufs : 0; i < sf_it; ++i)
-        mbar_wait(smem_addr(s_sraw + i % kBufs), (i / kBufs) & 1);
+        if (!mbar_wait(smem_addr(s_sraw + i % kBufs), (i / kBufs) & 1)) break;
     }
-  } else if (FP4 && warp == 3) {
+  } else if (FP4 && (warp == 3 || warp > 8)) {
     // Tensor memory wants word w of row r of a block of 128 at byte 16 (r % 32) + 4 (r / 32)
-    // of the word's 512 bytes; the copies left row r's four words at byte 16 r. Lane l
-    // transposes the 4 x 4 words of rows l, 32 + l, 64 + l and 96 + l where they are.
+    // of the word's 512 bytes; the copies left row r's four words at byte 16 r (gated: the
+    // tile's runs of 16 gate rows one after the other, and the up rows 1024 bytes on).
+    // Lane l transposes the 4 x 4 words of rows l, 32 + l, 64 + l and 96 + l.
+    // The pieces go round the warps: from a landed copy to the arrival takes one of them
+    // about as long as two blocks' products.
+    const int turn = warp == 3 ? 0 : warp - 8;
+    const int wfirst = !p.gated ? lane : lane < 16 ? lane : 48 + lane, wstep = p.gated ? 16 : 32;
     bool ok = true;
-    int sf_it = 0;
+    int sf_it = 0, at_stage = 0;
     for (Walk k = first(); ok && more(k); step(k)) {
       const Tile t = tile_at(k);
-      const int blocks = t.n > 128 ? 3 : 2;
       for (int kb = 0; kb < t.nkb; kb += kPerBuf, ++sf_it) {
+        const int s0 = at_stage, s1 = s0 + 1 == stages ? 0 : s0 + 1;
+        const bool two = kPerBuf > 1 && kb + 1 < t.nkb;
+        at_stage = two ? (s1 + 1 == stages ? 0 : s1 + 1) : s1;
+        if (sf_it % kTransposers != turn) continue;
         const int sb = sf_it % kBufs;
         if (!(ok = warp_wait_or_stop(smem_addr(s_sraw + sb), (sf_it / kBufs) & 1, &s_stop))) break;
         uint4* at = reinterpret_cast<uint4*>(s_scale + sb * kBufBytes) + lane;
-        for (int b = 0; b < blocks; ++b, at += 128) {
-          const uint4 r0 = at[0], r1 = at[32], r2 = at[64], r3 = at[96];
-          at[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
-          at[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
-          at[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
-          at[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
-        }
-        fence_proxy_async_smem();
+        uint4 r[3][4];
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+          if (b < 2 || t.n > 128)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r[b][i] = b > 0 ? at[b * 128 + i * 32] : at[wfirst - lane + i * wstep];
         __syncwarp();
-        if (lane == 0) mbar_arrive_mapped(map_to_rank(smem_addr(s_sfull + sb), leader));
+#pragma unroll
+        for (int b = 0; b < 3; ++b)
+          if (b < 2 || t.n > 128) {
+            at[b * 128] = make_uint4(r[b][0].x, r[b][1].x, r[b][2].x, r[b][3].x);
+            at[b * 128 + 32] = make_uint4(r[b][0].y, r[b][1].y, r[b][2].y, r[b][3].y);
+            at[b * 128 + 64] = make_uint4(r[b][0].z, r[b][1].z, r[b][2].z, r[b][3].z);
+            at[b * 128 + 96] = make_uint4(r[b][0].w, r[b][1].w, r[b][2].w, r[b][3].w);
+          }
+        fence_proxy_async_smem();
+        // The columns are free when the products of the piece before the last are done (before
+        // there was any, a buffer's first phase passes at once). Those of the blocks that had
+        // these blocks' stages are done then as well (there are at least four stages), so the
+        // arrivals count for these.
+        const int old = sf_it >= 2 ? sf_it - 2 : sf_it - 2 + kBufs;
+        const uint32_t oph = sf_it >= 2 ? (old / kBufs) & 1 : 1;
+        if (!(ok = warp_wait_or_stop(smem_addr(s_sempty + old % kBufs), oph, &s_stop))) break;
+        if (lane == 0) {
+          mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s0), leader));
+          if (two) mbar_arrive_mapped(map_to_rank(smem_addr(s_full + s1), leader));
+        }
       }
     }
   } else if (warp >= 4 && warp < 8) {
@@ -1074,7 +1162,7 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   err = opt_in_smem(matmul_kernel<MODE, KIND>, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kThreadsOf<KIND>);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1153,7 +1241,7 @@ cudaError_t launch_matmul(const MatmulArgs& m, int num_sms, cudaStream_t s) {
   }
   for (int i = 0; i < kBoxes; ++i) ok = ok && map_2d(&maps.b[i], m.type, m.x, K, m.R, m.ldx, span, box_rows(i));
   if (!ok) return cudaErrorInvalidValue;
-  const int64_t tile_rows = fp4 ? kRows<kFp4Mx> : fp8 ? kRows<kFp8> : kRows<kHalf>;
+  const int64_t tile_rows = fp4 ? kRows<kFp4Nv> : fp8 ? kRows<kFp8> : kRows<kHalf>;
   const int64_t tiles = max_row_tiles(m, (int)tile_rows) * nfp;
   if (m.type == kE2M1MX) return launch<kForward, kFp4Mx>(maps, a, tiles, num_sms, s);
   if (m.type == kE2M1NV) return launch<kForward, kFp4Nv>(maps, a, tiles, num_sms, s);

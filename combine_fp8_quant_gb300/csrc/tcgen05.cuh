@@ -201,6 +201,8 @@ __device__ __forceinline__ void mma_e2m1(uint32_t d, uint32_t a, uint32_t b, uin
                  "\n\t}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
                  : "memory");
 }
+// The same value in every lane, which the compiler then knows.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 // 32 rows of 16 bytes of shared memory to 4 tensor-memory columns, in all four
 // lane quarters; in both CTAs of the pair, each from its own shared memory.
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t lo) {
