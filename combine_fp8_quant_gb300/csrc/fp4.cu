@@ -190,72 +190,94 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_small_kernel(DispatchFp
   }
 }
 
-// After the route plan. Each warp works alone: it finds a token's rows, quantises the
-// token into its staging buffer, and copies the elements to every row with one bulk copy
-// each (lane k that of slot k) and the scales piece by piece.
+// After the route plan. The rows of all tokens of a CTA are found at once; then each warp
+// works alone on units of 2048 elements of a token: it quantises them into a staging
+// buffer, copies the elements to every row with one bulk copy each (lane k that of slot k)
+// and the scales piece by piece. (Whole tokens a warp left 4096 tokens of 7168 in one round
+// and an eighth of another: 48 us, units as below.)
+constexpr int kPart = 128;     // chunks of a unit
+constexpr int kStages = 4;     // units in flight a warp
+__host__ __device__ constexpr int part_pieces(int fmt) { return kPart / (fmt == kFp4NV ? 16 : 32); }
+__host__ __device__ constexpr int stage_bytes(int fmt) { return kPart * 8 + part_pieces(fmt) * 16; }
+// Shared memory before the staging buffers: table, starts, ends, rows of the CTA's slots.
+__host__ __device__ inline size_t plan_bytes(const ScatterArgs& s, int64_t ntok) {
+  const size_t ints = (size_t)s.nchunks * s.L + 2 * (size_t)s.L + (size_t)ntok * s.K;
+  return (ints * sizeof(int32_t) + 127) / 128 * 128;
+}
+
 template <int TYPE, int FMT>
-__global__ void __launch_bounds__(kThreads) dispatch_fp4_kernel(DispatchFp4Args p) {
+__global__ void __launch_bounds__(kThreads, TYPE == kF32 ? 2 : 3) dispatch_fp4_kernel(DispatchFp4Args p) {
   extern __shared__ __align__(128) int32_t sm[];
   __shared__ int32_t s_wsum[33];
   const ScatterArgs& a = p.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_live = live_count(a.d_num_tokens, a.T, nullptr, false);  // the route plan flags it
-  const int nch = a.H / 16, pieces = fp4_pieces(a.H, FMT), nchp = pieces * (FMT == kFp4NV ? 16 : 32);
-  const int row_bytes = a.H / 2, stage_bytes = row_bytes + pieces * 16;
+  const int ntok = n_live > (int)blockIdx.x ? (n_live - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
+  const int nch = a.H / 16, pieces = fp4_pieces(a.H, FMT), row_bytes = a.H / 2;
+  constexpr int kPieces = part_pieces(FMT), kStage = stage_bytes(FMT);
   int32_t* st = sm + a.nchunks * a.L;
   int32_t* ps = st + a.L;
-  const size_t plan = (((size_t)a.nchunks * a.L + 2 * (size_t)a.L) * sizeof(int32_t) + 127) / 128 * 128;
-  uint8_t* stage = reinterpret_cast<uint8_t*>(sm) + plan + (size_t)warp * p.stages * stage_bytes;
+  int32_t* rows = ps + a.L;
+  uint8_t* stage = reinterpret_cast<uint8_t*>(sm) + plan_bytes(a, ((int64_t)a.T + gridDim.x - 1) / gridDim.x) +
+                   (size_t)warp * kStages * kStage;
   const float ts = FMT == kFp4NV && p.tscale != nullptr ? __ldg(p.tscale) : 1.0f, ts6 = __fmul_rn(6.0f, ts);
   pdl_wait_primary();
   layout_prologue(a, sm, st, ps, s_wsum);
-  const int nwarps = gridDim.x * kWarps;
+  for (int i = tid; i < ntok * a.K; i += kThreads) {
+    const int64_t slot = (int64_t)(blockIdx.x + (i / a.K) * gridDim.x) * a.K + i % a.K;
+    const int row = slot_row(a, sm, st, slot, __ldg(a.ids + slot), __ldcg(a.src2dst + slot));
+    a.src2dst[slot] = row;
+    if (row >= 0 && a.row_weights != nullptr) a.row_weights[row] = __ldg(a.w + slot);
+    rows[i] = row;
+  }
+  __syncthreads();
   const bool wide = wide_rows(a.x, p.ldx_bytes);
+  const int parts = (nch + kPart - 1) / kPart;
   int buf = 0;
-  for (int64_t t = (int64_t)warp * gridDim.x + blockIdx.x; t < n_live; t += nwarps) {
-    int row = -1;
-    if (lane < a.K) {
-      const int64_t slot = t * a.K + lane;
-      row = slot_row(a, sm, st, slot, __ldg(a.ids + slot), __ldcg(a.src2dst + slot));
-      a.src2dst[slot] = row;
-      if (row >= 0 && a.row_weights != nullptr) a.row_weights[row] = __ldg(a.w + slot);
-    }
+  for (int u = warp; u < ntok * parts; u += kWarps) {
+    const int it = u / parts, c0 = (u - it * parts) * kPart;
+    const int row = lane < a.K ? rows[it * a.K + lane] : -1;
     if (!__any_sync(0xffffffffu, row >= 0)) continue;
-    uint8_t* out = stage + buf * stage_bytes;
-    // the copies that last read this buffer have left it
-    if (p.stages == 2) bulk_wait_read<1>(); else bulk_wait_read<0>();
-    __syncwarp();
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + t * p.ldx_bytes;
-    for (int c0 = 0; c0 < nchp; c0 += 32 * kAhead<TYPE>) {
-      Chunk<TYPE> x[kAhead<TYPE>];
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(a.x) + ((int64_t)blockIdx.x + (int64_t)it * gridDim.x) * p.ldx_bytes;
+    uint8_t* out = stage + buf * kStage;
+    constexpr int kSlices = kPart / 32, kBatch = TYPE == kF32 ? kSlices / 2 : kSlices;
 #pragma unroll
-      for (int i = 0; i < kAhead<TYPE>; ++i) {
-        const int c = c0 + 32 * i + lane;
+    for (int s0 = 0; s0 < kSlices; s0 += kBatch) {
+      Chunk<TYPE> x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int c = c0 + 32 * (s0 + i) + lane;
         x[i].load(src + (int64_t)c * kChunkBytes<TYPE>, c < nch, wide);
       }
+      if (s0 == 0) {  // the copies that last read this buffer have left it
+        bulk_wait_read<kStages - 1>();
+        __syncwarp();
+      }
 #pragma unroll
-      for (int i = 0; i < kAhead<TYPE>; ++i) {
-        const int c = c0 + 32 * i + lane;
+      for (int i = 0; i < kBatch; ++i) {
+        const int o = 32 * (s0 + i) + lane, c = c0 + o;
         uint32_t byte;
         const uint2 q = fp4_quant<TYPE, FMT>(x[i], ts, ts6, byte);
-        if (c < nch) *reinterpret_cast<uint2*>(out + c * 8) = q;
+        *reinterpret_cast<uint2*>(out + o * 8) = q;
         const uint32_t word = fp4_scale_word<FMT>(c < nch ? byte : 0u);
-        if (fp4_word_lane<FMT>(lane) && c < nchp)
-          *reinterpret_cast<uint32_t*>(out + row_bytes + fp4_piece_of<FMT>(c) * 16 + fp4_byte_of<FMT>(c)) = word;
+        if (fp4_word_lane<FMT>(lane))
+          *reinterpret_cast<uint32_t*>(out + kPart * 8 + fp4_piece_of<FMT>(o) * 16 + fp4_byte_of<FMT>(o)) = word;
       }
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (row >= 0) bulk_store_s2g(a.xq + (int64_t)row * row_bytes, smem_addr(out), (uint32_t)row_bytes);
+    if (row >= 0)
+      bulk_store_s2g(a.xq + (int64_t)row * row_bytes + c0 * 8, smem_addr(out), (uint32_t)min(kPart, nch - c0) * 8);
     bulk_commit();
-    for (int k = 0; k < a.K; ++k) {
-      const int64_t to = __shfl_sync(0xffffffffu, row, k);
-      if (to < 0) continue;
-      for (int c = lane; c < pieces; c += 32)
-        st_v4(static_cast<uint8_t*>(a.scales) + ((int64_t)c * a.ld_s + to) * 16,
-              *reinterpret_cast<const uint4*>(out + row_bytes + c * 16));
+    const int first = c0 / (FMT == kFp4NV ? 16 : 32);  // the unit's first piece
+    for (int i = lane; i < a.K * kPieces; i += 32) {
+      const int c = i % kPieces;
+      const int64_t to = rows[it * a.K + i / kPieces];
+      if (to >= 0 && first + c < pieces)
+        st_v4(static_cast<uint8_t*>(a.scales) + ((int64_t)(first + c) * a.ld_s + to) * 16,
+              *reinterpret_cast<const uint4*>(out + kPart * 8 + c * 16));
     }
-    buf = p.stages == 2 ? buf ^ 1 : 0;
+    buf = buf + 1 == kStages ? 0 : buf + 1;
   }
   // the layout's m_indices while the last copies drain
   fill_m_indices(a, st, ps, tid, kThreads);
@@ -329,24 +351,25 @@ cudaError_t launch_dispatch_fp4(const DispatchFp4Args& a0, int type, int fmt, in
       if (A <= 1024) return go(dispatch_fp4_small_kernel<kT, kF, 4>);
       return go(dispatch_fp4_small_kernel<kT, kF, 8>);
     }
-    const size_t plan = (((size_t)a.s.nchunks * a.s.L + 2 * (size_t)a.s.L) * sizeof(int32_t) + 127) / 128 * 128;
-    const size_t stage = (size_t)a.s.H / 2 + (size_t)fp4_pieces(a.s.H, kF) * 16;
-    int optin = 0;
-    cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerBlockOptin, &optin);
-    if (err != cudaSuccess) return err;
-    // two rows in flight a warp, one where shared memory is short (the widest rows
-    // with the largest chunk table: 64 KiB and 8 * 18 KiB fit)
-    a.stages = plan + 2 * kWarps * stage + 1024 <= (size_t)optin ? 2 : 1;
-    const size_t smem = plan + a.stages * kWarps * stage;
+    // as many CTAs per SM as registers and shared memory leave room for (the plan's share
+    // per CTA shrinks with the number of CTAs)
     auto kernel = dispatch_fp4_kernel<kT, kF>;
+    int sm_bytes = 0;
+    cudaError_t err = device_attr_cached(cudaDevAttrMaxSharedMemoryPerMultiprocessor, &sm_bytes);
+    if (err != cudaSuccess) return err;
+    const size_t ring = (size_t)kWarps * kStages * stage_bytes(kF);
+    int64_t grid = a.s.T;
+    size_t smem = 0;
+    for (int per_sm = kT == kF32 ? 2 : 3;; --per_sm) {
+      const int64_t g = a.s.T < (int64_t)num_sms * per_sm ? a.s.T : (int64_t)num_sms * per_sm;
+      smem = plan_bytes(a.s, (a.s.T + g - 1) / g) + ring;
+      if (per_sm == 1 || (smem + 2048) * per_sm <= (size_t)sm_bytes) {
+        grid = g;
+        break;
+      }
+    }
     err = opt_in_smem(kernel, smem);
     if (err != cudaSuccess) return err;
-    int per_sm = 0;
-    err = occupancy(kernel, kThreads, smem, &per_sm);
-    if (err != cudaSuccess) return err;
-    int64_t grid = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
-    const int64_t need = ((int64_t)a.s.T + kWarps - 1) / kWarps;
-    if (grid > need) grid = need;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kThreads);

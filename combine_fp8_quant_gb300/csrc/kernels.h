@@ -297,7 +297,6 @@ struct DispatchFp4Args {
   ScatterArgs s;
   int64_t ldx_bytes;
   const float* tscale;         // [1] or nullptr
-  int32_t stages;              // rows in flight per warp (set at launch)
 };
 cudaError_t launch_dispatch_fp4(const DispatchFp4Args& a, int type, int fmt, int num_sms, bool after_route_plan,
                                 cudaStream_t s);

@@ -11,6 +11,7 @@
 // One warp works on a token with its logits in registers (lane i holds the vectors i,
 // 32 + i, ... of the row), so a row is read once and everything about it is a few warp
 // reductions.
+#include <cfloat>
 #include <climits>
 #include <type_traits>
 
@@ -121,27 +122,42 @@ __device__ __forceinline__ uint32_t ordered(float f) {
   const uint32_t b = __float_as_uint(f + 0.0f);  // both zeros are one key
   return f > kNegInf ? b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u) : 0u;
 }
-__device__ __forceinline__ float unordered(uint32_t u) {
-  return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~u);
-}
 
+// e^x and 1 / x by the approximating instructions, results below 2^-126 as 0 (e^x to about
+// 2 + 1.2 |x| steps, 1 / x to one). The functions that keep such numbers take three to
+// four times the instructions, which are the bound here: the choice for 16384 tokens of
+// 256 experts 23.1 us with them.
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {  // a NaN is left out
-  return unordered(__reduce_max_sync(0xffffffffu, v > kNegInf ? ordered(v) : 0x007FFFFFu));
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
+// CTAs an SM that a kernel with N logits a lane is compiled for.
+__host__ __device__ constexpr int min_blocks(int N) { return N <= 8 ? 4 : N <= 16 ? 2 : 1; }
 
 // 1 / (1 + e^-l) and 1 minus that, neither with cancellation.
 __device__ __forceinline__ float sigmoid(float l) {
-  const float x = __expf(-fabsf(l));
-  return __fdividef(l < 0.0f ? x : 1.0f, 1.0f + x);
+  const float x = fast_exp(-fabsf(l));
+  return (l < 0.0f ? x : 1.0f) * fast_rcp(1.0f + x);
 }
 __device__ __forceinline__ float sigmoid_rest(float l) {
-  const float x = __expf(-fabsf(l));
-  return __fdividef(l < 0.0f ? 1.0f : x, 1.0f + x);
+  const float x = fast_exp(-fabsf(l));
+  return (l < 0.0f ? 1.0f : x) * fast_rcp(1.0f + x);
 }
 
 // Where every logit of a set is below this, its sigmoids are exponentials (to
@@ -165,20 +181,20 @@ __device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, f
   if (!sig || m < kFarBelow) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      p[i] = __expf(l[i] - m);
+      p[i] = fast_exp(l[i] - m);
       if (kRest) rest[i] = 1.0f;
       z += p[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float x = __expf(-fabsf(l[i])), r = __fdividef(1.0f, 1.0f + x), xr = x * r;
+      const float x = fast_exp(-fabsf(l[i])), r = fast_rcp(1.0f + x), xr = x * r;
       p[i] = l[i] < 0.0f ? xr : r;
       if (kRest) rest[i] = l[i] < 0.0f ? r : xr;
       z += p[i];
     }
   }
-  const float r = __fdividef(1.0f, warp_sum(z));
+  const float r = fast_rcp(warp_sum(z));
 #pragma unroll
   for (int i = 0; i < N; ++i) p[i] *= r;
 }
@@ -191,7 +207,7 @@ __device__ __forceinline__ void scores(const float (&l)[N], float m, bool sig, f
 // not settle: keys of KEY (uint32_t: ordered logits; double: scores with bias in 64
 // bits). Lane k gets the k-th id (-1: none).
 template <typename KEY, int TYPE, int N>
-__device__ __noinline__ int choose_by_rounds(const RouteArgs& a, int64_t at, int lane) {
+__device__ __forceinline__ int choose_by_rounds(const RouteArgs& a, int64_t at, int lane) {
   KEY key[N];
   const KEY none = std::is_same<KEY, double>::value ? (KEY)-INFINITY : (KEY)0;
   if constexpr (std::is_same<KEY, double>::value) {
@@ -203,14 +219,14 @@ __device__ __noinline__ int choose_by_rounds(const RouteArgs& a, int64_t at, int
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       key[i] = a.sigmoid ? 1.0 / (1.0 + exp(-key[i])) : exp(key[i] - m);
       z += key[i];
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < N; ++i) {
       const int e = i * 32 + lane;
       const bool may = e < a.E && load_elem<TYPE>(a.logits, at + (e < a.E ? e : 0)) > kNegInf;
@@ -248,115 +264,112 @@ __device__ __noinline__ int choose_by_rounds(const RouteArgs& a, int64_t at, int
   return mine;
 }
 
-// The quick way: at least K + 2 keys are no less than the (K + 2)-th largest of the 32
-// lanes' largest, and seldom many more (ten or eleven of 256 for K = 8). They go to
-// shared memory, one for each lane, which counts those that come before its own.
-//
-// 16384 tokens, 256 experts, K = 8, sigmoid with bias: see launch_route.
-template <int TYPE, int N, int V>
-__global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
-  __shared__ uint4 s_cand[kWarps][32];  // key, expert, logit, bias
-  const int lane = threadIdx.x & 31;
-  uint4* cand = s_cand[threadIdx.x >> 5];
-  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
-  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && threadIdx.x == 0);
-  int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  float next[N];
-  if (t < n_live) load_row<TYPE, N, V>(next, a.logits, t * a.ld, a.E, lane);
+// One token with logits l. The quick way: at least K + 2 keys are no less than the
+// (K + 2)-th largest of the 32 lanes' largest, and seldom many more (ten or eleven of 256
+// for K = 8). They go to shared memory, one for each lane, which counts those that come
+// before its own. Returns false, with nothing written, where that does not settle the
+// choice: more candidates than lanes, or, with a bias, keys too near each other for 32
+// bits. EXACT settles it: such candidates by keys in 64 bits, else rounds over all keys.
+template <bool EXACT, int TYPE, int N, int V>
+__device__ __forceinline__ bool route_token(const RouteArgs& a, int64_t t, const float (&l)[N], uint2* cand,
+                                            const float* s_bias, int lane) {
   const bool biased = a.bias != nullptr;
-  float bias[N];
+  float key[N], m = kNegInf, z = 1.0f;
+  if (!a.sigmoid && (biased || !a.renorm)) {  // the sum over all experts
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = expert_of<V>(i, lane);
-    bias[i] = biased && e < a.E ? __ldg(a.bias + e) : 0.0f;
+    for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+    z = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) z += fast_exp(l[i] - m);
+    z = warp_sum(z);
   }
-  for (; t < n_live; t += nwarps) {
-    float l[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) l[i] = next[i];
-    if (t + nwarps < n_live) load_row<TYPE, N, V>(next, a.logits, (t + nwarps) * a.ld, a.E, lane);
-    float m = kNegInf, z = 1.0f;
-    if (!a.sigmoid && (biased || !a.renorm)) {  // the sum over all experts
+  for (int i = 0; i < N; ++i) key[i] = l[i];
+  if (biased) {
+    const float r = a.sigmoid ? 0.0f : fast_rcp(z);
 #pragma unroll
-      for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
-      m = warp_max(m);
-      z = 0.0f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) z += __expf(l[i] - m);
-      z = warp_sum(z);
+    for (int i = 0; i < N; ++i) {
+      const int e = expert_of<V>(i, lane);
+      const float s = a.sigmoid ? sigmoid(l[i]) : fast_exp(l[i] - m) * r;
+      key[i] = l[i] > kNegInf ? s + s_bias[e < a.E ? e : 0] : kNegInf;
     }
-    uint32_t key[N];
+  }
+  // a key that at least K + 2 reach (or every one that may be chosen, where there are fewer)
+  float top = kNegInf, floor = -FLT_MAX;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, key[i]);
+  for (int have = 0; have < a.K + 2;) {
+    const float best = warp_max(top);
+    floor = fmaxf(best, -FLT_MAX);
+    if (best == kNegInf) break;
+    const bool is = top == best;
+    have += __popc(__ballot_sync(0xffffffffu, is));
+    if (is) top = kNegInf;
+  }
+  int mine = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mine += key[i] >= floor;
+  int upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int below = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += below;
+  }
+  const int n = __shfl_sync(0xffffffffu, upto, 31);
+  if (!EXACT && n > 32) return false;
+  int id = -1, rank = 32, got = min(n, a.K);
+  float lk = kNegInf;
+  bool rounds = n > 32;
+  if (!rounds) {
+    uint2* at = cand + (upto - mine);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (key[i] >= floor) *at++ = make_uint2(__float_as_uint(key[i]), (uint32_t)expert_of<V>(i, lane));
+    if (lane < 3) cand[n + lane] = make_uint2(0xFF800000u, 0);  // up to a whole four
+    __syncwarp();
+    float k = kNegInf;
+    if (lane < n) {
+      k = __uint_as_float(cand[lane].x);
+      id = (int)cand[lane].y;
+      lk = load_elem<TYPE>(a.logits, t * a.ld + id);
+      rank = 0;
+    }
+    // Keys in 32 bits are off by 2^-21 (sigmoid), or by (N + 12) 2^-24 (a sum of 32 N
+    // exponentials), and half a step of the sum with the bias. Two of them nearer than
+    // twice that, and not equal from equal parts, are told apart in 64 bits.
+    const float eps = (a.sigmoid ? 0x1p-19f : (N + 24) * 0x1p-23f) + fabsf(k) * 0x1p-22f;
+    int near = 0;  // (its own among them)
+    for (int j = 0; j < n; j += 4) {
+      const uint4 p0 = *reinterpret_cast<const uint4*>(cand + j), p1 = *reinterpret_cast<const uint4*>(cand + j + 2);
+      const uint2 o[4] = {make_uint2(p0.x, p0.y), make_uint2(p0.z, p0.w), make_uint2(p1.x, p1.y), make_uint2(p1.z, p1.w)};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float ok = __uint_as_float(o[u].x);
+        rank += ok > k || (ok == k && (int)o[u].y < id);
+        if (biased) near += !(fabsf(ok - k) > eps);
+      }
+    }
+    __syncwarp();
     if (biased) {
-      const float r = a.sigmoid ? 0.0f : __fdividef(1.0f, z);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float s = a.sigmoid ? sigmoid(l[i]) : __expf(l[i] - m) * r;
-        key[i] = l[i] > kNegInf ? ordered(s + bias[i]) : 0u;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) key[i] = ordered(l[i]);
-    }
-    // a key that at least K + 2 reach (or all, where there are fewer)
-    uint32_t top = key[0], floor = 1;
-#pragma unroll
-    for (int i = 1; i < N; ++i) top = max(top, key[i]);
-    for (int have = 0; have < a.K + 2;) {
-      const uint32_t best = __reduce_max_sync(0xffffffffu, top);
-      if (best == 0) {
-        floor = 1;
-        break;
-      }
-      floor = best;
-      const bool is = top == best;
-      have += __popc(__ballot_sync(0xffffffffu, is));
-      if (is) top = 0;
-    }
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) mine += key[i] >= floor;
-    int upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int below = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += below;
-    }
-    const int n = __shfl_sync(0xffffffffu, upto, 31);
-    int id = -1, rank = 32;
-    float lk = kNegInf;
-    bool settled = n <= 32;
-    if (settled) {
-      int at = upto - mine;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (key[i] >= floor) cand[at++] = make_uint4(key[i], (uint32_t)expert_of<V>(i, lane), __float_as_uint(l[i]), __float_as_uint(bias[i]));
-      __syncwarp();
-      uint4 c = make_uint4(0, 0, 0, 0);
-      if (lane < n) {
-        c = cand[lane];
-        id = (int)c.y;
-        lk = __uint_as_float(c.z);
-        rank = 0;
-      }
-      if (biased) {
-        // Keys in 32 bits are off by 2^-21 (sigmoid), or by (N + 12) 2^-24 (a sum of 32 N
-        // exponentials), and half a step of the sum with the bias. Two of them nearer than
-        // twice that, and not equal from equal parts, are told apart in 64 bits.
-        const float k = unordered(c.x);
-        const float eps = (a.sigmoid ? 0x1p-19f : (N + 24) * 0x1p-23f) + fabsf(k) * 0x1p-22f;
-        bool near = false;
+      // A key that is no candidate may be as near to the last chosen one only if that one
+      // is as near to the least candidate.
+      const bool in = lane < n && rank < a.K;
+      const bool open = __any_sync(0xffffffffu, in && n >= a.K + 2 && floor > -FLT_MAX && !(k - floor > 2.0f * eps));
+      if (open || __any_sync(0xffffffffu, in && near > 1)) {
+        const float bk = lane < n ? s_bias[id] : 0.0f;
+        bool unlike = false;  // a candidate near a chosen one, and not of equal parts
         for (int j = 0; j < n; ++j) {
-          const uint4 o = cand[j];
-          rank += o.x > c.x || (o.x == c.x && o.y < c.y);
-          near |= !(fabsf(unordered(o.x) - k) > eps) && (o.z != c.z || o.w != c.w);
+          const float ok = __shfl_sync(0xffffffffu, k, j), ol = __shfl_sync(0xffffffffu, lk, j);
+          const float ob = __shfl_sync(0xffffffffu, bk, j);
+          unlike |= !(fabsf(ok - k) > eps) && (ol != lk || ob != bk);
         }
-        // A key that is no candidate may be as near to the last chosen one only if that
-        // one is as near to the least candidate.
-        const bool open = lane < n && rank < a.K && n >= a.K + 2 && floor > 1 && !(k - unordered(floor) > 2.0f * eps);
-        if (__any_sync(0xffffffffu, (lane < n && near && rank < a.K) || open)) {
-          settled = a.sigmoid && !__any_sync(0xffffffffu, open);
-          if (settled) {
-            const double k64 = lane < n ? 1.0 / (1.0 + exp(-(double)lk)) + (double)__uint_as_float(c.w) : 0.0;
+        unlike = __any_sync(0xffffffffu, unlike && in);
+        if (!EXACT && (open || unlike)) return false;
+        if (EXACT) {
+          rounds = open || !a.sigmoid;
+          if (!rounds) {
+            const double k64 = lane < n ? 1.0 / (1.0 + exp(-(double)lk)) + (double)bk : 0.0;
             rank = lane < n ? 0 : 32;
             for (int j = 0; j < n; ++j) {
               const double o = __shfl_sync(0xffffffffu, k64, j);
@@ -365,38 +378,71 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
             }
           }
         }
-      } else {
-        for (int j = 0; j < n; ++j) {
-          const uint2 o = *reinterpret_cast<const uint2*>(cand + j);
-          rank += o.x > c.x || (o.x == c.x && o.y < c.y);
-        }
       }
-      __syncwarp();
     }
-    int got = min(n, a.K);
-    if (!settled) {
-      id = biased ? choose_by_rounds<double, TYPE, N>(a, t * a.ld, lane) : choose_by_rounds<uint32_t, TYPE, N>(a, t * a.ld, lane);
-      rank = id >= 0 ? lane : 32;
-      lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
-      got = __popc(__ballot_sync(0xffffffffu, id >= 0));
+  }
+  if (EXACT && rounds) {
+    id = biased ? choose_by_rounds<double, TYPE, N>(a, t * a.ld, lane) : choose_by_rounds<uint32_t, TYPE, N>(a, t * a.ld, lane);
+    rank = id >= 0 ? lane : 32;
+    lk = id >= 0 ? load_elem<TYPE>(a.logits, t * a.ld + id) : kNegInf;
+    got = __popc(__ballot_sync(0xffffffffu, id >= 0));
+  }
+  const bool chosen = rank < a.K;
+  float s = 0.0f;
+  if (a.renorm) {
+    const float mk = warp_max(chosen ? lk : kNegInf);
+    const bool soft = !a.sigmoid || mk < kFarBelow;
+    if (chosen) s = soft ? fast_exp(lk - mk) : sigmoid(lk);
+    s *= fast_rcp(warp_sum(s));
+  } else if (chosen) {
+    s = a.sigmoid ? sigmoid(lk) : fast_exp(lk - m) * fast_rcp(z);
+  }
+  if (chosen) {
+    a.ids[t * a.K + rank] = id;
+    a.weights[t * a.K + rank] = a.scale * s;
+  }
+  if (lane >= got && lane < a.K) {
+    a.ids[t * a.K + lane] = -1;
+    a.weights[t * a.K + lane] = 0.0f;
+  }
+  return true;
+}
+
+// Tokens that the quick way does not settle wait until the warp's others are done (at
+// most 64 at a time): as calls in the loop they cost every token 40% (registers), and in
+// 64 bits throughout they set the time of a batch (41 us). Bound by the instructions of
+// the quick way, some 600 a token of 256 experts with bias.
+template <int TYPE, int N, int V>
+__global__ void __launch_bounds__(kThreads, min_blocks(N)) route_kernel(RouteArgs a) {
+  __shared__ __align__(16) uint2 s_cand[kWarps][36];  // key, expert; in fours
+  __shared__ float s_bias[32 * N];
+  const int lane = threadIdx.x & 31;
+  uint2* cand = s_cand[threadIdx.x >> 5];
+  const int64_t nwarps = (int64_t)gridDim.x * kWarps;
+  const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && threadIdx.x == 0);
+  int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  float next[N];
+  if (t < n_live) load_row<TYPE, N, V>(next, a.logits, t * a.ld, a.E, lane);
+  if (a.bias != nullptr) {
+    for (int e = threadIdx.x; e < a.E; e += kThreads) s_bias[e] = __ldg(a.bias + e);
+    __syncthreads();
+  }
+  while (t < n_live) {
+    const int64_t first = t;
+    uint64_t open = 0;  // bit i: token first + i * nwarps
+    for (int i = 0; i < 64 && t < n_live; ++i, t += nwarps) {
+      float l[N];
+#pragma unroll
+      for (int j = 0; j < N; ++j) l[j] = next[j];
+      if (t + nwarps < n_live) load_row<TYPE, N, V>(next, a.logits, (t + nwarps) * a.ld, a.E, lane);
+      if (!route_token<false, TYPE, N, V>(a, t, l, cand, s_bias, lane)) open |= 1ull << i;
     }
-    const bool chosen = rank < a.K;
-    float s = 0.0f;
-    if (a.renorm) {
-      const float mk = warp_max(chosen ? lk : kNegInf);
-      const bool soft = !a.sigmoid || mk < kFarBelow;
-      if (chosen) s = soft ? __expf(lk - mk) : sigmoid(lk);
-      s = __fdividef(s, warp_sum(s));
-    } else if (chosen) {
-      s = a.sigmoid ? sigmoid(lk) : __fdividef(__expf(lk - m), z);
-    }
-    if (chosen) {
-      a.ids[t * a.K + rank] = id;
-      a.weights[t * a.K + rank] = a.scale * s;
-    }
-    if (lane >= got && lane < a.K) {
-      a.ids[t * a.K + lane] = -1;
-      a.weights[t * a.K + lane] = 0.0f;
+    while (open != 0) {
+      const int64_t late = first + (__ffsll((long long)open) - 1) * nwarps;
+      open &= open - 1;
+      float l[N];
+      load_row<TYPE, N, V>(l, a.logits, late * a.ld, a.E, lane);
+      route_token<true, TYPE, N, V>(a, late, l, cand, s_bias, lane);
     }
   }
 }
@@ -410,10 +456,19 @@ __global__ void __launch_bounds__(kThreads) route_kernel(RouteArgs a) {
 // not, the call has none (and flags it). Returns the tokens of all groups.
 __device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int32_t* cnt, int32_t* st, int32_t* scratch,
                                            int32_t* status, int& nonempty) {
+  if (g.begin == nullptr) {
+    if (threadIdx.x == 0) {
+      cnt[0] = n_live;
+      st[0] = 0;
+    }
+    __syncthreads();
+    nonempty = n_live > 0;
+    return n_live;
+  }
   bool ok = true;
   for (int q = threadIdx.x; q < g.Q; q += blockDim.x) {
-    const int b = g.begin != nullptr ? __ldg(g.begin + q) : 0, e = g.begin != nullptr ? __ldg(g.end + q) : n_live;
-    const int before = g.begin != nullptr && q > 0 ? __ldg(g.end + q - 1) : 0;
+    const int b = __ldg(g.begin + q), e = __ldg(g.end + q);
+    const int before = q > 0 ? __ldg(g.end + q - 1) : 0;
     ok &= before <= b && b >= 0 && b <= e && e <= n_live;
     cnt[q] = e - b;
   }
@@ -534,13 +589,13 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
         if (m != kNegInf) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            p[i] = __expf(l[u][i] - m);
+            p[i] = fast_exp(l[u][i] - m);
             zs += p[i];
           }
           zs = warp_sum(zs);
           const float lse = m + __logf(zs);
           z = fmaf(lse, lse, z);
-          const float r = __fdividef(1.0f, zs);
+          const float r = fast_rcp(zs);
 #pragma unroll
           for (int i = 0; i < N; ++i) p[i] *= r;
         }
@@ -573,54 +628,69 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
   }
 }
 
-// Joins the parts of group blockIdx.y for 32 experts; the last CTA joins the groups.
-__global__ void __launch_bounds__(1024) balance_join_kernel(BalanceArgs a) {
+// Joins the parts of group blockIdx.y for 32 experts; the last to finish joins the groups.
+// All latency: what it reads is in L2. With few groups (of many parts each) a CTA joins
+// them, a row of threads for every 32nd part; with many, a warp.
+constexpr int kFewGroups = 8;
+template <bool FEW>
+__global__ void __launch_bounds__(FEW ? 1024 : 128) balance_join_kernel(BalanceArgs a) {
   __shared__ float s_p[32][33];
   __shared__ int32_t s_c[32][33];
-  __shared__ bool s_last;
   pdl_wait_primary();
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, rows = blockDim.x >> 5;
-  const int q = blockIdx.y, e = blockIdx.x * 32 + lane, E = a.E;
+  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
+  const int q = blockIdx.y, E = a.E, slices = (E + 31) / 32, slice = FEW ? blockIdx.x : blockIdx.x * 4 + row;
+  if (slice >= slices) return;
+  const int e0 = slice * 32, e = e0 + lane;
   const BalanceWs w = balance_ws(a);
   const int first = __ldcg(w.meta + 3 * q), parts = __ldcg(w.meta + 3 * q + 1), n = __ldcg(w.meta + 3 * q + 2);
   float p = 0.0f;
   int c = 0;
   if (e < E) {
-#pragma unroll 4
-    for (int i = row; i < parts; i += rows) {
+#pragma unroll 8
+    for (int i = FEW ? row : 0; i < parts; i += FEW ? 32 : 1) {
       p += __ldcg(w.P + (int64_t)(first + i) * E + e);
       c += __ldcg(w.c + (int64_t)(first + i) * E + e);
     }
   }
-  s_p[row][lane] = p;
-  s_c[row][lane] = c;
-  __syncthreads();
-  if (row == 0) {
-    for (int i = 1; i < rows; ++i) {
-      p += s_p[i][lane];
-      c += s_c[i][lane];
-    }
-    if (e < E) {
-      a.counts[(int64_t)q * E + e] = c;
-      a.prob_sums[(int64_t)q * E + e] = p;
-    }
-    const float dot = warp_sum((float)c * p);
-    if (lane == 0) {
-      w.share[(int64_t)q * gridDim.x + blockIdx.x] = n > 0 ? dot / n / n * E / a.K : 0.0f;
-      if (blockIdx.x == 0) {
-        float z = 0.0f;
-        for (int i = 0; i < parts; ++i) z += __ldcg(w.z + first + i);
-        w.zshare[q] = z;
-      }
-      __threadfence();
-      s_last = atomicAdd(reinterpret_cast<unsigned*>(w.meta + 3 * a.g.Q + 2), 1u) == gridDim.x * gridDim.y - 1;
-    }
+  if (slice == 0 && (!FEW || row == 31)) {
+    float z = 0.0f;
+    for (int i = lane; i < parts; i += 32) z += __ldcg(w.z + first + i);
+    z = warp_sum(z);
+    if (lane == 0) w.zshare[q] = z;
   }
-  __syncthreads();
-  if (!s_last || row > 0) return;
+  if (FEW) {  // warp k joins the parts of expert e0 + k
+    s_p[row][lane] = p;
+    s_c[row][lane] = c;
+    __syncthreads();
+    p = warp_sum(s_p[lane][row]);
+    c = __reduce_add_sync(0xffffffffu, s_c[lane][row]);
+    __syncthreads();
+    if (lane == 0) {
+      s_p[0][row] = p;
+      s_c[0][row] = c;
+    }
+    __syncthreads();
+    if (row > 0) return;
+    p = s_p[0][lane];
+    c = s_c[0][lane];
+  }
+  if (e < E) {
+    a.counts[(int64_t)q * E + e] = c;
+    a.prob_sums[(int64_t)q * E + e] = p;
+  }
+  const float dot = warp_sum(e < E ? (float)c * p : 0.0f);
+  int last = 0;
+  if (lane == 0) {
+    w.share[(int64_t)q * slices + slice] = n > 0 ? dot / n / n * E / a.K : 0.0f;
+    __threadfence();
+    last = atomicAdd(reinterpret_cast<unsigned*>(w.meta + 3 * a.g.Q + 2), 1u) == (unsigned)(slices * a.g.Q - 1);
+  }
+  if (!__shfl_sync(0xffffffffu, last, 0)) return;
   __threadfence();
   float b = 0.0f, z = 0.0f;
-  for (int64_t i = lane; i < (int64_t)gridDim.x * gridDim.y; i += 32) b += __ldcg(w.share + i);
+#pragma unroll 8
+  for (int64_t i = lane; i < (int64_t)slices * a.g.Q; i += 32) b += __ldcg(w.share + i);
+#pragma unroll 4
   for (int i = lane; i < a.g.Q; i += 32) z += __ldcg(w.zshare + i);
   b = warp_sum(b);
   z = warp_sum(z);
@@ -635,34 +705,40 @@ __global__ void __launch_bounds__(1024) balance_join_kernel(BalanceArgs a) {
 // The gradient of the logits
 // ---------------------------------------------------------------------------
 
-// One warp a token, a run of tokens each, so that the group's counts stay in registers.
-// What the chosen experts add is spread over the row through a line of shared memory.
+// One warp a token; a warp takes runs of kRun tokens, so that a group's counts stay in
+// registers for some while the runs of a group are spread over the SMs (tokens of no group
+// cost half as much). What the chosen experts add is spread over the row through a line of
+// shared memory. Bound by latencies and issue: about 400 instructions a token of 256
+// experts, against 2 KB of traffic.
+constexpr int kRun = 4;
 template <int TYPE, int N, int V>
-__global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
+__global__ void __launch_bounds__(kThreads, min_blocks(N)) route_grad_kernel(RouteGradArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int32_t s_scratch[33];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E, K = a.K, Q = a.g.Q;
-  int32_t* cnt = sm;
-  int32_t* st = cnt + Q;
+  int32_t* cnt = sm;       // tokens of each group
+  int32_t* st = cnt + Q;   // its first token
   float* add = reinterpret_cast<float*>(st + Q) + warp * E;
   for (int e = lane; e < E; e += 32) add[e] = 0.0f;
   const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
-  int nonempty = 0, total = 0;
   float db = 0.0f, dz = 0.0f;
   if (a.dloss != nullptr) {  // uniform over the grid
-    total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
+    int nonempty;
+    const int total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
     if (nonempty > 0) {
       db = __ldg(a.dloss) * (float)E / ((float)K * (float)nonempty);
       dz = 2.0f * __ldg(a.dloss + 1) / (float)total;
     }
+    if (a.g.begin != nullptr) {
+      for (int q = tid; q < Q; q += kThreads) st[q] = __ldg(a.g.begin + q);
+      __syncthreads();
+    }
   }
   __syncwarp();
   const int64_t nwarps = (int64_t)gridDim.x * kWarps;
-  const int64_t per = (a.T + nwarps - 1) / nwarps;
-  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * per;
-  const int64_t stop = min(t + per, (int64_t)a.T);
-  int q = -1;                       // group that holds token t or comes next
-  int64_t gb = 0, ge = -1;          // its tokens
+  int64_t t = ((int64_t)blockIdx.x * kWarps + warp) * kRun;
+  auto following = [&](int64_t at) { return ++at % kRun ? at : at + (nwarps - 1) * kRun; };
+  int q = 0, have = -1;             // group that holds token t or comes next; the group of g
   float g[N];                       // its gradient of the sums of p
   float l[N], next[N], dw = 0.0f, ndw = 0.0f, lk, nlk = kNegInf;
   int id = -1, nid = -1;
@@ -679,11 +755,12 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
       }
     }
   };
-  if (t < stop && t < n_live) {
+  if (t < n_live) {
     load(t, next, nid, ndw);
     if (nid >= 0) nlk = load_elem<TYPE>(a.logits, t * a.ld + nid);
   }
-  for (; t < stop; ++t) {
+  for (int64_t after; t < a.T; t = after) {
+    after = following(t);
     if (t >= n_live) {
 #pragma unroll
       for (int i = 0; i < N; ++i) l[i] = 0.0f;
@@ -695,8 +772,8 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
 #pragma unroll
     for (int i = 0; i < N; ++i) l[i] = next[i];
     lk = nlk;
-    const bool more = t + 1 < stop && t + 1 < n_live;
-    if (more) load(t + 1, next, nid, ndw);
+    const bool more = after < n_live;
+    if (more) load(after, next, nid, ndw);
     float r[N], m = kNegInf;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -705,31 +782,24 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
     }
     m = warp_max(m);
     if (db != 0.0f || dz != 0.0f) {
-      if (t >= ge) {  // on to the group that ends behind t
-        if (q < 0 && a.g.begin != nullptr) {
-          q = 0;
-          for (int hi = Q; q < hi;) {
-            const int mid = (q + hi) >> 1;
-            if (__ldg(a.g.end + mid) <= t) q = mid + 1; else hi = mid;
-          }
+      if (t % kRun == 0) {  // the first group that ends behind t
+        int lo = q;
+        for (int hi = Q; lo < hi;) {
+          const int mid = (lo + hi) >> 1;
+          if (st[mid] + cnt[mid] <= t) lo = mid + 1; else hi = mid;
         }
-        if (a.g.begin == nullptr) {
-          q = 0;
-          ge = n_live;
-        } else {
-          while (q < Q && __ldg(a.g.end + q) <= t) ++q;
-          gb = q < Q ? __ldg(a.g.begin + q) : INT_MAX;
-          ge = q < Q ? __ldg(a.g.end + q) : INT_MAX;
-        }
-        if (q < Q) {
-          const float n = (float)cnt[q];
-          const float scale = n > 0.0f ? db / n / n : 0.0f;
+        q = lo;
+      } else {
+        while (q < Q && st[q] + cnt[q] <= t) ++q;
+      }
+      if (q < Q && t >= st[q]) {
+        if (have != q) {
+          have = q;
+          const float n = (float)cnt[q], scale = db / n / n;
 #pragma unroll
           for (int i = 0; i < N; ++i)
             g[i] = expert_of<V>(i, lane) < E ? scale * (float)__ldg(a.counts + (int64_t)q * E + expert_of<V>(i, lane)) : 0.0f;
         }
-      }
-      if (t >= gb && q < Q) {
         float p[N], rest[N], dot = 0.0f;
         scores<true>(l, m, a.sigmoid, p, rest);
 #pragma unroll
@@ -744,11 +814,11 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
           float z = 0.0f;
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            p[i] = __expf(l[i] - m);
+            p[i] = fast_exp(l[i] - m);
             z += p[i];
           }
           z = warp_sum(z);
-          const float c = __fdividef(dz * (m + __logf(z)), z);
+          const float c = dz * (m + __logf(z)) * fast_rcp(z);
 #pragma unroll
           for (int i = 0; i < N; ++i) r[i] = fmaf(c, p[i], r[i]);
         }
@@ -759,9 +829,9 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
       if (a.renorm) {
         const float mk = warp_max(lk);
         const bool soft = !a.sigmoid || mk < kFarBelow;
-        const float s = id >= 0 && mk != kNegInf ? (soft ? __expf(lk - mk) : sigmoid(lk)) : 0.0f;
+        const float s = id >= 0 && mk != kNegInf ? (soft ? fast_exp(lk - mk) : sigmoid(lk)) : 0.0f;
         const float sum = warp_sum(s);
-        const float u = id >= 0 && mk != kNegInf ? __fdividef(s, sum) : 0.0f;
+        const float u = id >= 0 && mk != kNegInf ? s * fast_rcp(sum) : 0.0f;
         dk = a.scale * u * (dw - warp_sum(u * dw));
         if (a.sigmoid) dk *= sigmoid_rest(lk);
       } else if (a.sigmoid) {
@@ -770,12 +840,12 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
         float z = 0.0f, p[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-          p[i] = __expf(l[i] - m);
+          p[i] = fast_exp(l[i] - m);
           z += p[i];
         }
         z = warp_sum(z);
-        dk = id >= 0 && m != kNegInf ? a.scale * dw * __fdividef(__expf(lk - m), z) : 0.0f;
-        const float c = m == kNegInf ? 0.0f : __fdividef(warp_sum(dk), z);
+        dk = id >= 0 && m != kNegInf ? a.scale * dw * fast_exp(lk - m) * fast_rcp(z) : 0.0f;
+        const float c = m == kNegInf ? 0.0f : warp_sum(dk) * fast_rcp(z);
         if (m != kNegInf) {
 #pragma unroll
           for (int i = 0; i < N; ++i) r[i] = fmaf(-c, p[i], r[i]);
@@ -799,7 +869,7 @@ __global__ void __launch_bounds__(kThreads) route_grad_kernel(RouteGradArgs a) {
       if (id >= 0) add[id] = 0.0f;
       __syncwarp();
     }
-    nlk = more && nid >= 0 ? load_elem<TYPE>(a.logits, (t + 1) * a.ld + nid) : kNegInf;
+    nlk = more && nid >= 0 ? load_elem<TYPE>(a.logits, after * a.ld + nid) : kNegInf;
     store_row<TYPE, N, V>(a.dlogits, t * a.ldd, E, lane, r);
   }
 }
@@ -868,16 +938,18 @@ cudaError_t launch_balance(const BalanceArgs& a, int type, int num_sms, cudaStre
     return cudaGetLastError();
   });
   if (err != cudaSuccess) return err;
+  const bool few = a.g.Q <= kFewGroups;
+  const unsigned slices = (unsigned)((a.E + 31) / 32);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.E + 31) / 32), (unsigned)a.g.Q);
-  cfg.blockDim = dim3(a.g.Q <= 8 ? 1024 : 128);  // a group of many has few parts
+  cfg.gridDim = dim3(few ? slices : (slices + 3) / 4, (unsigned)a.g.Q);
+  cfg.blockDim = dim3(few ? 1024 : 128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, balance_join_kernel, a);
+  return cudaLaunchKernelEx(&cfg, few ? balance_join_kernel<true> : balance_join_kernel<false>, a);
 }
 
 cudaError_t launch_route_grad(const RouteGradArgs& a, int type, int num_sms, cudaStream_t s) {
@@ -890,7 +962,7 @@ cudaError_t launch_route_grad(const RouteGradArgs& a, int type, int num_sms, cud
     int per_sm = 0;
     err = occupancy(kernel, kThreads, smem, &per_sm);
     if (err != cudaSuccess) return err;
-    const int64_t need = ((int64_t)a.T + kWarps - 1) / kWarps, most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
+    const int64_t need = ((int64_t)a.T + kWarps * kRun - 1) / (kWarps * kRun), most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);
     kernel<<<(unsigned)(need < most ? need : most), kThreads, smem, s>>>(a);
     return cudaGetLastError();
   });
