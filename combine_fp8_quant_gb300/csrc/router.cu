@@ -453,9 +453,10 @@ __global__ void __launch_bounds__(kThreads, min_blocks(N)) route_kernel(RouteArg
 
 // Sizes and first flattened tokens of the groups in shared memory: cnt, st [Q] (and 33
 // ints of scratch). Groups lie one after the other inside the live tokens; if any does
-// not, the call has none (and flags it). Returns the tokens of all groups.
-__device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int32_t* cnt, int32_t* st, int32_t* scratch,
-                                           int32_t* status, int& nonempty) {
+// not, the call has none (and flags it). In the flattened order a group is followed by
+// `pad` places without a token. Returns the places of all groups.
+__device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int pad, int32_t* cnt, int32_t* st,
+                                           int32_t* scratch, int32_t* status, int& nonempty) {
   if (g.begin == nullptr) {
     if (threadIdx.x == 0) {
       cnt[0] = n_live;
@@ -463,14 +464,14 @@ __device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int32
     }
     __syncthreads();
     nonempty = n_live > 0;
-    return n_live;
+    return n_live > 0 ? n_live + pad : 0;
   }
   bool ok = true;
   for (int q = threadIdx.x; q < g.Q; q += blockDim.x) {
     const int b = __ldg(g.begin + q), e = __ldg(g.end + q);
     const int before = q > 0 ? __ldg(g.end + q - 1) : 0;
     ok &= before <= b && b >= 0 && b <= e && e <= n_live;
-    cnt[q] = e - b;
+    cnt[q] = e > b ? e - b + pad : 0;
   }
   int some = 0;
   ok = __syncthreads_and(ok);
@@ -487,6 +488,11 @@ __device__ __forceinline__ int plan_groups(const GroupArgs& g, int n_live, int32
   if ((threadIdx.x & 31) == 0 && some > 0) atomicAdd(scratch, some);
   __syncthreads();
   nonempty = scratch[0];
+  if (pad > 0) {
+    for (int q = threadIdx.x; q < g.Q; q += blockDim.x)
+      if (cnt[q] > 0) cnt[q] -= pad;
+    __syncthreads();
+  }
   return total;
 }
 
@@ -519,13 +525,17 @@ __device__ __forceinline__ BalanceWs balance_ws(const BalanceArgs& a) {
   return w;
 }
 
-// Sums over a run of tokens, one warp a token, two at a time; bound by HBM where the
-// batch is large, by its two launches where it is small.
+// Sums over a run of tokens, one warp a token, four at a time. Joining the warps' sums
+// for a group costs a CTA about as much as kGroupCost tokens, so a run of short groups
+// counts for more. Bound by latencies: a batch of 65536 tokens leaves a warp about a
+// dozen.
+constexpr int kGroupCost = 32;
 template <int TYPE, int N, int V>
 __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) {
   extern __shared__ int32_t sm[];
   __shared__ int32_t s_scratch[33];
   __shared__ float s_z[kWarps];
+  pdl_launch_dependents();  // the second launch waits for this one's end on the device
   int32_t* cnt = sm;
   int32_t* st = cnt + a.g.Q;
   int32_t* hist = st + a.g.Q;                               // [E]
@@ -533,7 +543,7 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, E = a.E;
   const int n_live = live_count(a.d_num_tokens, a.T, a.status, blockIdx.x == 0 && tid == 0);
   int nonempty;
-  const int total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
+  const int total = plan_groups(a.g, n_live, kGroupCost, cnt, st, s_scratch, a.status, nonempty);
   const int per = (total + (int)gridDim.x - 1) / (int)gridDim.x;
   const BalanceWs w = balance_ws(a);
   if (blockIdx.x == 0) {
@@ -545,7 +555,7 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
     }
     if (tid == 0) {
       w.meta[3 * a.g.Q] = nonempty;
-      w.meta[3 * a.g.Q + 1] = total;
+      w.meta[3 * a.g.Q + 1] = total - nonempty * kGroupCost;
       w.meta[3 * a.g.Q + 2] = 0;
     }
   }
@@ -559,7 +569,10 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
   }
   for (; at < stop; ++q) {
     const int upto = min(stop, st[q] + cnt[q]);
-    if (upto <= at) continue;
+    if (upto <= at) {  // past the group's tokens
+      if (cnt[q] > 0) at = max(at, min(stop, st[q] + cnt[q] + kGroupCost));
+      continue;
+    }
     for (int e = tid; e < E; e += kThreads) hist[e] = 0;
     __syncthreads();
     const int64_t first = (a.g.begin != nullptr ? __ldg(a.g.begin + q) : 0) + (at - st[q]);
@@ -624,7 +637,7 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
       w.z[slot] = v;
     }
     __syncthreads();
-    at = upto;
+    at = min(stop, st[q] + cnt[q] + kGroupCost);  // (upto, where the run ends inside)
   }
 }
 
@@ -724,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, min_blocks(N)) route_grad_kernel(Rou
   float db = 0.0f, dz = 0.0f;
   if (a.dloss != nullptr) {  // uniform over the grid
     int nonempty;
-    const int total = plan_groups(a.g, n_live, cnt, st, s_scratch, a.status, nonempty);
+    const int total = plan_groups(a.g, n_live, 0, cnt, st, s_scratch, a.status, nonempty);
     if (nonempty > 0) {
       db = __ldg(a.dloss) * (float)E / ((float)K * (float)nonempty);
       dz = 2.0f * __ldg(a.dloss + 1) / (float)total;
