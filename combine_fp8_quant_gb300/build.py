@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libmoeperm.so")
 UNITS = ["api.cu", "route_plan.cu", "quant_scatter.cu", "combine.cu", "repack.cu", "requant.cu",
          "noalloc.cu", "dispatch_small.cu", "permute.cu", "combine_grad.cu", "block_norm.cu",
          "api_block.cu", "matmul.cu", "act_grad.cu", "router.cu", "api_router.cu",
-         "fp4.cu", "api_fp4.cu"]
+         "fp4.cu", "fp4_few_rows.cu", "api_fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v",
          "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

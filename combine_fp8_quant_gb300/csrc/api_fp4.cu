@@ -158,7 +158,7 @@ moe_status_t moe_expert_matmul_fp4(const void* x, int64_t ldx, const void* x_sca
   m.xs = static_cast<const uint32_t*>(x_scales); m.ld_xs = ld_xs;
   m.ws = static_cast<const uint32_t*>(w_scales); m.ld_ws = ld_ws;
   m.x_tscale = x_tscale; m.w_tscale = w_tscale; m.status = d_status;
-  return cuda_status(launch_matmul(m, sms, cu(stream)));
+  return cuda_status(few_rows_fp4(m) ? launch_matmul_few_rows(m, sms, cu(stream)) : launch_matmul(m, sms, cu(stream)));
 }
 
 }  // extern "C"

@@ -188,6 +188,9 @@ struct MatmulArgs {
 // Element types of the products beyond moe_elem_t's: four bits, by their scales.
 constexpr int kE2M1MX = 16, kE2M1NV = 17;
 cudaError_t launch_matmul(const MatmulArgs& a, int num_sms, cudaStream_t s);
+// The same product for a few rows of one dense matrix in four bits; false: not for it.
+bool few_rows_fp4(const MatmulArgs& a);
+cudaError_t launch_matmul_few_rows(const MatmulArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_matmul_grad_x(const MatmulArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_matmul_grad_w(const MatmulArgs& a, int num_sms, cudaStream_t s);
 

@@ -360,6 +360,38 @@ def test_product_dense(dev, R, K, N, fmt):
     check(out, quantise(x, fmt)[2], wv, bias[None], res, [(0, R)], N, "none", False)
 
 
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("gated,act,dtype", [(True, "silu", torch.bfloat16), (True, "gelu", torch.float16), (False, "relu", torch.float16)])
+@pytest.mark.parametrize("R,K,N", [(1, 64, 16), (2, 1024, 48), (3, 1088, 112), (4, 2048, 7168), (4, 7168, 32), (4, 14336, 16), (5, 2048, 64),
+                                   (1, 40960, 16), (2, 4096, 256), (2, 65536, 16)])
+def test_product_of_few_rows(dev, R, K, N, gated, act, dtype, fmt):
+    """One or two rows of one matrix, with every part of the epilogue; just more rows, and rows too long for it."""
+    Nw = 2 * N if gated else N
+    x = rand(R, R, K)
+    xts = torch.full((1,), 0.02, device=DEV) if fmt == "nv" else None
+    q = dev.quant_fp4(x, fmt=fmt, tensor_scale=xts)
+    w, wsc, wts, wv = weights(dev, 2, 1, Nw, K, fmt)
+    bias, res = rand(3, 1, Nw), rand(4, R, N + 5, dtype=dtype)[:, 3:N + 3]
+    call = lambda: dev.expert_matmul_fp4(q["xq"], w, q["scales"], wsc, fmt=fmt, x_tscale=xts, w_tscale=wts, bias=bias, act=act, gated=gated,
+                                         residual=res, out_dtype=dtype)
+    out = call()
+    check(out, quantise(x, fmt, xts)[2], wv, bias, res, [(0, R)], N, act, gated)
+    assert torch.equal(out, call())
+
+
+def test_few_rows_not_a_number(dev):
+    R, K, N = 2, 512, 72
+    x = rand(1, R, K)
+    x[1, 100] = math.nan
+    w = rand(2, N, K, gain=K ** -0.5)
+    w[5, 7] = math.inf
+    q, wq = dev.quant_fp4(x), dev.quant_fp4(w)
+    out = dev.expert_matmul_fp4(q["xq"], wq["xq"], q["scales"], wq["scales"])
+    bad = torch.zeros(R, N, dtype=torch.bool, device=DEV)
+    bad[1], bad[:, 5] = True, True
+    assert torch.equal(torch.isnan(out), bad) and torch.isfinite(out[~bad]).all()
+
+
 def test_product_of_slabs(dev):
     L, cap, K, N = 5, 48, 576, 96
     m = i32([0, 48, 5, 17, 1])
