@@ -12,7 +12,7 @@ cudaStream_t cu(moe_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 // Logits [T, ld] of a type, and a choice of K of E experts.
 bool logits_ok(const void* logits, int64_t ld, int es, int32_t T, int32_t E, int32_t K) {
-  if (es == 0 || T < 0 || E < 1 || E > kMaxRouted || K < 1 || K > kMaxK || K > E) return false;
+  if (es == 0 || T < 0 || T > (1 << 30) || E < 1 || E > kMaxRouted || K < 1 || K > kMaxK || K > E) return false;
   return T == 0 || (logits != nullptr && aligned_to(logits, es) && ld >= E);
 }
 bool score_ok(int s) { return s == MOE_SCORE_SOFTMAX || s == MOE_SCORE_SIGMOID; }

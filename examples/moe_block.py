@@ -1,20 +1,23 @@
 """One MoE block through the library's calls, for serving and for training.
 
     h  = rms(x) * w_in                        block_norm
-    route h to top-k experts                  (torch: logits, top-k, softmax)
+    route h to top-k experts                  (torch: logits) route
     serving    rows in e4m3                   dispatch_compact
                silu(gate) * up, in e4m3       expert_matmul, quant_group
                down projection                expert_matmul
+      or       rows in four bits              dispatch_fp4
+               silu(gate) * up, in four bits  expert_matmul_fp4, quant_fp4
+               down projection                expert_matmul_fp4
     training   rows in bf16                   permute
                silu(gate) * up, P kept        expert_matmul
                down projection                expert_matmul
     y  = sum_k w_k * expert output            combine
     x' = x + scale * gate * rms(y) * w_out    block_norm
 
-and for training the backward pass through the same steps, written out call by
-call: block_norm_grad, combine_grad, expert_matmul_grad twice, permute_grad and
-block_norm_grad again. The router's own gradient (through the top-k weights) is
-torch's.
+and for training the router's balance and z losses (balance_loss) and the backward
+pass through the same steps, written out call by call: block_norm_grad,
+combine_grad, expert_matmul_grad twice, permute_grad, route_grad (through the
+top-k weights and both losses) and block_norm_grad again.
 
 Run it on a GB300:  python examples/moe_block.py
 """
@@ -55,11 +58,14 @@ def make_weights(E, H, F, seed=0, device="cuda"):
                    up=bf(r(E, 2 * F, H) * H ** -0.5), up_bias=0.1 * r(E, 2 * F), down=bf(r(E, H, F) * F ** -0.5), scale=0.5)
 
 
+def router_logits(h, router):
+    return h.float() @ router.float().t()
+
+
 def route(h, router, top_k):
     """Top-k experts of each token and the softmax over their logits."""
-    logits = h.float() @ router.float().t()
-    top, ids = logits.topk(top_k, dim=1)
-    return ids.to(torch.int32).contiguous(), torch.softmax(top, dim=1).contiguous()
+    r = mp.route(router_logits(h, router), top_k)
+    return r["topk_ids"], r["topk_weights"]
 
 
 class Serving:
@@ -88,12 +94,47 @@ class Serving:
         return mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, gate_mode="channel", scale=w.scale)["x"]
 
 
-def forward(x, w: Weights, top_k):
-    """The training forward pass: (x', what the backward pass needs)."""
+class Serving4:
+    """The block with its expert weights laid out once in four bits: e2m1 with a float8
+    scale for each 16 elements and a float32 scale for each expert."""
+
+    def __init__(self, w: Weights):
+        self.w = w
+
+        def lay_out(t):
+            L, N, K = t.shape
+            ts = (t.abs().amax((1, 2)).float() / (6 * 448)).contiguous()
+            q = mp.quant_fp4(t.view(L * N, K), tensor_scale=ts)
+            return q["xq"].view(L, N, K // 2), q["scales"], ts
+
+        self.up, self.up_sc, self.up_ts = lay_out(w.up)
+        self.down, self.down_sc, self.down_ts = lay_out(w.down)
+
+    def __call__(self, x, top_k):
+        w, E = self.w, self.up.shape[0]
+        h = mp.block_norm(x, w_pre=w.w_in)["h"]
+        ids, tw = route(h, w.router, top_k)
+        d = mp.dispatch_fp4(h, ids, tw, E, E, block_e=BLOCK_E)
+        seg = dict(starts=d["starts"], psum=d["psum"], status=d["status"])
+        a = mp.expert_matmul_fp4(d["xq"], self.up, d["scales"], self.up_sc, w_tscale=self.up_ts, bias=w.up_bias,
+                                 act="silu", gated=True, **seg)
+        q = mp.quant_fp4(a, m_indices=d["m_indices"])
+        y = mp.expert_matmul_fp4(q["xq"], self.down, q["scales"], self.down_sc, w_tscale=self.down_ts, **seg)
+        out = mp.combine(y, d["src2dst"], tw, status=d["status"])
+        return mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, gate_mode="channel", scale=w.scale)["x"]
+
+
+def forward(x, w: Weights, top_k, coef=None):
+    """The training forward pass: (x', what the backward pass needs). coef: float32 [2],
+    what the balance and the z loss count for in the training loss; the losses
+    themselves are in saved["loss"]."""
     E = w.up.shape[0]
     pre_norm = mp.block_norm(x, w_pre=w.w_in, save_rstd=True)
     h = pre_norm["h"]
-    ids, tw = route(h, w.router, top_k)
+    logits = router_logits(h, w.router)
+    r = mp.route(logits, top_k)
+    ids, tw = r["topk_ids"], r["topk_weights"]
+    balance = mp.balance_loss(logits, ids) if coef is not None else dict(loss=None, counts=None)
     p = mp.permute(h, ids, tw, E, E, block_e=BLOCK_E)
     seg = dict(starts=p["starts"], psum=p["psum"], status=p["status"])
     P = torch.empty(p["bound"], w.up.shape[1], dtype=x.dtype, device=x.device)
@@ -101,7 +142,8 @@ def forward(x, w: Weights, top_k):
     y = mp.expert_matmul(a, w.down, **seg)
     out = mp.combine(y, p["src2dst"], tw, status=p["status"])
     post = mp.block_norm(x, out, w_post=w.w_out, gate=w.gate, gate_mode="channel", scale=w.scale, save_rstd=True)
-    saved = dict(x=x, h=h, ids=ids, tw=tw, xs=p["xs"], P=P, a=a, y=y, out=out, seg=seg, src2dst=p["src2dst"],
+    saved = dict(x=x, h=h, logits=logits, ids=ids, tw=tw, coef=coef, loss=balance["loss"], counts=balance["counts"],
+                 xs=p["xs"], P=P, a=a, y=y, out=out, seg=seg, src2dst=p["src2dst"],
                  x_out=post["x"], rstd_in=pre_norm["rstd_pre"], rstd_out=post["rstd_post"])
     return post["x"], saved
 
@@ -116,10 +158,8 @@ def backward(dx_out, s, w: Weights):
     up = mp.expert_matmul_grad(down["dx"], s["xs"], w.up, pre=s["P"], act="silu", gated=True,
                                need=("dx", "dw", "dbias"), **s["seg"])
     dh = mp.permute_grad(up["dx"], s["src2dst"], status=st)
-    # the router: through the softmax of the chosen logits
-    dtw, tw = c["dweights"], s["tw"]
-    dtop = tw * (dtw - (dtw * tw).sum(1, keepdim=True))
-    dlogits = torch.zeros(tw.shape[0], w.router.shape[0], device=dh.device).scatter_(1, s["ids"].long(), dtop)
+    # the router: through the softmax of the chosen logits and through its losses
+    dlogits = mp.route_grad(s["logits"], s["ids"], dweights=c["dweights"], dloss=s["coef"], counts=s["counts"])
     drouter = dlogits.t() @ s["h"].float()
     dh = (dh.float() + dlogits @ w.router.float()).to(dh.dtype)
     pre = mp.block_norm_grad(post["dx"], dh, s["x"], w_pre=w.w_in, rstd_pre=s["rstd_in"])
@@ -131,12 +171,13 @@ def main():
     T, H, F, E, top_k = 512, 2048, 1024, 16, 4
     w = make_weights(E, H, F)
     x = torch.randn(T, H, device="cuda").to(torch.bfloat16)
-    served = Serving(w)(x, top_k)
-    out, saved = forward(x, w, top_k)
+    served, served4 = Serving(w)(x, top_k), Serving4(w)(x, top_k)
+    out, saved = forward(x, w, top_k, coef=torch.tensor([0.01, 0.001], device="cuda"))
     grads = backward(torch.ones_like(out), saved, w)
     code = mp.moe_status_sync(saved["seg"]["status"])
-    diff = (served.float() - out.float()).norm() / out.float().norm()
-    print(f"status {code}; e4m3 against bf16 block output: relative difference {diff:.4f}")
+    diff, diff4 = ((t.float() - out.float()).norm() / out.float().norm() for t in (served, served4))
+    print(f"status {code}; e4m3 and four-bit against bf16 block output: relative difference {diff:.4f}, {diff4:.4f}")
+    print(f"balance loss {saved['loss'][0]:.4f}, z loss {saved['loss'][1]:.4f}")
     for k, g in grads.items():
         print(f"  d{k:8s} {str(tuple(g.shape)):18s} norm {g.float().norm():.4f}")
 

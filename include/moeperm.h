@@ -607,6 +607,7 @@ moe_status_t moe_expert_matmul_fp4(
 
 /* ------------------------------------------------------------------ */
 /* The router: choice of experts, its losses and their gradients        */
+/* (T <= 2^30)                                                          */
 /* ------------------------------------------------------------------ */
 
 typedef enum {

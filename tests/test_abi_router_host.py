@@ -32,7 +32,7 @@ def call(mp, name, args, over):
 
 ROUTE = dict(logits=FAKE, ldl=256, dtype=F32, T=64, d_num_tokens=None, E=256, K=8, score="softmax", bias=None, renorm=True,
              scale=1.0, topk_ids=FAKE, topk_weights=FAKE, d_status=None)
-LOGITS = [dict(dtype=E4), dict(T=-1), dict(E=0), dict(E=1025, ldl=1025), dict(K=0), dict(K=33), dict(E=7, K=8), dict(ldl=255),
+LOGITS = [dict(dtype=E4), dict(T=-1), dict(T=(1 << 30) + 1), dict(E=0), dict(E=1025, ldl=1025), dict(K=0), dict(K=33), dict(E=7, K=8), dict(ldl=255),
           dict(logits=None), dict(logits=FAKE + 2), dict(dtype=BF, logits=FAKE + 1), dict(d_num_tokens=FAKE + 2),
           dict(d_status=FAKE + 1)]
 
