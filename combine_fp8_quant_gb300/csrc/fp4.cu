@@ -1,8 +1,10 @@
 // fp4.cu -- rows to four bits and back (format in fp4.cuh), in place order and as a
 // dispatch into the compact layout.
 //
-// All of it is bound by HBM: a bf16 row is read once (2 bytes an element) and leaves as
-// 0.5 bytes and its scales (1/16 or 1/32). A lane owns 16 elements, so that a group of
+// Large batches are bound by HBM: a bf16 row is read once (2 bytes an element) and leaves as
+// 0.5 bytes and its scales (1/16 or 1/32): 16384 x 7168 in 48 us with scales per 32 (6.2
+// TB/s), 57 with scales per 16 (5.3 TB/s, the division and its correction), the way back in
+// 53 and 56 (5.6 and 5.3 TB/s). A lane owns 16 elements, so that a group of
 // 16 needs no exchange and one of 32 a single one; a warp covers 512 elements of a row
 // at a time, whose scales are one or two whole pieces.
 #include "common.cuh"
@@ -193,8 +195,9 @@ __global__ void __launch_bounds__(kThreads) dispatch_fp4_small_kernel(DispatchFp
 // After the route plan. The rows of all tokens of a CTA are found at once; then each warp
 // works alone on units of 2048 elements of a token: it quantises them into a staging
 // buffer, copies the elements to every row with one bulk copy each (lane k that of slot k)
-// and the scales piece by piece. (Whole tokens a warp left 4096 tokens of 7168 in one round
-// and an eighth of another: 48 us, units as below.)
+// and the scales piece by piece. Bound by latencies and
+// the layout's prologue: 4096 tokens of 7168, top-8 of 64 experts, 45 us with the route
+// plan (191 MB, 4.3 TB/s); whole tokens a warp, one round and an eighth of another, 49.
 constexpr int kPart = 128;     // chunks of a unit
 constexpr int kStages = 4;     // units in flight a warp
 __host__ __device__ constexpr int part_pieces(int fmt) { return kPart / (fmt == kFp4NV ? 16 : 32); }

@@ -968,11 +968,11 @@ def fp4_scale_tensor(rows: int, H: int, fmt: str, device, ld: int | None = None)
 def _fp4_scales(t, rows, H, fmt, name):
     """The leading dimension of a scale tensor that holds `rows` rows of H elements."""
     pieces = (H // (16 if fmt == "nv" else 32) + 15) // 16
-    if t.dtype != torch.uint8 or t.dim() != 3 or t.shape[0] < pieces or t.shape[1] < rows or t.shape[2] != 16 \
-            or not t.is_contiguous():
+    s = t.shape
+    if t.dtype is not torch.uint8 or len(s) != 3 or s[0] < pieces or s[1] < rows or s[2] != 16 or not t.is_contiguous():
         raise ValueError(f"moeperm: {name} must be contiguous uint8 scales [{pieces}, >= {rows}, 16] ({fmt}), not "
-                         f"{t.dtype} of shape {tuple(t.shape)}")
-    return t.shape[1]
+                         f"{t.dtype} of shape {tuple(s)}")
+    return s[1]
 
 
 def _tensor_scale(t, fmt, name, n=None):
@@ -987,11 +987,12 @@ def _tensor_scale(t, fmt, name, n=None):
 
 def _fp4_rows(R, num_live, m_indices, masked_m):
     """The rows to work on, named in one way at most: cap."""
-    if sum(v is not None for v in (num_live, m_indices, masked_m)) > 1:
+    if (num_live is not None) + (m_indices is not None) + (masked_m is not None) > 1:
         raise ValueError("moeperm: give one of num_live, m_indices and masked_m")
-    _vec(num_live, 1, "num_live", torch.int32)
-    _vec(m_indices, R, "m_indices", torch.int32)
+    if m_indices is not None:
+        _vec(m_indices, R, "m_indices", torch.int32)
     if masked_m is None:
+        _vec(num_live, 1, "num_live", torch.int32)
         return 0
     L = masked_m.numel()
     _vec(masked_m, L, "masked_m", torch.int32)
@@ -1073,18 +1074,28 @@ def dispatch_fp4(x, topk_ids, topk_weights, num_experts, num_local_experts, bloc
     _vec(topk_weights, T * K, "topk_weights")
     _tensor_scale(tensor_scale, fmt, "tensor_scale", 1)
     bound = moe_compact_bound(T * K, L, block_e)
-    m_indices, counts, starts, psum, total = _words(dev, bound, L, L, L, 1)
+    # one allocation for the small outputs, and for the workspace (first, so aligned) and the
+    # status word where the caller gives none: each costs the host as much as a short kernel
+    ws_words = 0 if workspace is not None else (moe_workspace_bytes(T, K, L) + 15) // 16 * 4
+    ws, m_indices, s2d, counts, starts, psum, total, rw, st = _words(
+        dev, ws_words, bound, T * K, L, L, L, 1, bound if row_weights else 0, int(status is None))
+    if workspace is not None:
+        ws, ws_bytes = workspace.buf, workspace.nbytes
+    else:
+        ws_bytes = ws_words * 4
+    if status is not None:
+        st = status
+    else:
+        _check(lib().moe_status_clear(*_on_current(st), _stream()), "moe_status_clear")
     o = dict(xq=torch.empty((bound, H // 2), dtype=torch.uint8, device=dev),
              scales=fp4_scale_tensor(bound, H, fmt, dev), ld_s=bound, bound=bound, m_indices=m_indices,
-             src2dst=torch.empty((T, K), dtype=torch.int32, device=dev), counts=counts, starts=starts, psum=psum,
-             total=total, row_weights=torch.empty(bound, dtype=torch.float32, device=dev) if row_weights else None)
-    ws = workspace if workspace is not None else Workspace(T, K, L, dev)
-    st = _status(status, True, dev)
+             src2dst=s2d.view(T, K), counts=counts, starts=starts, psum=psum, total=total,
+             row_weights=rw.view(torch.float32) if row_weights else None)
     px, pn, pi, pw, pt, *po, pws, pst = _on_current(
         x, num_tokens, topk_ids, topk_weights, tensor_scale, o["xq"], o["scales"], o["m_indices"], o["src2dst"],
-        o["counts"], o["starts"], o["psum"], o["total"], o["row_weights"], ws.buf, st)
+        o["counts"], o["starts"], o["psum"], o["total"], o["row_weights"], ws, st)
     _check(lib().moe_dispatch_fp4(px, ldx, ELEM[dtype], T, pn, H, pi, pw, K, num_experts, L, block_e, f, pt, po[0],
-                                  po[1], bound, po[2], bound, *po[3:], pws, ws.nbytes, pst, _stream()),
+                                  po[1], bound, po[2], bound, *po[3:], pws, ws_bytes, pst, _stream()),
            "moe_dispatch_fp4")
     o["status"] = st
     return o
@@ -1107,30 +1118,35 @@ def expert_matmul_fp4(x, w, x_scales, w_scales, fmt="nv", starts=None, psum=None
     if out_dtype not in FLOATS[:2]:
         raise ValueError(f"moeperm: out_dtype must be bfloat16 or float16, not {out_dtype}")
     masked = masked_m is not None
-    begin, end = _segments(starts, psum, masked_m, L)
-    shape3 = x.shape
+    begin = end = None
+    if L != 1 or masked or starts is not None or psum is not None:
+        begin, end = _segments(starts, psum, masked_m, L)
+    full = (*x.shape[:-1], N)
     x, cap = _expert_rows(x, masked, L, "x")
-    ldx = _rows(x, "x", (x.shape[0], K2))
     R, Nw = x.shape[0], (2 * N if gated else N)
+    ldx = _rows(x, "x", (R, K2))
     ld_xs = _fp4_scales(x_scales, R, 2 * K2, fmt, "x_scales")
     ld_ws = _fp4_scales(w_scales, L * Nw, 2 * K2, fmt, "w_scales")
-    _tensor_scale(x_tscale, fmt, "x_tscale", 1)
-    _tensor_scale(w_tscale, fmt, "w_tscale", L)
-    _vec(bias, L * Nw, "bias")
-    full = (*shape3[:-1], N)
+    if x_tscale is not None:
+        _tensor_scale(x_tscale, fmt, "x_tscale", 1)
+    if w_tscale is not None:
+        _tensor_scale(w_tscale, fmt, "w_tscale", L)
+    if bias is not None:
+        _vec(bias, L * Nw, "bias")
     if out is None:
-        out = torch.empty(full, dtype=out_dtype, device=x.device)
-    elif tuple(out.shape) != full:
-        raise ValueError(f"moeperm: out must have shape {full}")
-    odt = _elem(out, FLOATS[:2], "out")
-    o2 = _expert_rows(out, masked, L, "out")[0]
-    ldo = _rows(o2, "out", (R, N), odt)
+        out, odt, o2, ldo = torch.empty(full, dtype=out_dtype, device=x.device), out_dtype, None, N
+    else:
+        if tuple(out.shape) != full:
+            raise ValueError(f"moeperm: out must have shape {full}")
+        odt = _elem(out, FLOATS[:2], "out")
+        o2 = _expert_rows(out, masked, L, "out")[0]
+        ldo = _rows(o2, "out", (R, N), odt)
     res, ld_res = None, 0
     if residual is not None:
         res = _expert_rows(residual, masked, L, "residual")[0]
         ld_res = _rows(res, "residual", (R, N), odt)
     px, pxs, pxt, pw, pws, pwt, pb, p0, p1, pr, po, pst = _on_current(
-        x, x_scales, x_tscale, w, w_scales, w_tscale, bias, begin, end, res, o2, status)
+        x, x_scales, x_tscale, w, w_scales, w_tscale, bias, begin, end, res, out if o2 is None else o2, status)
     _check(lib().moe_expert_matmul_fp4(px, ldx, pxs, ld_xs, pxt, R, 2 * K2, pw, pws, ld_ws, pwt, f, L, N,
                                        1 if gated else 0, ACT[act], pb, p0, p1, cap, pr, ld_res, po, ldo, ELEM[odt],
                                        pst, _stream()), "moe_expert_matmul_fp4")
