@@ -637,13 +637,20 @@ __global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
                   for (int w = 0; w < 4; ++w) tmem_copy_scales(sfb + 8 * w + 4, sm + (4096 >> 4) + w * (512 >> 4));
                 }
               }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              auto product = [&](int k) {
                 const int w = KIND == kFp4Nv ? k : 2 * j + k / 2;
                 const uint32_t sf = KIND == kFp4Nv ? 0 : 2 * (k & 1);
-                if (k == 0 || k * 32 < left_red)
-                  mma_e2m1<KIND == kFp4Mx>(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc | (sf << 4) | (sf << 29),
-                                           sfa + 4 * w, sfb + 8 * w, k > 0 ? 1u : acc);
+                mma_e2m1<KIND == kFp4Mx>(d, lo + 2 * k, lo + (kABytes >> 4) + 2 * k, idesc | (sf << 4) | (sf << 29),
+                                         sfa + 4 * w, sfb + 8 * w, k > 0 ? 1u : acc);
+              };
+              product(0);
+              if (left_red > 96) {
+                product(1);
+                product(2);
+                product(3);
+              } else {
+                if (left_red > 32) product(1);
+                if (left_red > 64) product(2);
               }
               mma_commit_pair(empty, mask);
               if (j == kPerBuf - 1 || kb + j + 1 >= nkb) mma_commit_pair(sempty0 + 8 * buf, mask);
@@ -871,6 +878,9 @@ __global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
     // of the word's 512 bytes; the copies left row r's four words at byte 16 r (gated: the
     // tile's runs of 16 gate rows one after the other, and the up rows 1024 bytes on).
     // Lane l transposes the 4 x 4 words of rows l, 32 + l, 64 + l and 96 + l.
+    // A buffer always goes to the same warp: one that had not waited for its last phase
+    // could take that for the next.
+    static_assert(!FP4 || kBufs % kTransposers == 0, "a buffer's phases are waited for in order");
     // The pieces go round the warps: from a landed copy to the arrival takes one of them
     // about as long as two blocks' products.
     const int turn = warp == 3 ? 0 : warp - 8;
@@ -903,6 +913,7 @@ __global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
             at[b * 128 + 96] = make_uint4(r[b][0].w, r[b][1].w, r[b][2].w, r[b][3].w);
           }
         fence_proxy_async_smem();
+        __syncwarp();  // every lane's words before the arrival
         // The columns are free when the products of the piece before the last are done (before
         // there was any, a buffer's first phase passes at once). Those of the blocks that had
         // these blocks' stages are done then as well (there are at least four stages), so the
