@@ -600,12 +600,13 @@ __global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
   } else if (FP4 && warp == 1) {
     // --------------------------------------------------------- products, e2m1
     // A block of 128 bytes is four products, as with the other types, but they take half
-    // the time (332 cycles for 176 rows), and copies of scales come on top: issuing them is
-    // the bound. The warp stays converged, so that operands stay in uniform registers (a
-    // thread alone moves each there first), and waits once a block: 4096 tokens x top-8 of
-    // 64 experts, 7168 x 4096, scales per 16: 478 us with a thread alone and three waits, 430
-    // converged, 369 with one wait and three copies a piece of scales; 394 us even without
-    // any load, copy or layout of scales in the first form.
+    // the time (332 cycles for 176 rows), and copies of scales come on top. The warp stays
+    // converged, so that operands stay in uniform registers (a thread alone moves each there
+    // first), and waits once a block: 4096 tokens x top-8 of 64 experts, 7168 x 4096, scales
+    // per 16: 478 us with a thread alone and three waits, 430 converged, 371 with one wait and
+    // three copies a piece of scales, the tensor cores 58% active. Without loads of rows and
+    // weights it would take 345, without copies of scales 365; a warp of its own for the
+    // copies took 386 (scales per 32: 332 -> 324).
     if (uniform(rank) == 0) {
       const uint32_t lead = elect_one(), tm = uniform(tmem), lo_step = uniform(stage_bytes >> 4);
       const int nstages = (int)uniform(stages);
