@@ -486,3 +486,41 @@ def test_captured_chain(dev):
         graph.replay()
         got = out.clone()
         assert torch.equal(got, step()[0]) and dev.moe_status_sync(st) == dev.MOE_OK and torch.isfinite(got).all()
+
+
+def far_rows(R, W, dtype):
+    """Zeros of R rows of W elements whose starts are more than 2^31 elements apart (memory of them is needed all the same)."""
+    ld = 2 ** 31 + 64
+    return torch.zeros((R - 1) * ld + W, dtype=dtype, device=DEV).as_strided((R, W), (ld, 1))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_far_apart(dev, fmt):
+    """Offsets that 32 bits do not hold: of rows, of outputs and of residual rows, and of pieces of scales."""
+    R, K, N = 3, 1024, 48
+    near = rand(1, R, K, dtype=torch.bfloat16)
+    x = far_rows(R, K, torch.bfloat16)
+    x.copy_(near)
+    q, sc, val = quantise(near, fmt)
+    o = dev.quant_fp4(x, fmt=fmt)
+    assert torch.equal(o["scales"], sc) and same_codes(o["xq"], q)
+    ids = i32([[0, 1], [1, 0], [1, 1]])
+    d = dev.dispatch_fp4(x, ids, torch.ones(R, 2, device=DEV), 2, 2, block_e=1, fmt=fmt)
+    rows = d["src2dst"].long()
+    assert all(same_codes(d["xq"][rows[:, k]], o["xq"]) for k in range(2))
+    x.zero_()
+    assert dev.dequant_fp4(o["xq"], o["scales"], fmt=fmt, out=x) is x
+    assert torch.equal(x, val.float().to(torch.bfloat16))
+    w, wsc, wts, wv = weights(dev, 2, 1, N, K, fmt)
+    del x
+    ld = 2 ** 27 + 8  # of scales: with two pieces or more, the second is 2^31 bytes on
+    far = torch.zeros(pieces(K, fmt), ld, 16, dtype=torch.uint8, device=DEV)
+    far[:, :R] = sc
+    res, out = far_rows(R, N, torch.bfloat16), far_rows(R, N, torch.bfloat16)
+    res.copy_(rand(4, R, N, dtype=torch.bfloat16))
+    wide = far_rows(R, K // 2, torch.uint8)
+    wide.copy_(o["xq"])
+    for n in (R, 2):  # (two rows take no tensor cores)
+        out.fill_(9)
+        dev.expert_matmul_fp4(wide[:n], w, far, wsc, fmt=fmt, w_tscale=wts, residual=res[:n], out=out[:n])
+        check(out, val, wv, None, res, [(0, n)], N, "none", False)

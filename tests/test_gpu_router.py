@@ -383,6 +383,21 @@ def test_many_tokens(dev):
     assert ((g.double() - leaf.grad).abs() <= 4 * rel(l) * mag + 2.0 ** -48 * mag.sum(1, keepdim=True) + 2.0 ** -8 * leaf.grad.abs()).all()
 
 
+def test_rows_far_apart(dev):
+    """Rows of logits and of the gradient more than 2^31 elements apart."""
+    T, E, K, ld = 3, 40, 4, 2 ** 31 + 5
+    near = rand(1, T, E + 5, dtype=torch.bfloat16)[:, :E]  # (odd strides both: the same lanes read the same elements)
+    l = torch.zeros((T - 1) * ld + E, dtype=torch.bfloat16, device=DEV).as_strided((T, E), (ld, 1))
+    l.copy_(near)
+    a, b = dev.route(l, K), dev.route(near, K)
+    assert torch.equal(a["topk_ids"], b["topk_ids"]) and torch.equal(a["topk_weights"], b["topk_weights"])
+    a, b = dev.balance_loss(l, b["topk_ids"]), dev.balance_loss(near, b["topk_ids"])
+    assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["prob_sums"], b["prob_sums"])
+    ids, dw, dl = dev.route(near, K)["topk_ids"], rand(2, T, K), torch.ones(2, device=DEV)
+    g = [dev.route_grad(t, ids, dweights=dw, dloss=dl, counts=b["counts"]) for t in (l, near)]
+    assert torch.equal(*g)
+
+
 def test_captured_and_replayed(dev):
     """The router's calls in one graph, replayed with other logits, groups and live counts."""
     T, E, K, Q = 256, 64, 4, 3
