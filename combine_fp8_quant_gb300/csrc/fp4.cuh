@@ -120,7 +120,9 @@ struct Chunk {
 // its remainder (Markstein 1990, correct rounding of a division by fused
 // multiply-adds), two elements an instruction. That holds while d, 1/d and the
 // quotients are far from the ends of the range; otherwise the elements are divided one
-// by one.
+// by one. The quotients are formed with the other sign, which the codes then lose: a zero's
+// remainder is +0, and fma(+0, 1/d, -0) would be +0 for an element of -0, where fma(+0, -1/d, +0)
+// is the +0 that becomes -0.
 template <int TYPE, int FMT>
 __device__ __forceinline__ uint2 fp4_quant(const Chunk<TYPE>& x, float ts, float ts6, uint32_t& byte) {
   uint32_t am = x.amax();
@@ -128,28 +130,30 @@ __device__ __forceinline__ uint2 fp4_quant(const Chunk<TYPE>& x, float ts, float
   const bool finite = am < 0x7F800000u;
   float f[16];
   x.floats(f);
+  uint32_t flip = 0;  // signs of eight codes
   if constexpr (FMT == kFp4NV) {
+    flip = 0x88888888u;
     byte = cvt_e4m3x2(__fdiv_rn(__uint_as_float(am), ts6), 0.0f) & 0xFF;
     const float d = fp4_scale<kFp4NV>(byte, ts);
     if (!finite) byte = 0x7F;
     const bool some = finite && d > 0.0f;
     if (some && !(d > 0x1p-100f && d < 0x1p100f && __uint_as_float(am) < 0x1p20f * d)) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = __fdiv_rn(f[i], d);
+      for (int i = 0; i < 16; ++i) f[i] = __fdiv_rn(f[i], -d);
     } else {
       const float y = some ? __frcp_rn(d) : 0.0f;
-      const f32x2 y2 = pair(y, y), nd = pair(-d, -d);
+      const f32x2 ny = pair(-y, -y), dd = pair(d, d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const f32x2 v = pair(f[2 * i], f[2 * i + 1]), q = mul2(v, y2);
-        const float2 r = halves(fma2(fma2(q, nd, v), y2, q));
+        const f32x2 v = pair(f[2 * i], f[2 * i + 1]), q = mul2(v, ny);
+        const float2 r = halves(fma2(fma2(q, dd, v), ny, q));
         f[2 * i] = r.x;
         f[2 * i + 1] = r.y;
       }
     }
     if (!some) {  // nothing that a scale reaches, or no numbers
 #pragma unroll
-      for (int i = 0; i < 16; ++i) f[i] = 0.0f;
+      for (int i = 0; i < 16; ++i) f[i] = -0.0f;
     }
   } else {
     // amax = 1.m * 2^E, 6 = 1.5 * 2^2
@@ -166,7 +170,7 @@ __device__ __forceinline__ uint2 fp4_quant(const Chunk<TYPE>& x, float ts, float
     lo[i] = f[i];
     hi[i] = f[8 + i];
   }
-  return make_uint2(cvt_e2m1x8(lo), cvt_e2m1x8(hi));
+  return make_uint2(cvt_e2m1x8(lo) ^ flip, cvt_e2m1x8(hi) ^ flip);
 }
 
 // The bytes of four groups as a word, in the first lane of the 4 (nv) or 8 lanes that

@@ -522,9 +522,10 @@ moe_status_t moe_block_norm_grad(
  *                 (zero gives -127); elements above 6 saturate
  *   MOE_FP4_NV    groups of 16, UE4M3 scale s = RNE_e4m3(fl32(amax / fl32(6 * ts))), at
  *                 most 448, ts the float32 scale of the tensor (1 where there is none);
- *                 with d = fl32(s * ts), q = RNE(fl32(x / d)), saturating; 0 where s is 0
- * A value is its element times 2^(b - 127), or times d. A group that holds a NaN or an
- * infinity gets the scale NaN (0xFF, 0x7F) and elements 0: it is read as NaN.
+ *                 with d = fl32(s * ts), q = RNE(fl32(x / d)), saturating; +0 where d is 0
+ * An element that is zero or rounds to it keeps its sign (-0 is code 8). A value is its
+ * element times 2^(b - 127), or times d. A group that holds a NaN or an infinity gets the
+ * scale NaN (0xFF, 0x7F) and elements +0: it is read as NaN.
  * Scales [pieces, ld, 16] bytes: the 16 bytes at (c * ld + r) * 16 are the scales of
  * groups 16 c .. 16 c + 15 of row r (0 past the last group); pieces = ceil(groups / 16).
  * Row lengths are multiples of 64. A good ts of a tensor is amax / (6 * 448).

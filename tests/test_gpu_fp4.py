@@ -7,6 +7,7 @@ of K products is off by (K + 2) v times the sum of magnitudes and the tensor sca
 2 v; activations and the rounding to 16 bits as for the products of wider types."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -524,3 +525,76 @@ def test_rows_far_apart(dev, fmt):
         out.fill_(9)
         dev.expert_matmul_fp4(wide[:n], w, far, wsc, fmt=fmt, w_tscale=wts, residual=res[:n], out=out[:n])
         check(out, val, wv, None, res, [(0, n)], N, "none", False)
+
+
+# ---------------------------------------------------------------------------
+# Signs of zeros, and tensors of zeros
+# ---------------------------------------------------------------------------
+
+def codes_by_search(x, fmt, ts):
+    """The four-bit elements (sign and magnitude, one a byte) and the scale bytes of float32 rows, by the
+    definition: the nearest of all values, the even code among two as near, on the host. ts [R]."""
+    values = np.array([m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10) for e in range(16) for m in range(8)][:127])
+
+    def nearest_of(v, table):
+        off = np.abs(table - np.minimum(v, table[-1])[..., None].astype(np.float64))
+        best = off == off.min(-1, keepdims=True)
+        even = best & (np.arange(len(table)) % 2 == 0)
+        return np.where(even.any(-1), even.argmax(-1), best.argmax(-1))
+
+    R, H = x.shape
+    g = group(fmt)
+    v = x.reshape(R, H // g, g)
+    bad = ~np.isfinite(v).all(2)
+    amax = np.abs(np.where(bad[:, :, None], np.float32(0), v)).max(2)
+    with np.errstate(all="ignore"):
+        if fmt == "nv":
+            t = np.float32(ts)[:, None]
+            byte = nearest_of(np.where(amax > 0, amax / (np.float32(6) * t), np.float32(0)), values)
+            d = np.float32(values[byte]) * t
+            q = np.where(d[:, :, None] > 0, v / d[:, :, None], np.float32(0))
+        else:
+            e = np.frexp(np.float64(amax))[1] - 3
+            if fmt == "e8m0":
+                e = e + (6 * np.ldexp(1.0, e) < amax)
+            e = np.clip(np.where(amax > 0, e, -127), -127, 127)
+            byte, d = e + 127, np.ldexp(1.0, e)
+            q = np.float64(v) / d[:, :, None]
+        code = nearest_of(np.where(bad[:, :, None], 0, np.abs(q)), np.array(CODES))
+    code = code | np.where((d[:, :, None] > 0) & np.signbit(v), 8, 0)
+    code = np.where(bad[:, :, None], 0, code)
+    return code.reshape(R, H).astype(np.uint8), np.where(bad, 0x7F if fmt == "nv" else 0xFF, byte).astype(np.uint8)
+
+
+def elements(xq):
+    """Packed pairs, one element a byte."""
+    return torch.stack([xq & 15, xq >> 4], -1).flatten(-2)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(DT.values()), ids=list(DT))
+def test_codes_to_the_sign_of_zeros(dev, dtype, fmt):
+    """Every bit of every element and scale, zeros of both signs and values that round to them included,
+    alone and dispatched."""
+    R, H = 48, 192
+    x = rand(7, R, H)
+    x[:, 3::7], x[:, 5::11] = -0.0, 0.0
+    x[4:8] = -x[4:8].abs() * 10.0 ** -torch.arange(H, device=DEV).remainder(9).float()   # down to where a group's scale makes them zeros
+    x[8, :64], x[9] = -0.0, -0.0
+    x[10] = torch.where(rand(8, H) < 0, -6.0, 0.25)                    # ties between zero and the first code
+    x[11, 40], x[12, 70], x[13] = math.nan, -math.inf, x[13] * 1e-38   # (subnormal numbers in float32)
+    x[14, ::16], x[14, 1::16] = 3.0, -1e-30
+    x = x.to(dtype)
+    for ts in ([None] if fmt != "nv" else [None, 0.0137, 2.0 ** -100, 2.0 ** -130, 1.1e30, 2.0 ** 110]):
+        t = None if ts is None else torch.full((1,), ts, device=DEV)
+        code, byte = codes_by_search(x.float().cpu().numpy(), fmt, np.full(R, 1.0 if ts is None else ts, np.float32))
+        o = dev.quant_fp4(x, fmt=fmt, tensor_scale=t)
+        assert np.array_equal(o["scales"].transpose(0, 1).reshape(R, -1)[:, :H // group(fmt)].cpu().numpy(), byte)
+        assert np.array_equal(elements(o["xq"]).cpu().numpy(), code)
+        for n in (R, 700):  # both forms of the dispatch
+            y = x.repeat(-(-n // R), 1)[:n].contiguous()
+            ids = torch.arange(n * 4, device=DEV, dtype=torch.int32).view(n, 4) % 5
+            d = dev.dispatch_fp4(y, ids, torch.ones(n, 4, device=DEV), 5, 5, block_e=1, fmt=fmt, tensor_scale=t)
+            rows = d["src2dst"].long()
+            for k in (0, 3):
+                assert np.array_equal(elements(d["xq"][rows[:, k]]).cpu().numpy(), code[np.arange(n) % R])
