@@ -133,7 +133,8 @@ __device__ __forceinline__ uint2 fp4_quant(const Chunk<TYPE>& x, float ts, float
   uint32_t flip = 0;  // signs of eight codes
   if constexpr (FMT == kFp4NV) {
     flip = 0x88888888u;
-    byte = cvt_e4m3x2(__fdiv_rn(__uint_as_float(am), ts6), 0.0f) & 0xFF;
+    // (a group of zeros has scale 0 whatever the tensor's: that of a tensor of zeros is 0, too)
+    byte = am == 0 ? 0u : cvt_e4m3x2(__fdiv_rn(__uint_as_float(am), ts6), 0.0f) & 0xFF;
     const float d = fp4_scale<kFp4NV>(byte, ts);
     if (!finite) byte = 0x7F;
     const bool some = finite && d > 0.0f;

@@ -1005,7 +1005,7 @@ def quant_fp4(x, fmt="nv", tensor_scale=None, num_live=None, m_indices=None, mas
     """Rows to four bits (e2m1): x [R, H] (slabs [L, cap, H] with masked_m) in bfloat16,
     float16 or float32, H a multiple of 64. fmt "nv": a float8 scale for each 16
     elements and tensor_scale, float32 [1] or one for each of n equal blocks of rows
-    (amax / 2688 is a good one); "e8m0" and "mx": a power of two for each 32, the
+    (amax / 2688 is a good one, 0 for zeros); "e8m0" and "mx": a power of two for each 32, the
     smallest that saturates nothing, or OCP MX's. Only the first num_live rows, those
     with m_indices >= 0 as a dispatch writes it, or the first masked_m of each slab,
     where one is given. Returns a dict: xq uint8 [.., H / 2], scales uint8

@@ -521,7 +521,8 @@ moe_status_t moe_block_norm_grad(
  *   MOE_FP4_MX    groups of 32, the OCP MX rule e = floor(log2(amax)) - 2, at least -127
  *                 (zero gives -127); elements above 6 saturate
  *   MOE_FP4_NV    groups of 16, UE4M3 scale s = RNE_e4m3(fl32(amax / fl32(6 * ts))), at
- *                 most 448, ts the float32 scale of the tensor (1 where there is none);
+ *                 most 448, ts the float32 scale of the tensor (1 where there is none),
+ *                 s = 0 for a group of zeros;
  *                 with d = fl32(s * ts), q = RNE(fl32(x / d)), saturating; +0 where d is 0
  * An element that is zero or rounds to it keeps its sign (-0 is code 8). A value is its
  * element times 2^(b - 127), or times d. A group that holds a NaN or an infinity gets the
@@ -551,7 +552,8 @@ size_t moe_fp4_scale_bytes(int64_t ld, int32_t H, moe_fp4_t fmt);
  *   x [R, ldx]                   BF16, F16 or F32, rows 16-byte aligned
  *   tensor_scale [n_scales] f32  (optional, NV only) row r has tensor_scale[r / (R / n_scales)]:
  *                                one for all rows, or one for each expert's weight rows.
- *                                Positive and finite
+ *                                Positive and finite, or 0 (which amax / (6 * 448) of a
+ *                                tensor of zeros is): then every value is 0
  *   xq [R, H / 2], scales        dense rows; ld_s >= R; both 16-byte aligned
  * R < 2^31. Launches: 1.
  */

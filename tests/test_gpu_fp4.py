@@ -598,3 +598,38 @@ def test_codes_to_the_sign_of_zeros(dev, dtype, fmt):
             rows = d["src2dst"].long()
             for k in (0, 3):
                 assert np.array_equal(elements(d["xq"][rows[:, k]]).cpu().numpy(), code[np.arange(n) % R])
+
+
+@pytest.mark.parametrize("dtype", list(DT.values()), ids=list(DT))
+def test_tensor_of_zeros(dev, dtype):
+    """amax / 2688 of a tensor of zeros is 0: scales, elements and values are zeros, and so are products."""
+    L, N, K, R = 3, 16, 192, 5
+    w = rand(1, L, N, K)
+    w[1] = 0.0
+    w[1, :, ::3] = -0.0
+    w = w.to(dtype)
+    ts = (w.abs().amax((1, 2)).float() / 2688).contiguous()
+    assert ts[1] == 0
+    o = dev.quant_fp4(w.view(L * N, K), tensor_scale=ts)
+    q, sc, val = quantise(w.view(L * N, K), "nv", torch.where(ts > 0, ts, 1.0).repeat_interleave(N))
+    assert torch.equal(o["scales"], sc) and same_codes(o["xq"], q) and (o["scales"][:, N:2 * N] == 0).all()
+    assert torch.equal(dev.dequant_fp4(o["xq"], o["scales"], tensor_scale=ts, dtype=torch.float32), val.float())
+    bias = rand(2, L, N)
+    xr = rand(3, L * R, K)
+    x = dev.quant_fp4(xr)
+    seg = [(e * R, e * R + R) for e in range(L)]
+    out = dev.expert_matmul_fp4(x["xq"], o["xq"].view(L, N, K // 2), x["scales"], o["scales"], starts=i32([a for a, _ in seg]), w_tscale=ts,
+                                psum=i32([b for _, b in seg]), bias=bias)
+    check(out, quantise(xr, "nv")[2], val.view(L, N, K), bias, None, seg, N, "none", False)
+    assert torch.equal(out[R:2 * R], bias[1].bfloat16().expand(R, N))
+    one = dev.expert_matmul_fp4(x["xq"][:2], o["xq"].view(L, N, K // 2)[1], x["scales"], o["scales"][:, N:2 * N].contiguous(),
+                                w_tscale=ts[1:2], bias=bias[1])
+    assert torch.equal(one, bias[1].bfloat16().expand(2, N))
+    zero = torch.zeros(1, device=DEV)  # the rows too, alone and dispatched
+    rows = torch.zeros(700, K, dtype=dtype, device=DEV)
+    rows[:, ::2] = -0.0
+    z = dev.quant_fp4(rows, tensor_scale=zero)
+    assert (z["scales"] == 0).all() and (z["xq"] == 0).all()
+    for n in (40, 700):
+        d = dev.dispatch_fp4(rows[:n], i32([[0, 1, 2, 3]]).repeat(n, 1), torch.ones(n, 4, device=DEV), 4, 4, block_e=1, tensor_scale=zero)
+        assert (d["scales"] == 0).all() and (d["xq"] == 0).all()
