@@ -525,6 +525,16 @@ __device__ __forceinline__ BalanceWs balance_ws(const BalanceArgs& a) {
   return w;
 }
 
+// Square of the logsumexp of a row whose largest logit but for NaN is infinite (warp_max leaves
+// NaN out): NaN with one, 0 where all are -inf (such a token has no part in the loss).
+template <int N>
+__device__ __forceinline__ float odd_row(const float (&l)[N], float m) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) bad |= isnan(l[i]);
+  return __any_sync(0xffffffffu, bad) ? __uint_as_float(0x7FC00000u) : m > 0.0f ? INFINITY : 0.0f;
+}
+
 // Sums over a run of tokens, one warp a token, four at a time. Joining the warps' sums
 // for a group costs a CTA about as much as kGroupCost tokens, so a run of short groups
 // counts for more. Bound by latencies: a batch of 65536 tokens leaves a warp about a
@@ -598,8 +608,8 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
         for (int i = 0; i < N; ++i) m = fmaxf(m, l[u][i]);
         m = warp_max(m);
         float p[N], zs = 0.0f;
-        const bool apart = a.sigmoid && m != kNegInf;  // (the z loss is of the softmax's sum)
-        if (m != kNegInf) {
+        const bool odd = !(fabsf(m) < INFINITY);
+        if (!odd) {
 #pragma unroll
           for (int i = 0; i < N; ++i) {
             p[i] = fast_exp(l[u][i] - m);
@@ -611,8 +621,10 @@ __global__ void __launch_bounds__(kThreads) balance_parts_kernel(BalanceArgs a) 
           const float r = fast_rcp(zs);
 #pragma unroll
           for (int i = 0; i < N; ++i) p[i] *= r;
+        } else {
+          z += odd_row(l[u], m);
         }
-        if (apart || m == kNegInf) scores<false>(l[u], m, a.sigmoid, p, p);
+        if (a.sigmoid || odd) scores<false>(l[u], m, a.sigmoid, p, p);  // (the z loss is of the softmax's sum)
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += p[i];
       }

@@ -661,8 +661,9 @@ size_t moe_balance_loss_workspace_bytes(int32_t E, int32_t Q);
  *                                rows between them. If one does not, MOE_STATUS_BAD_LAYOUT is
  *                                set and all count as empty. Both NULL: Q = 1, all live tokens
  *   Q (1..4096), loss [2] f32, counts [Q, E] int32, prob_sums [Q, E] f32   written in full
- * A token whose logits are all -infinity has p = 0 and no part in loss[1]'s sum. Sums are
- * in fp32 and in a fixed order (deterministic). Launches: 2.
+ * A token whose logits are all -infinity has p = 0 and no part in loss[1]'s sum; one with a
+ * NaN makes both losses NaN, one with +infinity loss[1] infinite (and, with SOFTMAX, loss[0]
+ * NaN). Sums are in fp32 and in a fixed order (deterministic). Launches: 2.
  */
 moe_status_t moe_balance_loss(
     const void* logits, int64_t ldl, moe_elem_t type, int32_t T, const int32_t* d_num_tokens, int32_t E,

@@ -432,3 +432,27 @@ def test_captured_and_replayed(dev):
         assert torch.equal(got[0][:live], want[0][:live]) and torch.equal(got[1][:live], want[1][:live])
         assert all(torch.equal(x, y) for x, y in zip(got[2:], want[2:]))
         assert dev.moe_status_sync(st) == dev.MOE_OK
+
+
+# ---------------------------------------------------------------------------
+# Rows that are not numbers, and gradients where scores leave the range of a float
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [1, 33, 64, 256])
+@pytest.mark.parametrize("row,want", [("nan", math.nan), ("nan and -inf", math.nan), ("inf", math.inf), ("inf and nan", math.nan),
+                                      ("one nan", math.nan), ("-inf", None)])
+def test_z_loss_of_rows_that_are_not_numbers(dev, row, want, E, kind):
+    """The z loss holds what logsumexp of such a row is; a row of -inf alone has no part in it."""
+    T, K = 40, 1
+    l = rand(1, T, E)
+    l[11] = {"nan": math.nan, "nan and -inf": -math.inf, "inf": math.inf, "inf and nan": math.inf, "one nan": 0.0, "-inf": -math.inf}[row]
+    if row in ("nan and -inf", "inf and nan", "one nan"):
+        l[11, E // 2] = math.nan
+    ids = torch.zeros(T, K, dtype=torch.int32, device=DEV)
+    got = float(dev.balance_loss(l, ids, score=kind)["loss"][1])
+    if want is None:
+        z = float((torch.logsumexp(torch.cat([l[:11], l[12:]]).double(), 1) ** 2).sum() / T)
+        assert abs(got - z) <= 1e-4 * z  # (the rows' own error; what is tested is which rows count)
+    else:
+        assert got == want or (math.isnan(got) and math.isnan(want))
