@@ -1035,7 +1035,8 @@ def dequant_fp4(xq, scales, fmt="nv", tensor_scale=None, dtype=torch.bfloat16, n
                 masked_m=None, status=None, out=None):
     """The values of four-bit rows xq [R, H / 2] (slabs [L, cap, H / 2] with masked_m) with
     their scales, in dtype or into `out`; rows as for quant_fp4, others are not
-    written."""
+    written. status: the int32 word that a num_live above R is flagged in (quant_fp4's,
+    say)."""
     f = _fp4(fmt)
     if xq.dtype not in FP4_BYTES:
         raise ValueError(f"moeperm: xq must be uint8 pairs of elements, not {xq.dtype}")
@@ -1053,8 +1054,7 @@ def dequant_fp4(xq, scales, fmt="nv", tensor_scale=None, dtype=torch.bfloat16, n
     dtype = _elem(out, FLOATS, "out")
     o2 = out.view(R, H) if out.dim() == 3 else out
     ldx = _rows(o2, "out")
-    st = _status(status, num_live is not None, xq.device)
-    pq, ps, pt, pn, pi, pm, po, pst = _on_current(xq, scales, tensor_scale, num_live, m_indices, masked_m, o2, st)
+    pq, ps, pt, pn, pi, pm, po, pst = _on_current(xq, scales, tensor_scale, num_live, m_indices, masked_m, o2, status)
     _check(lib().moe_dequant_fp4(pq, ps, ld, R, H, f, pt, nts, pn, pi, pm, cap, po, ldx, ELEM[dtype], pst, _stream()),
            "moe_dequant_fp4")
     return out
@@ -1239,7 +1239,8 @@ def route_grad(logits, topk_ids, dweights=None, dloss=None, counts=None, seq_beg
     """Gradient of the logits through the weights of route (dweights [T, K]) and through
     both losses of balance_loss (dloss [2], with its counts and groups), in logits'
     type; 0 for tokens that are not live. score, renorm and scale as in the forward
-    calls."""
+    calls. status: the int32 word that groups out of order and a num_tokens above T
+    are flagged in (balance_loss's, which meets the same)."""
     T, E, ldl, code = _logits(logits)
     K, Q, dev = topk_ids.shape[1], _groups(seq_begin, seq_end), logits.device
     _vec(topk_ids, T * K, "topk_ids", torch.int32)

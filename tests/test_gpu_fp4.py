@@ -633,3 +633,15 @@ def test_tensor_of_zeros(dev, dtype):
     for n in (40, 700):
         d = dev.dispatch_fp4(rows[:n], i32([[0, 1, 2, 3]]).repeat(n, 1), torch.ones(n, 4, device=DEV), 4, 4, block_e=1, tensor_scale=zero)
         assert (d["scales"] == 0).all() and (d["xq"] == 0).all()
+
+
+def test_status_of_the_values_of_rows(dev):
+    """A live count that is too large is flagged in the caller's status word; where there is none the call makes none."""
+    R, H = 20, 128
+    o = dev.quant_fp4(rand(1, R, H))
+    st, n, out = i32([0]), i32([R + 1]), torch.empty(R, H, dtype=torch.bfloat16, device=DEV)
+    dev.dequant_fp4(o["xq"], o["scales"], num_live=n, status=st, out=out)
+    assert dev.moe_status_sync(st) == dev.MOE_ERR_LIVE_OVERFLOW
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    assert dev.dequant_fp4(o["xq"], o["scales"], num_live=n, out=out) is out
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
