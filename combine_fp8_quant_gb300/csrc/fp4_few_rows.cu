@@ -1,4 +1,5 @@
-// fp4_few_rows.cu -- the four-bit product for one or two rows of one dense matrix, the
+// fp4_few_rows.cu -- the four-bit product for one or two rows of one dense matrix of
+// moderate size, the
 // step of a single token.
 //
 //   P[r, f] = sum over groups g of s_w[f, g] * sum_{k in g} x[r, k] * w[f, k]
@@ -180,17 +181,27 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(FewArgs p) {
   }
 }
 
-// Rows up to which this is chosen. One pass after another, against the tensor cores':
-// 2048 -> 7168, scales per 16 (per 32): 1 row 7.2 (7.3) against 11.8 (10.8) us, 2 rows 8.3
-// (7.9) against 11.9 (10.7), 4 rows 10.1 (10.0) against 10.4 (9.0); 7168 -> 4096: 1 row 9.3
-// (9.4) against 14.4 (11.9), 2 rows 12.0 (11.5) against 14.4 (11.9), 4 rows 16.6 against 12.0.
-constexpr int kMostRows = 2;
+// A warp's step takes two weight rows 32 elements a lane: the time is that of the launch and of
+// x, which grows with K, and about 0.24 us for each 1024 steps of all weight rows (two rows of
+// x: 0.3). The tensor cores take 9 us and then the weights' time from HBM. Measured, matrices in
+// turn so that they come from HBM, here against there in us (scales per 16; those per 32 lie
+// within 0.8):
+//   one row    2048 -> 7168 4.9 / 9.3, 4096 -> 8192 10.3 / 11.5, 7168 -> 4096 11.0 / 12.2, 8192 -> 4096
+//              12.3 / 12.3; beyond: 4096 -> 10240 12.1 / 11.7, 7168 -> 6144 13.6 / 13.0, 10240 -> 2048
+//              11.8 / 11.5, 24576 -> 512 19.2 / 14.4, 8192 -> 28672 41 / 30, 64 -> 262144 55 / 19
+//   two rows   2048 -> 7168 6.0 / 9.2, 2048 -> 12288 9.7 / 10.0, 6144 -> 4096 11.6 / 11.3, 8192 -> 2048
+//              10.8 / 10.8; beyond: 2048 -> 14336 10.7 / 10.2, 7168 -> 4096 13.0 / 12.3, 10240 -> 1024
+//              12.9 / 11.2
+constexpr int kMostRows = 2, kMostLength = 8192;
+constexpr int64_t kMostSteps[kMostRows + 1] = {0, 32768, 24576};  // weight rows times steps of 1024 elements
 size_t smem_bytes(int K, int rows) { return (size_t)rows * ((K / 32 + 31) / 32) * 4 * 32 * 16; }
+static_assert(kMostRows * kMostLength * 2 <= 46 * 1024, "x fits the shared memory that needs no opt-in");
 
 }  // namespace
 
 bool few_rows_fp4(const MatmulArgs& a) {
-  return a.seg_end == nullptr && a.R <= kMostRows && smem_bytes(a.K, (int)a.R) <= 96 * 1024;
+  if (a.seg_end != nullptr || a.R > kMostRows || a.K > kMostLength) return false;
+  return (a.gated ? 2 : 1) * (int64_t)a.N * ((a.K + 1023) / 1024) <= kMostSteps[a.R];
 }
 
 cudaError_t launch_matmul_few_rows(const MatmulArgs& m, int num_sms, cudaStream_t s) {
@@ -202,10 +213,8 @@ cudaError_t launch_matmul_few_rows(const MatmulArgs& m, int num_sms, cudaStream_
   a.bias = m.bias; a.residual = m.residual; a.ld_res = m.ld_res; a.out = m.out; a.ldo = m.ldo;
   auto go = [&](auto kernel, int rows) -> cudaError_t {
     const size_t smem = smem_bytes(m.K, rows);
-    cudaError_t err = opt_in_smem(kernel, smem);
-    if (err != cudaSuccess) return err;
     int per_sm = 0;
-    err = occupancy(kernel, kThreads, smem, &per_sm);
+    cudaError_t err = occupancy(kernel, kThreads, smem, &per_sm);
     if (err != cudaSuccess) return err;
     const int64_t units = m.gated ? m.N : m.N / 2, need = (units + kWarps - 1) / kWarps;
     const int64_t most = (int64_t)num_sms * (per_sm < 1 ? 1 : per_sm);

@@ -645,3 +645,19 @@ def test_status_of_the_values_of_rows(dev):
     before = torch.cuda.memory_stats()["allocation.all.allocated"]
     assert dev.dequant_fp4(o["xq"], o["scales"], num_live=n, out=out) is out
     assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("R,K,N,gated", [(1, 4096, 10240, False), (1, 10240, 2048, False), (2, 2048, 14336, False), (2, 7168, 2048, True),
+                                         (1, 64, 40000, False), (2, 512, 32768, False), (1, 24576, 64, False)])
+def test_few_rows_of_large_matrices(dev, R, K, N, gated, fmt):
+    """Where the tensor cores are faster one or two rows take them too: the same sums, to the last bits that
+    a residual of the rounded output leaves, as of the same rows given as a segment."""
+    Nw = 2 * N if gated else N
+    # (magnitudes from group to group so far apart that sums in 24 bits depend on their order)
+    far = lambda seed, n: rand(seed, n, K) * torch.exp2(rand(seed + 9, n, K // 32, gain=3.0)).repeat_interleave(32, 1)
+    q, w = dev.quant_fp4(far(R, R), fmt=fmt), dev.quant_fp4(far(2, Nw) * K ** -0.5, fmt=fmt)
+    call = lambda **o: dev.expert_matmul_fp4(q["xq"], w["xq"], q["scales"], w["scales"], fmt=fmt, gated=gated, act="silu" if gated else "none",
+                                             out_dtype=torch.float16, **o)
+    less = -call()
+    assert torch.equal(call(residual=less), call(residual=less, starts=i32([0]), psum=i32([R])))
