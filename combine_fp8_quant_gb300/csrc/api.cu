@@ -11,6 +11,7 @@
 #include "api_util.h"
 #include "common.cuh"
 #include "kernels.h"
+#include "launch_cache.h"
 
 // Host-side caches of launch queries. An occupancy query or a device
 // attribute read costs the host about as much as a launch, and a
@@ -18,16 +19,14 @@
 // attributes are properties of the device; the shared-memory opt-in is a
 // function attribute of the CUDA context, so it is cached per context (a
 // context created again after cudaDeviceReset has a new id and opts in
-// afresh). The tables are small and fixed: once one is full, new keys are
-// simply asked every time.
+// afresh). The tables are small and fixed: answers of queries displace older
+// ones (launch_cache.h); once one of the others is full, new keys are simply
+// asked every time.
 namespace moeperm {
 namespace {
 std::mutex g_cache_mu;
-struct OccEntry { const void* kernel; int threads; size_t smem; int dev; int value; };
-OccEntry g_occ[256];
-int g_nocc = 0;
-OccEntry g_cl[32];  // resident clusters; `threads` holds the CTAs per cluster
-int g_ncl = 0;
+QueryCache<256> g_occ;
+QueryCache<16> g_cl;  // resident clusters; `threads` holds the CTAs per cluster
 struct SmemEntry { const void* kernel; unsigned long long ctx; size_t dyn; };
 SmemEntry g_smem[128];
 int g_nsmem = 0;
@@ -75,20 +74,15 @@ cudaError_t occupancy_cached(const void* kernel, int threads, size_t smem, int* 
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  const LaunchKey key{kernel, smem, threads, dev};
   {
     std::lock_guard<std::mutex> g(g_cache_mu);
-    for (int i = 0; i < g_nocc; ++i) {
-      const OccEntry& e = g_occ[i];
-      if (e.kernel == kernel && e.threads == threads && e.smem == smem && e.dev == dev) {
-        *per_sm = e.value;
-        return cudaSuccess;
-      }
-    }
+    if (g_occ.find(key, per_sm)) return cudaSuccess;
   }
   err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(per_sm, kernel, threads, smem);
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> g(g_cache_mu);
-  if (g_nocc < 256) g_occ[g_nocc++] = OccEntry{kernel, threads, smem, dev, *per_sm};
+  g_occ.keep(key, *per_sm);
   return cudaSuccess;
 }
 
@@ -96,20 +90,15 @@ cudaError_t max_clusters_cached(const void* kernel, const cudaLaunchConfig_t& cf
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
+  const LaunchKey key{kernel, cfg.dynamicSmemBytes, cl, dev};
   {
     std::lock_guard<std::mutex> g(g_cache_mu);
-    for (int i = 0; i < g_ncl; ++i) {
-      const OccEntry& e = g_cl[i];
-      if (e.kernel == kernel && e.threads == cl && e.smem == cfg.dynamicSmemBytes && e.dev == dev) {
-        *clusters = e.value;
-        return cudaSuccess;
-      }
-    }
+    if (g_cl.find(key, clusters)) return cudaSuccess;
   }
   err = cudaOccupancyMaxActiveClusters(clusters, kernel, &cfg);
   if (err != cudaSuccess) return err;
   std::lock_guard<std::mutex> g(g_cache_mu);
-  if (g_ncl < 32) g_cl[g_ncl++] = OccEntry{kernel, cl, cfg.dynamicSmemBytes, dev, *clusters};
+  g_cl.keep(key, *clusters);
   return cudaSuccess;
 }
 

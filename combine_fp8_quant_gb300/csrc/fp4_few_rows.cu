@@ -1,6 +1,5 @@
 // fp4_few_rows.cu -- the four-bit product for one or two rows of one dense matrix of
-// moderate size, the
-// step of a single token.
+// moderate size, the step of a single token.
 //
 //   P[r, f] = sum over groups g of s_w[f, g] * sum_{k in g} x[r, k] * w[f, k]
 //
