@@ -21,15 +21,13 @@
 // context created again after cudaDeviceReset has a new id and opts in
 // afresh). The tables are small and fixed: answers of queries displace older
 // ones (launch_cache.h); once one of the others is full, new keys are simply
-// asked every time.
+// asked, or set, every time.
 namespace moeperm {
 namespace {
 std::mutex g_cache_mu;
 QueryCache<256> g_occ;
 QueryCache<16> g_cl;  // resident clusters; `threads` holds the CTAs per cluster
-struct SmemEntry { const void* kernel; unsigned long long ctx; size_t dyn; };
-SmemEntry g_smem[128];
-int g_nsmem = 0;
+SmemOptIns<1024> g_smem;  // (a few hundred kernels)
 struct AttrEntry { int attr; int dev; int value; };
 AttrEntry g_attr[64];
 int g_nattr = 0;
@@ -104,27 +102,12 @@ cudaError_t max_clusters_cached(const void* kernel, const cudaLaunchConfig_t& cf
 
 cudaError_t opt_in_smem_cached(const void* kernel, size_t dyn) {
   unsigned long long ctx = 0;
-  // no context id (none current yet, or no driver entry point): set the
-  // attribute every time rather than trust a cache entry
-  const bool cacheable = current_context_id(&ctx) == cudaSuccess && ctx != 0;
-  if (cacheable) {
-    std::lock_guard<std::mutex> g(g_cache_mu);
-    for (int i = 0; i < g_nsmem; ++i)
-      if (g_smem[i].kernel == kernel && g_smem[i].ctx == ctx && g_smem[i].dyn >= dyn) return cudaSuccess;
-  }
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
-  if (err != cudaSuccess) return err;
-  if (!cacheable) return cudaSuccess;
-  err = current_context_id(&ctx);  // the call above may have created the context
-  if (err != cudaSuccess || ctx == 0) return cudaSuccess;
-  std::lock_guard<std::mutex> g(g_cache_mu);
-  for (int i = 0; i < g_nsmem; ++i)
-    if (g_smem[i].kernel == kernel && g_smem[i].ctx == ctx) {
-      if (g_smem[i].dyn < dyn) g_smem[i].dyn = dyn;
-      return cudaSuccess;
-    }
-  if (g_nsmem < 128) g_smem[g_nsmem++] = SmemEntry{kernel, ctx, dyn};
-  return cudaSuccess;
+  // no context id (none current yet, or no driver entry point): the attribute is set every
+  // time rather than a table trusted
+  if (current_context_id(&ctx) != cudaSuccess) ctx = 0;
+  return (cudaError_t)g_smem.raise(kernel, ctx, dyn, [&](size_t bytes) {
+    return (int)cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  });
 }
 
 cudaError_t device_attr_cached(cudaDeviceAttr attr, int* value) {

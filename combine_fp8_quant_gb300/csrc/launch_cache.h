@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace moeperm {
 
 struct LaunchKey {
@@ -50,6 +52,43 @@ class QueryCache {
     s.e[s.next] = {k, value};
     s.next = (s.next + 1) % 4;
     if (s.held < 4) ++s.held;
+  }
+};
+
+// How much dynamic shared memory each kernel may take in each context. It only ever rises: of
+// two threads whose launches need different sizes, neither may lower what the other has set
+// and is about to launch with, so a size is compared and set under one lock.
+template <int ENTRIES>
+class SmemOptIns {
+  struct Entry { const void* kernel; unsigned long long ctx; size_t dyn; };
+  std::mutex mu_;
+  Entry e_[ENTRIES] = {};
+  // The entry of a kernel in a context, or a free one; nullptr: none is free.
+  Entry* entry(const void* kernel, unsigned long long ctx) {
+    const uint64_t h = LaunchKey{kernel, (size_t)ctx, 0, 0}.hash();
+    for (uint64_t i = 0; i < ENTRIES; ++i) {
+      Entry& e = e_[(h + i) % ENTRIES];
+      if (e.kernel == nullptr || (e.kernel == kernel && e.ctx == ctx)) return &e;
+    }
+    return nullptr;
+  }
+
+ public:
+  // Calls set(bytes) unless as much was set for the kernel before in the context; bytes: the
+  // most that was ever asked for. ctx 0: the context is not known (none is current yet), so
+  // that every call sets it, and what was set so holds in a context that is known later.
+  // Returns what set returned, or 0.
+  template <typename SET>
+  int raise(const void* kernel, unsigned long long ctx, size_t dyn, SET set) {
+    std::lock_guard<std::mutex> lock(mu_);
+    Entry* e = entry(kernel, ctx);
+    if (e != nullptr && e->kernel != nullptr && ctx != 0 && e->dyn >= dyn) return 0;
+    const Entry* u = entry(kernel, 0);
+    if (e != nullptr && e->kernel != nullptr && e->dyn > dyn) dyn = e->dyn;
+    if (u != nullptr && u->kernel != nullptr && u->dyn > dyn) dyn = u->dyn;
+    const int err = set(dyn);
+    if (err == 0 && e != nullptr) *e = {kernel, ctx, dyn};
+    return err;
   }
 };
 
