@@ -456,3 +456,135 @@ def test_z_loss_of_rows_that_are_not_numbers(dev, row, want, E, kind):
         assert abs(got - z) <= 1e-4 * z  # (the rows' own error; what is tested is which rows count)
     else:
         assert got == want or (math.isnan(got) and math.isnan(want))
+
+
+def closed(l, ids, dw, dloss, counts, spans, kind, renorm, scale):
+    """(gradient, sum of the magnitudes of its terms, what exponentials below 2^-126 may add), in
+    64 bits from logarithms of the scores, so that no score leaves the range."""
+    E, K = l.shape[1], ids.shape[1]
+    soft = kind == "softmax"
+    ls = torch.log_softmax(l, 1) if soft else torch.nn.functional.logsigmoid(l)
+    rest = torch.ones_like(l) if soft else torch.sigmoid(-l)
+    p, sm, lse = torch.softmax(ls, 1), torch.softmax(l, 1), torch.logsumexp(l, 1, keepdim=True)
+    # sums of scores are at least the largest one's: a sigmoid where that is above e^-60, else 1
+    lost = lambda top: 2.0 ** -126 / torch.where((top >= -60) & (not soft), torch.sigmoid(top), 1.0)
+    g, mag, low = torch.zeros_like(l), torch.zeros_like(l), torch.zeros_like(l)
+    if dloss is not None:
+        Q, N = sum(b > a for a, b in spans), sum(b - a for a, b in spans)
+        f = lost(l.max(1, keepdim=True).values)
+        for q, (a, b) in enumerate(spans):
+            if b > a:
+                c = dloss[0] * E / (Q * K * (b - a) ** 2) * counts[q].double()
+                P, r = p[a:b], rest[a:b]
+                g[a:b] += P * (c - (P * c).sum(1, keepdim=True)) * r + 2 * dloss[1] / N * lse[a:b] * sm[a:b]
+                mag[a:b] += P * (c.abs() + (P * c.abs()).sum(1, keepdim=True)) * r + (2 * dloss[1] / N).abs() * (lse.abs() + 1)[a:b] * sm[a:b]
+                low[a:b] += 4 * E * f[a:b] * c.abs().max() + 2.0 ** -126 * (2 * dloss[1] / N).abs() * (lse.abs() + 1)[a:b]
+    if dw is not None:
+        at = ids.long()
+        a, r, d = ls.gather(1, at), rest.gather(1, at), dw.double()
+        u = torch.softmax(a, 1) if renorm else a.exp()
+        f = 4 * K * scale * (lost(l.gather(1, at).max(1, keepdim=True).values) if renorm else 2.0 ** -126) * d.abs().max(1, keepdim=True).values
+        if renorm:
+            t, m = scale * u * (d - (u * d).sum(1, keepdim=True)) * r, scale * u * (d.abs() + (u * d.abs()).sum(1, keepdim=True)) * r
+        else:
+            t, m = scale * u * d * r, scale * u * d.abs() * r
+        g.scatter_add_(1, at, t)
+        mag.scatter_add_(1, at, m)
+        low += f
+        if soft and not renorm:
+            g -= scale * p * (u * d).sum(1, keepdim=True)
+            mag += scale * p * (u * d.abs()).sum(1, keepdim=True)
+    return g, mag, low
+
+
+@pytest.mark.parametrize("kind,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("shift", [-200.0, -80.0, -61.0, -60.0, -59.0, 80.0])
+@pytest.mark.parametrize("parts", ["weights", "losses"])
+def test_gradient_of_far_logits(dev, parts, shift, kind, renorm):
+    """Every logit far from zero, only the chosen ones, or only the others: losses and gradients
+    where sigmoids become exponentials, on both sides of that border."""
+    T, E, K = 60, 48, 4
+    l = rand(5, T, E, gain=2.0)
+    ids = choose(rand(6, T, E), K, None, "softmax").to(torch.int32).contiguous()
+    chosen = torch.zeros(T, E, dtype=torch.bool, device=DEV).scatter_(1, ids.long(), True)
+    moved = torch.ones(T, E, dtype=torch.bool, device=DEV)
+    moved[20:40], moved[40:] = chosen[20:40], ~chosen[40:]
+    l = torch.where(moved, l + shift, l).contiguous()
+    spans = [(0, 10), (10, 33), (33, 60)]
+    begin, end = i32([a for a, _ in spans]), i32([b for _, b in spans])
+    d = l.double()
+    o = dev.balance_loss(l, ids, begin, end, score=kind)
+    balance, z, counts, sums, lse = losses(d, ids, spans, kind)
+    B, depth = rel(l), 320 * U
+    assert torch.equal(o["counts"].long(), counts)
+    assert ((o["prob_sums"].double() - sums).abs() <= (B + depth) * sums + T * 2.0 ** -126 / 2.0 ** -87).all()  # (e^-60 > 2^-87)
+    assert abs(float(o["loss"][0] - balance)) <= (B + depth + 64 * U) * float(balance) + 2.0 ** -30
+    top = float(lse.abs().max())
+    assert abs(float(o["loss"][1] - z)) <= 2 * top * (B + 2.0 ** -21 + top * U) + (depth + 64 * U) * float(z)
+    dw = rand(11, T, K) if parts == "weights" else None
+    dloss = torch.tensor([30.0, 0.5], device=DEV) if parts == "losses" else None
+    g = dev.route_grad(l, ids, dweights=dw, dloss=dloss, counts=o["counts"] if dloss is not None else None, seq_begin=begin, seq_end=end,
+                       score=kind, renorm=renorm, scale=1.5)
+    want, mag, low = closed(d, ids, dw, None if dloss is None else dloss.double(), counts, spans, kind, renorm, 1.5)
+    own = 2.0 ** -48 * mag.sum(1, keepdim=True)
+    assert ((g.double() - want).abs() <= 4 * B * mag + own + low + 1e-37).all()
+    if parts == "losses":  # the balance loss alone: the z loss's gradient is far larger where logits are
+        dloss = torch.tensor([30.0, 0.0], device=DEV)
+        g = dev.route_grad(l, ids, dloss=dloss, counts=o["counts"], seq_begin=begin, seq_end=end, score=kind, renorm=renorm)
+        want, mag, low = closed(d, ids, None, dloss.double(), counts, spans, kind, renorm, 1.0)
+        assert ((g.double() - want).abs() <= 4 * B * mag + 2.0 ** -48 * mag.sum(1, keepdim=True) + low + 1e-37).all()
+
+
+@pytest.mark.parametrize("kind,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("part", ["weights", "balance", "z"])
+def test_each_gradient_against_differences(dev, part, kind, renorm):
+    """Every part of the gradient alone, along itself, against differences of the forward calls.
+
+    With d the unit vector along the gradient, the difference over a step h is |g| but for three
+    errors: what the step cuts off (taken from the formulas in 64 bits, with the same d and h), the
+    forward values' rounding over h, and the gradient's own rounding. Together they may be a
+    twentieth of |g| at most, so that a gradient of zero, of half its size or of the other sign
+    fails."""
+    T, E, K, h, scale = 8, 16, 4, 0.5, 2.0
+    l, dw = rand(1, T, E), rand(2, T, K)
+    cols = torch.tensor([3, 7, 8, 14], device=DEV)
+    bias = torch.zeros(E, device=DEV).index_fill_(0, cols, 10.0)  # chooses these whatever the logits
+    ids = cols.to(torch.int32).repeat(T, 1).contiguous()
+    picked = torch.randint(0, E, (T, K), device=DEV, dtype=torch.int32, generator=torch.Generator(DEV).manual_seed(3))  # of the losses
+    counts = dev.balance_loss(l, picked, score=kind)["counts"]
+    c = {"weights": [0.0, 0.0], "balance": [1.0, 0.0], "z": [0.0, 1.0]}[part]
+    args = dict(dweights=dw) if part == "weights" else dict(dloss=torch.tensor(c, device=DEV), counts=counts)
+    g = dev.route_grad(l, ids if part == "weights" else picked, score=kind, renorm=renorm, scale=scale, **args).double()
+    size = float(g.norm())
+    d = g / size
+
+    def forward(x):  # the calls' value, and a bound on its rounding
+        if part == "weights":
+            o = dev.route(x, K, bias=bias, score=kind, renorm=renorm, scale=scale)
+            assert torch.equal(o["topk_ids"].sort(1).values, ids)
+            w = torch.zeros(T, E, device=DEV).scatter_(1, o["topk_ids"].long(), o["topk_weights"])[:, cols].double()
+            return float((w * dw).sum()), rel(x) * float((w * dw).abs().sum())
+        o = dev.balance_loss(x, picked, score=kind)["loss"]
+        depth, top = (1 + 8 + 304) * U / 2, float(torch.logsumexp(x.double(), 1).abs().max())
+        if part == "balance":
+            return float(o[0]), (rel(x) + depth + 64 * U) * float(o[0])
+        return float(o[1]), 2 * top * (rel(x) + 2.0 ** -21 + top * U) + (depth + 64 * U) * float(o[1])
+
+    def formula(x):
+        if part == "weights":
+            s = score(x, kind)[:, cols]
+            return (scale * (s / s.sum(1, keepdim=True) if renorm else s) * dw.double()).sum()
+        return losses(x, picked, [(0, T)], kind)[0 if part == "balance" else 1]
+
+    x0, x1 = (l.double() - h * d).float(), (l.double() + h * d).float()
+    moved = x1.double() - x0.double()  # the step as it is after its rounding
+    leaf = l.double().requires_grad_()
+    slope, = torch.autograd.grad(formula(leaf), leaf)
+    along = float((slope * moved).sum())
+    cut = abs(float(formula(x1.double()) - formula(x0.double())) - along)
+    (f0, e0), (f1, e1) = forward(x0), forward(x1)
+    mag = magnitudes(l.double(), ids if part == "weights" else picked, dw if part == "weights" else None,
+                     None if part == "weights" else torch.tensor(c, device=DEV, dtype=torch.float64), counts, [(0, T)], kind, renorm, scale)
+    tol = cut + e0 + e1 + float((4 * rel(l) * mag * moved.abs()).sum())
+    assert tol <= 0.05 * 2 * h * size
+    assert abs((f1 - f0) - float((g * moved).sum())) <= tol
