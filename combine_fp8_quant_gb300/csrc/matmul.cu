@@ -12,7 +12,7 @@
 //  - an expert's rows sit on the N side, whose size is set per instruction in
 //    steps of 16: a tile of 40 rows costs 48 columns, not 128 (experts of a
 //    prefill hold a few hundred rows, of a decode batch a few), and the rows of
-//    an expert are cut into equal tiles of at most 256;
+//    an expert are cut into equal tiles of at most 256 (e4m3: 240, e2m1: 208);
 //  - the epilogue reads tensor memory as 8x8 fragments, transposes them through
 //    a small staging area (stmatrix) and stores 16-byte pieces of output rows.
 // With a gated activation a tile of 128 weight rows is 64 gate and 64 up rows
@@ -26,9 +26,10 @@
 // 128 x 256 tile takes 768 cycles at 128 bytes a cycle where the products take
 // 512 (measured 727); a pair moves 32 KB.
 // Warp roles: 0 and 8 load (TMA), 1 (of the pair's first CTA) issues the products, 2
-// and 3 lay out the e4m3 scales, or 2 zeroes the last lines of kGradW, 4-7 the
-// epilogue, one warp per 32 lanes of tensor memory; two accumulators (columns
-// 0.. and kRows..) let the epilogue of a tile overlap the products of the next.
+// and 3 lay out the e4m3 scales, or 2 copies the e2m1 scales and 3, 9 and 10 lay them
+// out, or 2 zeroes the last lines of kGradW, 4-7 the epilogue, one warp per 32 lanes of
+// tensor memory; two accumulators (columns 0.. and kRows..) let the epilogue of a tile
+// overlap the products of the next.
 // The grid is persistent; the tile list is formed on the device from the
 // segment ends, so a captured graph can be replayed with other counts.
 //
@@ -157,7 +158,7 @@ struct Tile {
   int tail;         // kGradW: valid lines of the last block
 };
 
-__device__ __forceinline__ int box_index(int half) {  // smallest box of at least `half` rows
+__host__ __device__ constexpr int box_index(int half) {  // smallest box of at least `half` rows
   int i = 0;
   while (i < kBoxes - 1 && box_rows(i) < half) ++i;
   return i;
@@ -930,7 +931,7 @@ __global__ void __launch_bounds__(kThreadsOf<KIND>, 1)
         __syncwarp();  // every lane's words before the arrival
         // The columns are free when the products of the piece before the last are done (before
         // there was any, a buffer's first phase passes at once). Those of the blocks that had
-        // these blocks' stages are done then as well (there are at least four stages), so the
+        // these blocks' stages are done then as well (there are at least four stages: launch), so the
         // arrivals count for these.
         const int old = sf_it >= 2 ? sf_it - 2 : sf_it - 2 + kBufs;
         const uint32_t oph = sf_it >= 2 ? (old / kBufs) & 1 : 1;
@@ -1157,6 +1158,8 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
   const size_t lists = (size_t)(4 * a.L + 1) * sizeof(int32_t) + kStageBytes +
                        (KIND != kHalf ? kScaleBufs<KIND> * kScaleBytes<KIND> : 0);
   a.ring_bytes = (int32_t)((smem - 1024 - lists) / 1024 * 1024);
+  // the warps that lay out the scales of e2m1 operands count on four stages
+  if (is_fp4(KIND) && a.ring_bytes < 4 * (kABytes + box_rows(box_index(kRows<KIND> / 2)) * 128)) return cudaErrorInvalidConfiguration;
   err = opt_in_smem(matmul_kernel<MODE, KIND>, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -1194,7 +1197,7 @@ cudaError_t launch(const Maps& maps, Args a, int64_t max_tiles, int num_sms, cud
 Args common_args(const MatmulArgs& m) {
   Args a{};
   a.seg_begin = m.seg_begin; a.seg_end = m.seg_end; a.cap = m.cap;
-  a.R = (int32_t)m.R; a.L = m.L; 
+  a.R = (int32_t)m.R; a.L = m.L;
   a.f16 = m.type == kF16 || (m.type != kBF16 && m.out_type == kF16);
   a.terms = m.terms;
   a.status = m.status;

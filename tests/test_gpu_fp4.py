@@ -661,3 +661,19 @@ def test_few_rows_of_large_matrices(dev, R, K, N, gated, fmt):
                                              out_dtype=torch.float16, **o)
     less = -call()
     assert torch.equal(call(residual=less), call(residual=less, starts=i32([0]), psum=i32([R])))
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_product_of_the_most_experts(dev, fmt):
+    """1024 experts, whose lists leave the least room for stages, and tiles of the most rows."""
+    L, K, N = 1024, 1088, 16
+    counts = [e % 3 for e in range(L)]
+    counts[5], counts[700], counts[1023] = 208, 417, 208
+    starts, ends, R = segments(counts, 1)
+    x = rand(1, R, K)
+    q = dev.quant_fp4(x, fmt=fmt)
+    w, wsc, wts, wv = weights(dev, 2, L, 2 * N, K, fmt)
+    st = i32([0])
+    out = dev.expert_matmul_fp4(q["xq"], w, q["scales"], wsc, fmt=fmt, starts=i32(starts), psum=i32(ends), w_tscale=wts, act="silu", gated=True, status=st)
+    assert dev.moe_status_sync(st) == dev.MOE_OK
+    check(out, quantise(x, fmt)[2], wv, None, None, list(zip(starts, ends)), N, "silu", True)
