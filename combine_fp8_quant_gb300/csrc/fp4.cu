@@ -3,7 +3,7 @@
 //
 // Large batches are bound by HBM: a bf16 row is read once (2 bytes an element) and leaves as
 // 0.5 bytes and its scales (1/16 or 1/32): 16384 x 7168 in 48 us with scales per 32 (6.2
-// TB/s), 57 with scales per 16 (5.3 TB/s, the division and its correction), the way back in
+// TB/s), 58 with scales per 16 (5.2 TB/s, the division and its correction), the way back in
 // 53 and 56 (5.6 and 5.3 TB/s). A lane owns 16 elements, so that a group of
 // 16 needs no exchange and one of 32 a single one; a warp covers 512 elements of a row
 // at a time, whose scales are one or two whole pieces.

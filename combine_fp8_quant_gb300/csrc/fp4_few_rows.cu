@@ -181,8 +181,8 @@ __global__ void __launch_bounds__(kThreads) few_rows_kernel(FewArgs p) {
 }
 
 // A warp's step takes two weight rows 32 elements a lane: the time is that of the launch and of
-// x, which grows with K, and about 0.24 us for each 1024 steps of all weight rows (two rows of
-// x: 0.3). The tensor cores take 9 us and then the weights' time from HBM. Measured, matrices in
+// x, which grows with K, and about 0.25 us for each 1024 steps of all weight rows (two rows of
+// x: 0.35). The tensor cores take 9 us and then the weights' time from HBM. Measured, matrices in
 // turn so that they come from HBM, here against there in us (scales per 16; those per 32 lie
 // within 0.8):
 //   one row    2048 -> 7168 4.9 / 9.3, 4096 -> 8192 10.3 / 11.5, 7168 -> 4096 11.0 / 12.2, 8192 -> 4096

@@ -629,7 +629,9 @@ typedef enum {
  * left, the last ids are -1 (which the dispatches drop) with weight 0. With SOFTMAX a
  * logit of NaN or +infinity makes every s of its token NaN: weights with renorm 0, and
  * with a bias no expert is chosen. Keys are compared as if computed in 64 bits: two that
- * 32 bits cannot tell apart are computed again. Weights are computed in fp32.
+ * 32 bits cannot tell apart are computed again. Such tokens take longer; where they are most
+ * (a bias over softmax scores of close logits, or K of 14 and more), the call takes several
+ * times as long, forty at worst. Weights are computed in fp32.
  *   logits [T, ldl]              BF16, F16 or F32, ldl >= E, any alignment of the type
  *   d_num_tokens (optional)      live tokens n; rows t >= n of the outputs are not written
  *   E (1..1024), K (1..32, <= E), bias [E] f32 (optional)
