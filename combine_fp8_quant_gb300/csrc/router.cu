@@ -161,9 +161,10 @@ __device__ __forceinline__ float sigmoid_rest(float l) {
   return (l < 0.0f ? 1.0f : x) * fast_rcp(1.0f + x);
 }
 
-// Where every logit of a set is below this, its sigmoids are exponentials (to
-// 2^-86) that may leave the range of a float, and their ratios are those of a softmax.
-constexpr float kFarBelow = -60.0f;
+// Where every logit of a set is below this, its sigmoids are exponentials (to 2^-28, less than
+// fp32 rounds by) that may leave the range of a float, and their ratios are those of a
+// softmax. Above it a ratio is lost where its sigmoid is below 2^-126: one below 2^-97.
+constexpr float kFarBelow = -20.0f;
 
 // Normalised scores of a token over all experts: softmax, or sigmoids over their
 // sum. m: the largest logit (-inf: a row without any, whose scores are 0). rest: 1

@@ -466,8 +466,8 @@ def closed(l, ids, dw, dloss, counts, spans, kind, renorm, scale):
     ls = torch.log_softmax(l, 1) if soft else torch.nn.functional.logsigmoid(l)
     rest = torch.ones_like(l) if soft else torch.sigmoid(-l)
     p, sm, lse = torch.softmax(ls, 1), torch.softmax(l, 1), torch.logsumexp(l, 1, keepdim=True)
-    # sums of scores are at least the largest one's: a sigmoid where that is above e^-60, else 1
-    lost = lambda top: 2.0 ** -126 / torch.where((top >= -60) & (not soft), torch.sigmoid(top), 1.0)
+    # sums of scores are at least the largest one's: a sigmoid where that is above e^-20, else 1
+    lost = lambda top: 2.0 ** -126 / torch.where((top >= -20) & (not soft), torch.sigmoid(top), 1.0)
     g, mag, low = torch.zeros_like(l), torch.zeros_like(l), torch.zeros_like(l)
     if dloss is not None:
         Q, N = sum(b > a for a, b in spans), sum(b - a for a, b in spans)
@@ -498,7 +498,7 @@ def closed(l, ids, dw, dloss, counts, spans, kind, renorm, scale):
 
 
 @pytest.mark.parametrize("kind,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
-@pytest.mark.parametrize("shift", [-200.0, -80.0, -61.0, -60.0, -59.0, 80.0])
+@pytest.mark.parametrize("shift", [-200.0, -80.0, -61.0, -60.0, -59.0, -21.0, -20.0, -19.0, 80.0])
 @pytest.mark.parametrize("parts", ["weights", "losses"])
 def test_gradient_of_far_logits(dev, parts, shift, kind, renorm):
     """Every logit far from zero, only the chosen ones, or only the others: losses and gradients
@@ -517,7 +517,7 @@ def test_gradient_of_far_logits(dev, parts, shift, kind, renorm):
     balance, z, counts, sums, lse = losses(d, ids, spans, kind)
     B, depth = rel(l), 320 * U
     assert torch.equal(o["counts"].long(), counts)
-    assert ((o["prob_sums"].double() - sums).abs() <= (B + depth) * sums + T * 2.0 ** -126 / 2.0 ** -87).all()  # (e^-60 > 2^-87)
+    assert ((o["prob_sums"].double() - sums).abs() <= (B + depth) * sums + T * 2.0 ** -126 / 2.0 ** -29).all()  # (e^-20 > 2^-29)
     assert abs(float(o["loss"][0] - balance)) <= (B + depth + 64 * U) * float(balance) + 2.0 ** -30
     top = float(lse.abs().max())
     assert abs(float(o["loss"][1] - z)) <= 2 * top * (B + 2.0 ** -21 + top * U) + (depth + 64 * U) * float(z)
@@ -588,3 +588,27 @@ def test_each_gradient_against_differences(dev, part, kind, renorm):
     tol = cut + e0 + e1 + float((4 * rel(l) * mag * moved.abs()).sum())
     assert tol <= 0.05 * 2 * h * size
     assert abs((f1 - f0) - float((g * moved).sum())) <= tol
+
+
+@pytest.mark.parametrize("top", [-100.0, -61.0, -59.0, -40.0, -21.0, -20.5, -20.0, -19.5, -5.0])
+def test_sigmoid_ratios_of_spread_logits(dev, top):
+    """Renormalised sigmoids far below zero and far apart: every ratio above 2^-126 e^20 is there, in the
+    weights, their gradient, the probabilities and theirs."""
+    T, E, K = 30, 40, 6
+    l = top - rand(1, T, E).abs() * 15.0
+    l[:, 7] = top
+    o = dev.route(l, K, score="sigmoid", scale=2.0)
+    ids = choose(l, K, None, "sigmoid")
+    assert torch.equal(o["topk_ids"].long(), ids)
+    low = 2.0 ** -126 * math.exp(20.0)
+    d = torch.nn.functional.logsigmoid(l.double())
+    want = 2.0 * torch.softmax(d.gather(1, ids), 1)
+    assert ((o["topk_weights"].double() - want).abs() <= rel(l) * want + 2.0 * low).all()
+    p, b = torch.softmax(d, 1).sum(0), dev.balance_loss(l, o["topk_ids"], score="sigmoid")
+    assert ((b["prob_sums"][0].double() - p).abs() <= (rel(l) + 320 * U) * p + T * low).all()
+    dw, dloss = rand(3, T, K), torch.tensor([30.0, 0.0], device=DEV)
+    for kw in (dict(dweights=dw), dict(dloss=dloss, counts=b["counts"])):
+        g = dev.route_grad(l, o["topk_ids"], score="sigmoid", scale=2.0, **kw)
+        want, mag, less = closed(l.double(), o["topk_ids"], kw.get("dweights"), dloss.double() if "dloss" in kw else None, b["counts"], [(0, T)],
+                                 "sigmoid", True, 2.0)
+        assert ((g.double() - want).abs() <= 4 * rel(l) * mag + 2.0 ** -48 * mag.sum(1, keepdim=True) + less + 1e-37).all()
