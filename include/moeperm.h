@@ -599,7 +599,8 @@ moe_status_t moe_dispatch_fp4(
  *   w [L, N or 2N, K / 2]        dense; w_scales, ld_ws: pieces of the L*N (L*2N) weight rows
  *   x_tscale [1], w_tscale [L]   (optional, NV only)
  *   out [R, ldo], residual       BF16 or F16
- * MOE_FP4_E8M0 and MOE_FP4_MX are the same to this call. Launches: 1.
+ * Values and sums of 32 of them lie within fp32's range (beyond it P may be infinite, whatever
+ * the weights). MOE_FP4_E8M0 and MOE_FP4_MX are the same to this call. Launches: 1.
  */
 moe_status_t moe_expert_matmul_fp4(
     const void* x, int64_t ldx, const void* x_scales, int64_t ld_xs, const float* x_tscale, int64_t R,
